@@ -38,7 +38,7 @@ extern "C" {
 #endif
 
 /* ---- element types ---------------------------------------------------------------- */
-enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_I32 = 3 };
+enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_I32 = 3, PA_U8 = 4 };
 
 /* ---- return codes ------------------------------------------------------------------ */
 #define PA_OK                 0
@@ -63,6 +63,7 @@ enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_I32 = 3 };
 #define PA_DEV_BAD_LEN    0x4   /* decode: context_len < 0 or > max_blocks*block_size */
 #define PA_DEV_BAD_COPY   0x8   /* copy_blocks: frame id outside [0, num_blocks) */
 #define PA_DEV_TIMEOUT    0x10  /* a bounded wait inside a kernel gave up */
+#define PA_DEV_BAD_POS    0x20  /* rotating append: position >= rows of cos_sin */
 
 typedef struct pa_tensor {
   void*   data;       /* device (or host, where stated) pointer to element [0,...,0] */
@@ -103,6 +104,8 @@ int pa_cache_append(const pa_tensor* k_new, const pa_tensor* v_new,
  * [VM "Key Architectural Mechanics / 2. Zero-Copy Branching via Copy-on-Write":
  * only the one shared frame being written is duplicated.]
  *
+ *   k_cache, v_cache  any cache of frames: [num_blocks, B, H, D] as for pa_cache_append,
+ *           or the 4-bit rows [num_blocks, H, B, 5 D / 8] of PA_U8 (pa_cache_append_q4).
  *   pairs   int32 [n, 2], row = (src frame, dst frame); contiguous.  Both caches
  *           get cache[dst] = cache[src].  Ids outside [0, num_blocks) set
  *           PA_DEV_BAD_COPY and the pair is skipped.  Destinations must be
@@ -289,6 +292,147 @@ int pa_decode_ex(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
 int pa_decode_static(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
                      const pa_tensor* block_tables, const pa_tensor* context_lens,
                      float scale, const pa_tensor* out, pa_stream stream);
+
+/* ===================================================================================
+ * Rotary, 4-bit and block-sparse attention over the paged cache
+ * ===================================================================================
+ * These calls share query heads among key heads: q and out hold Hq = g * H heads, query
+ * head j reads key head j / g, 1 <= g <= 16.  dtype fp16 or bf16 where not said
+ * otherwise, D in {64, 128}, block sizes B in {8, 16, 32, 64, 128, 256}; else
+ * PA_ERR_UNSUPPORTED.
+ * Decode workspaces: as for pa_decode, one per (device, stream).  A CUDA graph keeps the
+ * workspace of the stream it was captured on, also when later calls need a larger one
+ * (the older buffer stays until pa_shutdown); two graphs captured on one stream share it,
+ * so they must not run at the same time.  A call under capture that needs a larger
+ * workspace than its stream has returns PA_ERR_SCRATCH_LIMIT and leaves the capture
+ * valid: make the same call once before capturing. */
+
+/*
+ * pa_cache_append_rope -- pa_cache_append with the position rotation applied to the keys
+ * on the way, and to the queries of the same tokens.
+ *
+ *   k_new, v_new, slot_mapping, k_cache, v_cache  as for pa_cache_append (f32, f16, bf16).
+ *   positions   int32 [T]: position of each token.  < 0 = padding: nothing of the token
+ *               is written.  >= P sets PA_DEV_BAD_POS, nothing of the token is written.
+ *   cos_sin     f32 [P, R], row stride free (16-byte multiple): row p holds cos(p w_i) for
+ *               i < R/2, then sin(p w_i).  R a multiple of 16, R <= D: the first R elements
+ *               of a head are rotated, the others copied.
+ *   interleaved 0: element i pairs with i + R/2;  1: element 2i pairs with 2i + 1.
+ *   q, q_out    [T, Hq, D] (cache dtype) or both NULL; rows as for k_new, any Hq >= 1.
+ *               q_out may be q itself.  A token whose slot is < 0 or out of range still
+ *               has its query rotated.
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin) in fp32, rounded once.
+ * D * element size must be a multiple of 16 and at most 512 bytes, else
+ * PA_ERR_UNSUPPORTED.  Slots within one call must be distinct.
+ */
+int pa_cache_append_rope(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* slot_mapping,
+                         const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* positions,
+                         const pa_tensor* cos_sin, int32_t interleaved, const pa_tensor* q,
+                         const pa_tensor* q_out, pa_stream stream);
+
+/* ---- the 4-bit cache: k_cache, v_cache PA_U8 [num_blocks, H, B, W], contiguous, W = 5 D / 8.
+ * The W bytes of a row hold one token of one head: D/2 bytes of codes, element 2i in the
+ * low half of byte i and element 2i + 1 in its high half, then for each group of 32
+ * elements two fp16 numbers, step and offset.  A code n stands for the fp16 number
+ * nearest to step * n + offset (one rounding).  A group is held as
+ *     offset = fp16(min x),  step = fp16((max x - offset) * fp32(1/15)),
+ *     n = round-half-even((x - offset) / step) clamped to [0, 15], 0 where step is 0,
+ * with x clamped to +-65024 first; a group with a NaN or an infinity gets n = 0, step = offset =
+ * NaN and reads back as NaN. */
+
+/*
+ * pa_cache_append_q4 -- append into the 4-bit cache: the arguments of
+ * pa_cache_append_rope (f16, bf16); keys are quantised from the fp32 rotated values.
+ * positions, cos_sin, q and q_out all NULL: no rotation.
+ */
+int pa_cache_append_q4(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* slot_mapping,
+                       const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* positions,
+                       const pa_tensor* cos_sin, int32_t interleaved, const pa_tensor* q,
+                       const pa_tensor* q_out, pa_stream stream);
+
+/*
+ * pa_cache_read_q4 -- rows of the 4-bit cache as 16-bit rows (for pa_prefill over a
+ * cached prefix, inspection): k_out, v_out [T, H, D] = the numbers held at slot_mapping
+ * [T].  slot < 0: that output row is left as it was; slot >= num_blocks * B:
+ * PA_DEV_BAD_SLOT and the row is left as it was.  The same slot may be read often.
+ */
+int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* slot_mapping,
+                     const pa_tensor* k_out, const pa_tensor* v_out, pa_stream stream);
+
+/*
+ * pa_decode_q4 -- pa_decode over the 4-bit cache.  q, out [S, Hq, D]; block_tables,
+ * context_lens, scale, empty sequences and status bits as for pa_decode.  Slots that hold no token
+ * of a sequence may hold any bits.  The numbers the codes stand for are exact in fp16;
+ * q.k and the weighted sums of values run on the tensor cores with fp32 accumulation,
+ * softmax in fp32, the weights carried as two fp16 parts for fp16 outputs (for bf16
+ * outputs one part where g > 4), one rounding to the output dtype.  bf16 queries are
+ * scaled by a power of two per head to fp16 range; an element below 2^-14 of its head's
+ * largest loses bits of weight below 2^-25 of that largest.
+ */
+int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                 const pa_tensor* block_tables, const pa_tensor* context_lens, float scale,
+                 const pa_tensor* out, pa_stream stream);
+
+/* ---- block-sparse decode: the frames of a sequence whose keys can give a query the
+ * largest products, and attention over those alone. */
+
+/*
+ * pa_block_bounds -- for each frame that holds tokens first_tokens[s] .. L_s - 1 of a
+ * sequence, the elementwise smallest and largest key over all its tokens (those before
+ * first_tokens[s] too): bounds[frame][h][0][:] and [1][:].  Call it after an append with
+ * the first new token of each sequence (after copy-on-write too: the new tail frame holds
+ * the first new token).
+ *
+ *   k_cache       [num_blocks, B, H, D] f16 / bf16, as for pa_cache_append.
+ *   block_tables, context_lens  as for pa_decode;  first_tokens int32 [S], or NULL: 0.
+ *   bounds        [num_blocks, H, 2, D] (k_cache dtype), contiguous.  Frames of no listed
+ *                 token are left as they were.
+ * first_tokens[s] >= L_s: nothing for s.  first_tokens[s] < 0 or a bad L_s:
+ * PA_DEV_BAD_LEN, nothing for s.  A NaN key element counts for neither bound unless the
+ * frame holds no other.
+ */
+int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, const pa_tensor* context_lens,
+                    const pa_tensor* first_tokens, const pa_tensor* bounds, pa_stream stream);
+
+/*
+ * pa_select_blocks -- the K frames of each sequence and key head with the largest scores.
+ *
+ *   score(query, frame) = sum_d max(q_d * min_d, q_d * max_d), an upper bound of q . k over
+ *   the frame's keys; a frame's score for a key head is the largest over its g queries.
+ *   The sum is one of fp32 in a fixed order, so that the choice does not depend on the
+ *   machine: neighbouring products (d = 0 and 1, 2 and 3, ...) are added, then
+ *   neighbouring sums, until one is left.
+ *   The first keep_first and the last keep_last frames of a sequence rank above all
+ *   others; equal ranks go to the lower frame position.
+ *
+ *   q             [S, Hq, D];  bounds [num_blocks, H, 2, D] of the same dtype.
+ *   block_tables, context_lens  as for pa_decode;  block_size = B of the cache.
+ *   selected      int32 [S, H, K], K >= 1, inner stride 1: positions in the sequence's
+ *                 block table, ascending; -1 behind the last where the sequence has fewer
+ *                 than K frames.
+ * Bounds and queries must be finite (a NaN or infinite score ranks somewhere, no more is
+ * said).  A bad length or frame id sets its status bit; a bad L_s selects nothing, a frame
+ * with a bad id ranks last.  Uses the (device, stream) workspace for the scores.
+ */
+int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tensor* block_tables,
+                     const pa_tensor* context_lens, int32_t block_size, int32_t keep_first,
+                     int32_t keep_last, const pa_tensor* selected, pa_stream stream);
+
+/*
+ * pa_decode_selected -- pa_decode over the listed frames alone.
+ *
+ *   q, out        [S, Hq, D];  k_cache, v_cache [num_blocks, B, H, D], same dtype.
+ *   selected      int32 [S, H, K] as pa_select_blocks leaves it: the list of a (sequence,
+ *                 key head) ends at its first -1, at K entries, or at as many entries as
+ *                 the sequence has frames; its order does not matter, and a frame listed
+ *                 twice counts twice.  An entry outside [0, ceil(L_s/B)) sets
+ *                 PA_DEV_BAD_BLOCK and zeroes the output rows of that head.
+ * Lists without a frame give zero rows.  Slots that hold no token may hold any bits.
+ * Arithmetic as for pa_decode_q4, the weights carried as two parts of the cache dtype.
+ */
+int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                       const pa_tensor* block_tables, const pa_tensor* context_lens,
+                       const pa_tensor* selected, float scale, const pa_tensor* out, pa_stream stream);
 
 /* Synchronises `stream` (and then the device), returns the current device's sticky
  * PA_DEV_* bits in *status_out and clears them.  When PA_DEV_TIMEOUT was set, the

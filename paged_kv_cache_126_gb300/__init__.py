@@ -15,6 +15,7 @@ from ._binding import (  # noqa: F401
     PA_DEV_BAD_BLOCK,
     PA_DEV_BAD_COPY,
     PA_DEV_BAD_LEN,
+    PA_DEV_BAD_POS,
     PA_DEV_BAD_SLOT,
     PA_DEV_TIMEOUT,
     PA_ERR_OUT_OF_BLOCKS,
@@ -33,6 +34,13 @@ from ._binding import (  # noqa: F401
     pa_decode_split,
     pa_decode_static,
     pa_prefill,
+    pa_cache_append_rope,
+    pa_cache_append_q4,
+    pa_cache_read_q4,
+    pa_decode_q4,
+    pa_block_bounds,
+    pa_select_blocks,
+    pa_decode_selected,
     pa_step_decode,
     pa_get_device_status,
     pa_selftest_wait_timeout,

@@ -15,7 +15,7 @@ import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa.so")
 
-PA_F32, PA_F16, PA_BF16, PA_I32 = 0, 1, 2, 3
+PA_F32, PA_F16, PA_BF16, PA_I32, PA_U8 = 0, 1, 2, 3, 4
 PA_OK = 0
 PA_WARN_DOUBLE_FREE = 1
 PA_ERR_INVALID = -1
@@ -32,8 +32,10 @@ PA_DEV_BAD_BLOCK = 0x2
 PA_DEV_BAD_LEN = 0x4
 PA_DEV_BAD_COPY = 0x8
 PA_DEV_TIMEOUT = 0x10
+PA_DEV_BAD_POS = 0x20
 
-_TORCH_DT = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.int32: PA_I32}
+_TORCH_DT = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.int32: PA_I32,
+             torch.uint8: PA_U8}
 
 
 class PaTensor(C.Structure):
@@ -78,6 +80,13 @@ def _load():
         "pa_prefill": ([P, P, P, P, P, P, C.c_float, P, vp], C.c_int),
         "pa_cache_append_split": ([P, P, P, P, P, vp], C.c_int),
         "pa_decode_split": ([P, P, P, P, P, C.c_float, P, vp], C.c_int),
+        "pa_cache_append_rope": ([P, P, P, P, P, P, P, C.c_int32, P, P, vp], C.c_int),
+        "pa_cache_append_q4": ([P, P, P, P, P, P, P, C.c_int32, P, P, vp], C.c_int),
+        "pa_cache_read_q4": ([P, P, P, P, P, vp], C.c_int),
+        "pa_decode_q4": ([P, P, P, P, P, C.c_float, P, vp], C.c_int),
+        "pa_block_bounds": ([P, P, P, P, P, vp], C.c_int),
+        "pa_select_blocks": ([P, P, P, P, C.c_int32, C.c_int32, C.c_int32, P, vp], C.c_int),
+        "pa_decode_selected": ([P, P, P, P, P, P, C.c_float, P, vp], C.c_int),
         "pa_get_device_status": ([vp, i32p], C.c_int),
         "pa_strerror": ([C.c_int], C.c_char_p),
         "pa_launch_count": ([], C.c_int64),
@@ -128,6 +137,8 @@ EXPORTED = (
     "pa_bm_num_seqs", "pa_bm_add_seq_cached", "pa_bm_step_tokens", "pa_bm_extend_tokens", "pa_bm_cached_frames",
     "pa_bm_fork_many", "pa_bm_free_many", "pa_step_decode", "pa_bm_usage", "pa_selftest_wait_timeout",
     "pa_bm_export",
+    "pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",
+    "pa_select_blocks", "pa_decode_selected",
 )
 
 
@@ -298,6 +309,76 @@ def pa_decode_split(q, k_cache, v_cache, block_tables, context_lens, scale, out,
     ds = [tensor_desc(t) for t in (q, k_cache, v_cache, block_tables, context_lens)]
     o = tensor_desc(out)
     _check(LIB.pa_decode_split(*map(_ref, ds), C.c_float(scale), C.byref(o), st), "pa_decode_split")
+    return out
+
+
+def _opt(t):
+    """Descriptor reference of an optional tensor argument (None: NULL)."""
+    return None if t is None else C.byref(tensor_desc(t))
+
+
+def pa_cache_append_rope(k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin, q=None, q_out=None,
+                         interleaved=False, stream=None) -> None:
+    """``pa_cache_append_rope``: append with the keys rotated on the way, and q rotated into q_out
+    (which may be q); positions int32 [T], cos_sin float32 [P, R]."""
+    st = _stream_of(k_cache, stream)
+    ds = [tensor_desc(t) for t in (k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin)]
+    _check(LIB.pa_cache_append_rope(*map(_ref, ds), int(interleaved), _opt(q), _opt(q_out), st), "pa_cache_append_rope")
+
+
+def pa_cache_append_q4(k_new, v_new, slot_mapping, k_cache, v_cache, positions=None, cos_sin=None, q=None, q_out=None,
+                       interleaved=False, stream=None) -> None:
+    """``pa_cache_append_q4``: append into the 4-bit caches, uint8 [num_blocks, H, B, 5 D / 8] (see
+    include/pa.h), rotated on the way where positions and cos_sin are given."""
+    st = _stream_of(k_cache, stream)
+    ds = [tensor_desc(t) for t in (k_new, v_new, slot_mapping, k_cache, v_cache)]
+    _check(LIB.pa_cache_append_q4(*map(_ref, ds), _opt(positions), _opt(cos_sin), int(interleaved), _opt(q), _opt(q_out),
+                                  st), "pa_cache_append_q4")
+
+
+def pa_cache_read_q4(k_cache, v_cache, slot_mapping, k_out, v_out, stream=None) -> None:
+    """``pa_cache_read_q4``: the 4-bit rows at slot_mapping [T] as 16-bit rows [T, H, D]."""
+    st = _stream_of(k_cache, stream)
+    ds = [tensor_desc(t) for t in (k_cache, v_cache, slot_mapping, k_out, v_out)]
+    _check(LIB.pa_cache_read_q4(*map(_ref, ds), st), "pa_cache_read_q4")
+
+
+def pa_decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out, stream=None):
+    """``pa_decode_q4``: decode attention over the 4-bit caches into ``out`` [S, Hq, D]."""
+    st = _stream_of(q, stream)
+    ds = [tensor_desc(t) for t in (q, k_cache, v_cache, block_tables, context_lens)]
+    o = tensor_desc(out)
+    _check(LIB.pa_decode_q4(*map(_ref, ds), scale, C.byref(o), st), "pa_decode_q4")
+    return out
+
+
+def pa_block_bounds(k_cache, block_tables, context_lens, first_tokens, bounds, stream=None):
+    """``pa_block_bounds``: smallest and largest key of each frame that holds tokens from
+    first_tokens[s] (None: 0) on, into ``bounds`` [num_blocks, H, 2, D]."""
+    st = _stream_of(k_cache, stream)
+    ds = [tensor_desc(t) for t in (k_cache, block_tables, context_lens)]
+    b = tensor_desc(bounds)
+    _check(LIB.pa_block_bounds(*map(_ref, ds), _opt(first_tokens), C.byref(b), st), "pa_block_bounds")
+    return bounds
+
+
+def pa_select_blocks(q, bounds, block_tables, context_lens, block_size, selected, keep_first=1, keep_last=1, stream=None):
+    """``pa_select_blocks``: positions of the frames with the largest scores, into ``selected``
+    (int32 [S, H, K], ascending, -1 behind the last)."""
+    st = _stream_of(q, stream)
+    ds = [tensor_desc(t) for t in (q, bounds, block_tables, context_lens)]
+    o = tensor_desc(selected)
+    _check(LIB.pa_select_blocks(*map(_ref, ds), int(block_size), int(keep_first), int(keep_last), C.byref(o), st),
+           "pa_select_blocks")
+    return selected
+
+
+def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, selected, scale, out, stream=None):
+    """``pa_decode_selected``: decode attention over the listed frames into ``out`` [S, Hq, D]."""
+    st = _stream_of(q, stream)
+    ds = [tensor_desc(t) for t in (q, k_cache, v_cache, block_tables, context_lens, selected)]
+    o = tensor_desc(out)
+    _check(LIB.pa_decode_selected(*map(_ref, ds), scale, C.byref(o), st), "pa_decode_selected")
     return out
 
 

@@ -21,7 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 
 SOURCES = ["block_manager.cpp", "api.cu", "append.cu", "decode_f16.cu", "decode_bf16.cu", "decode_f32.cu",
-           "prefill.cu", "decode_split.cu", "decode_shared.cu"]
+           "prefill.cu", "decode_split.cu", "decode_shared.cu", "rotary.cu", "decode_q4.cu", "decode_selected.cu",
+           "select.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 
 

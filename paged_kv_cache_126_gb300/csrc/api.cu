@@ -11,6 +11,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "decode_kernel.cuh"
 #include "pa.h"
@@ -190,16 +191,23 @@ int make_half_rows_map(CUtensorMap* map, void* base, int dtype, int64_t rows, in
 // Layout: [0, 256) scheduler counters | arrival counters, one per (sequence, head) |
 // per-launch offsets and split partials.  Both counter regions must hold zeros
 // when a launch starts; every decode launch leaves them zero.  They are zeroed when
-// first allocated and whenever the arrival-counter region grows.
+// first allocated.  A buffer keeps its address and its layout for good: a CUDA graph
+// captured from a call goes on using the buffer that the call was given, and its counters
+// stay where they were.  A call that needs more gets a new, larger buffer, and the old one
+// waits for pa_shutdown (each is at least twice the one before, so all old ones together
+// are smaller than the one in use).
 constexpr size_t kSchedBytes = 256;
+constexpr size_t kMinCntBytes = 64 * 1024;
 
 struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
-  size_t cnt_bytes = 0;  // arrival-counter region known to hold zeros
+  size_t cnt_bytes = 0;  // size of the arrival-counter region
+  bool zeroed = false;   // the counter regions hold zeros
 };
 std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+std::vector<std::pair<int, void*>> g_ws_old;  // (device, buffer) that captured graphs may still use
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -213,38 +221,43 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
     return PA_ERR_HOST_MEMORY;
   }
   Workspace& w = *wp;
-  const size_t cnt = std::max(round256(cnt_need), w.cnt_bytes);
-  const size_t bytes = kSchedBytes + cnt + rest_bytes;
-  if (w.bytes < bytes) {
-    if (w.ptr) {
-      // the old buffer may still be used by earlier launches on this stream
-      if (cudaStreamSynchronize(stream) != cudaSuccess) return PA_ERR_CUDA;
-      cudaFree(w.ptr);
-      w.ptr = nullptr;
-      w.bytes = 0;
-      w.cnt_bytes = 0;
+  size_t cnt = std::max(round256(cnt_need), std::max(w.cnt_bytes, kMinCntBytes));
+  if (!w.ptr || w.cnt_bytes < cnt || w.bytes < kSchedBytes + cnt + rest_bytes) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
+    // an allocation would end the capture with an error
+    if (cap != cudaStreamCaptureStatusNone) return PA_ERR_SCRATCH_LIMIT;
+    if (w.ptr && w.cnt_bytes < cnt) cnt = std::max(cnt, 2 * w.cnt_bytes);
+    const size_t bytes = std::max(std::max(kSchedBytes + cnt + rest_bytes, static_cast<size_t>(1) << 20), 2 * w.bytes);
+    try {
+      g_ws_old.reserve(g_ws_old.size() + 1);
+    } catch (...) {
+      return PA_ERR_HOST_MEMORY;
     }
-    const size_t grow = std::max(bytes, static_cast<size_t>(1) << 20);
-    if (cudaMalloc(&w.ptr, grow) != cudaSuccess) return PA_ERR_CUDA;
-    w.bytes = grow;
-  }
-  if (w.cnt_bytes < cnt || w.cnt_bytes == 0) {
-    // zero the scheduler counters and any counter bytes not known to be zero
-    if (w.cnt_bytes == 0) {
-      if (cudaMemsetAsync(w.ptr, 0, kSchedBytes + cnt, stream) != cudaSuccess) return PA_ERR_CUDA;
-    } else {
-      unsigned char* base = static_cast<unsigned char*>(w.ptr) + kSchedBytes + w.cnt_bytes;
-      if (cudaMemsetAsync(base, 0, cnt - w.cnt_bytes, stream) != cudaSuccess) return PA_ERR_CUDA;
+    void* p = nullptr;
+    if (cudaMalloc(&p, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return PA_ERR_CUDA;
     }
+    if (w.ptr) g_ws_old.emplace_back(dev, w.ptr);
+    w.ptr = p;
+    w.bytes = bytes;
     w.cnt_bytes = cnt;
+    w.zeroed = false;
+  }
+  if (!w.zeroed) {
+    if (cudaMemsetAsync(w.ptr, 0, kSchedBytes + w.cnt_bytes, stream) != cudaSuccess) return PA_ERR_CUDA;
+    w.zeroed = true;
   }
   *out = w.ptr;
-  *cnt_bytes = cnt;
+  *cnt_bytes = w.cnt_bytes;
   return PA_OK;
 }
 
 // ---- validation helpers ---------------------------------------------------------------------
-int elem_bytes(int dtype) { return dtype == PA_F32 || dtype == PA_I32 ? 4 : (dtype == PA_F16 || dtype == PA_BF16) ? 2 : 0; }
+int elem_bytes(int dtype) {
+  return dtype == PA_F32 || dtype == PA_I32 ? 4 : (dtype == PA_F16 || dtype == PA_BF16) ? 2 : dtype == PA_U8 ? 1 : 0;
+}
 bool is_float(int dtype) { return dtype == PA_F32 || dtype == PA_F16 || dtype == PA_BF16; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -269,16 +282,18 @@ int check_rows(const pa_tensor* t, int dtype, int64_t H, int64_t D) {
   return PA_OK;
 }
 
-int check_cache(const pa_tensor* c, const pa_tensor* other) {
+// [num_blocks, ., ., .] contiguous; frames of bytes (PA_U8) only where the caller takes them.
+int check_cache(const pa_tensor* c, const pa_tensor* other, bool bytes = false) {
   if (!c || !c->data) return PA_ERR_INVALID;
-  if (!is_float(c->dtype)) return PA_ERR_DTYPE;
+  if (!is_float(c->dtype) && !(bytes && c->dtype == PA_U8)) return PA_ERR_DTYPE;
   if (c->ndim != 4) return PA_ERR_SHAPE;
   for (int i = 0; i < 4; ++i)
     if (c->shape[i] <= 0) return PA_ERR_SHAPE;
   if (c->stride[3] != 1 || c->stride[2] != c->shape[3] || c->stride[1] != c->shape[2] * c->shape[3] ||
       c->stride[0] != c->shape[1] * c->shape[2] * c->shape[3])
     return PA_ERR_STRIDE;
-  if (!aligned16(c->data) || (c->shape[3] * elem_bytes(c->dtype)) % 16 != 0) return PA_ERR_ALIGN;
+  const int64_t unit = c->dtype == PA_U8 ? c->stride[0] : c->shape[3] * elem_bytes(c->dtype);  // copied as 16-byte vectors
+  if (!aligned16(c->data) || unit % 16 != 0) return PA_ERR_ALIGN;
   if (c->shape[0] * c->shape[1] > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (other) {
     if (other->dtype != c->dtype) return PA_ERR_DTYPE;
@@ -384,7 +399,7 @@ int pa_get_device_status(pa_stream stream, int32_t* status_out) {
     // mark every workspace of this device unknown, so its next use zeroes them.
     std::lock_guard<std::mutex> lk(g_ws_mu);
     for (auto& kv : g_ws)
-      if (kv.first.first == dev) kv.second.cnt_bytes = 0;
+      if (kv.first.first == dev) kv.second.zeroed = false;
   }
   *status_out = v;
   return PA_OK;
@@ -425,6 +440,11 @@ int pa_shutdown(void) {
       cudaFree(kv.second.ptr);
     }
   }
+  for (auto& old : g_ws_old) {
+    cudaSetDevice(old.first);
+    cudaFree(old.second);
+  }
+  g_ws_old.clear();
   g_ws.clear();
   if (prev >= 0) cudaSetDevice(prev);
   return PA_OK;
@@ -617,7 +637,7 @@ int pa_decode_split(const pa_tensor* q, const pa_tensor* k_cache, const pa_tenso
 }
 
 int pa_copy_blocks(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* pairs, pa_stream stream) {
-  PA_TRY(check_cache(k_cache, v_cache));
+  PA_TRY(check_cache(k_cache, v_cache, true));
   if (!pairs) return PA_ERR_INVALID;
   PA_TRY(check_i32(pairs, 2));
   if (pairs->shape[1] != 2 || (pairs->shape[0] > 1 && pairs->stride[0] != 2)) return PA_ERR_SHAPE;
@@ -1318,3 +1338,394 @@ extern "C" int pa_step_decode(pa_bm* bm, const int64_t* seq_ids, int32_t n, int3
   const pa_tensor lens = i32_view(d + 3 * n, n, 0);
   return pa_decode_ex(q, k_cache, v_cache, &tables, &lens, scale, out, pp, stream);
 }
+
+// ---- rotary, 4-bit and block-sparse attention ---------------------------------------------------
+namespace {
+
+// The 4-bit caches [num_blocks, H, B, 5 D / 8].
+struct Q4Shape {
+  int64_t nb, H, B, D;
+};
+int check_q4_caches(const pa_tensor* k, const pa_tensor* v, Q4Shape* z) {
+  if (!k || !v || !v->data) return PA_ERR_INVALID;
+  if (k->dtype != PA_U8 || v->dtype != PA_U8) return PA_ERR_DTYPE;
+  PA_TRY(check_cache(k, v, true));
+  PA_TRY(check_cache(v, nullptr, true));
+  z->nb = k->shape[0];
+  z->H = k->shape[1];
+  z->B = k->shape[2];
+  if (k->shape[3] != 40 && k->shape[3] != 80) return PA_ERR_UNSUPPORTED;
+  z->D = k->shape[3] / 5 * 8;
+  if (z->B < 8 || z->B > 256 || (z->B & (z->B - 1)) != 0) return PA_ERR_UNSUPPORTED;
+  if (z->nb * z->B > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// q or out [N, Hq, D] with Hq a multiple of H, at most 16 query heads a key head; *g = Hq / H.
+int check_grouped_rows(const pa_tensor* t, int dtype, int64_t H, int64_t D, int64_t* g) {
+  if (!t) return PA_ERR_INVALID;
+  if (t->ndim != 3 || t->shape[1] < H || t->shape[1] % H != 0) return PA_ERR_SHAPE;
+  PA_TRY(check_rows(t, dtype, t->shape[1], D));
+  *g = t->shape[1] / H;
+  return *g > 16 ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+// block_tables [S, max_blocks] and context_lens [S] of a call over blocks of B tokens.
+int check_tables(const pa_tensor* block_tables, const pa_tensor* context_lens, int64_t S, int64_t B) {
+  if (!block_tables || !context_lens) return PA_ERR_INVALID;
+  PA_TRY(check_i32(context_lens, 1));
+  if (block_tables->ndim == 2 && block_tables->shape[1] == 0) {  // every sequence is empty: never read, no memory
+    if (block_tables->dtype != PA_I32) return PA_ERR_DTYPE;
+  } else {
+    PA_TRY(check_i32(block_tables, 2));
+  }
+  if (block_tables->shape[0] != S || context_lens->shape[0] != S) return PA_ERR_SHAPE;
+  const int64_t max_blocks = block_tables->shape[1];
+  if (max_blocks < 0 || (S > 1 && block_tables->stride[0] < max_blocks)) return PA_ERR_STRIDE;
+  if (max_blocks * B > INT32_MAX || S > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+int check_selected(const pa_tensor* t, int64_t S, int64_t H) {
+  if (!t) return PA_ERR_INVALID;
+  PA_TRY(check_i32(t, 3));
+  if (t->shape[0] != S || t->shape[1] != H || t->shape[2] < 1) return PA_ERR_SHAPE;
+  if (t->shape[2] > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if ((H > 1 && t->stride[1] < t->shape[2]) || (S > 1 && t->stride[0] < H * t->shape[2])) return PA_ERR_STRIDE;
+  return PA_OK;
+}
+
+// What pa_cache_append_rope and pa_cache_append_q4 share; dt = dtype of the rows.
+int rope_args(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* slot_mapping,
+              const pa_tensor* positions, const pa_tensor* cos_sin, int32_t interleaved, const pa_tensor* q,
+              const pa_tensor* q_out, int dt, int64_t H, int64_t D, bool need_rotation, pa::RopeArgs* a) {
+  PA_TRY(check_rows(k_new, dt, H, D));
+  PA_TRY(check_rows(v_new, dt, H, D));
+  if (!slot_mapping) return PA_ERR_INVALID;
+  PA_TRY(check_i32(slot_mapping, 1));
+  const int64_t T = k_new->shape[0];
+  if (v_new->shape[0] != T || slot_mapping->shape[0] != T) return PA_ERR_SHAPE;
+  if (T > INT32_MAX || H > INT32_MAX / 4) return PA_ERR_UNSUPPORTED;
+  std::memset(a, 0, sizeof(*a));
+  if (!positions != !cos_sin || !q != !q_out || (!positions && (need_rotation || q))) return PA_ERR_INVALID;
+  if (interleaved != 0 && interleaved != 1) return PA_ERR_INVALID;
+  if (positions) {
+    PA_TRY(check_i32(positions, 1));
+    if (positions->shape[0] != T) return PA_ERR_SHAPE;
+    if (cos_sin->dtype != PA_F32) return PA_ERR_DTYPE;
+    if (cos_sin->ndim != 2 || cos_sin->shape[0] < 1 || cos_sin->shape[1] < 16) return PA_ERR_SHAPE;
+    if (!cos_sin->data) return PA_ERR_INVALID;
+    const int64_t P = cos_sin->shape[0], R = cos_sin->shape[1];
+    if (R % 16 != 0 || R > D) return PA_ERR_SHAPE;
+    if (P > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (cos_sin->stride[1] != 1 || (P > 1 && cos_sin->stride[0] < R)) return PA_ERR_STRIDE;
+    if (!aligned16(cos_sin->data) || (P > 1 && cos_sin->stride[0] % 4 != 0)) return PA_ERR_ALIGN;
+    a->positions = static_cast<const int32_t*>(positions->data);
+    a->cos_sin = static_cast<const float*>(cos_sin->data);
+    a->cs_row = cos_sin->stride[0];
+    a->P = static_cast<int32_t>(P);
+    a->R = static_cast<int32_t>(R);
+  }
+  if (q) {
+    if (q->ndim != 3 || q->shape[0] != T || q->shape[1] < 1 || q->shape[1] > INT32_MAX / 4) return PA_ERR_SHAPE;
+    PA_TRY(check_rows(q, dt, q->shape[1], D));
+    PA_TRY(check_rows(q_out, dt, q->shape[1], D));
+    if (q_out->shape[0] != T) return PA_ERR_SHAPE;
+    a->q = q->data;
+    a->q_out = q_out->data;
+    a->q_row = q->stride[0];
+    a->qo_row = q_out->stride[0];
+    a->Hq = static_cast<int32_t>(q->shape[1]);
+  }
+  a->k_new = k_new->data;
+  a->v_new = v_new->data;
+  a->k_row = k_new->stride[0];
+  a->v_row = v_new->stride[0];
+  a->slots = static_cast<const int32_t*>(slot_mapping->data);
+  a->T = static_cast<int32_t>(T);
+  a->H = static_cast<int32_t>(H);
+  a->D = static_cast<int32_t>(D);
+  a->interleaved = interleaved;
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_cache_append_rope(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* slot_mapping,
+                         const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* positions,
+                         const pa_tensor* cos_sin, int32_t interleaved, const pa_tensor* q, const pa_tensor* q_out,
+                         pa_stream stream) {
+  const Range range("pa_cache_append_rope");
+  PA_TRY(check_cache(k_cache, v_cache));
+  PA_TRY(check_cache(v_cache, nullptr));
+  const int dt = k_cache->dtype;
+  const int64_t H = k_cache->shape[2], D = k_cache->shape[3];
+  if (D * elem_bytes(dt) > 512) return PA_ERR_UNSUPPORTED;
+  pa::RopeArgs a;
+  PA_TRY(rope_args(k_new, v_new, slot_mapping, positions, cos_sin, interleaved, q, q_out, dt, H, D, true, &a));
+  if (a.T == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.k_cache = static_cast<unsigned char*>(k_cache->data);
+  a.v_cache = static_cast<unsigned char*>(v_cache->data);
+  a.B = static_cast<int32_t>(k_cache->shape[1]);
+  a.num_slots = k_cache->shape[0] * k_cache->shape[1];
+  a.status = g_dev[dev].status;
+  if (pa::launch_rope_append(dt, false, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_cache_append_q4(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* slot_mapping,
+                       const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* positions,
+                       const pa_tensor* cos_sin, int32_t interleaved, const pa_tensor* q, const pa_tensor* q_out,
+                       pa_stream stream) {
+  const Range range("pa_cache_append_q4");
+  Q4Shape z;
+  PA_TRY(check_q4_caches(k_cache, v_cache, &z));
+  if (!k_new) return PA_ERR_INVALID;
+  const int dt = k_new->dtype;
+  if (dt != PA_F16 && dt != PA_BF16) return PA_ERR_DTYPE;
+  pa::RopeArgs a;
+  PA_TRY(rope_args(k_new, v_new, slot_mapping, positions, cos_sin, interleaved, q, q_out, dt, z.H, z.D, false, &a));
+  if (a.T == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.k_cache = static_cast<unsigned char*>(k_cache->data);
+  a.v_cache = static_cast<unsigned char*>(v_cache->data);
+  a.B = static_cast<int32_t>(z.B);
+  a.num_slots = z.nb * z.B;
+  a.status = g_dev[dev].status;
+  if (pa::launch_rope_append(dt, true, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* slot_mapping,
+                     const pa_tensor* k_out, const pa_tensor* v_out, pa_stream stream) {
+  const Range range("pa_cache_read_q4");
+  Q4Shape z;
+  PA_TRY(check_q4_caches(k_cache, v_cache, &z));
+  if (!k_out || !v_out || !slot_mapping) return PA_ERR_INVALID;
+  const int dt = k_out->dtype;
+  if (dt != PA_F16 && dt != PA_BF16) return PA_ERR_DTYPE;
+  PA_TRY(check_rows(k_out, dt, z.H, z.D));
+  PA_TRY(check_rows(v_out, dt, z.H, z.D));
+  PA_TRY(check_i32(slot_mapping, 1));
+  const int64_t T = k_out->shape[0];
+  if (v_out->shape[0] != T || slot_mapping->shape[0] != T) return PA_ERR_SHAPE;
+  if (T > INT32_MAX || z.H > INT32_MAX / 4) return PA_ERR_UNSUPPORTED;
+  if (T == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  pa::ReadQ4Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.k_cache = static_cast<const unsigned char*>(k_cache->data);
+  a.v_cache = static_cast<const unsigned char*>(v_cache->data);
+  a.slots = static_cast<const int32_t*>(slot_mapping->data);
+  a.k_out = k_out->data;
+  a.v_out = v_out->data;
+  a.ko_row = k_out->stride[0];
+  a.vo_row = v_out->stride[0];
+  a.num_slots = z.nb * z.B;
+  a.T = static_cast<int32_t>(T);
+  a.H = static_cast<int32_t>(z.H);
+  a.D = static_cast<int32_t>(z.D);
+  a.B = static_cast<int32_t>(z.B);
+  a.status = g_dev[dev].status;
+  if (pa::launch_read_q4(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Arguments that pa_decode_q4 and pa_decode_selected share, checked; *S = 0: nothing to do.
+int gather_args(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* out, float scale,
+                int64_t nb, int64_t H, int64_t B, int64_t D, pa::GatherArgs* a) {
+  std::memset(a, 0, sizeof(*a));
+  if (!q || !out) return PA_ERR_INVALID;
+  const int dt = q->dtype;
+  if (dt != PA_F16 && dt != PA_BF16) return PA_ERR_DTYPE;
+  int64_t g = 0, go = 0;
+  PA_TRY(check_grouped_rows(q, dt, H, D, &g));
+  PA_TRY(check_grouped_rows(out, dt, H, D, &go));
+  const int64_t S = q->shape[0];
+  if (go != g || out->shape[0] != S) return PA_ERR_SHAPE;
+  PA_TRY(check_tables(block_tables, context_lens, S, B));
+  if (S * H * g > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  a->q = q->data;
+  a->out = out->data;
+  a->q_row = q->stride[0];
+  a->out_row = out->stride[0];
+  a->k_cache = static_cast<const unsigned char*>(k_cache->data);
+  a->v_cache = static_cast<const unsigned char*>(v_cache->data);
+  a->block_tables = static_cast<const int32_t*>(block_tables->data);
+  a->bt_row = block_tables->stride[0];
+  a->context_lens = static_cast<const int32_t*>(context_lens->data);
+  a->S = static_cast<int32_t>(S);
+  a->H = static_cast<int32_t>(H);
+  a->g = static_cast<int32_t>(g);
+  a->B = static_cast<int32_t>(B);
+  a->num_blocks = static_cast<int32_t>(nb);
+  a->max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  a->qk_scale_log2 = scale * 1.4426950408889634f;
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                 const pa_tensor* block_tables, const pa_tensor* context_lens, float scale, const pa_tensor* out,
+                 pa_stream stream) {
+  const Range range("pa_decode_q4");
+  Q4Shape z;
+  PA_TRY(check_q4_caches(k_cache, v_cache, &z));
+  pa::GatherArgs a;
+  PA_TRY(gather_args(q, k_cache, v_cache, block_tables, context_lens, out, scale, z.nb, z.H, z.B, z.D, &a));
+  if (a.S == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.status = g_dev[dev].status;
+  if (pa::launch_decode_q4(q->dtype, static_cast<int>(z.D), a, 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                       const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* selected,
+                       float scale, const pa_tensor* out, pa_stream stream) {
+  const Range range("pa_decode_selected");
+  PA_TRY(check_cache(k_cache, v_cache));
+  PA_TRY(check_cache(v_cache, nullptr));
+  const int64_t nb = k_cache->shape[0], B = k_cache->shape[1], H = k_cache->shape[2], D = k_cache->shape[3];
+  if (k_cache->dtype == PA_F32 || !(D == 64 || D == 128) || B < 8 || B > 256 || (B & (B - 1)) != 0)
+    return PA_ERR_UNSUPPORTED;
+  if (!q || q->dtype != k_cache->dtype) return q ? PA_ERR_DTYPE : PA_ERR_INVALID;
+  pa::GatherArgs a;
+  PA_TRY(gather_args(q, k_cache, v_cache, block_tables, context_lens, out, scale, nb, H, B, D, &a));
+  PA_TRY(check_selected(selected, a.S, H));
+  if (a.S == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.status = g_dev[dev].status;
+  a.selected = static_cast<const int32_t*>(selected->data);
+  a.sel_seq = selected->stride[0];
+  a.sel_head = selected->stride[1];
+  a.K = static_cast<int32_t>(selected->shape[2]);
+  CUtensorMap tk, tv;
+  std::memset(&tk, 0, sizeof(tk));
+  std::memset(&tv, 0, sizeof(tv));
+  if (pa::launch_decode_selected(q->dtype, static_cast<int>(D), a, tk, tv, 0, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, const pa_tensor* context_lens,
+                    const pa_tensor* first_tokens, const pa_tensor* bounds, pa_stream stream) {
+  const Range range("pa_block_bounds");
+  PA_TRY(check_cache(k_cache, nullptr));
+  const int64_t nb = k_cache->shape[0], B = k_cache->shape[1], H = k_cache->shape[2], D = k_cache->shape[3];
+  if (k_cache->dtype == PA_F32 || !(D == 64 || D == 128) || B < 8 || B > 256 || (B & (B - 1)) != 0)
+    return PA_ERR_UNSUPPORTED;
+  PA_TRY(check_cache(bounds, nullptr));
+  if (bounds->dtype != k_cache->dtype) return PA_ERR_DTYPE;
+  if (bounds->shape[0] != nb || bounds->shape[1] != H || bounds->shape[2] != 2 || bounds->shape[3] != D)
+    return PA_ERR_SHAPE;
+  if (!context_lens) return PA_ERR_INVALID;
+  const int64_t S = context_lens->shape[0];
+  PA_TRY(check_tables(block_tables, context_lens, S, B));
+  if (first_tokens) {
+    PA_TRY(check_i32(first_tokens, 1));
+    if (first_tokens->shape[0] != S) return PA_ERR_SHAPE;
+  }
+  if (S == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  pa::BoundsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k_cache = k_cache->data;
+  a.bounds = bounds->data;
+  a.block_tables = static_cast<const int32_t*>(block_tables->data);
+  a.bt_row = block_tables->stride[0];
+  a.context_lens = static_cast<const int32_t*>(context_lens->data);
+  a.first = first_tokens ? static_cast<const int32_t*>(first_tokens->data) : nullptr;
+  a.S = static_cast<int32_t>(S);
+  a.H = static_cast<int32_t>(H);
+  a.D = static_cast<int32_t>(D);
+  a.B = static_cast<int32_t>(B);
+  a.num_blocks = static_cast<int32_t>(nb);
+  a.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  a.status = g_dev[dev].status;
+  if (pa::launch_block_bounds(k_cache->dtype, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tensor* block_tables,
+                     const pa_tensor* context_lens, int32_t block_size, int32_t keep_first, int32_t keep_last,
+                     const pa_tensor* selected, pa_stream stream) {
+  const Range range("pa_select_blocks");
+  PA_TRY(check_cache(bounds, nullptr));
+  const int dt = bounds->dtype;
+  const int64_t nb = bounds->shape[0], H = bounds->shape[1], D = bounds->shape[3], B = block_size;
+  if (bounds->shape[2] != 2) return PA_ERR_SHAPE;
+  if (dt == PA_F32 || !(D == 64 || D == 128) || B < 8 || B > 256 || (B & (B - 1)) != 0) return PA_ERR_UNSUPPORTED;
+  if (keep_first < 0 || keep_last < 0) return PA_ERR_INVALID;
+  int64_t g = 0;
+  PA_TRY(check_grouped_rows(q, dt, H, D, &g));
+  const int64_t S = q->shape[0];
+  PA_TRY(check_tables(block_tables, context_lens, S, B));
+  PA_TRY(check_selected(selected, S, H));
+  if (S * H * g > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (S == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  pa::SelectArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q->data;
+  a.q_row = q->stride[0];
+  a.bounds = bounds->data;
+  a.block_tables = static_cast<const int32_t*>(block_tables->data);
+  a.bt_row = block_tables->stride[0];
+  a.context_lens = static_cast<const int32_t*>(context_lens->data);
+  a.selected = static_cast<int32_t*>(selected->data);
+  a.sel_seq = selected->stride[0];
+  a.sel_head = selected->stride[1];
+  a.S = static_cast<int32_t>(S);
+  a.H = static_cast<int32_t>(H);
+  a.g = static_cast<int32_t>(g);
+  a.D = static_cast<int32_t>(D);
+  a.B = static_cast<int32_t>(B);
+  a.K = static_cast<int32_t>(selected->shape[2]);
+  a.num_blocks = static_cast<int32_t>(nb);
+  a.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  a.keep_first = keep_first;
+  a.keep_last = keep_last;
+  a.status = g_dev[dev].status;
+  void* ws = nullptr;
+  size_t cnt_bytes = 0;
+  const size_t scores = static_cast<size_t>(S * H) * std::max<int64_t>(a.max_blocks, 1) * sizeof(float);
+  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, scores, &ws, &cnt_bytes));
+  a.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kSchedBytes + cnt_bytes);
+  if (pa::launch_select_blocks(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(2);
+  return PA_OK;
+}
+
+}  // extern "C"

@@ -211,11 +211,91 @@ cudaError_t launch_append_split(int dtype, const void* k_new, const void* v_new,
                                 int32_t num_blocks, void* k_cache, void* v_cache, int32_t* status,
                                 int grid, cudaStream_t stream);
 
+// ---- rotating appends, the 4-bit cache (rotary.cu) -------------------------------------------
+struct RopeArgs {
+  const void *k_new, *v_new, *q;  // [T, H, D], [T, H, D], [T, Hq, D]; q null: none
+  void* q_out;
+  int64_t k_row, v_row, q_row, qo_row;  // elements between token rows
+  const int32_t* slots;           // [T]
+  const int32_t* positions;       // [T]; null: no rotation
+  const float* cos_sin;           // [P, R], row stride cs_row elements
+  int64_t cs_row;
+  unsigned char *k_cache, *v_cache;
+  int64_t num_slots;
+  int32_t T, H, Hq, D, B, R, P, interleaved;
+  int32_t splits;                 // warps that share a token's rows
+  int32_t* status;
+};
+cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, int num_sms, cudaStream_t stream);
+
+struct ReadQ4Args {
+  const unsigned char *k_cache, *v_cache;  // [num_blocks, H, B, 5 D / 8]
+  const int32_t* slots;                    // [T]
+  void *k_out, *v_out;                     // [T, H, D]
+  int64_t ko_row, vo_row;
+  int64_t num_slots;
+  int32_t T, H, D, B;
+  int32_t* status;
+};
+cudaError_t launch_read_q4(int dtype, const ReadQ4Args& a, int num_sms, cudaStream_t stream);
+
+// ---- decode over gathered tiles of 16 keys: the 4-bit cache, and listed frames ---------------
+struct GatherArgs {
+  const void* q;                // [S, g * H, D], row stride q_row elements
+  void* out;
+  int64_t q_row, out_row;
+  const unsigned char *k_cache, *v_cache;
+  const int32_t* block_tables;  // [S, max_blocks], row stride bt_row
+  int64_t bt_row;
+  const int32_t* context_lens;  // [S]
+  const int32_t* selected;      // [S, H, K]; null: every frame
+  int64_t sel_seq, sel_head;    // elements between sequences, heads of `selected`
+  int32_t K;
+  int32_t S, H, g, B, num_blocks, max_blocks;
+  float qk_scale_log2;          // scale * log2(e)
+  int32_t* cnt;                 // [S * H] partials finished per (sequence, head), zero between launches
+  float* ws_ml;                 // [slots][g][2] partial (max, sum)
+  float* ws_o;                  // [slots][g][D] partial unnormalised outputs
+  int32_t* status;
+};
+cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int grid, cudaStream_t stream);
+cudaError_t launch_decode_selected(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, int grid, cudaStream_t stream);
+
+// ---- frame bounds and selection (select.cu) ---------------------------------------------------
+struct BoundsArgs {
+  const void* k_cache;          // [num_blocks, B, H, D]
+  void* bounds;                 // [num_blocks, H, 2, D]
+  const int32_t* block_tables;
+  int64_t bt_row;
+  const int32_t* context_lens;
+  const int32_t* first;         // [S] first new token; null: 0
+  int32_t S, H, D, B, num_blocks, max_blocks;
+  int32_t* status;
+};
+cudaError_t launch_block_bounds(int dtype, const BoundsArgs& a, int num_sms, cudaStream_t stream);
+
+struct SelectArgs {
+  const void* q;                // [S, g * H, D]
+  int64_t q_row;
+  const void* bounds;           // [num_blocks, H, 2, D]
+  const int32_t* block_tables;
+  int64_t bt_row;
+  const int32_t* context_lens;
+  float* scores;                // [S, H, max_blocks]
+  int32_t* selected;            // [S, H, K]
+  int64_t sel_seq, sel_head;
+  int32_t S, H, g, D, B, K, num_blocks, max_blocks, keep_first, keep_last;
+  int32_t* status;
+};
+cudaError_t launch_select_blocks(int dtype, const SelectArgs& a, int num_sms, cudaStream_t stream);
+
 // status bits (mirror pa.h)
 constexpr int32_t kDevBadSlot = 0x1;
 constexpr int32_t kDevBadBlock = 0x2;
 constexpr int32_t kDevBadLen = 0x4;
 constexpr int32_t kDevBadCopy = 0x8;
 constexpr int32_t kDevTimeout = 0x10;
+constexpr int32_t kDevBadPos = 0x20;
 
 }  // namespace pa
