@@ -1575,10 +1575,40 @@ int gather_args(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v
   a->H = static_cast<int32_t>(H);
   a->g = static_cast<int32_t>(g);
   a->B = static_cast<int32_t>(B);
+  while ((1 << a->log2_B) < B) ++a->log2_B;
   a->num_blocks = static_cast<int32_t>(nb);
   a->max_blocks = static_cast<int32_t>(block_tables->shape[1]);
   a->qk_scale_log2 = scale * 1.4426950408889634f;
   return PA_OK;
+}
+
+// Workspace of a gathered decode on `workers` warps: arrival counters, and two partials a warp.
+int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, pa::GatherArgs* a) {
+  const size_t slots = 2 * static_cast<size_t>(workers) * a->g;
+  void* ws = nullptr;
+  size_t cnt_bytes = 0;
+  PA_TRY(workspace(dev, stream, static_cast<size_t>(a->S) * a->H * sizeof(int32_t), slots * (D + 2) * sizeof(float), &ws,
+                   &cnt_bytes));
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  a->cnt = reinterpret_cast<int32_t*>(base + kSchedBytes);
+  a->ws_o = reinterpret_cast<float*>(base + kSchedBytes + cnt_bytes);
+  a->ws_ml = a->ws_o + slots * D;
+  return PA_OK;
+}
+
+// View {64 elements, slots, D / 64 column groups, H} of a 16-bit cache, box {64, 8, D / 64, 1}, 128-byte
+// swizzle: 8 rows of one head as [D / 64][8][64].
+int make_rows8_map(CUtensorMap* map, void* base, int dtype, int64_t rows, int64_t H, int64_t D) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return PA_ERR_CUDA;
+  CUtensorMapDataType t = dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(H)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(H * D * 2), 128, static_cast<cuuint64_t>(D * 2)};
+  cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, t, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -1597,7 +1627,12 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
   int dev;
   PA_TRY(current_device(&dev));
   a.status = g_dev[dev].status;
-  if (pa::launch_decode_q4(q->dtype, static_cast<int>(z.D), a, 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int workers = 0;
+  if (pa::launch_decode_q4(q->dtype, static_cast<int>(z.D), a, g_dev[dev].num_sms, st, &workers) != cudaSuccess)
+    return PA_ERR_CUDA;
+  PA_TRY(gather_scratch(dev, st, z.D, workers, &a));
+  if (pa::launch_decode_q4(q->dtype, static_cast<int>(z.D), a, g_dev[dev].num_sms, st, nullptr) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;
@@ -1625,10 +1660,14 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
   a.sel_head = selected->stride[1];
   a.K = static_cast<int32_t>(selected->shape[2]);
   CUtensorMap tk, tv;
-  std::memset(&tk, 0, sizeof(tk));
-  std::memset(&tv, 0, sizeof(tv));
-  if (pa::launch_decode_selected(q->dtype, static_cast<int>(D), a, tk, tv, 0, static_cast<cudaStream_t>(stream)) !=
-      cudaSuccess)
+  PA_TRY(make_rows8_map(&tk, k_cache->data, q->dtype, nb * B, H, D));
+  PA_TRY(make_rows8_map(&tv, v_cache->data, q->dtype, nb * B, H, D));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int workers = 0;
+  if (pa::launch_decode_selected(q->dtype, static_cast<int>(D), a, tk, tv, g_dev[dev].num_sms, st, &workers) != cudaSuccess)
+    return PA_ERR_CUDA;
+  PA_TRY(gather_scratch(dev, st, D, workers, &a));
+  if (pa::launch_decode_selected(q->dtype, static_cast<int>(D), a, tk, tv, g_dev[dev].num_sms, st, nullptr) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;

@@ -3,13 +3,27 @@
 #include "pa.h"
 
 namespace pa {
+namespace {
 
-cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int grid, cudaStream_t stream) {
-  (void)grid;
+// Weights go to the tensor cores as two fp16 parts where the output is fp16 (one part alone would add an
+// error as large as the output's own rounding); a bf16 output rounds 8 times coarser than one part.
+template <typename T, int D>
+cudaError_t by_group(const GatherArgs& a, int num_sms, cudaStream_t stream, int* workers) {
+  using F = gk::Q4Format<T, D>;
+  constexpr int parts = F::kScaleQ ? gk::kOnePart : gk::kTwoParts;
+  const typename F::Maps maps{};
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, false, 4, 4>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, parts, false, 4, 4>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, parts, false, 4, 2>(a, maps, num_sms, stream, workers);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int num_sms, cudaStream_t stream, int* workers) {
   if (dtype == PA_F16)
-    return D == 128 ? gk::launch_simple<__half, true, 128>(a, stream) : gk::launch_simple<__half, true, 64>(a, stream);
-  return D == 128 ? gk::launch_simple<__nv_bfloat16, true, 128>(a, stream)
-                  : gk::launch_simple<__nv_bfloat16, true, 64>(a, stream);
+    return D == 128 ? by_group<__half, 128>(a, num_sms, stream, workers) : by_group<__half, 64>(a, num_sms, stream, workers);
+  return D == 128 ? by_group<__nv_bfloat16, 128>(a, num_sms, stream, workers)
+                  : by_group<__nv_bfloat16, 64>(a, num_sms, stream, workers);
 }
 
 }  // namespace pa

@@ -3,16 +3,142 @@
 #include "pa.h"
 
 namespace pa {
+namespace gk {
 
-cudaError_t launch_decode_selected(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk,
-                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  (void)tk;
-  (void)tv;
-  (void)grid;
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&x)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&x)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// 16-bit rows.  A half tile, 8 keys, is one TMA box [D / 64 column groups][8 rows][64 elements] with the
+// 128-byte swizzle: row y of a column group keeps its 16-byte chunk x at x ^ y, so that the eight row
+// addresses of an ldmatrix fall into different banks.
+template <typename T, int D_>
+struct RowFormat {
+  using In = T;
+  using M = T;
+  static constexpr int D = D_;
+  static constexpr bool kScaleQ = false;
+  static constexpr int kSecond = 8;
+  static constexpr uint32_t kHalfTile = 8 * D * 2, kTile = 2 * kHalfTile;
+  __device__ __forceinline__ static int key_of(int r) { return r; }
+
+  struct Maps {
+    CUtensorMap k, v;
+  };
+  __device__ __forceinline__ static uint32_t load(const GatherArgs& a, const Maps& maps, const TilePlan& p, int h,
+                                                  uint32_t dst, uint32_t bar, bool issue) {
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (p.frame[i] < 0) continue;
+      if (issue) {
+        const int row = p.frame[i] * a.B + p.row + (a.B >= 16 ? 8 * i : 0);  // a slot: fits int32
+        tma_load_4d(dst + i * kHalfTile, &maps.k, 0, row, 0, h, bar);
+        tma_load_4d(dst + kTile + i * kHalfTile, &maps.v, 0, row, 0, h, bar);
+      }
+      bytes += 2 * kHalfTile;
+    }
+    return bytes;
+  }
+
+  __device__ __forceinline__ static int q_element(int c, int i) { return 16 * (i >> 2) + 2 * c + (i & 1) + ((i & 2) << 2); }
+  __device__ __forceinline__ static void load_q(const float (&q)[D / 4], uint32_t (&f)[D / 16][2]) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      f[k][0] = pack2<M>(q[4 * k], q[4 * k + 1]);
+      f[k][1] = pack2<M>(q[4 * k + 2], q[4 * k + 3]);
+    }
+  }
+
+  template <int NT>
+  __device__ __forceinline__ static void scores(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
+                                                float (&acc)[NT][4]) {
+    const int lane = 4 * r + c, y = lane & 7, mat = lane >> 3;
+    const uint32_t row = kst + (mat & 1) * kHalfTile + y * 128;  // matrices: keys 0..7, 8..15, then the next 8 elements
+    float odd[NT][4] = {};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t x[4];
+      ldmatrix4(row + (k >> 2) * 1024 + ((((k & 3) * 2 + (mat >> 1)) ^ y) << 4), x);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma(k & 1 ? odd[n] : acc[n], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1], M());
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] += odd[n][i];
+  }
+
+  template <int NT, int PARTS>
+  __device__ __forceinline__ static void values(uint32_t vst, int r, int c, int meta, const uint32_t (&p)[PARTS][NT][2],
+                                                float (&o)[D / 16][NT][4]) {
+    const int lane = 4 * r + c, y = lane & 7, mat = lane >> 3;
+    const uint32_t row = vst + (mat >> 1) * kHalfTile + y * 128;  // matrices: elements 0..7, 8..15 of keys 0..7, then of 8..15
+    uint32_t keep0 = ~0u, keep1 = ~0u;
+    if (meta != 0x0808) {  // slots that hold no key: any bits, and the weight is 0
+      const int n0 = meta & 255, n1 = (meta >> 8) & 255;
+      keep0 = (2 * c < n0 ? 0xffffu : 0u) | (2 * c + 1 < n0 ? 0xffff0000u : 0u);
+      keep1 = (2 * c < n1 ? 0xffffu : 0u) | (2 * c + 1 < n1 ? 0xffff0000u : 0u);
+    }
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+      uint32_t x[4];
+      ldmatrix4_trans(row + (t >> 2) * 1024 + ((((t & 3) * 2 + (mat & 1)) ^ y) << 4), x);
+      x[0] &= keep0;
+      x[1] &= keep0;
+      x[2] &= keep1;
+      x[3] &= keep1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) mma(o[t][n], x[0], x[1], x[2], x[3], p[q][n][0], p[q][n][1], M());
+    }
+  }
+  __device__ __forceinline__ static int o_element(int t, int r, int hi) { return 16 * t + 8 * hi + r; }
+};
+
+}  // namespace gk
+
+namespace {
+
+template <typename T, int D>
+cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
+                     int* workers) {
+  using F = gk::RowFormat<T, D>;
+  typename F::Maps maps;
+  maps.k = tk;
+  maps.v = tv;
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 3, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 3, 2>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, true, 3, 2>(a, maps, num_sms, stream, workers);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_selected(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   int num_sms, cudaStream_t stream, int* workers) {
   if (dtype == PA_F16)
-    return D == 128 ? gk::launch_simple<__half, false, 128>(a, stream) : gk::launch_simple<__half, false, 64>(a, stream);
-  return D == 128 ? gk::launch_simple<__nv_bfloat16, false, 128>(a, stream)
-                  : gk::launch_simple<__nv_bfloat16, false, 64>(a, stream);
+    return D == 128 ? by_group<__half, 128>(a, tk, tv, num_sms, stream, workers)
+                    : by_group<__half, 64>(a, tk, tv, num_sms, stream, workers);
+  return D == 128 ? by_group<__nv_bfloat16, 128>(a, tk, tv, num_sms, stream, workers)
+                  : by_group<__nv_bfloat16, 64>(a, tk, tv, num_sms, stream, workers);
 }
 
 }  // namespace pa

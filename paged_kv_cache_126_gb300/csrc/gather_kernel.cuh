@@ -1,8 +1,25 @@
 // Single-query attention over gathered keys: every token of a sequence held in the 4-bit
 // cache, or the tokens of listed frames of a 16-bit cache.
 //
-// out = sum_j w_j v_j / sum_j w_j, w_j = exp(q . k_j * scale - m), in one pass with the
-// running maximum m and sum per warp.
+// For each sequence s and key head h, with the g query heads that share it:
+//     out = sum_j w_j v_j / sum_j w_j,   w_j = exp2(q . k_j * scale * log2(e) - m),
+// in one pass, m being a running maximum that moves only when a score passes it by 2^8.
+//
+// Work.  A tile is 16 keys of one (s, h).  All tiles of the batch, numbered by sequence,
+// head and position, are cut into one consecutive range per resident warp, equal to within
+// a tile: every warp is its own worker with its own ring of shared-memory stages, and no
+// barrier joins the warps of a block.  A (s, h) that lies in one range is written straight
+// out; one that is cut leaves a partial (max, sum, weighted values) per piece, and the warp
+// that brings the arrival counter to the number of pieces joins them, in order, so that
+// results do not depend on timing.  The cut follows from the lengths, which each warp reads
+// on the device.
+//
+// Tensor cores (mma.sync m16n8k16): scores are C[16 keys x 8 queries] = K (A operand) times
+// q^T (B), and the values O^T[16 elements x 8 queries] += V^T (A) times P (B).  Keys and
+// elements, of which there are many, fill the 16 rows; the few queries need only 8 columns.
+// P comes out of the score layout by one movmatrix per 8 x 8 and is never in memory.  With
+// g <= 4 the queries stand twice, in columns 0..3 and 4..7, and the second copy carries what
+// the first one's rounding of the weights to 16 bits left over: the second part is free.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -10,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "decode_kernel.cuh"
 #include "pa_internal.h"
@@ -18,102 +36,656 @@ namespace pa {
 namespace gk {
 
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 4;        // warps of a block (they share nothing but the abort flag)
+constexpr int kMinTiles = 4;     // fewest tiles a warp is given
+constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
 
+enum Parts { kOnePart = 0, kTwinColumns = 1, kTwoParts = 2 };
+
+// ---- instructions -----------------------------------------------------------------------------
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, __nv_bfloat16) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 of 16-bit elements, transposed across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+
+template <typename M>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y) { return as_u32(__floats2half2_rn(x, y)); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) { return as_u32(__floats2bfloat162_rn(x, y)); }
+template <typename M>
+__device__ __forceinline__ float round_to(float x);
+template <>
+__device__ __forceinline__ float round_to<__half>(float x) { return __half2float(__float2half_rn(x)); }
+template <>
+__device__ __forceinline__ float round_to<__nv_bfloat16>(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// One block per (query head, sequence), a warp per token in turn, D / 32 elements a lane.
-template <typename T, bool Q4, int D>
-__global__ void __launch_bounds__(128) simple_kernel(const GatherArgs a) {
-  constexpr int E = D / 32, W = D / 2 + D / 8;
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-  __shared__ int bad;
-  const int s = blockIdx.y, hq = blockIdx.x, h = hq / a.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) bad = 0;
-  __syncthreads();
-  int L = a.context_lens[s];
-  if (L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks) * a.B) {
-    if (threadIdx.x == 0) atomicOr(a.status, kDevBadLen);
-    L = 0;
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[2]) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[1]) {
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds(uint32_t addr) {
+  uint32_t w;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr));
+  return w;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// ---- the cursor over a batch's tiles ------------------------------------------------------------
+struct Cursor {
+  int s, h, t;               // tile t of (s, h)
+  int L, blocks, tiles;      // of sequence s
+};
+
+__device__ __forceinline__ int checked_len(const GatherArgs& a, int s) {
+  const int L = a.context_lens[s];
+  return L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks) * a.B ? -1 : L;
+}
+
+template <bool SEL>
+__device__ __forceinline__ int tiles_of(const GatherArgs& a, int L) {
+  if (!SEL) return max(1, (max(L, 0) + 15) >> 4);
+  const int n = min(a.K, (max(L, 0) + a.B - 1) >> a.log2_B);
+  return max(1, a.B >= 16 ? n << (a.log2_B - 4) : (n + 1) >> 1);
+}
+
+template <bool SEL>
+__device__ __forceinline__ void enter_seq(const GatherArgs& a, Cursor& c) {
+  const int L = checked_len(a, c.s);
+  if (L < 0) atomicOr(a.status, kDevBadLen);
+  c.L = max(L, 0);
+  c.blocks = (c.L + a.B - 1) >> a.log2_B;
+  c.tiles = tiles_of<SEL>(a, L);
+}
+
+template <bool SEL>
+__device__ __forceinline__ void advance(const GatherArgs& a, Cursor& c) {
+  if (++c.t < c.tiles) return;
+  c.t = 0;
+  if (++c.h < a.H) return;
+  c.h = 0;
+  if (++c.s < a.S) enter_seq<SEL>(a, c);
+}
+
+// Frame ids of up to 32 consecutive entries of one table or list, one per lane.
+struct Ids {
+  int s, h, base;   // where they start (base: entry of lane 0)
+  int frame;        // this lane's frame id; -1: bad, -2: none
+  int entry;        // its position in the sequence's table
+  bool ended;       // the list ended before `base`
+};
+
+template <bool SEL>
+__device__ __forceinline__ void refill(const GatherArgs& a, const Cursor& c, int base, int lane, Ids& ids) {
+  const bool on = ids.s == c.s && (!SEL || ids.h == c.h) && base > ids.base;
+  const int32_t* table = a.block_tables + c.s * a.bt_row;
+  const int j = base + lane;
+  int e = j;
+  bool have = j < c.blocks;
+  if (SEL) {
+    const int32_t* list = a.selected + c.s * a.sel_seq + c.h * a.sel_head;
+    const int n = min(a.K, c.blocks);
+    if (!on) ids.ended = false;
+    for (int b = on ? ids.base + 32 : 0; b < base && !ids.ended; b += 32)  // entries passed over unseen
+      ids.ended = __any_sync(kAll, b + lane < n && list[min(b + lane, n - 1)] == -1);
+    e = j < n && !ids.ended ? list[j] : -1;
+    const unsigned ends = __ballot_sync(kAll, e == -1);
+    have = (ends & ((2u << lane) - 1u)) == 0;  // no end at this lane or before
+    ids.ended = ids.ended || ends != 0;
   }
-  const int blocks = (L + a.B - 1) / a.B;
-  const int count = a.selected ? min(a.K, blocks) : blocks;
-  const T* q = static_cast<const T*>(a.q) + s * a.q_row + hq * D;
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < E; ++i) {
-    qv[i] = to_float(q[lane * E + i]);
-    o[i] = 0.f;
-  }
-  for (int j = 0; j < count; ++j) {
-    int e = j;
-    if (a.selected) {
-      e = a.selected[s * a.sel_seq + h * a.sel_head + j];
-      if (e == -1) break;
-    }
-    const int frame = e >= 0 && e < blocks ? a.block_tables[s * a.bt_row + e] : -1;
+  int frame = -2;
+  if (have) {
+    frame = e >= 0 && e < c.blocks ? table[e] : -1;
     if (frame < 0 || frame >= a.num_blocks) {
-      if (lane == 0) {
-        atomicOr(a.status, kDevBadBlock);
-        bad = 1;
+      atomicOr(a.status, kDevBadBlock);
+      frame = -1;
+    }
+  }
+  ids.s = c.s;
+  ids.h = c.h;
+  ids.base = base;
+  ids.frame = frame;
+  ids.entry = e;
+}
+
+// One tile as the producer sees it: two halves of 8 keys, each inside one frame.
+struct TilePlan {
+  int frame[2];   // < 0: nothing to load
+  int row;        // first key's row in its frame (both halves of one frame: row, row + 8)
+  int meta;       // keys of the halves (0..8 each) | 1 << 16 for a bad frame id
+};
+
+template <bool SEL>
+__device__ __forceinline__ TilePlan plan_tile(const GatherArgs& a, const Cursor& c, int lane, Ids& ids) {
+  TilePlan p;
+  const bool pairs = a.B < 16;
+  const int per = a.log2_B - 4;                      // log2(tiles of a frame)
+  const int j = pairs ? 2 * c.t : c.t >> per;
+  p.row = pairs ? 0 : (c.t & ((1 << per) - 1)) << 4;
+  if (ids.s != c.s || (SEL && ids.h != c.h) || j < ids.base || j >= ids.base + 32)
+    refill<SEL>(a, c, j & ~31, lane, ids);
+  const int at = j - ids.base;
+  p.frame[0] = __shfl_sync(kAll, ids.frame, at);
+  const int e0 = __shfl_sync(kAll, ids.entry, at);
+  p.frame[1] = pairs ? __shfl_sync(kAll, ids.frame, at + 1) : p.frame[0];
+  const int e1 = pairs ? __shfl_sync(kAll, ids.entry, at + 1) : e0;
+  const int n0 = p.frame[0] >= 0 ? min(8, max(0, c.L - e0 * a.B - p.row)) : 0;
+  const int n1 = p.frame[1] >= 0 ? min(8, max(0, c.L - e1 * a.B - (pairs ? 0 : p.row + 8))) : 0;
+  p.meta = n0 | (n1 << 8) | (p.frame[0] == -1 || p.frame[1] == -1 ? 1 << 16 : 0);
+  if (n0 == 0) p.frame[0] = -2;
+  if (n1 == 0) p.frame[1] = -2;
+  return p;
+}
+
+// ---- formats: how a tile is loaded and multiplied ------------------------------------------------
+// 4-bit rows of D / 2 bytes of codes and D / 8 bytes of (step, offset) pairs.  A code n is made fp16 by
+// putting it into the mantissa of 1024 (low bits) or 64 (bits 4..7): 1024 + n and 64 + n are exact, so is
+// the difference, and one fused multiply-add with (step, offset) gives the number that the code
+// stands for.  Two codes of a 32-bit word at a time: five logic operations and eight half2
+// operations for eight codes.
+//
+// Rows of the score tile are keys in the order perm(0..15) = 0,12,2,14,4,8,6,10,1,13,3,15,5,9,7,11:
+// with 80-byte rows (20 banks) the 16-byte reads of K (rows r and r + 1 of a tile together) and the
+// 8-byte reads of V (rows 2c) then touch every bank once.
+__device__ __forceinline__ void codes8(uint32_t w, __half2 step, __half2 off, uint32_t (&x)[4]) {
+  const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k64 = __half2half2(__ushort_as_half(0x5400));
+  const uint32_t w8 = w >> 8;
+  const __half2 y0 = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), k1024);
+  const __half2 y1 = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), k64);
+  const __half2 y2 = __hsub2(as_half2((w8 & 0x000f000fu) | 0x64006400u), k1024);
+  const __half2 y3 = __hsub2(as_half2((w8 & 0x00f000f0u) | 0x54005400u), k64);
+  x[0] = as_u32(__hfma2(y0, step, off));
+  x[1] = as_u32(__hfma2(y1, step, off));
+  x[2] = as_u32(__hfma2(y2, step, off));
+  x[3] = as_u32(__hfma2(y3, step, off));
+}
+
+template <typename T, int D_>
+struct Q4Format {
+  using In = T;          // queries and outputs
+  using M = __half;      // operands of the tensor cores
+  static constexpr int D = D_;
+  static constexpr bool kScaleQ = !std::is_same<T, __half>::value;  // bf16 queries to fp16 range
+  static constexpr int kRow = D / 2 + D / 8;
+  static constexpr uint32_t kHalfTile = 8 * kRow, kTile = 16 * kRow;
+  static constexpr int kWordsK = D / 32, kWordsV = D / 64;  // words of codes a lane reads of a key
+
+  static constexpr int kSecond = 1;  // key of score row r + 8 behind that of row r
+  __device__ __forceinline__ static int key_of(int r) { return (r & 1) ? ((r + 3) & 7) + 8 : r; }
+
+  struct Maps {};
+  __device__ __forceinline__ static uint32_t load(const GatherArgs& a, const Maps&, const TilePlan& p, int h, uint32_t dst,
+                                                  uint32_t bar, bool issue) {
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (p.frame[i] < 0) continue;
+      const bool whole = i == 0 && p.frame[0] == p.frame[1] && a.B >= 16;
+      const uint32_t n = whole ? kTile : kHalfTile;
+      if (issue) {
+        const int row = p.row + (a.B >= 16 ? 8 * i : 0);
+        const int64_t at = ((static_cast<int64_t>(p.frame[i]) * a.H + h) * a.B + row) * kRow;
+        bulk_load(dst + i * kHalfTile, a.k_cache + at, n, bar);
+        bulk_load(dst + kTile + i * kHalfTile, a.v_cache + at, n, bar);
       }
+      bytes += 2 * n;
+      if (whole) break;
+    }
+    return bytes;
+  }
+
+  // B operands of a query's D elements for the D / 16 score steps of lane (r, c)
+  __device__ __forceinline__ static void load_q(const float (&q)[D / 4], uint32_t (&f)[D / 16][2]) {
+#pragma unroll
+    for (int w = 0; w < kWordsK; ++w) {
+      const float* e = q + 8 * w;
+      f[2 * w][0] = pack2<M>(e[0], e[4]);
+      f[2 * w][1] = pack2<M>(e[1], e[5]);
+      f[2 * w + 1][0] = pack2<M>(e[2], e[6]);
+      f[2 * w + 1][1] = pack2<M>(e[3], e[7]);
+    }
+  }
+  // element of the query that load_q takes as q[i] in lane column c
+  __device__ __forceinline__ static int q_element(int c, int i) { return c * (D / 4) + i; }
+
+  template <int NT>
+  __device__ __forceinline__ static void scores(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
+                                                float (&acc)[NT][4]) {
+    const uint32_t row = kst + key_of(r) * kRow;
+    uint32_t w0[kWordsK], w1[kWordsK];
+    lds(row + c * (D / 8), w0);
+    lds(row + kRow + c * (D / 8), w1);
+    const uint32_t group = D / 2 + (D == 128 ? 4 * c : 4 * (c >> 1));
+    const uint32_t p0 = lds(row + group), p1 = lds(row + kRow + group);
+    const __half2 s0 = as_half2(prmt(p0, p0, 0x1010)), o0 = as_half2(prmt(p0, p0, 0x3232));
+    const __half2 s1 = as_half2(prmt(p1, p1, 0x1010)), o1 = as_half2(prmt(p1, p1, 0x3232));
+    float odd[NT][4] = {};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWordsK; ++w) {
+      uint32_t x[4], y[4];
+      codes8(w0[w], s0, o0, x);
+      codes8(w1[w], s1, o1, y);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma(acc[n], x[0], y[0], x[1], y[1], qf[n][2 * w][0], qf[n][2 * w][1], M());
+        mma(odd[n], x[2], y[2], x[3], y[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1], M());
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] += odd[n][i];
+  }
+
+  // o[t] += V^T P for the D / 16 groups of 16 elements; p[part][n]: B operands of the weights
+  template <int NT, int PARTS>
+  __device__ __forceinline__ static void values(uint32_t vst, int r, int c, int meta, const uint32_t (&p)[PARTS][NT][2],
+                                                float (&o)[D / 16][NT][4]) {
+    const int k0 = 2 * c, k1 = ((2 * c + 4) & 7) + 8;
+    const uint32_t r0 = vst + k0 * kRow, r1 = vst + k1 * kRow;
+    uint32_t w[4][kWordsV], par[4];
+    const uint32_t group = D / 2 + (D == 128 ? 4 * (r >> 1) : 4 * (r >> 2));
+    lds(r0 + r * (D / 16), w[0]);
+    lds(r1 + r * (D / 16), w[1]);
+    lds(r0 + kRow + r * (D / 16), w[2]);
+    lds(r1 + kRow + r * (D / 16), w[3]);
+    par[0] = lds(r0 + group);
+    par[1] = lds(r1 + group);
+    par[2] = lds(r0 + kRow + group);
+    par[3] = lds(r1 + kRow + group);
+    if (meta != 0x0808) {  // slots that hold no key: step and offset may be anything, the weight is 0
+      const int n0 = meta & 255, n1 = (meta >> 8) & 255;
+      if (k0 >= n0) par[0] = 0;
+      if (k1 - 8 >= n1) par[1] = 0;
+      if (k0 + 1 >= n0) par[2] = 0;
+      if (k1 - 7 >= n1) par[3] = 0;
+    }
+    const __half2 sa = as_half2(prmt(par[0], par[1], 0x5410)), oa = as_half2(prmt(par[0], par[1], 0x7632));
+    const __half2 sb = as_half2(prmt(par[2], par[3], 0x5410)), ob = as_half2(prmt(par[2], par[3], 0x7632));
+#pragma unroll
+    for (int y = 0; y < kWordsV; ++y)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {  // codes 0..3, 4..7 of the word
+        uint32_t xa[4], xb[4];
+        codes8(prmt(w[0][y], w[1][y], z ? 0x7632 : 0x5410), sa, oa, xa);
+        codes8(prmt(w[2][y], w[3][y], z ? 0x7632 : 0x5410), sb, ob, xb);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+              mma(o[4 * y + 2 * z + u][n], xa[2 * u], xa[2 * u + 1], xb[2 * u], xb[2 * u + 1], p[q][n][0], p[q][n][1], M());
+      }
+  }
+  // element that o[t][.][0 or 1] (hi = 0) and [2 or 3] (hi = 1) of lane row r hold
+  __device__ __forceinline__ static int o_element(int t, int r, int hi) { return r * (D / 8) + 2 * t + hi; }
+};
+
+// ---- the kernel -------------------------------------------------------------------------------------
+template <class F, int STAGES>
+__host__ __device__ constexpr uint32_t warp_smem() {
+  return STAGES * 2 * F::kTile + STAGES * 16;  // stages, then mbarriers (8 bytes), then metas (8 bytes)
+}
+
+template <class F, int NT, int PARTS, bool SEL, int STAGES, int BLOCKS>
+__global__ void __launch_bounds__(kWarps * 32, BLOCKS)
+    gather_kernel(const GatherArgs a, const __grid_constant__ typename F::Maps maps) {
+  using T = typename F::In;
+  using M = typename F::M;
+  constexpr int D = F::D;
+  constexpr int kB = PARTS == kTwoParts ? 2 : 1;  // B operands of the weights
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * 2 * F::kTile);
+  const uint32_t bars = dk::smem_u32(smem) + kWarps * (STAGES * 2 * F::kTile) + warp * STAGES * 16;
+  volatile int32_t* metas = reinterpret_cast<volatile int32_t*>(smem + kWarps * (STAGES * 2 * F::kTile) + warp * STAGES * 16 + STAGES * 8);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kWarps * warp_smem<F, STAGES>());
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) dk::mbar_init(bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // this warp's range [b0, b1) of the batch's tiles
+  int64_t total = 0;
+  for (int s0 = 0; s0 < a.S; s0 += 32) {
+    const int n = s0 + lane < a.S ? tiles_of<SEL>(a, checked_len(a, s0 + lane)) : 0;
+    total += __reduce_add_sync(kAll, n);
+  }
+  total *= a.H;
+  const int64_t all_warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t workers = min(all_warps, (total + kMinTiles - 1) / kMinTiles);
+  const int64_t id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
+  if (id >= workers) return;
+  const int64_t b0 = id * total / workers, b1 = (id + 1) * total / workers;
+  const int count = static_cast<int>(b1 - b0);
+
+  Cursor cur;
+  int64_t before = 0;
+  for (int s0 = 0; s0 < a.S; s0 += 32) {
+    const int n = s0 + lane < a.S ? tiles_of<SEL>(a, checked_len(a, s0 + lane)) : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned past = __ballot_sync(kAll, before + static_cast<int64_t>(upto) * a.H > b0);
+    if (past) {
+      const int f = __ffs(past) - 1;
+      const int nf = __shfl_sync(kAll, n, f), uf = __shfl_sync(kAll, upto, f);
+      const int64_t rest = b0 - before - static_cast<int64_t>(uf - nf) * a.H;
+      cur.s = s0 + f;
+      cur.h = static_cast<int>(rest / nf);
+      cur.t = static_cast<int>(rest - static_cast<int64_t>(cur.h) * nf);
       break;
     }
-    for (int i = warp; i < a.B && e * a.B + i < L; i += 4) {
-      float k[E], v[E], x = 0.f;
-      for (int y = 0; y < 2; ++y) {
-        const unsigned char* base = y ? a.v_cache : a.k_cache;
-        float* dst = y ? v : k;
-        if (Q4) {
-          const unsigned char* row = base + ((static_cast<int64_t>(frame) * a.H + h) * a.B + i) * W;
-          const __half* par = reinterpret_cast<const __half*>(row + D / 2 + (lane * E / 32) * 4);
-          for (int u = 0; u < E; ++u) {
-            const int d = lane * E + u;
-            const int n = (row[d >> 1] >> (4 * (d & 1))) & 15;
-            dst[u] = __half2float(__hfma(__int2half_rn(n), par[0], par[1]));
+    before += static_cast<int64_t>(__shfl_sync(kAll, upto, 31)) * a.H;
+  }
+  enter_seq<SEL>(a, cur);
+
+  Cursor ahead = cur;  // the producer's place
+  Ids ids;
+  ids.s = -1;
+  ids.base = 0;
+  int issued = 0;
+  auto issue = [&]() {
+    const int st = issued % STAGES;
+    const TilePlan p = plan_tile<SEL>(a, ahead, lane, ids);
+    if (lane == 0) {
+      metas[st] = p.meta;
+      const uint32_t dst = stages + st * 2 * F::kTile, bar = bars + 8 * st;
+      dk::mbar_arrive_expect_tx(bar, F::load(a, maps, p, ahead.h, dst, bar, false));
+      F::load(a, maps, p, ahead.h, dst, bar, true);
+    }
+    ++issued;
+    if (issued < count) advance<SEL>(a, ahead);
+  };
+  for (int i = 0; i < STAGES && i < count; ++i) issue();
+  __syncwarp();
+
+  uint32_t qf[NT][D / 16][2];
+  float o[D / 16][NT][4];
+  float m[NT][2], l[NT][2], f[NT][2];
+  bool poison = false;
+  int first_t = 0;
+  bool fresh = true;
+
+  for (int i = 0; i < count; ++i) {
+    if (fresh) {  // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
+      fresh = false;
+      poison = false;
+      first_t = cur.t;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int col = PARTS == kTwinColumns ? (r & 3) : 8 * n + r;
+        const T* q = static_cast<const T*>(a.q) + cur.s * a.q_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
+        float x[D / 4], top = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 4; ++j) {
+          x[j] = col < a.g ? to_float(q[F::q_element(c, j)]) : 0.f;
+          top = fmaxf(top, fabsf(x[j]));
+        }
+        float back = a.qk_scale_log2;
+        if (F::kScaleQ) {
+          top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+          // 2^-e with top in [2^e, 2^(e+1)): zero, subnormal and non-finite heads stay as they are
+          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          const bool in = top > 0.f && e > -126 && e < 126;
+          const float down = in ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+          const float up = in ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
+#pragma unroll
+          for (int j = 0; j < D / 4; ++j) x[j] *= down;
+          back *= up;
+        }
+        F::load_q(x, qf[n]);
+        f[n][0] = __shfl_sync(kAll, back, 8 * c);       // column 2c is lane row 2c
+        f[n][1] = __shfl_sync(kAll, back, 8 * c + 4);
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+      }
+    }
+    const int st = i % STAGES;
+    if (!__all_sync(kAll, dk::mbar_wait(bars + 8 * st, (i / STAGES) & 1, abort_flag, a.status))) {
+      // a copy is stuck: let those in flight land (bounded) before the block retires
+      const long long t0 = clock64();
+      for (int j = i; j < issued; ++j)
+        while (!dk::mbar_try_wait(bars + 8 * (j % STAGES), (j / STAGES) & 1) && clock64() - t0 < dk::kDrainCycles) {
+        }
+      return;
+    }
+    const int meta = metas[st];
+    if (meta >> 16) poison = true;
+    if (meta & 0xffff) {
+      const uint32_t kst = stages + st * 2 * F::kTile, vst = kst + F::kTile;
+      float x[NT][4];
+      F::template scores<NT>(kst, r, c, qf, x);
+      uint32_t p[kB][NT][2];
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] *= f[n][j & 1];
+        if ((meta & 0xffff) != 0x0808) {
+          const int k0 = F::key_of(r), k1 = F::key_of(r) + F::kSecond;
+          const int n0 = meta & 255, n1 = (meta >> 8) & 255;
+          const bool in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1, in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
+          if (!in0) x[n][0] = x[n][1] = -INFINITY;
+          if (!in1) x[n][2] = x[n][3] = -INFINITY;
+        }
+        over = over || fmaxf(x[n][0], x[n][2]) > m[n][0] + kSlack || fmaxf(x[n][1], x[n][3]) > m[n][1] + kSlack;
+      }
+      if (__any_sync(kAll, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float t = fmaxf(x[n][j], x[n][j + 2]);
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, s));
+            const float now = fmaxf(m[n][j], t);
+            const float less = m[n][j] == now ? 1.f : dk::ex2(m[n][j] - now);
+            m[n][j] = now;
+            l[n][j] *= less;
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) {
+              o[u][n][j] *= less;
+              o[u][n][j + 2] *= less;
+            }
           }
-        } else {
-          const T* row = reinterpret_cast<const T*>(base) + ((static_cast<int64_t>(frame) * a.B + i) * a.H + h) * D;
-          for (int u = 0; u < E; ++u) dst[u] = to_float(row[lane * E + u]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = dk::ex2(x[n][j] - m[n][j & 1]);
+        l[n][0] += w[0] + w[2];
+        l[n][1] += w[1] + w[3];
+        if (PARTS == kTwinColumns) {
+          if (c >= 2) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
+          }
+        }
+        p[0][n][0] = transpose8(pack2<M>(w[0], w[1]));
+        p[0][n][1] = transpose8(pack2<M>(w[2], w[3]));
+        if (PARTS == kTwoParts) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
+          p[kB - 1][n][0] = transpose8(pack2<M>(w[0], w[1]));
+          p[kB - 1][n][1] = transpose8(pack2<M>(w[2], w[3]));
         }
       }
-      for (int u = 0; u < E; ++u) x = fmaf(qv[u], k[u], x);
-      for (int b = 16; b; b >>= 1) x += __shfl_xor_sync(kAll, x, b);
-      x *= a.qk_scale_log2;
-      const float mn = fmaxf(m, x), al = exp2f(m - mn), p = exp2f(x - mn);
-      l = l * al + p;
-      for (int u = 0; u < E; ++u) o[u] = o[u] * al + p * v[u];
-      m = mn;
+      F::template values<NT, kB>(vst, r, c, meta & 0xffff, p, o);
     }
-  }
-  sm_m[warp] = m;
-  sm_l[warp] = l;
-  for (int u = 0; u < E; ++u) sm_o[warp][lane * E + u] = o[u];
-  __syncthreads();
-  T* out = static_cast<T*>(a.out) + s * a.out_row + hq * D;
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float mm = -INFINITY, ll = 0.f, oo = 0.f;
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sm_m[w]);
-    for (int w = 0; w < 4; ++w) {
-      if (sm_l[w] == 0.f) continue;
-      const float al = exp2f(sm_m[w] - mm);
-      ll += al * sm_l[w];
-      oo += al * sm_o[w][d];
+    __syncwarp();
+    if (issued < count) issue();
+
+    const bool ends = cur.t + 1 == cur.tiles;
+    if (ends || i + 1 == count) {
+      // ---- the end of a piece of (s, h) ----
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) l[n][j] += __shfl_xor_sync(kAll, l[n][j], s);
+          if (PARTS == kTwinColumns) {
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              o[t][n][j] += __shfl_xor_sync(kAll, o[t][n][j], 2);
+              o[t][n][j + 2] += __shfl_xor_sync(kAll, o[t][n][j + 2], 2);
+            }
+          }
+        }
+      const bool whole = first_t == 0 && ends;
+      const int64_t slot = 2 * id + (first_t == 0 ? 1 : 0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = 8 * n + 2 * c + j;
+          if (col >= a.g || (PARTS == kTwinColumns && c >= 2)) continue;
+          if (whole) {
+            const float inv = poison || !(l[n][j] != 0.f) ? 0.f : 1.f / l[n][j];
+            T* out = static_cast<T*>(a.out) + cur.s * a.out_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+              for (int hi = 0; hi < 2; ++hi) {
+                const float y = poison ? 0.f : o[t][n][j + 2 * hi] * inv;
+                dk::Chunk<T>::store1(out + F::o_element(t, r, hi), y);
+              }
+          } else {
+            float* ml = a.ws_ml + (slot * a.g + col) * 2;
+            float* wo = a.ws_o + (slot * a.g + col) * D;
+            if (r == 0) {
+              ml[0] = m[n][j];
+              ml[1] = poison ? -1.f : l[n][j];
+            }
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+              for (int hi = 0; hi < 2; ++hi) wo[F::o_element(t, r, hi)] = o[t][n][j + 2 * hi];
+          }
+        }
+      if (!whole) {
+        __threadfence();
+        __syncwarp();
+        const int64_t p0 = b0 + i - cur.t, p1 = p0 + cur.tiles;  // the tiles of (s, h)
+        const int64_t w0 = ((p0 + 1) * workers - 1) / total, w1 = (p1 * workers - 1) / total;
+        const int pieces = static_cast<int>(w1 - w0) + 1;
+        int32_t* cnt = a.cnt + static_cast<int64_t>(cur.s) * a.H + cur.h;
+        int done = 0;
+        if (lane == 0) done = atomicAdd(cnt, 1);
+        done = __shfl_sync(kAll, done, 0);
+        if (done == pieces - 1) {
+          __threadfence();
+          if (lane == 0) *cnt = 0;
+          for (int col = 0; col < a.g; ++col) {
+            auto at = [&](int k) { return (2 * (w0 + k) + (k == 0 ? 1 : 0)) * a.g + col; };
+            float top = -INFINITY, sum = 0.f;
+            bool bad = false;
+            for (int k = lane; k < pieces; k += 32) {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at(k));
+              bad = bad || x.y < 0.f;
+              if (x.y != 0.f) top = fmaxf(top, x.x);
+            }
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
+            bad = __any_sync(kAll, bad);
+            constexpr int E = D / 32;
+            float y[E] = {};
+            for (int k = 0; k < pieces; ++k) {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at(k));
+              if (x.y == 0.f) continue;
+              const float w = dk::ex2(x.x - top);
+              sum += w * x.y;
+              const float* wo = a.ws_o + at(k) * D + lane * E;
+#pragma unroll
+              for (int u = 0; u < E; ++u) y[u] += w * __ldcg(wo + u);
+            }
+            const float inv = bad || !(sum != 0.f) ? 0.f : 1.f / sum;
+            T* out = static_cast<T*>(a.out) + cur.s * a.out_row + (static_cast<int64_t>(cur.h) * a.g + col) * D + lane * E;
+#pragma unroll
+            for (int u = 0; u < E; ++u) dk::Chunk<T>::store1(out + u, bad ? 0.f : y[u] * inv);
+          }
+        }
+      }
+      fresh = true;
     }
-    out[d] = from_float<T>(bad || ll == 0.f ? 0.f : oo / ll);
+    if (i + 1 < count) advance<SEL>(a, cur);
   }
 }
 
-template <typename T, bool Q4, int D>
-cudaError_t launch_simple(const GatherArgs& a, cudaStream_t stream) {
-  simple_kernel<T, Q4, D><<<dim3(a.g * a.H, a.S), 128, 0, stream>>>(a);
-  return cudaGetLastError();
+// Blocks per SM and partial slots of a launch; launches when `query` is null.
+template <class F, int NT, int PARTS, bool SEL, int STAGES, int BLOCKS>
+cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
+  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, BLOCKS>);
+  constexpr uint32_t smem = kWarps * warp_smem<F, STAGES>() + 16;  // + the abort flag
+  int occ = 0;
+  cudaError_t e = kernel_prep(fn, kWarps * 32, smem, &occ);
+  if (e != cudaSuccess) return e;
+  if (occ < 1) return cudaErrorInvalidConfiguration;
+  const int grid = num_sms * (occ < BLOCKS ? occ : BLOCKS);
+  if (query) {
+    *query = grid * kWarps;
+    return cudaSuccess;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, SEL, STAGES, BLOCKS>, a, maps);
 }
 
 }  // namespace gk

@@ -251,16 +251,17 @@ struct GatherArgs {
   const int32_t* selected;      // [S, H, K]; null: every frame
   int64_t sel_seq, sel_head;    // elements between sequences, heads of `selected`
   int32_t K;
-  int32_t S, H, g, B, num_blocks, max_blocks;
+  int32_t S, H, g, B, log2_B, num_blocks, max_blocks;
   float qk_scale_log2;          // scale * log2(e)
   int32_t* cnt;                 // [S * H] partials finished per (sequence, head), zero between launches
   float* ws_ml;                 // [slots][g][2] partial (max, sum)
   float* ws_o;                  // [slots][g][D] partial unnormalised outputs
   int32_t* status;
 };
-cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int grid, cudaStream_t stream);
+// workers: not null: only report the launch's warps (each may leave two partials)
+cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int num_sms, cudaStream_t stream, int* workers);
 cudaError_t launch_decode_selected(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk,
-                                   const CUtensorMap& tv, int grid, cudaStream_t stream);
+                                   const CUtensorMap& tv, int num_sms, cudaStream_t stream, int* workers);
 
 // ---- frame bounds and selection (select.cu) ---------------------------------------------------
 struct BoundsArgs {

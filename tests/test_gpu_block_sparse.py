@@ -150,16 +150,25 @@ def test_selection_bad_indexes(pa):
 # ---- decode over listed frames ---------------------------------------------------------------------------
 def check_selected(pa, case, sel, scale, dtype):
     q, kc, vc, tables, lens = case
-    B, H = kc.shape[1], kc.shape[2]
-    g = q.shape[1] // H
     out = torch.full_like(q, float("nan"))
     pa.pa_decode_selected(q, kc, vc, tables, lens, sel, scale, out)
     torch.cuda.synchronize()
     assert pa.pa_get_device_status() == 0
+    compare_selected(out, case, sel, scale, dtype)
+    return out
+
+
+def compare_selected(out, case, sel, scale, dtype, only=None):
+    """out against 64 bits; only: the (sequence, key head) pairs looked at."""
+    q, kc, vc, tables, lens = case
+    B, H = kc.shape[1], kc.shape[2]
+    g = q.shape[1] // H
     got, qh = host64(out), host64(q)
     kh, vh, th = kc.cpu(), vc.cpu(), tables.cpu().long()
     for s, n in enumerate(lens.tolist()):
         for h in range(H):
+            if only is not None and (s, h) not in only:
+                continue
             tok = []
             for e in sel[s, h].tolist()[: -(-n // B)]:
                 if e == -1:
@@ -171,7 +180,6 @@ def check_selected(pa, case, sel, scale, dtype):
             tol = attention_tolerance(ref, TD[dtype], qh[s, h * g:h * g + g], k, v, scale, 2.0 ** (-22 if dtype == "f16" else -16))
             err = np.abs(got[s, h * g:h * g + g] - ref)
             assert (err <= tol).all(), (s, h, n, float((err - tol).max()), float(err.max()))
-    return out
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -229,7 +237,9 @@ def test_selected_decode_bad_indexes(pa):
     torch.cuda.synchronize()
     assert pa.pa_get_device_status() == pa.PA_DEV_BAD_BLOCK | pa.PA_DEV_BAD_LEN
     assert not out[0].any() and not out[1].any() and not out[2, 2:].any() and not out[3, :2].any()
-    assert torch.equal(out[2, :2], good[2, :2]) and torch.equal(out[3, 2:], good[3, 2:])
+    # the batch is cut among the warps by its lengths: with one of them bad the cuts lie elsewhere and the other
+    # heads' fp32 sums are taken in another order, so they are held to the 64-bit result and not to equal bits
+    compare_selected(out, case, sel, 0.1, "bf16", only={(2, 0), (3, 1)})
     assert torch.equal(check_selected(pa, case, sel, 0.1, "bf16"), good)
 
 

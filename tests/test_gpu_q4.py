@@ -201,7 +201,9 @@ def test_decode_bad_indexes(pa):
     torch.cuda.synchronize()
     assert pa.pa_get_device_status() == pa.PA_DEV_BAD_BLOCK | pa.PA_DEV_BAD_LEN
     assert not out[:3].any()
-    assert torch.equal(out[3], good[3])
+    # cut among the warps by its lengths, a batch with one of them bad sums in another order: held to the 64-bit result
+    ref, k, v = decode_reference(q, kc, vc, tables, lens, 16, 0.125, 3)
+    assert (np.abs(host64(out[3]) - ref) <= attention_tolerance(ref, torch.float16, host64(q[3]), k, v, 0.125, 2.0 ** -22)).all()
     bad_l[2] = -1
     pa.pa_decode_q4(q.cuda(), kc.cuda(), vc.cuda(), tables.cuda(), bad_l.cuda(), 0.125, out)
     torch.cuda.synchronize()
