@@ -40,20 +40,24 @@ struct RowFormat {
   struct Maps {
     CUtensorMap k, v;
   };
-  __device__ __forceinline__ static uint32_t load(const GatherArgs& a, const Maps& maps, const TilePlan& p, int h,
-                                                  uint32_t dst, uint32_t bar, bool issue) {
-    uint32_t bytes = 0;
+  struct Place {
+    int slot[2];     // first slot of each half; < 0: nothing to load
+  };
+  __device__ __forceinline__ static Place place(const GatherArgs& a, const TilePlan& p, int) {
+    Place x;
+    x.slot[0] = p.frame[0] >= 0 ? p.frame[0] * a.B + p.row : -1;
+    x.slot[1] = p.frame[1] >= 0 ? p.frame[1] * a.B + p.row + (a.B >= 16 ? 8 : 0) : -1;
+    return x;
+  }
+  __device__ __forceinline__ static void load(const GatherArgs&, const Maps& maps, const Place& x, int h, uint32_t dst,
+                                              uint32_t bar) {
+    dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * 2 * kHalfTile);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (p.frame[i] < 0) continue;
-      if (issue) {
-        const int row = p.frame[i] * a.B + p.row + (a.B >= 16 ? 8 * i : 0);  // a slot: fits int32
-        tma_load_4d(dst + i * kHalfTile, &maps.k, 0, row, 0, h, bar);
-        tma_load_4d(dst + kTile + i * kHalfTile, &maps.v, 0, row, 0, h, bar);
-      }
-      bytes += 2 * kHalfTile;
+      if (x.slot[i] < 0) continue;
+      tma_load_4d(dst + i * kHalfTile, &maps.k, 0, x.slot[i], 0, h, bar);
+      tma_load_4d(dst + kTile + i * kHalfTile, &maps.v, 0, x.slot[i], 0, h, bar);
     }
-    return bytes;
   }
 
   __device__ __forceinline__ static int q_element(int c, int i) { return 16 * (i >> 2) + 2 * c + (i & 1) + ((i & 2) << 2); }

@@ -131,54 +131,13 @@ __device__ __forceinline__ void enter_seq(const GatherArgs& a, Cursor& c) {
   c.tiles = tiles_of<SEL>(a, L);
 }
 
+// To the next (s, h).
 template <bool SEL>
-__device__ __forceinline__ void advance(const GatherArgs& a, Cursor& c) {
-  if (++c.t < c.tiles) return;
+__device__ __forceinline__ void next_head(const GatherArgs& a, Cursor& c) {
   c.t = 0;
   if (++c.h < a.H) return;
   c.h = 0;
   if (++c.s < a.S) enter_seq<SEL>(a, c);
-}
-
-// Frame ids of up to 32 consecutive entries of one table or list, one per lane.
-struct Ids {
-  int s, h, base;   // where they start (base: entry of lane 0)
-  int frame;        // this lane's frame id; -1: bad, -2: none
-  int entry;        // its position in the sequence's table
-  bool ended;       // the list ended before `base`
-};
-
-template <bool SEL>
-__device__ __forceinline__ void refill(const GatherArgs& a, const Cursor& c, int base, int lane, Ids& ids) {
-  const bool on = ids.s == c.s && (!SEL || ids.h == c.h) && base > ids.base;
-  const int32_t* table = a.block_tables + c.s * a.bt_row;
-  const int j = base + lane;
-  int e = j;
-  bool have = j < c.blocks;
-  if (SEL) {
-    const int32_t* list = a.selected + c.s * a.sel_seq + c.h * a.sel_head;
-    const int n = min(a.K, c.blocks);
-    if (!on) ids.ended = false;
-    for (int b = on ? ids.base + 32 : 0; b < base && !ids.ended; b += 32)  // entries passed over unseen
-      ids.ended = __any_sync(kAll, b + lane < n && list[min(b + lane, n - 1)] == -1);
-    e = j < n && !ids.ended ? list[j] : -1;
-    const unsigned ends = __ballot_sync(kAll, e == -1);
-    have = (ends & ((2u << lane) - 1u)) == 0;  // no end at this lane or before
-    ids.ended = ids.ended || ends != 0;
-  }
-  int frame = -2;
-  if (have) {
-    frame = e >= 0 && e < c.blocks ? table[e] : -1;
-    if (frame < 0 || frame >= a.num_blocks) {
-      atomicOr(a.status, kDevBadBlock);
-      frame = -1;
-    }
-  }
-  ids.s = c.s;
-  ids.h = c.h;
-  ids.base = base;
-  ids.frame = frame;
-  ids.entry = e;
 }
 
 // One tile as the producer sees it: two halves of 8 keys, each inside one frame.
@@ -188,22 +147,54 @@ struct TilePlan {
   int meta;       // keys of the halves (0..8 each) | 1 << 16 for a bad frame id
 };
 
+// Where the list of (s, h) ends, as far as it has been read (SEL).
+struct List {
+  int seen;    // entries read so far
+  bool ended;
+};
+
+// Table position and frame of entry j of (s, h), one entry per lane: frame -1 bad, -2 none.  `list`: for SEL,
+// entries [0, list.seen) have been read; j - lane is at or behind that.
+__device__ __forceinline__ int checked_frame(const GatherArgs& a, const Cursor& c, int e) {
+  int frame = e >= 0 && e < c.blocks ? a.block_tables[c.s * a.bt_row + e] : -1;
+  if (frame < 0 || frame >= a.num_blocks) {
+    atomicOr(a.status, kDevBadBlock);
+    frame = -1;
+  }
+  return frame;
+}
+
+// Plans of the 32 tiles t0 .. t0 + 31 of (s, h), one per lane.
 template <bool SEL>
-__device__ __forceinline__ TilePlan plan_tile(const GatherArgs& a, const Cursor& c, int lane, Ids& ids) {
+__device__ __forceinline__ TilePlan plan_tiles(const GatherArgs& a, const Cursor& c, int t0, int lane, List& list) {
   TilePlan p;
-  const bool pairs = a.B < 16;
-  const int per = a.log2_B - 4;                      // log2(tiles of a frame)
-  const int j = pairs ? 2 * c.t : c.t >> per;
-  p.row = pairs ? 0 : (c.t & ((1 << per) - 1)) << 4;
-  if (ids.s != c.s || (SEL && ids.h != c.h) || j < ids.base || j >= ids.base + 32)
-    refill<SEL>(a, c, j & ~31, lane, ids);
-  const int at = j - ids.base;
-  p.frame[0] = __shfl_sync(kAll, ids.frame, at);
-  const int e0 = __shfl_sync(kAll, ids.entry, at);
-  p.frame[1] = pairs ? __shfl_sync(kAll, ids.frame, at + 1) : p.frame[0];
-  const int e1 = pairs ? __shfl_sync(kAll, ids.entry, at + 1) : e0;
-  const int n0 = p.frame[0] >= 0 ? min(8, max(0, c.L - e0 * a.B - p.row)) : 0;
-  const int n1 = p.frame[1] >= 0 ? min(8, max(0, c.L - e1 * a.B - (pairs ? 0 : p.row + 8))) : 0;
+  const bool pairs = a.B < 16;             // a tile is two frames of 8
+  const int per = a.log2_B - 4;            // log2(tiles of a frame)
+  const int t = t0 + lane;
+  const int j = pairs ? 2 * t : t >> per;  // first entry of this lane's tile
+  p.row = pairs ? 0 : (t & ((1 << per) - 1)) << 4;
+  int e[2] = {j, j + 1};
+  const int n = SEL ? min(a.K, c.blocks) : c.blocks;
+  bool have[2] = {t < c.tiles && j < n, t < c.tiles && pairs && j + 1 < n};
+  if (SEL) {
+    const int32_t* entries = a.selected + c.s * a.sel_seq + c.h * a.sel_head;
+    const int j0 = pairs ? 2 * t0 : t0 >> per;
+    for (int b = list.seen; b < j0 && !list.ended; b += 32)  // entries of other warps' tiles
+      list.ended = __any_sync(kAll, b + lane < j0 && entries[min(b + lane, n - 1)] == -1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) e[i] = have[i] && !list.ended ? entries[e[i]] : -1;
+    const unsigned end0 = __ballot_sync(kAll, e[0] == -1), end1 = __ballot_sync(kAll, pairs && e[1] == -1);
+    const unsigned upto = (2u << lane) - 1u, before = upto >> 1;  // lanes 0 .. lane, 0 .. lane - 1
+    have[0] = (end0 & upto) == 0 && (end1 & before) == 0;
+    have[1] = pairs && (end0 & upto) == 0 && (end1 & upto) == 0;
+    list.ended = list.ended || end0 != 0 || end1 != 0;
+    list.seen = max(list.seen, j0);
+  }
+  p.frame[0] = have[0] ? checked_frame(a, c, e[0]) : -2;
+  p.frame[1] = pairs ? (have[1] ? checked_frame(a, c, e[1]) : -2) : p.frame[0];
+  if (!pairs) e[1] = e[0];
+  const int n0 = p.frame[0] >= 0 ? min(8, max(0, c.L - e[0] * a.B - p.row)) : 0;
+  const int n1 = p.frame[1] >= 0 ? min(8, max(0, c.L - e[1] * a.B - (pairs ? 0 : p.row + 8))) : 0;
   p.meta = n0 | (n1 << 8) | (p.frame[0] == -1 || p.frame[1] == -1 ? 1 << 16 : 0);
   if (n0 == 0) p.frame[0] = -2;
   if (n1 == 0) p.frame[1] = -2;
@@ -247,24 +238,34 @@ struct Q4Format {
   __device__ __forceinline__ static int key_of(int r) { return (r & 1) ? ((r + 3) & 7) + 8 : r; }
 
   struct Maps {};
-  __device__ __forceinline__ static uint32_t load(const GatherArgs& a, const Maps&, const TilePlan& p, int h, uint32_t dst,
-                                                  uint32_t bar, bool issue) {
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (p.frame[i] < 0) continue;
-      const bool whole = i == 0 && p.frame[0] == p.frame[1] && a.B >= 16;
-      const uint32_t n = whole ? kTile : kHalfTile;
-      if (issue) {
-        const int row = p.row + (a.B >= 16 ? 8 * i : 0);
-        const int64_t at = ((static_cast<int64_t>(p.frame[i]) * a.H + h) * a.B + row) * kRow;
-        bulk_load(dst + i * kHalfTile, a.k_cache + at, n, bar);
-        bulk_load(dst + kTile + i * kHalfTile, a.v_cache + at, n, bar);
-      }
-      bytes += 2 * n;
-      if (whole) break;
+  // What the lane that plans a tile keeps of it.
+  struct Place {
+    int64_t at[2];    // byte offsets of the halves
+    uint32_t bytes;   // of K and V together
+    bool whole, on[2];
+  };
+  __device__ __forceinline__ static Place place(const GatherArgs& a, const TilePlan& p, int h) {
+    Place x;
+    x.whole = a.B >= 16 && p.frame[0] >= 0 && p.frame[1] >= 0;
+    x.on[0] = p.frame[0] >= 0;
+    x.on[1] = p.frame[1] >= 0 && !x.whole;
+    x.at[0] = ((static_cast<int64_t>(p.frame[0]) * a.H + h) * a.B + p.row) * kRow;
+    x.at[1] = ((static_cast<int64_t>(p.frame[1]) * a.H + h) * a.B + p.row + (a.B >= 16 ? 8 : 0)) * kRow;
+    x.bytes = 2 * (x.whole ? kTile : (x.on[0] ? kHalfTile : 0) + (x.on[1] ? kHalfTile : 0));
+    return x;
+  }
+  __device__ __forceinline__ static void load(const GatherArgs& a, const Maps&, const Place& x, int, uint32_t dst,
+                                              uint32_t bar) {
+    dk::mbar_arrive_expect_tx(bar, x.bytes);
+    if (x.on[0]) {
+      const uint32_t n = x.whole ? kTile : kHalfTile;
+      bulk_load(dst, a.k_cache + x.at[0], n, bar);
+      bulk_load(dst + kTile, a.v_cache + x.at[0], n, bar);
     }
-    return bytes;
+    if (x.on[1]) {
+      bulk_load(dst + kHalfTile, a.k_cache + x.at[1], kHalfTile, bar);
+      bulk_load(dst + kTile + kHalfTile, a.v_cache + x.at[1], kHalfTile, bar);
+    }
   }
 
   // B operands of a query's D elements for the D / 16 score steps of lane (r, c)
@@ -424,22 +425,32 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   }
   enter_seq<SEL>(a, cur);
 
-  Cursor ahead = cur;  // the producer's place
-  Ids ids;
-  ids.s = -1;
-  ids.base = 0;
-  int issued = 0;
+  // The producer's place.  Lane i plans the tiles i, i + 32, ... of a (s, h) and issues their copies itself.
+  Cursor ahead = cur;
+  List list = {0, false};
+  int planned = -1;  // first tile of the window of 32 that the lanes have planned; -1: none
+  typename F::Place place;
+  int plan_meta = 0;
+  int issued = 0, issue_st = 0;
   auto issue = [&]() {
-    const int st = issued % STAGES;
-    const TilePlan p = plan_tile<SEL>(a, ahead, lane, ids);
-    if (lane == 0) {
-      metas[st] = p.meta;
-      const uint32_t dst = stages + st * 2 * F::kTile, bar = bars + 8 * st;
-      dk::mbar_arrive_expect_tx(bar, F::load(a, maps, p, ahead.h, dst, bar, false));
-      F::load(a, maps, p, ahead.h, dst, bar, true);
+    if ((ahead.t & ~31) != planned) {
+      planned = ahead.t & ~31;
+      const TilePlan p = plan_tiles<SEL>(a, ahead, planned, lane, list);
+      place = F::place(a, p, ahead.h);
+      plan_meta = p.meta;
     }
+    if (lane == (ahead.t & 31)) {
+      metas[issue_st] = plan_meta;
+      F::load(a, maps, place, ahead.h, stages + issue_st * 2 * F::kTile, bars + 8 * issue_st);
+    }
+    if (++issue_st == STAGES) issue_st = 0;
     ++issued;
-    if (issued < count) advance<SEL>(a, ahead);
+    if (++ahead.t == ahead.tiles && issued < count) {
+      next_head<SEL>(a, ahead);
+      planned = -1;
+      list.seen = 0;
+      list.ended = false;
+    }
   };
   for (int i = 0; i < STAGES && i < count; ++i) issue();
   __syncwarp();
@@ -447,125 +458,130 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
-  bool poison = false;
-  int first_t = 0;
-  bool fresh = true;
+  int st = 0, phase = 0;
 
-  for (int i = 0; i < count; ++i) {
-    if (fresh) {  // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
-      fresh = false;
-      poison = false;
-      first_t = cur.t;
+  for (int i = 0; i < count;) {
+    // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
+    const int first_t = cur.t;
+    bool poison = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int col = PARTS == kTwinColumns ? (r & 3) : 8 * n + r;
-        const T* q = static_cast<const T*>(a.q) + cur.s * a.q_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
-        float x[D / 4], top = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      const int col = PARTS == kTwinColumns ? (r & 3) : 8 * n + r;
+      const T* q = static_cast<const T*>(a.q) + cur.s * a.q_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
+      float x[D / 4], top = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 4; ++j) {
-          x[j] = col < a.g ? to_float(q[F::q_element(c, j)]) : 0.f;
-          top = fmaxf(top, fabsf(x[j]));
-        }
-        float back = a.qk_scale_log2;
-        if (F::kScaleQ) {
-          top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-          // 2^-e with top in [2^e, 2^(e+1)): zero, subnormal and non-finite heads stay as they are
-          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-          const bool in = top > 0.f && e > -126 && e < 126;
-          const float down = in ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
-          const float up = in ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
-#pragma unroll
-          for (int j = 0; j < D / 4; ++j) x[j] *= down;
-          back *= up;
-        }
-        F::load_q(x, qf[n]);
-        f[n][0] = __shfl_sync(kAll, back, 8 * c);       // column 2c is lane row 2c
-        f[n][1] = __shfl_sync(kAll, back, 8 * c + 4);
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+      for (int j = 0; j < D / 4; ++j) {
+        x[j] = col < a.g ? to_float(q[F::q_element(c, j)]) : 0.f;
+        top = fmaxf(top, fabsf(x[j]));
       }
+      float back = a.qk_scale_log2;
+      if (F::kScaleQ) {
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        // 2^-e with top in [2^e, 2^(e+1)): zero, subnormal and non-finite heads stay as they are
+        const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        const bool in = top > 0.f && e > -126 && e < 126;
+        const float down = in ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+        const float up = in ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
+#pragma unroll
+        for (int j = 0; j < D / 4; ++j) x[j] *= down;
+        back *= up;
+      }
+      F::load_q(x, qf[n]);
+      f[n][0] = __shfl_sync(kAll, back, 8 * c);       // column 2c is lane row 2c
+      f[n][1] = __shfl_sync(kAll, back, 8 * c + 4);
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
     }
-    const int st = i % STAGES;
-    if (!__all_sync(kAll, dk::mbar_wait(bars + 8 * st, (i / STAGES) & 1, abort_flag, a.status))) {
-      // a copy is stuck: let those in flight land (bounded) before the block retires
-      const long long t0 = clock64();
-      for (int j = i; j < issued; ++j)
-        while (!dk::mbar_try_wait(bars + 8 * (j % STAGES), (j / STAGES) & 1) && clock64() - t0 < dk::kDrainCycles) {
+    const int stop = min(count, i + cur.tiles - cur.t);
+    cur.t += stop - i;
+    for (; i < stop; ++i) {
+      if (!__all_sync(kAll, dk::mbar_wait(bars + 8 * st, phase, abort_flag, a.status))) {
+        // a copy is stuck: let those in flight land (bounded) before the block retires
+        const long long t0 = clock64();
+        for (; i < issued; ++i) {
+          while (!dk::mbar_try_wait(bars + 8 * st, phase) && clock64() - t0 < dk::kDrainCycles) {
+          }
+          if (++st == STAGES) st = 0, phase ^= 1;
         }
-      return;
-    }
-    const int meta = metas[st];
-    if (meta >> 16) poison = true;
-    if (meta & 0xffff) {
-      const uint32_t kst = stages + st * 2 * F::kTile, vst = kst + F::kTile;
-      float x[NT][4];
-      F::template scores<NT>(kst, r, c, qf, x);
-      uint32_t p[kB][NT][2];
-      bool over = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] *= f[n][j & 1];
-        if ((meta & 0xffff) != 0x0808) {
+        return;
+      }
+      const int meta = metas[st];
+      if (meta >> 16) poison = true;
+      if (meta & 0xffff) {
+        const uint32_t kst = stages + st * 2 * F::kTile, vst = kst + F::kTile;
+        float x[NT][4], y[NT][4];
+        F::template scores<NT>(kst, r, c, qf, x);
+        const bool part = (meta & 0xffff) != 0x0808;
+        bool in0 = true, in1 = true;
+        if (part) {
           const int k0 = F::key_of(r), k1 = F::key_of(r) + F::kSecond;
           const int n0 = meta & 255, n1 = (meta >> 8) & 255;
-          const bool in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1, in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
-          if (!in0) x[n][0] = x[n][1] = -INFINITY;
-          if (!in1) x[n][2] = x[n][3] = -INFINITY;
+          in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1;
+          in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
         }
-        over = over || fmaxf(x[n][0], x[n][2]) > m[n][0] + kSlack || fmaxf(x[n][1], x[n][3]) > m[n][1] + kSlack;
-      }
-      if (__any_sync(kAll, over)) {
+        float top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float t = fmaxf(x[n][j], x[n][j + 2]);
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, s));
-            const float now = fmaxf(m[n][j], t);
-            const float less = m[n][j] == now ? 1.f : dk::ex2(m[n][j] - now);
-            m[n][j] = now;
-            l[n][j] *= less;
-#pragma unroll
-            for (int u = 0; u < D / 16; ++u) {
-              o[u][n][j] *= less;
-              o[u][n][j + 2] *= less;
-            }
+          for (int j = 0; j < 4; ++j) {
+            y[n][j] = fmaf(x[n][j], f[n][j & 1], -m[n][j & 1]);
+            if (!(j < 2 ? in0 : in1)) y[n][j] = -INFINITY;
+            top = fmaxf(top, y[n][j]);
           }
-      }
+        if (__any_sync(kAll, top > kSlack)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float w[4];
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = dk::ex2(x[n][j] - m[n][j & 1]);
-        l[n][0] += w[0] + w[2];
-        l[n][1] += w[1] + w[3];
-        if (PARTS == kTwinColumns) {
-          if (c >= 2) {
+            for (int j = 0; j < 2; ++j) {
+              const float z0 = in0 ? x[n][j] * f[n][j] : -INFINITY, z1 = in1 ? x[n][j + 2] * f[n][j] : -INFINITY;
+              float t = fmaxf(z0, z1);
+#pragma unroll
+              for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, s));
+              const float now = fmaxf(m[n][j], t);
+              const float less = m[n][j] == now ? 1.f : dk::ex2(m[n][j] - now);
+              m[n][j] = now;
+              y[n][j] = z0 - now;
+              y[n][j + 2] = z1 - now;
+              l[n][j] *= less;
+#pragma unroll
+              for (int u = 0; u < D / 16; ++u) {
+                o[u][n][j] *= less;
+                o[u][n][j + 2] *= less;
+              }
+            }
+        }
+        uint32_t p[kB][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = dk::ex2(y[n][j]);
+          l[n][0] += w[0] + w[2];
+          l[n][1] += w[1] + w[3];
+          if (PARTS == kTwinColumns) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] -= c >= 2 ? round_to<M>(w[j]) : 0.f;
+          }
+          p[0][n][0] = transpose8(pack2<M>(w[0], w[1]));
+          p[0][n][1] = transpose8(pack2<M>(w[2], w[3]));
+          if (PARTS == kTwoParts) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
+            p[kB - 1][n][0] = transpose8(pack2<M>(w[0], w[1]));
+            p[kB - 1][n][1] = transpose8(pack2<M>(w[2], w[3]));
           }
         }
-        p[0][n][0] = transpose8(pack2<M>(w[0], w[1]));
-        p[0][n][1] = transpose8(pack2<M>(w[2], w[3]));
-        if (PARTS == kTwoParts) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
-          p[kB - 1][n][0] = transpose8(pack2<M>(w[0], w[1]));
-          p[kB - 1][n][1] = transpose8(pack2<M>(w[2], w[3]));
-        }
+        F::template values<NT, kB>(vst, r, c, meta & 0xffff, p, o);
       }
-      F::template values<NT, kB>(vst, r, c, meta & 0xffff, p, o);
+      __syncwarp();
+      if (issued < count) issue();
+      if (++st == STAGES) st = 0, phase ^= 1;
     }
-    __syncwarp();
-    if (issued < count) issue();
 
-    const bool ends = cur.t + 1 == cur.tiles;
-    if (ends || i + 1 == count) {
+    {
       // ---- the end of a piece of (s, h) ----
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -581,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
             }
           }
         }
-      const bool whole = first_t == 0 && ends;
+      const bool whole = first_t == 0 && cur.t == cur.tiles;
       const int64_t slot = 2 * id + (first_t == 0 ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -655,9 +671,8 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
           }
         }
       }
-      fresh = true;
     }
-    if (i + 1 < count) advance<SEL>(a, cur);
+    if (i < count) next_head<SEL>(a, cur);
   }
 }
 
