@@ -211,13 +211,19 @@ __device__ __forceinline__ TilePlan plan_tiles(const GatherArgs& a, const Cursor
 // Rows of the score tile are keys in the order perm(0..15) = 0,12,2,14,4,8,6,10,1,13,3,15,5,9,7,11:
 // with 80-byte rows (20 banks) the 16-byte reads of K (rows r and r + 1 of a tile together) and the
 // 8-byte reads of V (rows 2c) then touch every bank once.
+// (w & mask) | magic in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "r"(mask), "r"(magic));
+  return y;
+}
 __device__ __forceinline__ void codes8(uint32_t w, __half2 step, __half2 off, uint32_t (&x)[4]) {
   const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k64 = __half2half2(__ushort_as_half(0x5400));
   const uint32_t w8 = w >> 8;
-  const __half2 y0 = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), k1024);
-  const __half2 y1 = __hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), k64);
-  const __half2 y2 = __hsub2(as_half2((w8 & 0x000f000fu) | 0x64006400u), k1024);
-  const __half2 y3 = __hsub2(as_half2((w8 & 0x00f000f0u) | 0x54005400u), k64);
+  const __half2 y0 = __hsub2(as_half2(and_or(w, 0x000f000fu, 0x64006400u)), k1024);
+  const __half2 y1 = __hsub2(as_half2(and_or(w, 0x00f000f0u, 0x54005400u)), k64);
+  const __half2 y2 = __hsub2(as_half2(and_or(w8, 0x000f000fu, 0x64006400u)), k1024);
+  const __half2 y3 = __hsub2(as_half2(and_or(w8, 0x00f000f0u, 0x54005400u)), k64);
   x[0] = as_u32(__hfma2(y0, step, off));
   x[1] = as_u32(__hfma2(y1, step, off));
   x[2] = as_u32(__hfma2(y2, step, off));
