@@ -12,9 +12,9 @@ cudaError_t by_group(const GatherArgs& a, int num_sms, cudaStream_t stream, int*
   using F = gk::Q4Format<T, D>;
   constexpr bool one = F::kScaleQ;  // bf16
   const typename F::Maps maps{};
-  if (a.g <= 4 && !one) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwinColumns, false, 4, 4>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwoParts, false, 4, 4>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4 && !one) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwinColumns, false, 2, 2, 3>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwoParts, false, 2, 2, 3>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

@@ -74,7 +74,6 @@ struct RowFormat {
                                                 float (&acc)[NT][4]) {
     const int lane = 4 * r + c, y = lane & 7, mat = lane >> 3;
     const uint32_t row = kst + (mat & 1) * kHalfTile + y * 128;  // matrices: keys 0..7, 8..15, then the next 8 elements
-    float odd[NT][4] = {};
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
@@ -82,12 +81,8 @@ struct RowFormat {
       uint32_t x[4];
       ldmatrix4(row + (k >> 2) * 1024 + ((((k & 3) * 2 + (mat >> 1)) ^ y) << 4), x);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma(k & 1 ? odd[n] : acc[n], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1], M());
+      for (int n = 0; n < NT; ++n) mma(acc[n], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1], M());
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] += odd[n][i];
   }
 
   template <int NT, int PARTS>
@@ -129,9 +124,9 @@ cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorM
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 3, 2>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 3, 2>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, gk::kTwoParts, true, 3, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 1, 3, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 1, 3, 2>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, true, 1, 3, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

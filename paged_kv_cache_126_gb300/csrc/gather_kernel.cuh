@@ -5,7 +5,7 @@
 //     out = sum_j w_j v_j / sum_j w_j,   w_j = exp2(q . k_j * scale * log2(e) - m),
 // in one pass, m being a running maximum that moves only when a score passes it by 2^8.
 //
-// Work.  A tile is 16 keys of one (s, h).  All tiles of the batch, numbered by sequence,
+// Work.  A tile is 16 or 32 keys (one or two score tiles) of one (s, h).  All tiles of the batch, numbered by sequence,
 // head and position, are cut into one consecutive range per resident warp, equal to within
 // a tile: every warp is its own worker with its own ring of shared-memory stages, and no
 // barrier joins the warps of a block.  A (s, h) that lies in one range is written straight
@@ -37,7 +37,7 @@ namespace gk {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;        // warps of a block (they share nothing but the abort flag)
-constexpr int kMinTiles = 4;     // fewest tiles a warp is given
+constexpr int kMinKeys = 64;     // fewest keys a warp is given
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
 
 enum Parts { kOnePart = 0, kTwinColumns = 1, kTwoParts = 2 };
@@ -107,7 +107,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // ---- the cursor over a batch's tiles ------------------------------------------------------------
 struct Cursor {
   int s, h, t;               // tile t of (s, h)
-  int L, blocks, tiles;      // of sequence s
+  int L, blocks, parts, tiles;  // of sequence s
 };
 
 __device__ __forceinline__ int checked_len(const GatherArgs& a, int s) {
@@ -115,32 +115,38 @@ __device__ __forceinline__ int checked_len(const GatherArgs& a, int s) {
   return L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks) * a.B ? -1 : L;
 }
 
+// Parts of 16 keys of a sequence or list (16 slots of a listed frame, or two frames of 8); at least one.
 template <bool SEL>
-__device__ __forceinline__ int tiles_of(const GatherArgs& a, int L) {
+__device__ __forceinline__ int parts_of(const GatherArgs& a, int L) {
   if (!SEL) return max(1, (max(L, 0) + 15) >> 4);
   const int n = min(a.K, (max(L, 0) + a.B - 1) >> a.log2_B);
   return max(1, a.B >= 16 ? n << (a.log2_B - 4) : (n + 1) >> 1);
 }
+template <bool SEL, int SUBS>
+__device__ __forceinline__ int tiles_of(const GatherArgs& a, int L) {
+  return (parts_of<SEL>(a, L) + SUBS - 1) / SUBS;
+}
 
-template <bool SEL>
+template <bool SEL, int SUBS>
 __device__ __forceinline__ void enter_seq(const GatherArgs& a, Cursor& c) {
   const int L = checked_len(a, c.s);
   if (L < 0) atomicOr(a.status, kDevBadLen);
   c.L = max(L, 0);
   c.blocks = (c.L + a.B - 1) >> a.log2_B;
-  c.tiles = tiles_of<SEL>(a, L);
+  c.parts = parts_of<SEL>(a, L);
+  c.tiles = (c.parts + SUBS - 1) / SUBS;
 }
 
 // To the next (s, h).
-template <bool SEL>
+template <bool SEL, int SUBS>
 __device__ __forceinline__ void next_head(const GatherArgs& a, Cursor& c) {
   c.t = 0;
   if (++c.h < a.H) return;
   c.h = 0;
-  if (++c.s < a.S) enter_seq<SEL>(a, c);
+  if (++c.s < a.S) enter_seq<SEL, SUBS>(a, c);
 }
 
-// One tile as the producer sees it: two halves of 8 keys, each inside one frame.
+// A part of a tile as the producer sees it: 16 keys, two halves of 8, each inside one frame.
 struct TilePlan {
   int frame[2];   // < 0: nothing to load
   int row;        // first key's row in its frame (both halves of one frame: row, row + 8)
@@ -164,18 +170,18 @@ __device__ __forceinline__ int checked_frame(const GatherArgs& a, const Cursor& 
   return frame;
 }
 
-// Plans of the 32 tiles t0 .. t0 + 31 of (s, h), one per lane.
+// Plans of the 32 parts t0 .. t0 + 31 of (s, h), one per lane.
 template <bool SEL>
 __device__ __forceinline__ TilePlan plan_tiles(const GatherArgs& a, const Cursor& c, int t0, int lane, List& list) {
   TilePlan p;
-  const bool pairs = a.B < 16;             // a tile is two frames of 8
-  const int per = a.log2_B - 4;            // log2(tiles of a frame)
+  const bool pairs = a.B < 16;             // a part is two frames of 8
+  const int per = a.log2_B - 4;            // log2(parts of a frame)
   const int t = t0 + lane;
-  const int j = pairs ? 2 * t : t >> per;  // first entry of this lane's tile
+  const int j = pairs ? 2 * t : t >> per;  // first entry of this lane's part
   p.row = pairs ? 0 : (t & ((1 << per) - 1)) << 4;
   int e[2] = {j, j + 1};
   const int n = SEL ? min(a.K, c.blocks) : c.blocks;
-  bool have[2] = {t < c.tiles && j < n, t < c.tiles && pairs && j + 1 < n};
+  bool have[2] = {t < c.parts && j < n, t < c.parts && pairs && j + 1 < n};
   if (SEL) {
     const int32_t* entries = a.selected + c.s * a.sel_seq + c.h * a.sel_head;
     const int j0 = pairs ? 2 * t0 : t0 >> per;
@@ -299,7 +305,6 @@ struct Q4Format {
     const uint32_t p0 = lds(row + group), p1 = lds(row + kRow + group);
     const __half2 s0 = as_half2(prmt(p0, p0, 0x1010)), o0 = as_half2(prmt(p0, p0, 0x3232));
     const __half2 s1 = as_half2(prmt(p1, p1, 0x1010)), o1 = as_half2(prmt(p1, p1, 0x3232));
-    float odd[NT][4] = {};
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
@@ -310,13 +315,9 @@ struct Q4Format {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         mma(acc[n], x[0], y[0], x[1], y[1], qf[n][2 * w][0], qf[n][2 * w][1], M());
-        mma(odd[n], x[2], y[2], x[3], y[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1], M());
+        mma(acc[n], x[2], y[2], x[3], y[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1], M());
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] += odd[n][i];
   }
 
   // o[t] += V^T P for the D / 16 groups of 16 elements; p[part][n]: B operands of the weights
@@ -365,12 +366,12 @@ struct Q4Format {
 };
 
 // ---- the kernel -------------------------------------------------------------------------------------
-template <class F, int STAGES>
+template <class F, int SUBS, int STAGES>
 __host__ __device__ constexpr uint32_t warp_smem() {
-  return STAGES * 2 * F::kTile + STAGES * 16;  // stages, then mbarriers (8 bytes), then metas (8 bytes)
+  return STAGES * SUBS * 2 * F::kTile + STAGES * 16;  // stages, then mbarriers (8 bytes), then metas (8 bytes)
 }
 
-template <class F, int NT, int PARTS, bool SEL, int STAGES, int BLOCKS>
+template <class F, int NT, int PARTS, bool SEL, int SUBS, int STAGES, int BLOCKS>
 __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
     gather_kernel(const GatherArgs a, const __grid_constant__ typename F::Maps maps) {
   using T = typename F::In;
@@ -381,13 +382,14 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * 2 * F::kTile);
-  const uint32_t bars = dk::smem_u32(smem) + kWarps * (STAGES * 2 * F::kTile) + warp * STAGES * 16;
-  volatile int32_t* metas = reinterpret_cast<volatile int32_t*>(smem + kWarps * (STAGES * 2 * F::kTile) + warp * STAGES * 16 + STAGES * 8);
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kWarps * warp_smem<F, STAGES>());
+  constexpr uint32_t kPart = 2 * F::kTile, kStage = SUBS * kPart;  // a part: 16 keys, then their values
+  const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * kStage);
+  const uint32_t bars = dk::smem_u32(smem) + kWarps * (STAGES * kStage) + warp * STAGES * 16;
+  const uint32_t metas = bars + STAGES * 8;  // [stage][2]
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kWarps * warp_smem<F, SUBS, STAGES>());
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) dk::mbar_init(bars + 8 * i, 1);
+    for (int i = 0; i < STAGES; ++i) dk::mbar_init(bars + 8 * i, SUBS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -396,12 +398,12 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   // this warp's range [b0, b1) of the batch's tiles
   int64_t total = 0;
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    const int n = s0 + lane < a.S ? tiles_of<SEL>(a, checked_len(a, s0 + lane)) : 0;
+    const int n = s0 + lane < a.S ? tiles_of<SEL, SUBS>(a, checked_len(a, s0 + lane)) : 0;
     total += __reduce_add_sync(kAll, n);
   }
   total *= a.H;
   const int64_t all_warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t workers = min(all_warps, (total + kMinTiles - 1) / kMinTiles);
+  const int64_t workers = min(all_warps, (total + kMinKeys / (16 * SUBS) - 1) / (kMinKeys / (16 * SUBS)));
   const int64_t id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
   if (id >= workers) return;
   const int64_t b0 = id * total / workers, b1 = (id + 1) * total / workers;
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   Cursor cur;
   int64_t before = 0;
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    const int n = s0 + lane < a.S ? tiles_of<SEL>(a, checked_len(a, s0 + lane)) : 0;
+    const int n = s0 + lane < a.S ? tiles_of<SEL, SUBS>(a, checked_len(a, s0 + lane)) : 0;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -429,30 +431,32 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
     }
     before += static_cast<int64_t>(__shfl_sync(kAll, upto, 31)) * a.H;
   }
-  enter_seq<SEL>(a, cur);
+  enter_seq<SEL, SUBS>(a, cur);
 
-  // The producer's place.  Lane i plans the tiles i, i + 32, ... of a (s, h) and issues their copies itself.
+  // The producer's place.  Lane i plans the parts i, i + 32, ... of a (s, h) and issues their copies itself.
   Cursor ahead = cur;
   List list = {0, false};
-  int planned = -1;  // first tile of the window of 32 that the lanes have planned; -1: none
+  int planned = -1;  // first part of the window of 32 that the lanes have planned; -1: none
   typename F::Place place;
   int plan_meta = 0;
   int issued = 0, issue_st = 0;
   auto issue = [&]() {
-    if ((ahead.t & ~31) != planned) {
-      planned = ahead.t & ~31;
+    const int part = ahead.t * SUBS;
+    if ((part & ~31) != planned) {
+      planned = part & ~31;
       const TilePlan p = plan_tiles<SEL>(a, ahead, planned, lane, list);
       place = F::place(a, p, ahead.h);
       plan_meta = p.meta;
     }
-    if (lane == (ahead.t & 31)) {
-      metas[issue_st] = plan_meta;
-      F::load(a, maps, place, ahead.h, stages + issue_st * 2 * F::kTile, bars + 8 * issue_st);
+    const int sub = lane - (part & 31);
+    if (static_cast<unsigned>(sub) < SUBS) {
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 8 + sub * 4), "r"(plan_meta) : "memory");
+      F::load(a, maps, place, ahead.h, stages + issue_st * kStage + sub * kPart, bars + 8 * issue_st);
     }
     if (++issue_st == STAGES) issue_st = 0;
     ++issued;
     if (++ahead.t == ahead.tiles && issued < count) {
-      next_head<SEL>(a, ahead);
+      next_head<SEL, SUBS>(a, ahead);
       planned = -1;
       list.seen = 0;
       list.ended = false;
@@ -514,44 +518,64 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
         }
         return;
       }
-      const int meta = metas[st];
-      if (meta >> 16) poison = true;
-      if (meta & 0xffff) {
-        const uint32_t kst = stages + st * 2 * F::kTile, vst = kst + F::kTile;
-        float x[NT][4], y[NT][4];
-        F::template scores<NT>(kst, r, c, qf, x);
-        const bool part = (meta & 0xffff) != 0x0808;
-        bool in0 = true, in1 = true;
-        if (part) {
-          const int k0 = F::key_of(r), k1 = F::key_of(r) + F::kSecond;
-          const int n0 = meta & 255, n1 = (meta >> 8) & 255;
-          in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1;
-          in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
-        }
+      uint32_t meta[SUBS], both = 0x0808, any = 0;
+      lds(metas + st * 8, meta);
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        both = both == 0x0808 ? meta[u] : both;  // 0x0808: every slot of every part holds a key
+        any |= meta[u];
+      }
+      if (any >> 16) poison = true;
+      if (any & 0xffff) {
+        const uint32_t at = stages + st * kStage;
+        float x[SUBS][NT][4], y[SUBS][NT][4];
+        bool in[SUBS][2];
         float top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int u = 0; u < SUBS; ++u) F::template scores<NT>(at + u * kPart, r, c, qf, x[u]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y[n][j] = fmaf(x[n][j], f[n][j & 1], -m[n][j & 1]);
-            if (!(j < 2 ? in0 : in1)) y[n][j] = -INFINITY;
-            top = fmaxf(top, y[n][j]);
+        for (int u = 0; u < SUBS; ++u) {
+          in[u][0] = in[u][1] = true;
+          if (both != 0x0808) {
+            const int k0 = F::key_of(r), k1 = F::key_of(r) + F::kSecond;
+            const int n0 = meta[u] & 255, n1 = (meta[u] >> 8) & 255;
+            in[u][0] = k0 < 8 ? k0 < n0 : k0 - 8 < n1;
+            in[u][1] = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[u][n][j] = fmaf(x[u][n][j], f[n][j & 1], -m[n][j & 1]);
+              if (!in[u][j >> 1]) y[u][n][j] = -INFINITY;
+              top = fmaxf(top, y[u][n][j]);
+            }
+        }
         if (__any_sync(kAll, top > kSlack)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float z0 = in0 ? x[n][j] * f[n][j] : -INFINITY, z1 = in1 ? x[n][j + 2] * f[n][j] : -INFINITY;
-              float t = fmaxf(z0, z1);
+              float t = -INFINITY;
+#pragma unroll
+              for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+                for (int i2 = 0; i2 < 2; ++i2) {
+                  const float z = in[u][i2] ? x[u][n][j + 2 * i2] * f[n][j] : -INFINITY;
+                  y[u][n][j + 2 * i2] = z;
+                  t = fmaxf(t, z);
+                }
 #pragma unroll
               for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, s));
               const float now = fmaxf(m[n][j], t);
               const float less = m[n][j] == now ? 1.f : dk::ex2(m[n][j] - now);
               m[n][j] = now;
-              y[n][j] = z0 - now;
-              y[n][j + 2] = z1 - now;
               l[n][j] *= less;
+#pragma unroll
+              for (int u = 0; u < SUBS; ++u) {
+                y[u][n][j] -= now;
+                y[u][n][j + 2] -= now;
+              }
 #pragma unroll
               for (int u = 0; u < D / 16; ++u) {
                 o[u][n][j] *= less;
@@ -559,28 +583,31 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
               }
             }
         }
-        uint32_t p[kB][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float w[4];
+        for (int u = 0; u < SUBS; ++u) {
+          uint32_t p[kB][NT][2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = dk::ex2(y[n][j]);
-          l[n][0] += w[0] + w[2];
-          l[n][1] += w[1] + w[3];
-          if (PARTS == kTwinColumns) {
+          for (int n = 0; n < NT; ++n) {
+            float w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] -= c >= 2 ? round_to<M>(w[j]) : 0.f;
+            for (int j = 0; j < 4; ++j) w[j] = dk::ex2(y[u][n][j]);
+            l[n][0] += w[0] + w[2];
+            l[n][1] += w[1] + w[3];
+            if (PARTS == kTwinColumns) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] -= c >= 2 ? round_to<M>(w[j]) : 0.f;
+            }
+            p[0][n][0] = transpose8(pack2<M>(w[0], w[1]));
+            p[0][n][1] = transpose8(pack2<M>(w[2], w[3]));
+            if (PARTS == kTwoParts) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
+              p[kB - 1][n][0] = transpose8(pack2<M>(w[0], w[1]));
+              p[kB - 1][n][1] = transpose8(pack2<M>(w[2], w[3]));
+            }
           }
-          p[0][n][0] = transpose8(pack2<M>(w[0], w[1]));
-          p[0][n][1] = transpose8(pack2<M>(w[2], w[3]));
-          if (PARTS == kTwoParts) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
-            p[kB - 1][n][0] = transpose8(pack2<M>(w[0], w[1]));
-            p[kB - 1][n][1] = transpose8(pack2<M>(w[2], w[3]));
-          }
+          F::template values<NT, kB>(at + u * kPart + F::kTile, r, c, both != 0x0808 ? meta[u] & 0xffff : 0x0808, p, o);
         }
-        F::template values<NT, kB>(vst, r, c, meta & 0xffff, p, o);
       }
       __syncwarp();
       if (issued < count) issue();
@@ -678,15 +705,15 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
         }
       }
     }
-    if (i < count) next_head<SEL>(a, cur);
+    if (i < count) next_head<SEL, SUBS>(a, cur);
   }
 }
 
 // Blocks per SM and partial slots of a launch; launches when `query` is null.
-template <class F, int NT, int PARTS, bool SEL, int STAGES, int BLOCKS>
+template <class F, int NT, int PARTS, bool SEL, int SUBS, int STAGES, int BLOCKS>
 cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
-  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, BLOCKS>);
-  constexpr uint32_t smem = kWarps * warp_smem<F, STAGES>() + 16;  // + the abort flag
+  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, SUBS, STAGES, BLOCKS>);
+  constexpr uint32_t smem = kWarps * warp_smem<F, SUBS, STAGES>() + 16;  // + the abort flag
   int occ = 0;
   cudaError_t e = kernel_prep(fn, kWarps * 32, smem, &occ);
   if (e != cudaSuccess) return e;
@@ -706,7 +733,7 @@ cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, SEL, STAGES, BLOCKS>, a, maps);
+  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, SEL, SUBS, STAGES, BLOCKS>, a, maps);
 }
 
 }  // namespace gk
