@@ -76,11 +76,13 @@ __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) { return as_
 template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) { return as_u32(__floats2bfloat162_rn(x, y)); }
 template <typename M>
-__device__ __forceinline__ float round_to(float x);
+__device__ __forceinline__ float2 unpack2(uint32_t x);
 template <>
-__device__ __forceinline__ float round_to<__half>(float x) { return __half2float(__float2half_rn(x)); }
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 template <>
-__device__ __forceinline__ float round_to<__nv_bfloat16>(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
@@ -368,7 +370,7 @@ struct Q4Format {
 // ---- the kernel -------------------------------------------------------------------------------------
 template <class F, int SUBS, int STAGES>
 __host__ __device__ constexpr uint32_t warp_smem() {
-  return STAGES * SUBS * 2 * F::kTile + STAGES * 16;  // stages, then mbarriers (8 bytes), then metas (8 bytes)
+  return STAGES * SUBS * 2 * F::kTile + STAGES * 32;  // stages, then mbarriers (8 bytes) and metas (4 bytes a part)
 }
 
 template <class F, int NT, int PARTS, bool SEL, int SUBS, int STAGES, int BLOCKS>
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr uint32_t kPart = 2 * F::kTile, kStage = SUBS * kPart;  // a part: 16 keys, then their values
   const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * kStage);
-  const uint32_t bars = dk::smem_u32(smem) + kWarps * (STAGES * kStage) + warp * STAGES * 16;
-  const uint32_t metas = bars + STAGES * 8;  // [stage][2]
+  const uint32_t metas = dk::smem_u32(smem) + kWarps * (STAGES * kStage) + warp * STAGES * 32;  // [stage][SUBS]
+  const uint32_t bars = metas + STAGES * 16;
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kWarps * warp_smem<F, SUBS, STAGES>());
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
     }
     const int sub = lane - (part & 31);
     if (static_cast<unsigned>(sub) < SUBS) {
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 8 + sub * 4), "r"(plan_meta) : "memory");
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + (issue_st * SUBS + sub) * 4), "r"(plan_meta) : "memory");
       F::load(a, maps, place, ahead.h, stages + issue_st * kStage + sub * kPart, bars + 8 * issue_st);
     }
     if (++issue_st == STAGES) issue_st = 0;
@@ -468,6 +470,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
+  const float rest = PARTS == kTwinColumns ? (c >= 2 ? 1.f : 0.f) : 1.f;
   int st = 0, phase = 0;
 
   for (int i = 0; i < count;) {
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
         return;
       }
       uint32_t meta[SUBS], both = 0x0808, any = 0;
-      lds(metas + st * 8, meta);
+      lds(metas + st * SUBS * 4, meta);
 #pragma unroll
       for (int u = 0; u < SUBS; ++u) {
         both = both == 0x0808 ? meta[u] : both;  // 0x0808: every slot of every part holds a key
@@ -593,17 +596,16 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
             for (int j = 0; j < 4; ++j) w[j] = dk::ex2(y[u][n][j]);
             l[n][0] += w[0] + w[2];
             l[n][1] += w[1] + w[3];
-            if (PARTS == kTwinColumns) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] -= c >= 2 ? round_to<M>(w[j]) : 0.f;
-            }
-            p[0][n][0] = transpose8(pack2<M>(w[0], w[1]));
-            p[0][n][1] = transpose8(pack2<M>(w[2], w[3]));
-            if (PARTS == kTwoParts) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] -= round_to<M>(w[j]);
-              p[kB - 1][n][0] = transpose8(pack2<M>(w[0], w[1]));
-              p[kB - 1][n][1] = transpose8(pack2<M>(w[2], w[3]));
+            for (int j = 0; j < 2; ++j) {
+              uint32_t hi = pack2<M>(w[2 * j], w[2 * j + 1]);
+              if (PARTS != kOnePart) {  // what the rounding leaves over: `rest` is 1 in the lanes that carry it, else 0
+                const float2 back = unpack2<M>(hi);
+                const uint32_t lo = pack2<M>(fmaf(-rest, back.x, w[2 * j]), fmaf(-rest, back.y, w[2 * j + 1]));
+                if (PARTS == kTwoParts) p[kB - 1][n][j] = transpose8(lo);
+                if (PARTS == kTwinColumns) hi = lo;
+              }
+              p[0][n][j] = transpose8(hi);
             }
           }
           F::template values<NT, kB>(at + u * kPart + F::kTile, r, c, both != 0x0808 ? meta[u] & 0xffff : 0x0808, p, o);
