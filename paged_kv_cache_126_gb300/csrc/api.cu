@@ -1596,6 +1596,22 @@ int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, pa::Gat
   return PA_OK;
 }
 
+// A 4-bit cache as a matrix of rows of min(B, 16) tokens of one head, box one row (tile::gather4 takes four
+// such rows by their indexes).  The type is 8 bytes wide so that a row, up to 1280 bytes, is at most 256 elements.
+int make_q4_map(CUtensorMap* map, void* base, int64_t nb, int64_t H, int64_t B, int64_t D) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return PA_ERR_CUDA;
+  const int64_t unit = std::min<int64_t>(B, 16), rows = nb * H * (B / unit), bytes = unit * D / 8 * 5;
+  if (rows > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(bytes / 8), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(bytes / 8), 1};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PA_OK : PA_ERR_UNSUPPORTED;
+}
+
 // View {64 elements, slots, D / 64 column groups, H} of a 16-bit cache, box {64, 8, D / 64, 1}, 128-byte
 // swizzle: 8 rows of one head as [D / 64][8][64].
 int make_rows8_map(CUtensorMap* map, void* base, int dtype, int64_t rows, int64_t H, int64_t D) {
@@ -1629,10 +1645,13 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
   a.status = g_dev[dev].status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int workers = 0;
-  if (pa::launch_decode_q4(q->dtype, static_cast<int>(z.D), a, g_dev[dev].num_sms, st, &workers) != cudaSuccess)
-    return PA_ERR_CUDA;
+  const int D = static_cast<int>(z.D), sms = g_dev[dev].num_sms;
+  CUtensorMap tk, tv;
+  PA_TRY(make_q4_map(&tk, k_cache->data, z.nb, z.H, z.B, z.D));
+  PA_TRY(make_q4_map(&tv, v_cache->data, z.nb, z.H, z.B, z.D));
+  if (pa::launch_decode_q4(q->dtype, D, a, tk, tv, sms, st, &workers) != cudaSuccess) return PA_ERR_CUDA;
   PA_TRY(gather_scratch(dev, st, z.D, workers, &a));
-  if (pa::launch_decode_q4(q->dtype, static_cast<int>(z.D), a, g_dev[dev].num_sms, st, nullptr) != cudaSuccess)
+  if (pa::launch_decode_q4(q->dtype, D, a, tk, tv, sms, st, nullptr) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;

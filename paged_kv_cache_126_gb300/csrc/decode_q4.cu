@@ -8,22 +8,28 @@ namespace {
 // Weights go to the tensor cores as two fp16 parts where the output is fp16 (one part alone would add an
 // error as large as the output's own rounding); a bf16 output rounds 8 times coarser than one part.
 template <typename T, int D>
-cudaError_t by_group(const GatherArgs& a, int num_sms, cudaStream_t stream, int* workers) {
+cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
+                     int* workers) {
   using F = gk::Q4Format<T, D>;
   constexpr bool one = F::kScaleQ;  // bf16
-  const typename F::Maps maps{};
-  if (a.g <= 4 && !one) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwinColumns, false, 2, 2, 3>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwoParts, false, 2, 2, 3>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  typename F::Maps maps;
+  maps.k = tk;
+  maps.v = tv;
+  if (a.g <= 4 && !one)
+    return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwinColumns, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 2, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int num_sms, cudaStream_t stream, int* workers) {
+cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms,
+                             cudaStream_t stream, int* workers) {
   if (dtype == PA_F16)
-    return D == 128 ? by_group<__half, 128>(a, num_sms, stream, workers) : by_group<__half, 64>(a, num_sms, stream, workers);
-  return D == 128 ? by_group<__nv_bfloat16, 128>(a, num_sms, stream, workers)
-                  : by_group<__nv_bfloat16, 64>(a, num_sms, stream, workers);
+    return D == 128 ? by_group<__half, 128>(a, tk, tv, num_sms, stream, workers)
+                    : by_group<__half, 64>(a, tk, tv, num_sms, stream, workers);
+  return D == 128 ? by_group<__nv_bfloat16, 128>(a, tk, tv, num_sms, stream, workers)
+                  : by_group<__nv_bfloat16, 64>(a, tk, tv, num_sms, stream, workers);
 }
 
 }  // namespace pa

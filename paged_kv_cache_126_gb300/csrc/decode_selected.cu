@@ -40,6 +40,7 @@ struct RowFormat {
   struct Maps {
     CUtensorMap k, v;
   };
+  static constexpr int kLoads = 1;
   struct Place {
     int slot[2];     // first slot of each half; < 0: nothing to load
   };
@@ -49,15 +50,12 @@ struct RowFormat {
     x.slot[1] = p.frame[1] >= 0 ? p.frame[1] * a.B + p.row + (a.B >= 16 ? 8 : 0) : -1;
     return x;
   }
-  __device__ __forceinline__ static void load(const GatherArgs&, const Maps& maps, const Place& x, int h, uint32_t dst,
-                                              uint32_t bar) {
-    dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * 2 * kHalfTile);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (x.slot[i] < 0) continue;
-      tma_load_4d(dst + i * kHalfTile, &maps.k, 0, x.slot[i], 0, h, bar);
-      tma_load_4d(dst + kTile + i * kHalfTile, &maps.v, 0, x.slot[i], 0, h, bar);
-    }
+  __device__ __forceinline__ static void load(const GatherArgs&, const CUtensorMap* map, const Place& x, int h, int lane,
+                                              int part, uint32_t dst, uint32_t bar) {
+    if (lane != part) return;
+    dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * kHalfTile);
+    if (x.slot[0] >= 0) tma_load_4d(dst, map, 0, x.slot[0], 0, h, bar);
+    if (x.slot[1] >= 0) tma_load_4d(dst + kHalfTile, map, 0, x.slot[1], 0, h, bar);
   }
 
   __device__ __forceinline__ static int q_element(int c, int i) { return 16 * (i >> 2) + 2 * c + (i & 1) + ((i & 2) << 2); }
@@ -124,9 +122,9 @@ cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorM
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 1, 3, 2>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 1, 3, 2>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, gk::kTwoParts, true, 1, 3, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 3, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 3, 4, 2>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, true, 3, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

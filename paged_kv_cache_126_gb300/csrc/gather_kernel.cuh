@@ -5,7 +5,8 @@
 //     out = sum_j w_j v_j / sum_j w_j,   w_j = exp2(q . k_j * scale * log2(e) - m),
 // in one pass, m being a running maximum that moves only when a score passes it by 2^8.
 //
-// Work.  A tile is 16 or 32 keys (one or two score tiles) of one (s, h).  All tiles of the batch, numbered by sequence,
+// Work.  A tile is up to four parts of 16 keys of one (s, h): its keys are one copy, its values another,
+// and each is loaded again as soon as the warp has read it.  All tiles of the batch, numbered by sequence,
 // head and position, are cut into one consecutive range per resident warp, equal to within
 // a tile: every warp is its own worker with its own ring of shared-memory stages, and no
 // barrier joins the warps of a block.  A (s, h) that lies in one range is written straight
@@ -36,7 +37,6 @@ namespace pa {
 namespace gk {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 4;        // warps of a block (they share nothing but the abort flag)
 constexpr int kMinKeys = 64;     // fewest keys a warp is given
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
 
@@ -100,10 +100,13 @@ __device__ __forceinline__ uint32_t lds(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr));
   return w;
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// four rows of a two-dimensional tensor, one after the other
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int r0, int r1, int r2, int r3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
 }
 
 // ---- the cursor over a batch's tiles ------------------------------------------------------------
@@ -124,28 +127,28 @@ __device__ __forceinline__ int parts_of(const GatherArgs& a, int L) {
   const int n = min(a.K, (max(L, 0) + a.B - 1) >> a.log2_B);
   return max(1, a.B >= 16 ? n << (a.log2_B - 4) : (n + 1) >> 1);
 }
-template <bool SEL, int SUBS>
+template <bool SEL, int LOADS>
 __device__ __forceinline__ int tiles_of(const GatherArgs& a, int L) {
-  return (parts_of<SEL>(a, L) + SUBS - 1) / SUBS;
+  return (parts_of<SEL>(a, L) + LOADS - 1) / LOADS;
 }
 
-template <bool SEL, int SUBS>
+template <bool SEL, int LOADS>
 __device__ __forceinline__ void enter_seq(const GatherArgs& a, Cursor& c) {
   const int L = checked_len(a, c.s);
   if (L < 0) atomicOr(a.status, kDevBadLen);
   c.L = max(L, 0);
   c.blocks = (c.L + a.B - 1) >> a.log2_B;
   c.parts = parts_of<SEL>(a, L);
-  c.tiles = (c.parts + SUBS - 1) / SUBS;
+  c.tiles = (c.parts + LOADS - 1) / LOADS;
 }
 
 // To the next (s, h).
-template <bool SEL, int SUBS>
+template <bool SEL, int LOADS>
 __device__ __forceinline__ void next_head(const GatherArgs& a, Cursor& c) {
   c.t = 0;
   if (++c.h < a.H) return;
   c.h = 0;
-  if (++c.s < a.S) enter_seq<SEL, SUBS>(a, c);
+  if (++c.s < a.S) enter_seq<SEL, LOADS>(a, c);
 }
 
 // A part of a tile as the producer sees it: 16 keys, two halves of 8, each inside one frame.
@@ -251,34 +254,42 @@ struct Q4Format {
   static constexpr int kSecond = 1;  // key of score row r + 8 behind that of row r
   __device__ __forceinline__ static int key_of(int r) { return (r & 1) ? ((r + 3) & 7) + 8 : r; }
 
-  struct Maps {};
-  // What the lane that plans a tile keeps of it.
+  // The caches as rows of 16 tokens of one head (of 8 where a frame holds 8): four rows a copy.
+  struct Maps {
+    CUtensorMap k, v;
+  };
+  static constexpr int kLoads = 4;
+  // What the lane that plans a part keeps of it.  A half without a key loads row 0, which is always there
+  // and never counted, so that every tile brings the same number of bytes.
   struct Place {
-    int64_t at[2];    // byte offsets of the halves
-    uint32_t bytes;   // of K and V together
-    bool whole, on[2];
+    int row[2];
   };
   __device__ __forceinline__ static Place place(const GatherArgs& a, const TilePlan& p, int h) {
+    const int per = a.B >= 16 ? a.log2_B - 4 : 0;
     Place x;
-    x.whole = a.B >= 16 && p.frame[0] >= 0 && p.frame[1] >= 0;
-    x.on[0] = p.frame[0] >= 0;
-    x.on[1] = p.frame[1] >= 0 && !x.whole;
-    x.at[0] = ((static_cast<int64_t>(p.frame[0]) * a.H + h) * a.B + p.row) * kRow;
-    x.at[1] = ((static_cast<int64_t>(p.frame[1]) * a.H + h) * a.B + p.row + (a.B >= 16 ? 8 : 0)) * kRow;
-    x.bytes = 2 * (x.whole ? kTile : (x.on[0] ? kHalfTile : 0) + (x.on[1] ? kHalfTile : 0));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      x.row[i] = p.frame[i] >= 0 ? static_cast<int>((static_cast<int64_t>(p.frame[i]) * a.H + h) << per) + (p.row >> 4) : 0;
     return x;
   }
-  __device__ __forceinline__ static void load(const GatherArgs& a, const Maps&, const Place& x, int, uint32_t dst,
-                                              uint32_t bar) {
-    dk::mbar_arrive_expect_tx(bar, x.bytes);
-    if (x.on[0]) {
-      const uint32_t n = x.whole ? kTile : kHalfTile;
-      bulk_load(dst, a.k_cache + x.at[0], n, bar);
-      bulk_load(dst + kTile, a.v_cache + x.at[0], n, bar);
-    }
-    if (x.on[1]) {
-      bulk_load(dst + kHalfTile, a.k_cache + x.at[1], kHalfTile, bar);
-      bulk_load(dst + kTile + kHalfTile, a.v_cache + x.at[1], kHalfTile, bar);
+  // All lanes: the keys (or values) of a tile whose parts were planned by lanes part .. part + kLoads - 1.
+  __device__ __forceinline__ static void load(const GatherArgs& a, const CUtensorMap* map, const Place& x, int, int lane,
+                                              int part, uint32_t dst, uint32_t bar) {
+    const int r0 = __shfl_sync(kAll, x.row[0], part), r1 = __shfl_sync(kAll, x.row[0], part + 1);
+    const int r2 = __shfl_sync(kAll, x.row[0], part + 2), r3 = __shfl_sync(kAll, x.row[0], part + 3);
+    if (a.B >= 16) {
+      if (lane == 0) {
+        dk::mbar_arrive_expect_tx(bar, kLoads * kTile);
+        tma_gather4(dst, map, r0, r1, r2, r3, bar);
+      }
+    } else {
+      const int s0 = __shfl_sync(kAll, x.row[1], part), s1 = __shfl_sync(kAll, x.row[1], part + 1);
+      const int s2 = __shfl_sync(kAll, x.row[1], part + 2), s3 = __shfl_sync(kAll, x.row[1], part + 3);
+      if (lane == 0) {
+        dk::mbar_arrive_expect_tx(bar, kLoads * kTile);
+        tma_gather4(dst, map, r0, s0, r1, s1, bar);
+        tma_gather4(dst + 2 * kTile, map, r2, s2, r3, s3, bar);
+      }
     }
   }
 
@@ -368,13 +379,13 @@ struct Q4Format {
 };
 
 // ---- the kernel -------------------------------------------------------------------------------------
-template <class F, int SUBS, int STAGES>
+template <class F, int STAGES>
 __host__ __device__ constexpr uint32_t warp_smem() {
-  return STAGES * SUBS * 2 * F::kTile + STAGES * 32;  // stages, then mbarriers (8 bytes) and metas (4 bytes a part)
+  return STAGES * F::kLoads * 2 * F::kTile + STAGES * 32;  // stages, then metas (4 bytes a part) and two mbarriers each
 }
 
-template <class F, int NT, int PARTS, bool SEL, int SUBS, int STAGES, int BLOCKS>
-__global__ void __launch_bounds__(kWarps * 32, BLOCKS)
+template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
+__global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     gather_kernel(const GatherArgs a, const __grid_constant__ typename F::Maps maps) {
   using T = typename F::In;
   using M = typename F::M;
@@ -384,14 +395,16 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr uint32_t kPart = 2 * F::kTile, kStage = SUBS * kPart;  // a part: 16 keys, then their values
+  constexpr int LOADS = F::kLoads;
+  static_assert(LOADS <= 4, "a stage's metas are 16 bytes");
+  constexpr uint32_t kKeys = LOADS * F::kTile, kStage = 2 * kKeys;  // the tile's keys, then its values
   const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * kStage);
-  const uint32_t metas = dk::smem_u32(smem) + kWarps * (STAGES * kStage) + warp * STAGES * 32;  // [stage][SUBS]
-  const uint32_t bars = metas + STAGES * 16;
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kWarps * warp_smem<F, SUBS, STAGES>());
+  const uint32_t metas = dk::smem_u32(smem) + WARPS * (STAGES * kStage) + warp * STAGES * 32;  // [stage][4]
+  const uint32_t bars = metas + STAGES * 16;  // [stage][2]: keys, values
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + WARPS * warp_smem<F, STAGES>());
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) dk::mbar_init(bars + 8 * i, SUBS);
+    for (int i = 0; i < 2 * STAGES; ++i) dk::mbar_init(bars + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -400,12 +413,13 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   // this warp's range [b0, b1) of the batch's tiles
   int64_t total = 0;
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    const int n = s0 + lane < a.S ? tiles_of<SEL, SUBS>(a, checked_len(a, s0 + lane)) : 0;
+    const int n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     total += __reduce_add_sync(kAll, n);
   }
   total *= a.H;
-  const int64_t all_warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t workers = min(all_warps, (total + kMinKeys / (16 * SUBS) - 1) / (kMinKeys / (16 * SUBS)));
+  constexpr int kMinTiles = kMinKeys / (16 * LOADS);
+  const int64_t all_warps = static_cast<int64_t>(gridDim.x) * WARPS;
+  const int64_t workers = min(all_warps, (total + kMinTiles - 1) / kMinTiles);
   const int64_t id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
   if (id >= workers) return;
   const int64_t b0 = id * total / workers, b1 = (id + 1) * total / workers;
@@ -414,7 +428,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   Cursor cur;
   int64_t before = 0;
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    const int n = s0 + lane < a.S ? tiles_of<SEL, SUBS>(a, checked_len(a, s0 + lane)) : 0;
+    const int n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -433,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
     }
     before += static_cast<int64_t>(__shfl_sync(kAll, upto, 31)) * a.H;
   }
-  enter_seq<SEL, SUBS>(a, cur);
+  enter_seq<SEL, LOADS>(a, cur);
 
   // The producer's place.  Lane i plans the parts i, i + 32, ... of a (s, h) and issues their copies itself.
   Cursor ahead = cur;
@@ -442,8 +456,8 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   typename F::Place place;
   int plan_meta = 0;
   int issued = 0, issue_st = 0;
-  auto issue = [&]() {
-    const int part = ahead.t * SUBS;
+  auto issue_keys = [&]() {
+    const int part = ahead.t * LOADS;
     if ((part & ~31) != planned) {
       planned = part & ~31;
       const TilePlan p = plan_tiles<SEL>(a, ahead, planned, lane, list);
@@ -451,20 +465,25 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
       plan_meta = p.meta;
     }
     const int sub = lane - (part & 31);
-    if (static_cast<unsigned>(sub) < SUBS) {
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + (issue_st * SUBS + sub) * 4), "r"(plan_meta) : "memory");
-      F::load(a, maps, place, ahead.h, stages + issue_st * kStage + sub * kPart, bars + 8 * issue_st);
-    }
+    if (static_cast<unsigned>(sub) < LOADS)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 16 + sub * 4), "r"(plan_meta) : "memory");
+    F::load(a, &maps.k, place, ahead.h, lane, part & 31, stages + issue_st * kStage, bars + 16 * issue_st);
+  };
+  auto issue_values = [&]() {  // of the same tile, and on to the next
+    F::load(a, &maps.v, place, ahead.h, lane, (ahead.t * LOADS) & 31, stages + issue_st * kStage + kKeys, bars + 16 * issue_st + 8);
     if (++issue_st == STAGES) issue_st = 0;
     ++issued;
     if (++ahead.t == ahead.tiles && issued < count) {
-      next_head<SEL, SUBS>(a, ahead);
+      next_head<SEL, LOADS>(a, ahead);
       planned = -1;
       list.seen = 0;
       list.ended = false;
     }
   };
-  for (int i = 0; i < STAGES && i < count; ++i) issue();
+  for (int i = 0; i < STAGES && i < count; ++i) {
+    issue_keys();
+    issue_values();
+  }
   __syncwarp();
 
   uint32_t qf[NT][D / 16][2];
@@ -472,6 +491,18 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
   float m[NT][2], l[NT][2], f[NT][2];
   const float rest = PARTS == kTwinColumns ? (c >= 2 ? 1.f : 0.f) : 1.f;
   int st = 0, phase = 0;
+
+  // A copy is stuck: let those in flight land (bounded) before the block retires.  Tile i's keys were waited
+  // for last, or its values (then the keys of tile i + STAGES may be in flight too).
+  auto drain = [&](int i, bool at_values) {
+    const long long t0 = clock64();
+    for (int j = i; j < issued + (at_values && issued < count ? 1 : 0); ++j) {
+      const uint32_t bar = bars + 16 * (j % STAGES), ph = (j / STAGES) & 1;
+      for (int b = j == i && at_values ? 1 : 0; b < (j < issued ? 2 : 1); ++b)
+        while (!dk::mbar_try_wait(bar + 8 * b, ph) && clock64() - t0 < dk::kDrainCycles) {
+        }
+    }
+  };
 
   for (int i = 0; i < count;) {
     // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
@@ -511,63 +542,60 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
     const int stop = min(count, i + cur.tiles - cur.t);
     cur.t += stop - i;
     for (; i < stop; ++i) {
-      if (!__all_sync(kAll, dk::mbar_wait(bars + 8 * st, phase, abort_flag, a.status))) {
-        // a copy is stuck: let those in flight land (bounded) before the block retires
-        const long long t0 = clock64();
-        for (; i < issued; ++i) {
-          while (!dk::mbar_try_wait(bars + 8 * st, phase) && clock64() - t0 < dk::kDrainCycles) {
-          }
-          if (++st == STAGES) st = 0, phase ^= 1;
-        }
-        return;
-      }
-      uint32_t meta[SUBS], both = 0x0808, any = 0;
-      lds(metas + st * SUBS * 4, meta);
+      const uint32_t kst = stages + st * kStage, vst = kst + kKeys, bar = bars + 16 * st;
+      if (!__all_sync(kAll, dk::mbar_wait(bar, phase, abort_flag, a.status))) return drain(i, false);
+      uint32_t meta[LOADS], full = 0x0808, any = 0;
+      lds(metas + st * 16, meta);
 #pragma unroll
-      for (int u = 0; u < SUBS; ++u) {
-        both = both == 0x0808 ? meta[u] : both;  // 0x0808: every slot of every part holds a key
+      for (int u = 0; u < LOADS; ++u) {
+        full = full == 0x0808 ? meta[u] : full;  // 0x0808: every slot of every part holds a key
         any |= meta[u];
       }
       if (any >> 16) poison = true;
+      float x[LOADS][NT][4];
       if (any & 0xffff) {
-        const uint32_t at = stages + st * kStage;
-        float x[SUBS][NT][4], y[SUBS][NT][4];
-        bool in[SUBS][2];
-        float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u) F::template scores<NT>(at + u * kPart, r, c, qf, x[u]);
+        for (int u = 0; u < LOADS; ++u) F::template scores<NT>(kst + u * F::kTile, r, c, qf, x[u]);
+      }
+      __syncwarp();
+      const bool more = issued < count;
+      if (more) issue_keys();
+      if (any & 0xffff) {
+        float over = -INFINITY, top[NT][2];
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u) {
-          in[u][0] = in[u][1] = true;
-          if (both != 0x0808) {
-            const int k0 = F::key_of(r), k1 = F::key_of(r) + F::kSecond;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) x[u][n][j] *= f[n][j & 1];
+        if (full != 0x0808) {
+          const int k0 = F::key_of(r), k1 = F::key_of(r) + F::kSecond;
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) {
             const int n0 = meta[u] & 255, n1 = (meta[u] >> 8) & 255;
-            in[u][0] = k0 < 8 ? k0 < n0 : k0 - 8 < n1;
-            in[u][1] = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
+            const bool in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1, in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!(j < 2 ? in0 : in1)) x[u][n][j] = -INFINITY;
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[u][n][j] = fmaf(x[u][n][j], f[n][j & 1], -m[n][j & 1]);
-              if (!in[u][j >> 1]) y[u][n][j] = -INFINITY;
-              top = fmaxf(top, y[u][n][j]);
-            }
         }
-        if (__any_sync(kAll, top > kSlack)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            top[n][j] = fmaxf(x[0][n][j], x[0][n][j + 2]);
+#pragma unroll
+            for (int u = 1; u < LOADS; ++u) top[n][j] = fmaxf(top[n][j], fmaxf(x[u][n][j], x[u][n][j + 2]));
+            over = fmaxf(over, top[n][j] - m[n][j]);
+          }
+        if (__any_sync(kAll, over > kSlack)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float t = -INFINITY;
-#pragma unroll
-              for (int u = 0; u < SUBS; ++u)
-#pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2) {
-                  const float z = in[u][i2] ? x[u][n][j + 2 * i2] * f[n][j] : -INFINITY;
-                  y[u][n][j + 2 * i2] = z;
-                  t = fmaxf(t, z);
-                }
+              float t = top[n][j];
 #pragma unroll
               for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, s));
               const float now = fmaxf(m[n][j], t);
@@ -575,25 +603,23 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
               m[n][j] = now;
               l[n][j] *= less;
 #pragma unroll
-              for (int u = 0; u < SUBS; ++u) {
-                y[u][n][j] -= now;
-                y[u][n][j + 2] -= now;
-              }
-#pragma unroll
               for (int u = 0; u < D / 16; ++u) {
                 o[u][n][j] *= less;
                 o[u][n][j + 2] *= less;
               }
             }
         }
+      }
+      if (!__all_sync(kAll, dk::mbar_wait(bar + 8, phase, abort_flag, a.status))) return drain(i, true);
+      if (any & 0xffff) {
 #pragma unroll
-        for (int u = 0; u < SUBS; ++u) {
+        for (int u = 0; u < LOADS; ++u) {
           uint32_t p[kB][NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = dk::ex2(y[u][n][j]);
+            for (int j = 0; j < 4; ++j) w[j] = dk::ex2(x[u][n][j] - m[n][j & 1]);
             l[n][0] += w[0] + w[2];
             l[n][1] += w[1] + w[3];
 #pragma unroll
@@ -608,11 +634,11 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
               p[0][n][j] = transpose8(hi);
             }
           }
-          F::template values<NT, kB>(at + u * kPart + F::kTile, r, c, both != 0x0808 ? meta[u] & 0xffff : 0x0808, p, o);
+          F::template values<NT, kB>(vst + u * F::kTile, r, c, full != 0x0808 ? meta[u] & 0xffff : 0x0808, p, o);
         }
       }
       __syncwarp();
-      if (issued < count) issue();
+      if (more) issue_values();
       if (++st == STAGES) st = 0, phase ^= 1;
     }
 
@@ -707,27 +733,27 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS)
         }
       }
     }
-    if (i < count) next_head<SEL, SUBS>(a, cur);
+    if (i < count) next_head<SEL, LOADS>(a, cur);
   }
 }
 
-// Blocks per SM and partial slots of a launch; launches when `query` is null.
-template <class F, int NT, int PARTS, bool SEL, int SUBS, int STAGES, int BLOCKS>
+// Launches, or only reports the launch's warps where `query` is not null.
+template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
 cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
-  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, SUBS, STAGES, BLOCKS>);
-  constexpr uint32_t smem = kWarps * warp_smem<F, SUBS, STAGES>() + 16;  // + the abort flag
+  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>);
+  constexpr uint32_t smem = WARPS * warp_smem<F, STAGES>() + 16;  // + the abort flag
   int occ = 0;
-  cudaError_t e = kernel_prep(fn, kWarps * 32, smem, &occ);
+  cudaError_t e = kernel_prep(fn, WARPS * 32, smem, &occ);
   if (e != cudaSuccess) return e;
   if (occ < 1) return cudaErrorInvalidConfiguration;
   const int grid = num_sms * (occ < BLOCKS ? occ : BLOCKS);
   if (query) {
-    *query = grid * kWarps;
+    *query = grid * WARPS;
     return cudaSuccess;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(WARPS * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -735,7 +761,7 @@ cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, SEL, SUBS, STAGES, BLOCKS>, a, maps);
+  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>, a, maps);
 }
 
 }  // namespace gk

@@ -259,7 +259,8 @@ struct GatherArgs {
   int32_t* status;
 };
 // workers: not null: only report the launch's warps (each may leave two partials)
-cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, int num_sms, cudaStream_t stream, int* workers);
+cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int num_sms, cudaStream_t stream, int* workers);
 cudaError_t launch_decode_selected(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int num_sms, cudaStream_t stream, int* workers);
 
