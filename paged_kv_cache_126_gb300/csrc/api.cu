@@ -1473,8 +1473,7 @@ int pa_cache_append_rope(const pa_tensor* k_new, const pa_tensor* v_new, const p
   a.B = static_cast<int32_t>(k_cache->shape[1]);
   a.num_slots = k_cache->shape[0] * k_cache->shape[1];
   a.status = g_dev[dev].status;
-  if (pa::launch_rope_append(dt, false, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (pa::launch_rope_append(dt, false, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;
 }
@@ -1499,8 +1498,7 @@ int pa_cache_append_q4(const pa_tensor* k_new, const pa_tensor* v_new, const pa_
   a.B = static_cast<int32_t>(z.B);
   a.num_slots = z.nb * z.B;
   a.status = g_dev[dev].status;
-  if (pa::launch_rope_append(dt, true, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (pa::launch_rope_append(dt, true, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;
 }
@@ -1537,8 +1535,7 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
   a.D = static_cast<int32_t>(z.D);
   a.B = static_cast<int32_t>(z.B);
   a.status = g_dev[dev].status;
-  if (pa::launch_read_q4(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (pa::launch_read_q4(dt, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;
 }

@@ -223,10 +223,9 @@ struct RopeArgs {
   unsigned char *k_cache, *v_cache;
   int64_t num_slots;
   int32_t T, H, Hq, D, B, R, P, interleaved;
-  int32_t splits;                 // warps that share a token's rows
   int32_t* status;
 };
-cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stream);
 
 struct ReadQ4Args {
   const unsigned char *k_cache, *v_cache;  // [num_blocks, H, B, 5 D / 8]
@@ -237,7 +236,7 @@ struct ReadQ4Args {
   int32_t T, H, D, B;
   int32_t* status;
 };
-cudaError_t launch_read_q4(int dtype, const ReadQ4Args& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_read_q4(int dtype, ReadQ4Args a, cudaStream_t stream);
 
 // ---- decode over gathered tiles of 16 keys: the 4-bit cache, and listed frames ---------------
 struct GatherArgs {
