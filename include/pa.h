@@ -406,7 +406,8 @@ int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, con
  *   others; equal ranks go to the lower frame position.
  *
  *   q             [S, Hq, D];  bounds [num_blocks, H, 2, D] of the same dtype.
- *   block_tables, context_lens  as for pa_decode;  block_size = B of the cache.
+ *   block_tables, context_lens  as for pa_decode, at most 2^20 columns;  block_size = B of
+ *                 the cache.
  *   selected      int32 [S, H, K], K >= 1, inner stride 1: positions in the sequence's
  *                 block table, ascending; -1 behind the last where the sequence has fewer
  *                 than K frames.

@@ -1746,7 +1746,7 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
   const int64_t S = q->shape[0];
   PA_TRY(check_tables(block_tables, context_lens, S, B));
   PA_TRY(check_selected(selected, S, H));
-  if (S * H * g > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (S * H * g > INT32_MAX || block_tables->shape[1] > 1 << 20) return PA_ERR_UNSUPPORTED;
   if (S == 0) return PA_OK;
   int dev;
   PA_TRY(current_device(&dev));
@@ -1777,9 +1777,10 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
   const size_t scores = static_cast<size_t>(S * H) * std::max<int64_t>(a.max_blocks, 1) * sizeof(float);
   PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, scores, &ws, &cnt_bytes));
   a.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kSchedBytes + cnt_bytes);
-  if (pa::launch_select_blocks(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  int launched = 0;
+  if (pa::launch_select_blocks(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream), &launched) != cudaSuccess)
     return PA_ERR_CUDA;
-  g_launches.fetch_add(2);
+  g_launches.fetch_add(launched);
   return PA_OK;
 }
 

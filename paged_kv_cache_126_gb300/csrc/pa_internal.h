@@ -274,7 +274,7 @@ struct BoundsArgs {
   int32_t S, H, D, B, num_blocks, max_blocks;
   int32_t* status;
 };
-cudaError_t launch_block_bounds(int dtype, const BoundsArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_bounds(int dtype, BoundsArgs a, int num_sms, cudaStream_t stream);
 
 struct SelectArgs {
   const void* q;                // [S, g * H, D]
@@ -289,7 +289,8 @@ struct SelectArgs {
   int32_t S, H, g, D, B, K, num_blocks, max_blocks, keep_first, keep_last;
   int32_t* status;
 };
-cudaError_t launch_select_blocks(int dtype, const SelectArgs& a, int num_sms, cudaStream_t stream);
+// *launched: kernels launched
+cudaError_t launch_select_blocks(int dtype, SelectArgs a, int num_sms, cudaStream_t stream, int* launched);
 
 // status bits (mirror pa.h)
 constexpr int32_t kDevBadSlot = 0x1;

@@ -2,6 +2,11 @@
 //
 // bounds[frame][h][0 / 1][d] = min / max over the frame's tokens of k[d].  For a query q and any
 // key k of the frame, q . k <= sum_d max(q_d min_d, q_d max_d): the frame's score.
+//
+// The bounds and the scores read memory once and compute little: both give consecutive ranges
+// of their (sequence, frame, head) units to resident warps, found from the lengths on the
+// device, and keep several 16-byte loads a lane in flight.  The selection holds a list's
+// ranks in registers and finds the K-th by counting, two bits of it at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,184 +21,435 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// One block per (position in the table, sequence), a thread per two elements of a token row.
-template <typename T2>
-__global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
-  const int s = blockIdx.y;
-  const int L = a.context_lens[s];
-  const int first = a.first ? a.first[s] : 0;
-  if (L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks) * a.B || first < 0) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.status, kDevBadLen);
-    return;
-  }
-  const int pairs = a.H * a.D / 2;
-  for (int j = first / a.B + blockIdx.x; j < (first < L ? (L + a.B - 1) / a.B : 0); j += gridDim.x) {
-    const int frame = a.block_tables[s * a.bt_row + j];
-    if (frame < 0 || frame >= a.num_blocks) {
-      if (threadIdx.x == 0) atomicOr(a.status, kDevBadBlock);
-      continue;
-    }
-    const int n = min(a.B, L - j * a.B);
-    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-      const T2* k = static_cast<const T2*>(a.k_cache) + static_cast<int64_t>(frame) * a.B * pairs + i;
-      T2 lo = k[0], hi = k[0];
-      for (int u = 1; u < n; ++u) {
-        lo = __hmin2(lo, k[static_cast<int64_t>(u) * pairs]);
-        hi = __hmax2(hi, k[static_cast<int64_t>(u) * pairs]);
-      }
-      const int h = i / (a.D / 2), d = i - h * (a.D / 2);
-      T2* b = static_cast<T2*>(a.bounds) + (static_cast<int64_t>(frame) * a.H + h) * a.D + d;
-      b[0] = lo;
-      b[a.D / 2] = hi;
-    }
-  }
+__device__ __forceinline__ bool bad_len(int L, int max_blocks, int B) {
+  return L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(max_blocks) * B;
 }
 
-// A warp per (frame position, key head, sequence): scores [S, H, max_blocks].
-template <typename T>
-__global__ void __launch_bounds__(256) score_kernel(const SelectArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y, s = blockIdx.z;
-  const int L = a.context_lens[s];
-  if (L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks) * a.B) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.status, kDevBadLen);
-    return;
+__device__ __forceinline__ void pdl_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Where unit x lies when sequence s has count(s) * per units: its sequence, and the unit's number in it.
+// Every lane of the warp calls it; x < the total.
+template <typename Count>
+__device__ __forceinline__ int find_unit(int S, int per, int64_t x, int lane, Count count, int64_t* rest) {
+  int64_t before = 0;
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int n = s0 + lane < S ? count(s0 + lane) : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned past = __ballot_sync(kAll, before + static_cast<int64_t>(upto) * per > x);
+    if (past) {
+      const int f = __ffs(past) - 1;
+      *rest = x - before - static_cast<int64_t>(__shfl_sync(kAll, upto, f) - __shfl_sync(kAll, n, f)) * per;
+      return s0 + f;
+    }
+    before += static_cast<int64_t>(__shfl_sync(kAll, upto, 31)) * per;
   }
-  const int blocks = (L + a.B - 1) / a.B, E = a.D / 32;
-  for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < blocks; j += gridDim.x * 8) {
+  return -1;
+}
+template <typename Count>
+__device__ __forceinline__ int64_t all_units(int S, int per, int lane, Count count) {
+  int64_t total = 0;
+  for (int s0 = 0; s0 < S; s0 += 32) total += __reduce_add_sync(kAll, s0 + lane < S ? count(s0 + lane) : 0);
+  return total * per;
+}
+
+template <typename T2>
+__device__ __forceinline__ uint32_t bits(T2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+template <typename T2>
+__device__ __forceinline__ T2 pair_of(uint32_t x) { return *reinterpret_cast<const T2*>(&x); }
+
+// ---- bounds -----------------------------------------------------------------------------------------
+// A unit is one frame of one head: its rows, 32 * 8 / D at a time, as 16-byte vectors.
+template <typename T2, int D>
+__global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
+  constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 8;
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / kRowLanes, vec = lane % kRowLanes;
+  auto count = [&](int s) {  // frames to look at
+    const int L = a.context_lens[s], first = a.first ? a.first[s] : 0;
+    return bad_len(L, a.max_blocks, a.B) || first < 0 || first >= L ? 0 : (L + a.B - 1) / a.B - first / a.B;
+  };
+  const int64_t total = all_units(a.S, a.H, lane, count);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  const int64_t id = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  if (id < a.S) {  // bad lengths are reported by one warp each
+    for (int64_t s = id; s < a.S; s += warps)
+      if (lane == 0 && (bad_len(a.context_lens[s], a.max_blocks, a.B) || (a.first && a.first[s] < 0)))
+        atomicOr(a.status, kDevBadLen);
+  }
+  const int64_t workers = min(warps, total);
+  if (id >= workers) return;
+  const int64_t x0 = id * total / workers, x1 = (id + 1) * total / workers;
+  int64_t rest;
+  int s = find_unit(a.S, a.H, x0, lane, count, &rest);
+  int left = count(s) - static_cast<int>(rest / a.H), h = static_cast<int>(rest % a.H);
+  int L = a.context_lens[s];
+  int j = (L + a.B - 1) / a.B - left;
+  for (int64_t x = x0; x < x1; ++x) {
     const int frame = a.block_tables[s * a.bt_row + j];
-    float best = -INFINITY;
     if (frame < 0 || frame >= a.num_blocks) {
       if (lane == 0) atomicOr(a.status, kDevBadBlock);
     } else {
-      const T* b = static_cast<const T*>(a.bounds) + (static_cast<int64_t>(frame) * a.H + h) * 2 * a.D;
-      for (int g = 0; g < a.g; ++g) {
-        const T* q = static_cast<const T*>(a.q) + s * a.q_row + (h * a.g + g) * a.D;
-        float x[4];
-        for (int u = 0; u < 4; ++u) {
-          x[u] = 0.f;
-          if (u >= E) continue;
-          const int d = lane * E + u;
-          const float qd = to_float(q[d]);
-          x[u] = qd * to_float(qd >= 0.f ? b[a.D + d] : b[d]);
+      const int n = min(a.B, L - j * a.B);
+      const uint4* k = static_cast<const uint4*>(a.k_cache) + (static_cast<int64_t>(frame) * a.B * a.H + h) * kRowLanes + vec;
+      const int64_t row = static_cast<int64_t>(a.H) * kRowLanes;
+      T2 lo[4], hi[4];
+      for (int i0 = 0; i0 < n; i0 += kAhead * kRows) {
+        uint4 u[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) u[i] = __ldg(k + min(i0 + i * kRows + sub, n - 1) * row);  // the last row again behind it
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const T2 y = pair_of<T2>(w[v]);
+            lo[v] = i0 == 0 && i == 0 ? y : __hmin2(lo[v], y);
+            hi[v] = i0 == 0 && i == 0 ? y : __hmax2(hi[v], y);
+          }
         }
-        float y = E == 4 ? __fadd_rn(__fadd_rn(x[0], x[1]), __fadd_rn(x[2], x[3])) : __fadd_rn(x[0], x[1]);
-        for (int o = 1; o < 32; o <<= 1) y = __fadd_rn(y, __shfl_xor_sync(kAll, y, o));
-        best = fmaxf(best, y);
+      }
+#pragma unroll
+      for (int o = kRowLanes; o < 32; o <<= 1)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          lo[v] = __hmin2(lo[v], __shfl_xor_sync(kAll, lo[v], o));
+          hi[v] = __hmax2(hi[v], __shfl_xor_sync(kAll, hi[v], o));
+        }
+      if (sub < 2) {  // the row's first lanes store the minima, the next the maxima
+        uint32_t y[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] = sub == 0 ? bits(lo[v]) : bits(hi[v]);
+        static_cast<uint4*>(a.bounds)[((static_cast<int64_t>(frame) * a.H + h) * 2 + sub) * kRowLanes + vec] =
+            make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
-    if (lane == 0) a.scores[(static_cast<int64_t>(s) * a.H + h) * a.max_blocks + j] = best;
+    if (++h == a.H) {
+      h = 0;
+      ++j;
+      if (--left == 0 && x + 1 < x1) {
+        do left = count(++s);
+        while (left == 0);
+        L = a.context_lens[s];
+        j = (L + a.B - 1) / a.B - left;
+      }
+    }
   }
 }
 
-// Keys whose unsigned order is the order of the floats; frames that are always kept come
-// above all others.
-__device__ __forceinline__ uint32_t rank_of(const SelectArgs& a, const float* scores, int j, int blocks) {
+// ---- scores -----------------------------------------------------------------------------------------
+// A unit is 32 consecutive frames of one (sequence, head); a bounds row is D / 8 lanes, and kStep frames are
+// loaded ahead.  With q split into its positive and negative part one product is zero and the other
+// exact, so x_d = max(q_d min_d, q_d max_d) comes from a product and a fused multiply-add.  The order of
+// the sum (neighbours first) is a tree: eight elements in a lane, then lanes by xor 1, 2, 4, ...; the
+// four frames of a lane are reduced together, each lane passing on half of what it holds, which adds
+// the same pairs.  kQueries queries at a time; more queries read the (cached) rows again.
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 2 && __is_same(T, __half)) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ bool scored(const SelectArgs& a, int blocks) { return blocks > a.K; }
+
+template <typename T, int D, int kQueries>
+__global__ void __launch_bounds__(256) score_kernel(const SelectArgs a) {
+  constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 4;  // frames: kRows side by side, kAhead deep
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / kRowLanes, vec = lane % kRowLanes;
+  auto count = [&](int s) {
+    const int L = a.context_lens[s];
+    const int blocks = bad_len(L, a.max_blocks, a.B) ? 0 : (L + a.B - 1) / a.B;
+    return scored(a, blocks) ? (blocks + 31) >> 5 : 0;
+  };
+  const int64_t total = all_units(a.S, a.H, lane, count);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  const int64_t id = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const int64_t workers = min(warps, total);
+  if (id >= workers) return;
+  const int64_t x0 = id * total / workers, x1 = (id + 1) * total / workers;
+  int64_t rest;
+  int s = find_unit(a.S, a.H, x0, lane, count, &rest);
+  int chunks = count(s);
+  int h = static_cast<int>(rest / chunks), chunk = static_cast<int>(rest % chunks);
+  int blocks = (a.context_lens[s] + a.B - 1) / a.B;
+  float qp[kQueries][8], qn[kQueries][8];
+  auto load_q = [&](int g0) {
+#pragma unroll
+    for (int g = 0; g < kQueries; ++g) {
+      // a query behind the group's last is its last again: the largest score stays
+      const T* q = static_cast<const T*>(a.q) + s * a.q_row + (static_cast<int64_t>(h) * a.g + min(g0 + g, a.g - 1)) * D;
+      float f[8];
+      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(q) + vec), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        qp[g][i] = fmaxf(f[i], 0.f);
+        qn[g][i] = fminf(f[i], 0.f);
+      }
+    }
+  };
+  bool fresh = true;
+  for (int64_t x = x0; x < x1; ++x) {
+    if (fresh && a.g <= kQueries) load_q(0);
+    fresh = false;
+    const int j0 = chunk * 32;
+    int frame = -1;
+    if (j0 + lane < blocks) {
+      frame = a.block_tables[s * a.bt_row + j0 + lane];
+      if (frame < 0 || frame >= a.num_blocks) {
+        atomicOr(a.status, kDevBadBlock);
+        frame = -1;
+      }
+    }
+    float* out = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks + j0;
+    const int live = min(32, blocks - j0);
+    for (int f0 = 0; f0 < live; f0 += kRows * kAhead) {
+      uint4 lo[kAhead], hi[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int f = __shfl_sync(kAll, frame, f0 + i * kRows + sub);
+        const uint4* b = static_cast<const uint4*>(a.bounds) + (static_cast<int64_t>(max(f, 0)) * a.H + h) * 2 * kRowLanes + vec;
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        if (f0 + i * kRows + sub < live) {
+          lo[i] = __ldg(b);
+          hi[i] = __ldg(b + kRowLanes);
+        }
+      }
+      float best = -INFINITY;
+      for (int g0 = 0; g0 < a.g; g0 += kQueries) {
+        if (a.g > kQueries) load_q(g0);
+        float y[kQueries][kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float l8[8], h8[8];
+          unpack8<T>(lo[i], l8);
+          unpack8<T>(hi[i], h8);
+#pragma unroll
+          for (int g = 0; g < kQueries; ++g) {
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = fmaf(qn[g][e], l8[e], __fmul_rn(qp[g][e], h8[e]));
+            y[g][i] = __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
+                                __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7])));
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < kQueries; ++g) {
+          // lane bits 0 and 1 choose which of the four frames a lane ends with
+          const bool b0 = lane & 1, b1 = lane & 2;
+          const float k0 = b0 ? y[g][1] : y[g][0], k1 = b0 ? y[g][3] : y[g][2];
+          const float p0 = b0 ? y[g][0] : y[g][1], p1 = b0 ? y[g][2] : y[g][3];
+          const float z0 = __fadd_rn(k0, __shfl_xor_sync(kAll, p0, 1)), z1 = __fadd_rn(k1, __shfl_xor_sync(kAll, p1, 1));
+          float z = __fadd_rn(b1 ? z1 : z0, __shfl_xor_sync(kAll, b1 ? z0 : z1, 2));
+#pragma unroll
+          for (int o = 4; o < kRowLanes; o <<= 1) z = __fadd_rn(z, __shfl_xor_sync(kAll, z, o));
+          best = fmaxf(best, z);
+        }
+      }
+      const int at = f0 + (lane & 3) * kRows + sub;  // frame (b1, b0) = step 2 b1 + b0
+      const int known = __shfl_sync(kAll, frame, at & 31);
+      if ((vec & ~3) == 0 && at < live) out[at] = known < 0 ? -INFINITY : best;
+    }
+    if (++chunk == chunks) {
+      chunk = 0;
+      fresh = true;
+      if (++h == a.H && x + 1 < x1) {
+        h = 0;
+        do chunks = count(++s);
+        while (chunks == 0);
+        blocks = (a.context_lens[s] + a.B - 1) / a.B;
+      }
+    }
+  }
+}
+
+// ---- selection --------------------------------------------------------------------------------------
+// Numbers whose unsigned order is the order of the scores (-0 as 0); frames that are always kept come above
+// all others.
+__device__ __forceinline__ uint32_t rank_of(const SelectArgs& a, float score, int j, int blocks) {
   if (j < a.keep_first || j >= blocks - a.keep_last) return 0xffffffffu;
-  const uint32_t u = __float_as_uint(__fadd_rn(scores[j], 0.f));  // -0 ranks as 0
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(__fadd_rn(score, 0.f));
+  return max(u & 0x80000000u ? ~u : u | 0x80000000u, 1u);  // 0 is no frame's, not even one with a NaN score
 }
 
-constexpr int kTopThreads = 256;
-
-__device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {  // exclusive
+// One block per (sequence, head).  Thread t holds the ranks of frames t * R .. t * R + R - 1 in registers, so
+// that thread order is frame order; lists longer than kThreads * R frames (LONG) are read again for each
+// count.  The K-th largest rank is found from its top bits down: the largest T such that at least K
+// ranks are >= T, two bits a step, three counts packed into one sum.
+template <int kThreads, int R, bool LONG>
+__global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
+  constexpr int kWarpsOf = kThreads / 32;
+  __shared__ uint64_t sums[2][kWarpsOf];
+  pdl_begin();
+  const int h = blockIdx.x % a.H, s = blockIdx.x / a.H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kAll, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kTopThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
-  }
-  *total = all;
-  return before + x - v;
-}
-
-// One block per (key head, sequence): the K largest ranks, found digit by digit.
-__global__ void __launch_bounds__(kTopThreads) top_kernel(const SelectArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[kTopThreads / 32];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_need;
-  const int h = blockIdx.x, s = blockIdx.y;
   int32_t* sel = a.selected + s * a.sel_seq + h * a.sel_head;
   int L = a.context_lens[s];
-  if (L < 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_blocks) * a.B) L = 0;
+  if (bad_len(L, a.max_blocks, a.B)) {
+    if (threadIdx.x == 0) atomicOr(a.status, kDevBadLen);
+    L = 0;
+  }
   const int blocks = (L + a.B - 1) / a.B;
-  if (blocks <= a.K) {
-    for (int j = threadIdx.x; j < a.K; j += kTopThreads) sel[j] = j < blocks ? j : -1;
+  if (!scored(a, blocks)) {
+    for (int j = threadIdx.x; j < a.K; j += kThreads) sel[j] = j < blocks ? j : -1;
     return;
   }
   const float* scores = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks;
-  uint32_t prefix = 0, mask = 0;
-  int need = a.K;  // how many of the ranks that match the prefix are taken
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kTopThreads) hist[i] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < blocks; j += kTopThreads) {
-      const uint32_t r = rank_of(a, scores, j, blocks);
-      if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int left = need, d = 255;
-      while (d > 0 && hist[d] < left) left -= hist[d--];
-      sh_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-      sh_need = left;
-    }
-    __syncthreads();
-    prefix = sh_prefix;
-    need = sh_need;
-    mask |= 0xffu << shift;
+  const int mine = LONG ? (blocks + kThreads - 1) / kThreads : R;  // frames of a thread
+  const int j0 = threadIdx.x * mine;
+  uint32_t held[R];
+  if (!LONG) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) held[i] = j0 + i < blocks ? rank_of(a, scores[j0 + i], j0 + i, blocks) : 0;
   }
-  int taken = 0, ties = 0;  // before this stretch of positions
-  for (int j0 = 0; j0 < blocks; j0 += kTopThreads) {
-    const int j = j0 + threadIdx.x;
-    const uint32_t r = j < blocks ? rank_of(a, scores, j, blocks) : 0;
-    const bool tie = j < blocks && r == prefix;
-    int all;
-    const int tie_at = ties + block_scan(tie, &all, warp_sums);
-    ties += all;
-    const bool take = j < blocks && (r > prefix || (tie && tie_at < need));
-    const int at = taken + block_scan(take, &all, warp_sums);
-    taken += all;
-    if (take) sel[at] = j;
+  // calls f(rank, position) for each of this thread's frames; ranks of frames are above 0
+  auto each = [&](auto f) {
+    if (LONG) {
+      for (int i = 0; i < mine && j0 + i < blocks; ++i) f(rank_of(a, scores[j0 + i], j0 + i, blocks), j0 + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) f(held[i], j0 + i);
+    }
+  };
+  uint32_t T = 0;
+  for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
+    const uint32_t step = 1u << shift;
+    uint32_t c1 = 0, c2 = 0, c3 = 0;
+    each([&](uint32_t r, int) {
+      c1 += r >= T + step;
+      c2 += r >= T + 2 * step;
+      c3 += r >= T + 3 * step;
+    });
+    c1 = __reduce_add_sync(kAll, c1);
+    c2 = __reduce_add_sync(kAll, c2);
+    c3 = __reduce_add_sync(kAll, c3);
+    if (kWarpsOf > 1) {
+      // 21 bits a count: tables have at most 2^20 columns
+      if (lane == 0) sums[turn][warp] = c1 | static_cast<uint64_t>(c2) << 21 | static_cast<uint64_t>(c3) << 42;
+      __syncthreads();
+      uint64_t all = 0;
+      for (int w = 0; w < kWarpsOf; ++w) all += sums[turn][w];
+      c1 = all & 0x1fffff;
+      c2 = all >> 21 & 0x1fffff;
+      c3 = static_cast<uint32_t>(all >> 42);
+    }
+    const uint32_t K = a.K;
+    T += c3 >= K ? 3 * step : c2 >= K ? 2 * step : c1 >= K ? step : 0;
   }
+  // above T: all; equal to T: the first K - above
+  uint32_t above = 0, equal = 0;
+  each([&](uint32_t r, int) {
+    above += r > T;
+    equal += r == T;
+  });
+  uint64_t upto = above | static_cast<uint64_t>(equal) << 32;
+  const uint64_t own = upto;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kAll, upto, o);
+    if (lane >= o) upto += y;
+  }
+  uint64_t before = upto - own, total = __shfl_sync(kAll, upto, 31);
+  if (kWarpsOf > 1) {
+    __syncthreads();
+    if (lane == 31) sums[0][warp] = upto;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kWarpsOf; ++w) {
+      if (w < warp) before += sums[0][w];
+      total += sums[0][w];
+    }
+  }
+  const uint32_t need = a.K - static_cast<uint32_t>(total);
+  uint32_t a0 = static_cast<uint32_t>(before), e0 = static_cast<uint32_t>(before >> 32);
+  each([&](uint32_t r, int j) {
+    if (r > T)
+      sel[a0++ + min(e0, need)] = j;
+    else if (r == T) {
+      if (e0 < need) sel[a0 + e0] = j;
+      ++e0;
+    }
+  });
+}
+
+cudaError_t launch_pdl(const void* fn, int64_t grid, int threads, void** args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <typename F>
+const void* ptr(F* f) { return reinterpret_cast<const void*>(f); }
+
+// as many blocks as are resident, and no more than there can be units for 8 warps each
+cudaError_t launch_resident(const void* fn, int64_t units, int num_sms, void** args, cudaStream_t stream) {
+  int occ = 0;
+  cudaError_t e = kernel_prep(fn, 256, 0, &occ);
+  if (e != cudaSuccess) return e;
+  if (occ < 1) return cudaErrorInvalidConfiguration;
+  int64_t grid = static_cast<int64_t>(num_sms) * occ;
+  if (units < grid) grid = units < 1 ? 1 : units;
+  return launch_pdl(fn, grid, 256, args, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_block_bounds(int dtype, const BoundsArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const dim3 grid(a.max_blocks < 1 ? 1 : a.max_blocks < 64 ? a.max_blocks : 64, a.S);
-  if (dtype == PA_F16)
-    block_bounds_kernel<__half2><<<grid, 256, 0, stream>>>(a);
-  else
-    block_bounds_kernel<__nv_bfloat162><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_block_bounds(int dtype, BoundsArgs a, int num_sms, cudaStream_t stream) {
+  const void* fn = dtype == PA_F16 ? (a.D == 128 ? ptr(block_bounds_kernel<__half2, 128>) : ptr(block_bounds_kernel<__half2, 64>))
+                                   : (a.D == 128 ? ptr(block_bounds_kernel<__nv_bfloat162, 128>) : ptr(block_bounds_kernel<__nv_bfloat162, 64>));
+  void* args[1] = {&a};
+  return launch_resident(fn, static_cast<int64_t>(a.S) * a.H * (a.max_blocks < 1 ? 1 : a.max_blocks), num_sms, args, stream);
 }
 
-cudaError_t launch_select_blocks(int dtype, const SelectArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const int chunks = (a.max_blocks + 7) / 8;
-  const dim3 grid(chunks < 1 ? 1 : chunks < 64 ? chunks : 64, a.H, a.S);
-  if (dtype == PA_F16)
-    score_kernel<__half><<<grid, 256, 0, stream>>>(a);
-  else
-    score_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  top_kernel<<<dim3(a.H, a.S), kTopThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+template <typename T>
+static const void* score_fn(int D, int g) {
+  if (D == 128) return g == 1 ? ptr(score_kernel<T, 128, 1>) : g == 2 ? ptr(score_kernel<T, 128, 2>) : ptr(score_kernel<T, 128, 4>);
+  return g == 1 ? ptr(score_kernel<T, 64, 1>) : g == 2 ? ptr(score_kernel<T, 64, 2>) : ptr(score_kernel<T, 64, 4>);
+}
+
+cudaError_t launch_select_blocks(int dtype, SelectArgs a, int num_sms, cudaStream_t stream, int* launched) {
+  void* args[1] = {&a};
+  *launched = 0;
+  if (a.max_blocks > a.K) {
+    const void* fn = dtype == PA_F16 ? score_fn<__half>(a.D, a.g) : score_fn<__nv_bfloat16>(a.D, a.g);
+    const cudaError_t e = launch_resident(fn, static_cast<int64_t>(a.S) * a.H * ((a.max_blocks + 31) / 32), num_sms, args, stream);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+  }
+  // threads by the longest list that a table can hold: a rank a register, eight a thread
+  const int n = a.max_blocks;
+  const int64_t lists = static_cast<int64_t>(a.S) * a.H;
+  ++*launched;
+  if (n <= 1024) return launch_pdl(ptr(top_kernel<128, 8, false>), lists, 128, args, stream);
+  if (n <= 4096) return launch_pdl(ptr(top_kernel<512, 8, false>), lists, 512, args, stream);
+  if (n <= 16384) return launch_pdl(ptr(top_kernel<1024, 16, false>), lists, 1024, args, stream);
+  return launch_pdl(ptr(top_kernel<1024, 16, true>), lists, 1024, args, stream);
 }
 
 }  // namespace pa
