@@ -146,12 +146,14 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 }
 
 // ---- scores -----------------------------------------------------------------------------------------
-// A unit is 32 consecutive frames of one (sequence, head); a bounds row is D / 8 lanes, and kStep frames are
-// loaded ahead.  With q split into its positive and negative part one product is zero and the other
-// exact, so x_d = max(q_d min_d, q_d max_d) comes from a product and a fused multiply-add.  The order of
+// A unit is kRows * kAhead consecutive frames of one (sequence, head): a bounds row is D / 8 lanes, kRows
+// frames lie side by side in a warp and kAhead deep, all loaded before the first is used.  With q split
+// into its positive and negative part (in shared memory) one product is zero and the other exact,
+// so x_d = max(q_d min_d, q_d max_d) comes from a product and a fused multiply-add.  The order of
 // the sum (neighbours first) is a tree: eight elements in a lane, then lanes by xor 1, 2, 4, ...; the
 // four frames of a lane are reduced together, each lane passing on half of what it holds, which adds
-// the same pairs.  kQueries queries at a time; more queries read the (cached) rows again.
+// the same pairs.  kQueries queries at a time; more queries read the rows of the unit again from
+// registers and their own numbers from the cache.
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -170,112 +172,124 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 
 __device__ __forceinline__ bool scored(const SelectArgs& a, int blocks) { return blocks > a.K; }
 
+constexpr int kScoreWarps = 4;
+
 template <typename T, int D, int kQueries>
-__global__ void __launch_bounds__(256) score_kernel(const SelectArgs a) {
-  constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 4;  // frames: kRows side by side, kAhead deep
+__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArgs a) {
+  constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 4, kUnit = kRows * kAhead;
+  __shared__ float4 q_parts[kScoreWarps][kQueries][4][kRowLanes];  // positive part (two vectors a lane), negative part
   pdl_begin();
   const int lane = threadIdx.x & 31;
   const int sub = lane / kRowLanes, vec = lane % kRowLanes;
   auto count = [&](int s) {
     const int L = a.context_lens[s];
     const int blocks = bad_len(L, a.max_blocks, a.B) ? 0 : (L + a.B - 1) / a.B;
-    return scored(a, blocks) ? (blocks + 31) >> 5 : 0;
+    return scored(a, blocks) ? (blocks + kUnit - 1) / kUnit : 0;
   };
   const int64_t total = all_units(a.S, a.H, lane, count);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kScoreWarps;
   const int64_t id = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   const int64_t workers = min(warps, total);
   if (id >= workers) return;
   const int64_t x0 = id * total / workers, x1 = (id + 1) * total / workers;
   int64_t rest;
   int s = find_unit(a.S, a.H, x0, lane, count, &rest);
-  int chunks = count(s);
-  int h = static_cast<int>(rest / chunks), chunk = static_cast<int>(rest % chunks);
+  int units = count(s);
+  int h = static_cast<int>(rest / units), unit = static_cast<int>(rest % units);
   int blocks = (a.context_lens[s] + a.B - 1) / a.B;
-  float qp[kQueries][8], qn[kQueries][8];
+  float4 (*qs)[4][kRowLanes] = q_parts[threadIdx.x >> 5];
   auto load_q = [&](int g0) {
-#pragma unroll
-    for (int g = 0; g < kQueries; ++g) {
+    __syncwarp();
+    for (int g = sub; g < kQueries; g += kRows) {
       // a query behind the group's last is its last again: the largest score stays
       const T* q = static_cast<const T*>(a.q) + s * a.q_row + (static_cast<int64_t>(h) * a.g + min(g0 + g, a.g - 1)) * D;
       float f[8];
       unpack8<T>(__ldg(reinterpret_cast<const uint4*>(q) + vec), f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        qp[g][i] = fmaxf(f[i], 0.f);
-        qn[g][i] = fminf(f[i], 0.f);
+      for (int i = 0; i < 2; ++i) {
+        qs[g][i][vec] = make_float4(fmaxf(f[4 * i], 0.f), fmaxf(f[4 * i + 1], 0.f), fmaxf(f[4 * i + 2], 0.f), fmaxf(f[4 * i + 3], 0.f));
+        qs[g][2 + i][vec] = make_float4(fminf(f[4 * i], 0.f), fminf(f[4 * i + 1], 0.f), fminf(f[4 * i + 2], 0.f), fminf(f[4 * i + 3], 0.f));
       }
     }
+    __syncwarp();
   };
   bool fresh = true;
+  int known = -1;   // which 32 positions `frame` is of
+  int frame = -1;
   for (int64_t x = x0; x < x1; ++x) {
+    const int j0 = unit * kUnit;
+    if (fresh || (j0 >> 5) != known) {
+      known = j0 >> 5;
+      const int j = known * 32 + lane;
+      frame = -1;
+      if (j < blocks) {
+        frame = a.block_tables[s * a.bt_row + j];
+        if (frame < 0 || frame >= a.num_blocks) {
+          atomicOr(a.status, kDevBadBlock);
+          frame = -1;
+        }
+      }
+    }
+    uint4 lo[kAhead], hi[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * kRows + sub;
+      const int f = __shfl_sync(kAll, frame, j & 31);
+      const uint4* b = static_cast<const uint4*>(a.bounds) + (static_cast<int64_t>(max(f, 0)) * a.H + h) * 2 * kRowLanes + vec;
+      lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+      if (j < blocks) {
+        lo[i] = __ldg(b);
+        hi[i] = __ldg(b + kRowLanes);
+      }
+    }
     if (fresh && a.g <= kQueries) load_q(0);
     fresh = false;
-    const int j0 = chunk * 32;
-    int frame = -1;
-    if (j0 + lane < blocks) {
-      frame = a.block_tables[s * a.bt_row + j0 + lane];
-      if (frame < 0 || frame >= a.num_blocks) {
-        atomicOr(a.status, kDevBadBlock);
-        frame = -1;
-      }
-    }
-    float* out = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks + j0;
-    const int live = min(32, blocks - j0);
-    for (int f0 = 0; f0 < live; f0 += kRows * kAhead) {
-      uint4 lo[kAhead], hi[kAhead];
+    float best = -INFINITY;
+    for (int g0 = 0; g0 < a.g; g0 += kQueries) {
+      if (a.g > kQueries) load_q(g0);
+      float y[kQueries][kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int f = __shfl_sync(kAll, frame, f0 + i * kRows + sub);
-        const uint4* b = static_cast<const uint4*>(a.bounds) + (static_cast<int64_t>(max(f, 0)) * a.H + h) * 2 * kRowLanes + vec;
-        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-        if (f0 + i * kRows + sub < live) {
-          lo[i] = __ldg(b);
-          hi[i] = __ldg(b + kRowLanes);
-        }
-      }
-      float best = -INFINITY;
-      for (int g0 = 0; g0 < a.g; g0 += kQueries) {
-        if (a.g > kQueries) load_q(g0);
-        float y[kQueries][kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          float l8[8], h8[8];
-          unpack8<T>(lo[i], l8);
-          unpack8<T>(hi[i], h8);
-#pragma unroll
-          for (int g = 0; g < kQueries; ++g) {
-            float t[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = fmaf(qn[g][e], l8[e], __fmul_rn(qp[g][e], h8[e]));
-            y[g][i] = __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
-                                __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7])));
-          }
-        }
+        float l8[8], h8[8];
+        unpack8<T>(lo[i], l8);
+        unpack8<T>(hi[i], h8);
 #pragma unroll
         for (int g = 0; g < kQueries; ++g) {
-          // lane bits 0 and 1 choose which of the four frames a lane ends with
-          const bool b0 = lane & 1, b1 = lane & 2;
-          const float k0 = b0 ? y[g][1] : y[g][0], k1 = b0 ? y[g][3] : y[g][2];
-          const float p0 = b0 ? y[g][0] : y[g][1], p1 = b0 ? y[g][2] : y[g][3];
-          const float z0 = __fadd_rn(k0, __shfl_xor_sync(kAll, p0, 1)), z1 = __fadd_rn(k1, __shfl_xor_sync(kAll, p1, 1));
-          float z = __fadd_rn(b1 ? z1 : z0, __shfl_xor_sync(kAll, b1 ? z0 : z1, 2));
+          float z[2];
 #pragma unroll
-          for (int o = 4; o < kRowLanes; o <<= 1) z = __fadd_rn(z, __shfl_xor_sync(kAll, z, o));
-          best = fmaxf(best, z);
+          for (int e = 0; e < 2; ++e) {
+            const float4 p = qs[g][e][vec], n = qs[g][2 + e][vec];
+            const float t0 = fmaf(n.x, l8[4 * e], __fmul_rn(p.x, h8[4 * e])), t1 = fmaf(n.y, l8[4 * e + 1], __fmul_rn(p.y, h8[4 * e + 1]));
+            const float t2 = fmaf(n.z, l8[4 * e + 2], __fmul_rn(p.z, h8[4 * e + 2])), t3 = fmaf(n.w, l8[4 * e + 3], __fmul_rn(p.w, h8[4 * e + 3]));
+            z[e] = __fadd_rn(__fadd_rn(t0, t1), __fadd_rn(t2, t3));
+          }
+          y[g][i] = __fadd_rn(z[0], z[1]);
         }
       }
-      const int at = f0 + (lane & 3) * kRows + sub;  // frame (b1, b0) = step 2 b1 + b0
-      const int known = __shfl_sync(kAll, frame, at & 31);
-      if ((vec & ~3) == 0 && at < live) out[at] = known < 0 ? -INFINITY : best;
+#pragma unroll
+      for (int g = 0; g < kQueries; ++g) {
+        // lane bits 0 and 1 choose which of the four frames a lane ends with
+        const bool b0 = lane & 1, b1 = lane & 2;
+        const float k0 = b0 ? y[g][1] : y[g][0], k1 = b0 ? y[g][3] : y[g][2];
+        const float p0 = b0 ? y[g][0] : y[g][1], p1 = b0 ? y[g][2] : y[g][3];
+        const float z0 = __fadd_rn(k0, __shfl_xor_sync(kAll, p0, 1)), z1 = __fadd_rn(k1, __shfl_xor_sync(kAll, p1, 1));
+        float z = __fadd_rn(b1 ? z1 : z0, __shfl_xor_sync(kAll, b1 ? z0 : z1, 2));
+#pragma unroll
+        for (int o = 4; o < kRowLanes; o <<= 1) z = __fadd_rn(z, __shfl_xor_sync(kAll, z, o));
+        best = fmaxf(best, z);
+      }
     }
-    if (++chunk == chunks) {
-      chunk = 0;
+    const int at = j0 + (lane & 3) * kRows + sub;  // frame (b1, b0) = step 2 b1 + b0
+    const int its = __shfl_sync(kAll, frame, at & 31);
+    if ((vec & ~3) == 0 && at < blocks)
+      a.scores[(static_cast<int64_t>(s) * a.H + h) * a.max_blocks + at] = its < 0 ? -INFINITY : best;
+    if (++unit == units) {
+      unit = 0;
       fresh = true;
       if (++h == a.H && x + 1 < x1) {
         h = 0;
-        do chunks = count(++s);
-        while (chunks == 0);
+        do units = count(++s);
+        while (units == 0);
         blocks = (a.context_lens[s] + a.B - 1) / a.B;
       }
     }
@@ -346,14 +360,18 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
       // 21 bits a count: tables have at most 2^20 columns
       if (lane == 0) sums[turn][warp] = c1 | static_cast<uint64_t>(c2) << 21 | static_cast<uint64_t>(c3) << 42;
       __syncthreads();
-      uint64_t all = 0;
-      for (int w = 0; w < kWarpsOf; ++w) all += sums[turn][w];
-      c1 = all & 0x1fffff;
-      c2 = all >> 21 & 0x1fffff;
-      c3 = static_cast<uint32_t>(all >> 42);
+      const uint64_t w = lane < kWarpsOf ? sums[turn][lane] : 0;
+      c1 = __reduce_add_sync(kAll, static_cast<uint32_t>(w) & 0x1fffff);
+      c2 = __reduce_add_sync(kAll, static_cast<uint32_t>(w >> 21) & 0x1fffff);
+      c3 = __reduce_add_sync(kAll, static_cast<uint32_t>(w >> 42));
     }
     const uint32_t K = a.K;
+    const uint32_t most = c3 >= K ? c3 : c2 >= K ? c2 : c1 >= K ? c1 : 0;
     T += c3 >= K ? 3 * step : c2 >= K ? 2 * step : c1 >= K ? step : 0;
+    if (most == K) {  // exactly K ranks from T on: they are the ranks above T - 1, whatever its other digits
+      --T;
+      break;
+    }
   }
   // above T: all; equal to T: the first K - above
   uint32_t above = 0, equal = 0;
@@ -407,15 +425,15 @@ cudaError_t launch_pdl(const void* fn, int64_t grid, int threads, void** args, c
 template <typename F>
 const void* ptr(F* f) { return reinterpret_cast<const void*>(f); }
 
-// as many blocks as are resident, and no more than there can be units for 8 warps each
-cudaError_t launch_resident(const void* fn, int64_t units, int num_sms, void** args, cudaStream_t stream) {
+// as many blocks as are resident, and no more than there can be units
+cudaError_t launch_resident(const void* fn, int threads, int64_t units, int num_sms, void** args, cudaStream_t stream) {
   int occ = 0;
-  cudaError_t e = kernel_prep(fn, 256, 0, &occ);
+  cudaError_t e = kernel_prep(fn, threads, 0, &occ);
   if (e != cudaSuccess) return e;
   if (occ < 1) return cudaErrorInvalidConfiguration;
   int64_t grid = static_cast<int64_t>(num_sms) * occ;
   if (units < grid) grid = units < 1 ? 1 : units;
-  return launch_pdl(fn, grid, 256, args, stream);
+  return launch_pdl(fn, grid, threads, args, stream);
 }
 
 }  // namespace
@@ -424,7 +442,7 @@ cudaError_t launch_block_bounds(int dtype, BoundsArgs a, int num_sms, cudaStream
   const void* fn = dtype == PA_F16 ? (a.D == 128 ? ptr(block_bounds_kernel<__half2, 128>) : ptr(block_bounds_kernel<__half2, 64>))
                                    : (a.D == 128 ? ptr(block_bounds_kernel<__nv_bfloat162, 128>) : ptr(block_bounds_kernel<__nv_bfloat162, 64>));
   void* args[1] = {&a};
-  return launch_resident(fn, static_cast<int64_t>(a.S) * a.H * (a.max_blocks < 1 ? 1 : a.max_blocks), num_sms, args, stream);
+  return launch_resident(fn, 256, static_cast<int64_t>(a.S) * a.H * (a.max_blocks < 1 ? 1 : a.max_blocks), num_sms, args, stream);
 }
 
 template <typename T>
@@ -438,7 +456,7 @@ cudaError_t launch_select_blocks(int dtype, SelectArgs a, int num_sms, cudaStrea
   *launched = 0;
   if (a.max_blocks > a.K) {
     const void* fn = dtype == PA_F16 ? score_fn<__half>(a.D, a.g) : score_fn<__nv_bfloat16>(a.D, a.g);
-    const cudaError_t e = launch_resident(fn, static_cast<int64_t>(a.S) * a.H * ((a.max_blocks + 31) / 32), num_sms, args, stream);
+    const cudaError_t e = launch_resident(fn, kScoreWarps * 32, static_cast<int64_t>(a.S) * a.H * ((a.max_blocks + 7) / 8), num_sms, args, stream);
     if (e != cudaSuccess) return e;
     ++*launched;
   }
