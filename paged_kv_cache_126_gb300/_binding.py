@@ -1,13 +1,16 @@
 """Thin ctypes binding of libpa (include/pa.h): argument marshalling only.
 
 Every device operation runs in libpa's CUDA kernels; this module turns torch
-tensors into ``pa_tensor`` descriptors and return codes into exceptions.  If
-``libpa.so`` is missing the import fails: there is no fallback path.
+tensors into ``pa_tensor`` descriptors and return codes into exceptions.  The calls of
+the rotary, 4-bit and block-sparse operators take many tensors and are marshalled by the
+extension module ``_marshal`` instead of ctypes.  If ``libpa.so`` or ``_marshal.so`` is
+missing the import fails: there is no fallback path.
 """
 
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 
 import numpy as np
@@ -312,73 +315,81 @@ def pa_decode_split(q, k_cache, v_cache, block_tables, context_lens, scale, out,
     return out
 
 
-def _opt(t):
-    """Descriptor reference of an optional tensor argument (None: NULL)."""
-    return None if t is None else C.byref(tensor_desc(t))
+def _load_marshal():
+    path = os.path.join(os.path.dirname(_LIB_PATH), "_marshal.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_marshal.so not found at {path}; build it first "
+                          "(python paged_kv_cache_126_gb300/build.py)")
+    spec = importlib.util.spec_from_file_location("_marshal", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for name in ("pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",
+                 "pa_select_blocks", "pa_decode_selected"):
+        mod.bind(name, C.cast(getattr(LIB, name), C.c_void_p).value)
+    return mod
+
+
+_marshal = _load_marshal()
 
 
 def pa_cache_append_rope(k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin, q=None, q_out=None,
                          interleaved=False, stream=None) -> None:
     """``pa_cache_append_rope``: append with the keys rotated on the way, and q rotated into q_out
     (which may be q); positions int32 [T], cos_sin float32 [P, R]."""
-    st = _stream_of(k_cache, stream)
-    ds = [tensor_desc(t) for t in (k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin)]
-    _check(LIB.pa_cache_append_rope(*map(_ref, ds), int(interleaved), _opt(q), _opt(q_out), st), "pa_cache_append_rope")
+    rc = _marshal.pa_cache_append_rope(k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin, interleaved, q, q_out,
+                                       stream)
+    if rc:
+        _check(rc, "pa_cache_append_rope")
 
 
 def pa_cache_append_q4(k_new, v_new, slot_mapping, k_cache, v_cache, positions=None, cos_sin=None, q=None, q_out=None,
                        interleaved=False, stream=None) -> None:
     """``pa_cache_append_q4``: append into the 4-bit caches, uint8 [num_blocks, H, B, 5 D / 8] (see
     include/pa.h), rotated on the way where positions and cos_sin are given."""
-    st = _stream_of(k_cache, stream)
-    ds = [tensor_desc(t) for t in (k_new, v_new, slot_mapping, k_cache, v_cache)]
-    _check(LIB.pa_cache_append_q4(*map(_ref, ds), _opt(positions), _opt(cos_sin), int(interleaved), _opt(q), _opt(q_out),
-                                  st), "pa_cache_append_q4")
+    rc = _marshal.pa_cache_append_q4(k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin, interleaved, q, q_out,
+                                     stream)
+    if rc:
+        _check(rc, "pa_cache_append_q4")
 
 
 def pa_cache_read_q4(k_cache, v_cache, slot_mapping, k_out, v_out, stream=None) -> None:
     """``pa_cache_read_q4``: the 4-bit rows at slot_mapping [T] as 16-bit rows [T, H, D]."""
-    st = _stream_of(k_cache, stream)
-    ds = [tensor_desc(t) for t in (k_cache, v_cache, slot_mapping, k_out, v_out)]
-    _check(LIB.pa_cache_read_q4(*map(_ref, ds), st), "pa_cache_read_q4")
+    rc = _marshal.pa_cache_read_q4(k_cache, v_cache, slot_mapping, k_out, v_out, stream)
+    if rc:
+        _check(rc, "pa_cache_read_q4")
 
 
 def pa_decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out, stream=None):
     """``pa_decode_q4``: decode attention over the 4-bit caches into ``out`` [S, Hq, D]."""
-    st = _stream_of(q, stream)
-    ds = [tensor_desc(t) for t in (q, k_cache, v_cache, block_tables, context_lens)]
-    o = tensor_desc(out)
-    _check(LIB.pa_decode_q4(*map(_ref, ds), scale, C.byref(o), st), "pa_decode_q4")
+    rc = _marshal.pa_decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out, stream)
+    if rc:
+        _check(rc, "pa_decode_q4")
     return out
 
 
 def pa_block_bounds(k_cache, block_tables, context_lens, first_tokens, bounds, stream=None):
     """``pa_block_bounds``: smallest and largest key of each frame that holds tokens from
     first_tokens[s] (None: 0) on, into ``bounds`` [num_blocks, H, 2, D]."""
-    st = _stream_of(k_cache, stream)
-    ds = [tensor_desc(t) for t in (k_cache, block_tables, context_lens)]
-    b = tensor_desc(bounds)
-    _check(LIB.pa_block_bounds(*map(_ref, ds), _opt(first_tokens), C.byref(b), st), "pa_block_bounds")
+    rc = _marshal.pa_block_bounds(k_cache, block_tables, context_lens, first_tokens, bounds, stream)
+    if rc:
+        _check(rc, "pa_block_bounds")
     return bounds
 
 
 def pa_select_blocks(q, bounds, block_tables, context_lens, block_size, selected, keep_first=1, keep_last=1, stream=None):
     """``pa_select_blocks``: positions of the frames with the largest scores, into ``selected``
     (int32 [S, H, K], ascending, -1 behind the last)."""
-    st = _stream_of(q, stream)
-    ds = [tensor_desc(t) for t in (q, bounds, block_tables, context_lens)]
-    o = tensor_desc(selected)
-    _check(LIB.pa_select_blocks(*map(_ref, ds), int(block_size), int(keep_first), int(keep_last), C.byref(o), st),
-           "pa_select_blocks")
+    rc = _marshal.pa_select_blocks(q, bounds, block_tables, context_lens, block_size, keep_first, keep_last, selected, stream)
+    if rc:
+        _check(rc, "pa_select_blocks")
     return selected
 
 
 def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, selected, scale, out, stream=None):
     """``pa_decode_selected``: decode attention over the listed frames into ``out`` [S, Hq, D]."""
-    st = _stream_of(q, stream)
-    ds = [tensor_desc(t) for t in (q, k_cache, v_cache, block_tables, context_lens, selected)]
-    o = tensor_desc(out)
-    _check(LIB.pa_decode_selected(*map(_ref, ds), scale, C.byref(o), st), "pa_decode_selected")
+    rc = _marshal.pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, selected, scale, out, stream)
+    if rc:
+        _check(rc, "pa_decode_selected")
     return out
 
 
