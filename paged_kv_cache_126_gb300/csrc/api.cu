@@ -1579,13 +1579,15 @@ int gather_args(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v
   return PA_OK;
 }
 
-// Workspace of a gathered decode on `workers` warps: arrival counters, and two partials a warp.
+// Workspace of a gathered decode on `workers` warps: an arrival counter per (sequence, head) and two per group
+// of 16 workers, and as many partials as workers and groups have sides.
 int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, pa::GatherArgs* a) {
-  const size_t slots = 2 * static_cast<size_t>(workers) * a->g;
+  const size_t groups = 2 * (static_cast<size_t>(workers) / 16 + 1);
+  const size_t slots = (2 * static_cast<size_t>(workers) + groups) * a->g;
   void* ws = nullptr;
   size_t cnt_bytes = 0;
-  PA_TRY(workspace(dev, stream, static_cast<size_t>(a->S) * a->H * sizeof(int32_t), slots * (D + 2) * sizeof(float), &ws,
-                   &cnt_bytes));
+  PA_TRY(workspace(dev, stream, (static_cast<size_t>(a->S) * a->H + groups) * sizeof(int32_t), slots * (D + 2) * sizeof(float),
+                   &ws, &cnt_bytes));
   unsigned char* base = static_cast<unsigned char*>(ws);
   a->cnt = reinterpret_cast<int32_t*>(base + kSchedBytes);
   a->ws_o = reinterpret_cast<float*>(base + kSchedBytes + cnt_bytes);

@@ -58,7 +58,15 @@ struct RowFormat {
     if (x.slot[1] >= 0) tma_load_4d(dst + kHalfTile, map, 0, x.slot[1], 0, h, bar);
   }
 
-  __device__ __forceinline__ static int q_element(int c, int i) { return 16 * (i >> 2) + 2 * c + (i & 1) + ((i & 2) << 2); }
+  // the elements of a query that load_q takes in lane column c: 16 k + 2 c + {0, 1, 8, 9}
+  __device__ __forceinline__ static void read_q(const T* q, int c, bool on, float (&x)[D / 4]) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const float2 y = unpack2<T>(on ? __ldg(reinterpret_cast<const uint32_t*>(q + 8 * i + 2 * c)) : 0u);
+      x[2 * i] = y.x;
+      x[2 * i + 1] = y.y;
+    }
+  }
   __device__ __forceinline__ static void load_q(const float (&q)[D / 4], uint32_t (&f)[D / 16][2]) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
@@ -108,7 +116,14 @@ struct RowFormat {
         for (int q = 0; q < PARTS; ++q) mma(o[t][n], x[0], x[1], x[2], x[3], p[q][n][0], p[q][n][1], M());
     }
   }
-  __device__ __forceinline__ static int o_element(int t, int r, int hi) { return 16 * t + 8 * hi + r; }
+  // where lane row r stores its D / 8 elements of one query: r of every 8
+  template <typename U>
+  __device__ __forceinline__ static void store(U* row, int r, const float (&y)[D / 16][2]) {
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) dk::Chunk<U>::store1(row + 16 * t + 8 * hi + r, y[t][hi]);
+  }
 };
 
 }  // namespace gk

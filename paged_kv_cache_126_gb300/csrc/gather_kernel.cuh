@@ -38,6 +38,8 @@ namespace gk {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMinKeys = 64;     // fewest keys a warp is given
+constexpr int kGroup = 16;       // pieces of one (s, h) are joined in groups of this many workers
+constexpr int kFlat = 24;        // where there are fewer pieces than this they are joined at once
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
 
 enum Parts { kOnePart = 0, kTwinColumns = 1, kTwoParts = 2 };
@@ -304,8 +306,21 @@ struct Q4Format {
       f[2 * w + 1][1] = pack2<M>(e[3], e[7]);
     }
   }
-  // element of the query that load_q takes as q[i] in lane column c
-  __device__ __forceinline__ static int q_element(int c, int i) { return c * (D / 4) + i; }
+  // the elements of a query that load_q takes in lane column c: a run of D / 4
+  __device__ __forceinline__ static void read_q(const T* q, int c, bool on, float (&x)[D / 4]) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (on) u = __ldg(reinterpret_cast<const uint4*>(q + c * (D / 4)) + i);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = unpack2<T>(w[j]);
+        x[8 * i + 2 * j] = y.x;
+        x[8 * i + 2 * j + 1] = y.y;
+      }
+    }
+  }
 
   template <int NT>
   __device__ __forceinline__ static void scores(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
@@ -374,11 +389,136 @@ struct Q4Format {
               mma(o[4 * y + 2 * z + u][n], xa[2 * u], xa[2 * u + 1], xb[2 * u], xb[2 * u + 1], p[q][n][0], p[q][n][1], M());
       }
   }
-  // element that o[t][.][0 or 1] (hi = 0) and [2 or 3] (hi = 1) of lane row r hold
-  __device__ __forceinline__ static int o_element(int t, int r, int hi) { return r * (D / 8) + 2 * t + hi; }
+  // where lane row r stores its D / 8 elements of one query (o[t] holds elements 2 t and 2 t + 1 of a run)
+  __device__ __forceinline__ static void store(float* row, int r, const float (&y)[D / 16][2]) {
+#pragma unroll
+    for (int t = 0; t < D / 16; t += 2)
+      *reinterpret_cast<float4*>(row + r * (D / 8) + 2 * t) = make_float4(y[t][0], y[t][1], y[t + 1][0], y[t + 1][1]);
+  }
+  __device__ __forceinline__ static void store(T* row, int r, const float (&y)[D / 16][2]) {
+#pragma unroll
+    for (int t = 0; t < D / 16; t += 4)
+      *reinterpret_cast<uint4*>(row + r * (D / 8) + 2 * t) =
+          make_uint4(pack2<T>(y[t][0], y[t][1]), pack2<T>(y[t + 1][0], y[t + 1][1]), pack2<T>(y[t + 2][0], y[t + 2][1]),
+                     pack2<T>(y[t + 3][0], y[t + 3][1]));
+  }
 };
 
 // ---- the kernel -------------------------------------------------------------------------------------
+// The sum of n partials, in order, of g queries: partial k is slot s0 + 2 k, and s0 + e for k = 0.  `done` takes
+// (query, top, sum, bad, y): the maximum, the weights' sum and this lane's D / 32 elements of the weighted
+// values.  CG queries at a time; lane k weighs partial k of 32, and 16 reads of the values are in flight.
+template <int D, int CG, typename Done>
+__device__ __forceinline__ void join_queries(const GatherArgs& a, int64_t s0, int e, int n, int lane, Done done) {
+  constexpr int E = D / 32, kDeep = 16 / CG;
+  for (int c0 = 0; c0 < a.g; c0 += CG) {
+    auto at = [&](int k, int c) { return (s0 + 2 * k + (k == 0 ? e : 0)) * a.g + min(c0 + c, a.g - 1); };
+    float2 x[CG];
+    float top[CG];
+    bool bad = false;
+    auto read = [&](int k0) {
+#pragma unroll
+      for (int c = 0; c < CG; ++c)
+        x[c] = k0 + lane < n ? __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at(k0 + lane, c)) : make_float2(-INFINITY, 0.f);
+    };
+#pragma unroll
+    for (int c = 0; c < CG; ++c) top[c] = -INFINITY;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      read(k0);
+#pragma unroll
+      for (int c = 0; c < CG; ++c) {
+        bad = bad || x[c].y < 0.f;
+        if (x[c].y != 0.f) top[c] = fmaxf(top[c], x[c].x);  // an empty piece has no maximum
+      }
+    }
+    bad = __any_sync(kAll, bad);
+#pragma unroll
+    for (int c = 0; c < CG; ++c)
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(kAll, top[c], o));
+    float sum[CG] = {}, y[CG][E] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      if (n > 32) read(k0);
+      float mine[CG];
+#pragma unroll
+      for (int c = 0; c < CG; ++c) {
+        mine[c] = x[c].y != 0.f ? dk::ex2(x[c].x - top[c]) : 0.f;
+        sum[c] += mine[c] * x[c].y;
+      }
+      const int m = min(32, n - k0);
+      for (int k = 0; k < m; k += kDeep) {
+        float v[kDeep][CG][E];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+          for (int c = 0; c < CG; ++c) {
+            const float* p = a.ws_o + at(k0 + min(k + u, m - 1), c) * D + lane * E;
+            if constexpr (E == 4) {
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(p));
+              v[u][c][0] = z.x, v[u][c][1] = z.y, v[u][c][2] = z.z, v[u][c][3] = z.w;
+            } else {
+              const float2 z = __ldcg(reinterpret_cast<const float2*>(p));
+              v[u][c][0] = z.x, v[u][c][1] = z.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+          for (int c = 0; c < CG; ++c) {
+            const float z = __shfl_sync(kAll, mine[c], (k + u) & 31), w = k + u < m ? z : 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+              if (w != 0.f) y[c][i] = fmaf(w, v[u][c][i], y[c][i]);
+          }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CG; ++c) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) sum[c] += __shfl_xor_sync(kAll, sum[c], o);
+      if (c0 + c < a.g) done(c0 + c, top[c], sum[c], bad, y[c]);
+    }
+  }
+}
+
+// Joins n partials into the output row (into >= 0: into partial `into` instead).
+template <typename T, int D>
+__device__ __forceinline__ void join(const GatherArgs& a, int64_t s0, int e, int n, int64_t into, int s, int h, int lane) {
+  constexpr int E = D / 32;
+  auto done = [&](int col, float top, float sum, bool bad, const float (&y)[E]) {
+    if (into >= 0) {
+      float* p = a.ws_o + (into * a.g + col) * D + lane * E;
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[i] = y[i];
+      if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + (into * a.g + col) * 2) = make_float2(top, bad ? -1.f : sum);
+      return;
+    }
+    const float inv = bad || !(sum != 0.f) ? 0.f : 1.f / sum;
+    T* out = static_cast<T*>(a.out) + s * a.out_row + (static_cast<int64_t>(h) * a.g + col) * D + lane * E;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(out + i) = bad ? 0u : pack2<T>(y[i] * inv, y[i + 1] * inv);
+  };
+  if (a.g == 1)
+    join_queries<D, 1>(a, s0, e, n, lane, done);
+  else if (a.g == 2)
+    join_queries<D, 2>(a, s0, e, n, lane, done);
+  else
+    join_queries<D, 4>(a, s0, e, n, lane, done);
+}
+
+// Raises a counter of `n` arrivals; whether this one was the last, which leaves it zero again.
+__device__ __forceinline__ bool last_of(int32_t* cnt, int n, int lane) {
+  __threadfence();
+  __syncwarp();
+  int before = 0;
+  if (lane == 0) before = atomicAdd(cnt, 1);
+  before = __shfl_sync(kAll, before, 0);
+  if (before != n - 1) return false;
+  __threadfence();
+  if (lane == 0) *cnt = 0;
+  return true;
+}
+
 template <class F, int STAGES>
 __host__ __device__ constexpr uint32_t warp_smem() {
   return STAGES * F::kLoads * 2 * F::kTile + STAGES * 32;  // stages, then metas (4 bytes a part) and two mbarriers each
@@ -412,8 +552,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 
   // this warp's range [b0, b1) of the batch's tiles
   int64_t total = 0;
+  int n = 0;  // tiles of sequence s0 + lane
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    const int n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
+    n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     total += __reduce_add_sync(kAll, n);
   }
   total *= a.H;
@@ -428,7 +569,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   Cursor cur;
   int64_t before = 0;
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    const int n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
+    if (a.S > 32) n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -489,6 +630,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
+  int4* owed = reinterpret_cast<int4*>(smem + WARPS * warp_smem<F, STAGES>() + 16) + 2 * warp;  // (s, h, first and last piece)
+  int pending = 0;
   const float rest = PARTS == kTwinColumns ? (c >= 2 ? 1.f : 0.f) : 1.f;
   int st = 0, phase = 0;
 
@@ -513,11 +656,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       const int col = PARTS == kTwinColumns ? (r & 3) : 8 * n + r;
       const T* q = static_cast<const T*>(a.q) + cur.s * a.q_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
       float x[D / 4], top = 0.f;
+      F::read_q(q, c, col < a.g, x);
 #pragma unroll
-      for (int j = 0; j < D / 4; ++j) {
-        x[j] = col < a.g ? to_float(q[F::q_element(c, j)]) : 0.f;
-        top = fmaxf(top, fabsf(x[j]));
-      }
+      for (int j = 0; j < D / 4; ++j) top = fmaxf(top, fabsf(x[j]));
       float back = a.qk_scale_log2;
       if (F::kScaleQ) {
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
@@ -666,74 +807,65 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         for (int j = 0; j < 2; ++j) {
           const int col = 8 * n + 2 * c + j;
           if (col >= a.g || (PARTS == kTwinColumns && c >= 2)) continue;
+          float inv = 1.f;
+          if (whole) inv = poison || !(l[n][j] != 0.f) ? 0.f : 1.f / l[n][j];
+          float y[D / 16][2];
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) y[t][hi] = poison ? 0.f : o[t][n][j + 2 * hi] * inv;
           if (whole) {
-            const float inv = poison || !(l[n][j] != 0.f) ? 0.f : 1.f / l[n][j];
-            T* out = static_cast<T*>(a.out) + cur.s * a.out_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-              for (int hi = 0; hi < 2; ++hi) {
-                const float y = poison ? 0.f : o[t][n][j + 2 * hi] * inv;
-                dk::Chunk<T>::store1(out + F::o_element(t, r, hi), y);
-              }
+            F::store(static_cast<T*>(a.out) + cur.s * a.out_row + (static_cast<int64_t>(cur.h) * a.g + col) * D, r, y);
           } else {
-            float* ml = a.ws_ml + (slot * a.g + col) * 2;
-            float* wo = a.ws_o + (slot * a.g + col) * D;
-            if (r == 0) {
-              ml[0] = m[n][j];
-              ml[1] = poison ? -1.f : l[n][j];
-            }
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-              for (int hi = 0; hi < 2; ++hi) wo[F::o_element(t, r, hi)] = o[t][n][j + 2 * hi];
+            F::store(a.ws_o + (slot * a.g + col) * D, r, y);
+            if (r == 0)
+              *reinterpret_cast<float2*>(a.ws_ml + (slot * a.g + col) * 2) = make_float2(m[n][j], poison ? -1.f : l[n][j]);
           }
         }
       if (!whole) {
-        __threadfence();
-        __syncwarp();
+        // pieces are the workers w0 .. w1: the first's second partial, the others' first
         const int64_t p0 = b0 + i - cur.t, p1 = p0 + cur.tiles;  // the tiles of (s, h)
-        const int64_t w0 = ((p0 + 1) * workers - 1) / total, w1 = (p1 * workers - 1) / total;
-        const int pieces = static_cast<int>(w1 - w0) + 1;
-        int32_t* cnt = a.cnt + static_cast<int64_t>(cur.s) * a.H + cur.h;
-        int done = 0;
-        if (lane == 0) done = atomicAdd(cnt, 1);
-        done = __shfl_sync(kAll, done, 0);
-        if (done == pieces - 1) {
-          __threadfence();
-          if (lane == 0) *cnt = 0;
-          for (int col = 0; col < a.g; ++col) {
-            auto at = [&](int k) { return (2 * (w0 + k) + (k == 0 ? 1 : 0)) * a.g + col; };
-            float top = -INFINITY, sum = 0.f;
-            bool bad = false;
-            for (int k = lane; k < pieces; k += 32) {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at(k));
-              bad = bad || x.y < 0.f;
-              if (x.y != 0.f) top = fmaxf(top, x.x);
-            }
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
-            bad = __any_sync(kAll, bad);
-            constexpr int E = D / 32;
-            float y[E] = {};
-            for (int k = 0; k < pieces; ++k) {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at(k));
-              if (x.y == 0.f) continue;
-              const float w = dk::ex2(x.x - top);
-              sum += w * x.y;
-              const float* wo = a.ws_o + at(k) * D + lane * E;
-#pragma unroll
-              for (int u = 0; u < E; ++u) y[u] += w * __ldcg(wo + u);
-            }
-            const float inv = bad || !(sum != 0.f) ? 0.f : 1.f / sum;
-            T* out = static_cast<T*>(a.out) + cur.s * a.out_row + (static_cast<int64_t>(cur.h) * a.g + col) * D + lane * E;
-#pragma unroll
-            for (int u = 0; u < E; ++u) dk::Chunk<T>::store1(out + u, bad ? 0.f : y[u] * inv);
-          }
-        }
+        if (lane == 0)
+          owed[pending] = make_int4(cur.s, cur.h, static_cast<int>(((p0 + 1) * workers - 1) / total),
+                                    static_cast<int>((p1 * workers - 1) / total));
+        ++pending;
       }
     }
     if (i < count) next_head<SEL, LOADS>(a, cur);
+  }
+
+  // The arrivals of this warp's partials (of its first (s, h) and of its last), and the joins that fall to it.
+  // They wait for the end so that the loop above has the registers to itself.
+  __threadfence();
+  __syncwarp();
+#pragma unroll 1
+  for (int k = 0; k < pending; ++k) {
+    const int4 x = owed[k];
+    const int w0 = x.z, w1 = x.w;
+    int32_t* cnt = a.cnt + static_cast<int64_t>(x.x) * a.H + x.y;
+    int32_t* group_cnt = nullptr;
+    int64_t from = 2 * static_cast<int64_t>(w0), into = -1;  // partials to join, and where to
+    int e = 1, n = w1 - w0 + 1;
+    if (n > kFlat) {
+      // Many pieces: the last of each group of kGroup workers joins the group's, the last group joins the groups.
+      // A group can hold the end of one such (s, h) and the start of another: two counters and partials.
+      const int g = static_cast<int>(id) / kGroup, lo = max(w0, g * kGroup);
+      e = g == w0 / kGroup ? 1 : 0;
+      n = min(w1, (g + 1) * kGroup - 1) - lo + 1;
+      from = 2 * static_cast<int64_t>(lo);
+      into = 2 * all_warps + 2 * g + e;  // partials of groups follow those of workers
+      group_cnt = a.cnt + static_cast<int64_t>(a.S) * a.H + 2 * g + e;
+    }
+#pragma unroll 1
+    while (last_of(group_cnt ? group_cnt : cnt, n, lane)) {
+      join<T, D>(a, from, e, n, into, x.x, x.y, lane);
+      if (!group_cnt) break;
+      group_cnt = nullptr;
+      from = 2 * all_warps + 2 * (w0 / kGroup);
+      into = -1;
+      e = 1;
+      n = w1 / kGroup - w0 / kGroup + 1;
+    }
   }
 }
 
@@ -741,7 +873,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
 cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
   const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>);
-  constexpr uint32_t smem = WARPS * warp_smem<F, STAGES>() + 16;  // + the abort flag
+  constexpr uint32_t smem = WARPS * (warp_smem<F, STAGES>() + 32) + 16;  // + the abort flag and what is owed
   int occ = 0;
   cudaError_t e = kernel_prep(fn, WARPS * 32, smem, &occ);
   if (e != cudaSuccess) return e;
