@@ -6,14 +6,17 @@
 // in one pass, m being a running maximum that moves only when a score passes it by 2^8.
 //
 // Work.  A tile is up to four parts of 16 keys of one (s, h): its keys are one copy, its values another,
-// and each is loaded again as soon as the warp has read it.  All tiles of the batch, numbered by sequence,
-// head and position, are cut into one consecutive range per resident warp, equal to within
-// a tile: every warp is its own worker with its own ring of shared-memory stages, and no
-// barrier joins the warps of a block.  A (s, h) that lies in one range is written straight
-// out; one that is cut leaves a partial (max, sum, weighted values) per piece, and the warp
-// that brings the arrival counter to the number of pieces joins them, in order, so that
-// results do not depend on timing.  The cut follows from the lengths, which each warp reads
-// on the device.
+// and each is loaded again as soon as the warp has read it.  All tiles of the batch, numbered by
+// sequence, head and position, are cut into one consecutive range per resident warp, equal to within
+// a tile: every warp is its own worker with its own ring of shared-memory stages, and no barrier
+// joins the warps of a block before they are done.  The cut follows from the lengths, which each warp
+// reads on the device.  A (s, h) that lies in one range is written straight out.  One that is cut leaves
+// a partial (max, sum, weighted values) per piece in the workspace, and the warp that brings the arrival
+// counter to the number of pieces has its block join them (in groups of 16 where they are many),
+// in order, so that results do not depend on timing.  What runs once a warp, the joins above all, is
+// kept short in code rather than unrolled: instructions that are not in the cache cost more
+// than the loads do (joins unrolled over four queries and sixteen pieces: 102 us for 64
+// sequences of 512 .. 2048 tokens where the loop alone takes 87).
 //
 // Tensor cores (mma.sync m16n8k16): scores are C[16 keys x 8 queries] = K (A operand) times
 // q^T (B), and the values O^T[16 elements x 8 queries] += V^T (A) times P (B).  Keys and
@@ -405,105 +408,67 @@ struct Q4Format {
 };
 
 // ---- the kernel -------------------------------------------------------------------------------------
-// The sum of n partials, in order, of g queries: partial k is slot s0 + 2 k, and s0 + e for k = 0.  `done` takes
-// (query, top, sum, bad, y): the maximum, the weights' sum and this lane's D / 32 elements of the weighted
-// values.  CG queries at a time; lane k weighs partial k of 32, and 16 reads of the values are in flight.
-template <int D, int CG, typename Done>
-__device__ __forceinline__ void join_queries(const GatherArgs& a, int64_t s0, int e, int n, int lane, Done done) {
-  constexpr int E = D / 32, kDeep = 16 / CG;
-  for (int c0 = 0; c0 < a.g; c0 += CG) {
-    auto at = [&](int k, int c) { return (s0 + 2 * k + (k == 0 ? e : 0)) * a.g + min(c0 + c, a.g - 1); };
-    float2 x[CG];
-    float top[CG];
-    bool bad = false;
-    auto read = [&](int k0) {
+// One query's sum of n partials, in order: partial k is slot first + 2 k, and first + e for k = 0.  Into the output
+// row, or into slot `into` (>= 0).
+struct Join {
+  int64_t first, into;
+  int e, n, s, h;
+};
+template <typename T, int D>
+__device__ __forceinline__ void join_query(const GatherArgs& a, const Join& x, int col, int lane) {
+  constexpr int E = D / 32, kDeep = 16;
+  using V = typename std::conditional<E == 4, float4, float2>::type;
+  float top = -INFINITY, sum = 0.f, y[E] = {};
+  bool bad = false;
+  const int64_t row = 2 * static_cast<int64_t>(a.g);  // rows of [g] between one piece and the next
+  const int64_t at0 = x.first * a.g + col;
+#pragma unroll 1
+  for (int k0 = 0; k0 < x.n; k0 += kDeep) {
+    const int m = min(kDeep, x.n - k0);
+    float2 p = make_float2(-INFINITY, 0.f);
+    if (lane < m) p = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at0 + (k0 + lane) * row + (k0 + lane == 0 ? x.e * a.g : 0));
+    V v[kDeep];
+    int64_t at = at0 + k0 * row + (k0 == 0 ? x.e * a.g : 0);
 #pragma unroll
-      for (int c = 0; c < CG; ++c)
-        x[c] = k0 + lane < n ? __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at(k0 + lane, c)) : make_float2(-INFINITY, 0.f);
-    };
-#pragma unroll
-    for (int c = 0; c < CG; ++c) top[c] = -INFINITY;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      read(k0);
-#pragma unroll
-      for (int c = 0; c < CG; ++c) {
-        bad = bad || x[c].y < 0.f;
-        if (x[c].y != 0.f) top[c] = fmaxf(top[c], x[c].x);  // an empty piece has no maximum
-      }
+    for (int u = 0; u < kDeep; ++u) {
+      if (u < m) v[u] = __ldcg(reinterpret_cast<const V*>(a.ws_o + at * D) + lane);
+      if (u == 0) at = at0 + k0 * row;
+      at += row;
     }
-    bad = __any_sync(kAll, bad);
+    bad = bad || __any_sync(kAll, p.y < 0.f);
+    float t = p.y != 0.f ? p.x : -INFINITY;  // an empty piece has no maximum
 #pragma unroll
-    for (int c = 0; c < CG; ++c)
+    for (int o = 1; o < kDeep; o <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
+    t = fmaxf(__shfl_sync(kAll, t, 0), top);
+    const float less = top == t ? 1.f : dk::ex2(top - t);
+    top = t;
+    const float mine = p.y != 0.f ? dk::ex2(p.x - top) : 0.f;
+    sum = sum * less + mine * p.y;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(kAll, top[c], o));
-    float sum[CG] = {}, y[CG][E] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      if (n > 32) read(k0);
-      float mine[CG];
+    for (int i = 0; i < E; ++i) y[i] *= less;
 #pragma unroll
-      for (int c = 0; c < CG; ++c) {
-        mine[c] = x[c].y != 0.f ? dk::ex2(x[c].x - top[c]) : 0.f;
-        sum[c] += mine[c] * x[c].y;
+    for (int u = 0; u < kDeep; ++u) {
+      const float w = __shfl_sync(kAll, mine, u);
+      if (w != 0.f) {
+        const float* z = reinterpret_cast<const float*>(&v[u]);
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = fmaf(w, z[i], y[i]);
       }
-      const int m = min(32, n - k0);
-      for (int k = 0; k < m; k += kDeep) {
-        float v[kDeep][CG][E];
-#pragma unroll
-        for (int u = 0; u < kDeep; ++u)
-#pragma unroll
-          for (int c = 0; c < CG; ++c) {
-            const float* p = a.ws_o + at(k0 + min(k + u, m - 1), c) * D + lane * E;
-            if constexpr (E == 4) {
-              const float4 z = __ldcg(reinterpret_cast<const float4*>(p));
-              v[u][c][0] = z.x, v[u][c][1] = z.y, v[u][c][2] = z.z, v[u][c][3] = z.w;
-            } else {
-              const float2 z = __ldcg(reinterpret_cast<const float2*>(p));
-              v[u][c][0] = z.x, v[u][c][1] = z.y;
-            }
-          }
-#pragma unroll
-        for (int u = 0; u < kDeep; ++u)
-#pragma unroll
-          for (int c = 0; c < CG; ++c) {
-            const float z = __shfl_sync(kAll, mine[c], (k + u) & 31), w = k + u < m ? z : 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-              if (w != 0.f) y[c][i] = fmaf(w, v[u][c][i], y[c][i]);
-          }
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < CG; ++c) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) sum[c] += __shfl_xor_sync(kAll, sum[c], o);
-      if (c0 + c < a.g) done(c0 + c, top[c], sum[c], bad, y[c]);
     }
   }
-}
-
-// Joins n partials into the output row (into >= 0: into partial `into` instead).
-template <typename T, int D>
-__device__ __forceinline__ void join(const GatherArgs& a, int64_t s0, int e, int n, int64_t into, int s, int h, int lane) {
-  constexpr int E = D / 32;
-  auto done = [&](int col, float top, float sum, bool bad, const float (&y)[E]) {
-    if (into >= 0) {
-      float* p = a.ws_o + (into * a.g + col) * D + lane * E;
 #pragma unroll
-      for (int i = 0; i < E; ++i) p[i] = y[i];
-      if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + (into * a.g + col) * 2) = make_float2(top, bad ? -1.f : sum);
-      return;
-    }
-    const float inv = bad || !(sum != 0.f) ? 0.f : 1.f / sum;
-    T* out = static_cast<T*>(a.out) + s * a.out_row + (static_cast<int64_t>(h) * a.g + col) * D + lane * E;
+  for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (x.into >= 0) {
+    float* p = a.ws_o + (x.into * a.g + col) * D + lane * E;
 #pragma unroll
-    for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(out + i) = bad ? 0u : pack2<T>(y[i] * inv, y[i + 1] * inv);
-  };
-  if (a.g == 1)
-    join_queries<D, 1>(a, s0, e, n, lane, done);
-  else if (a.g == 2)
-    join_queries<D, 2>(a, s0, e, n, lane, done);
-  else
-    join_queries<D, 4>(a, s0, e, n, lane, done);
+    for (int i = 0; i < E; ++i) p[i] = y[i];
+    if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + (x.into * a.g + col) * 2) = make_float2(top, bad ? -1.f : sum);
+    return;
+  }
+  const float inv = bad || !(sum != 0.f) ? 0.f : 1.f / sum;
+  T* out = static_cast<T*>(a.out) + x.s * a.out_row + (static_cast<int64_t>(x.h) * a.g + col) * D + lane * E;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(out + i) = bad ? 0u : pack2<T>(y[i] * inv, y[i + 1] * inv);
 }
 
 // Raises a counter of `n` arrivals; whether this one was the last, which leaves it zero again.
@@ -517,6 +482,25 @@ __device__ __forceinline__ bool last_of(int32_t* cnt, int n, int lane) {
   __threadfence();
   if (lane == 0) *cnt = 0;
   return true;
+}
+
+// Where there are at least kFlat + 1 pieces, the last to arrive of each group of kGroup workers joins the group's, and the
+// last group the groups.  A group can hold the end of one such (s, h) and the start of another: two counters and
+// two partials a group.
+// A piece of (s, h) that a warp leaves: workers w0 .. w1 hold one each.  state 0: none, 1: counted, 2: counted as the last.
+struct Left {
+  int s, h, w0, w1, state;
+};
+
+// The counter that worker w's piece raises, and to what.
+__device__ __forceinline__ int32_t* arrivals(const GatherArgs& a, const Left& x, int w) {
+  const int g = w / kGroup;
+  return x.w1 - x.w0 < kFlat ? a.cnt + static_cast<int64_t>(x.s) * a.H + x.h
+                             : a.cnt + static_cast<int64_t>(a.S) * a.H + 2 * g + (x.w0 >= g * kGroup ? 1 : 0);
+}
+__device__ __forceinline__ int arrivals_of(const Left& x, int w) {
+  const int g = w / kGroup;
+  return x.w1 - x.w0 < kFlat ? x.w1 - x.w0 + 1 : min(x.w1, (g + 1) * kGroup - 1) - max(x.w0, g * kGroup) + 1;
 }
 
 template <class F, int STAGES>
@@ -562,13 +546,14 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   const int64_t all_warps = static_cast<int64_t>(gridDim.x) * WARPS;
   const int64_t workers = min(all_warps, (total + kMinTiles - 1) / kMinTiles);
   const int64_t id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
-  if (id >= workers) return;
-  const int64_t b0 = id * total / workers, b1 = (id + 1) * total / workers;
-  const int count = static_cast<int>(b1 - b0);
+  if (blockIdx.x >= workers) return;
+  const int64_t b0 = min(id, workers) * total / workers, b1 = min(id + 1, workers) * total / workers;
+  const int count = static_cast<int>(b1 - b0);  // 0: no worker
 
   Cursor cur;
+  cur.s = cur.h = cur.t = 0;
   int64_t before = 0;
-  for (int s0 = 0; s0 < a.S; s0 += 32) {
+  for (int s0 = 0; s0 < a.S && count > 0; s0 += 32) {
     if (a.S > 32) n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     int upto = n;
 #pragma unroll
@@ -630,8 +615,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
-  int4* owed = reinterpret_cast<int4*>(smem + WARPS * warp_smem<F, STAGES>() + 16) + 2 * warp;  // (s, h, first and last piece)
-  int pending = 0;
+  Left(*left)[2] = reinterpret_cast<Left(*)[2]>(smem + WARPS * warp_smem<F, STAGES>() + 16);  // side 0: begun before
+  if (lane < 2) left[warp][lane].state = 0;
+  __syncwarp();
+  bool stuck = false;
   const float rest = PARTS == kTwinColumns ? (c >= 2 ? 1.f : 0.f) : 1.f;
   int st = 0, phase = 0;
 
@@ -647,7 +634,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     }
   };
 
-  for (int i = 0; i < count;) {
+  for (int i = 0; i < count && !stuck;) {
     // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
     const int first_t = cur.t;
     bool poison = false;
@@ -684,7 +671,11 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     cur.t += stop - i;
     for (; i < stop; ++i) {
       const uint32_t kst = stages + st * kStage, vst = kst + kKeys, bar = bars + 16 * st;
-      if (!__all_sync(kAll, dk::mbar_wait(bar, phase, abort_flag, a.status))) return drain(i, false);
+      if (!__all_sync(kAll, dk::mbar_wait(bar, phase, abort_flag, a.status))) {
+        drain(i, false);
+        stuck = true;
+        break;
+      }
       uint32_t meta[LOADS], full = 0x0808, any = 0;
       lds(metas + st * 16, meta);
 #pragma unroll
@@ -751,7 +742,11 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
             }
         }
       }
-      if (!__all_sync(kAll, dk::mbar_wait(bar + 8, phase, abort_flag, a.status))) return drain(i, true);
+      if (!__all_sync(kAll, dk::mbar_wait(bar + 8, phase, abort_flag, a.status))) {
+        drain(i, true);
+        stuck = true;
+        break;
+      }
       if (any & 0xffff) {
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
@@ -825,46 +820,60 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (!whole) {
         // pieces are the workers w0 .. w1: the first's second partial, the others' first
         const int64_t p0 = b0 + i - cur.t, p1 = p0 + cur.tiles;  // the tiles of (s, h)
-        if (lane == 0)
-          owed[pending] = make_int4(cur.s, cur.h, static_cast<int>(((p0 + 1) * workers - 1) / total),
-                                    static_cast<int>((p1 * workers - 1) / total));
-        ++pending;
+        Left x;
+        x.s = cur.s;
+        x.h = cur.h;
+        x.w0 = static_cast<int>(((p0 + 1) * workers - 1) / total);
+        x.w1 = static_cast<int>((p1 * workers - 1) / total);
+        x.state = last_of(arrivals(a, x, static_cast<int>(id)), arrivals_of(x, static_cast<int>(id)), lane) ? 2 : 1;
+        if (lane == 0) left[warp][first_t == 0 ? 1 : 0] = x;
       }
     }
     if (i < count) next_head<SEL, LOADS>(a, cur);
   }
 
-  // The arrivals of this warp's partials (of its first (s, h) and of its last), and the joins that fall to it.
-  // They wait for the end so that the loop above has the registers to itself.
-  __threadfence();
-  __syncwarp();
+  // The joins that fall to this block, a query a warp at a time; then those of groups.
 #pragma unroll 1
-  for (int k = 0; k < pending; ++k) {
-    const int4 x = owed[k];
-    const int w0 = x.z, w1 = x.w;
-    int32_t* cnt = a.cnt + static_cast<int64_t>(x.x) * a.H + x.y;
-    int32_t* group_cnt = nullptr;
-    int64_t from = 2 * static_cast<int64_t>(w0), into = -1;  // partials to join, and where to
-    int e = 1, n = w1 - w0 + 1;
-    if (n > kFlat) {
-      // Many pieces: the last of each group of kGroup workers joins the group's, the last group joins the groups.
-      // A group can hold the end of one such (s, h) and the start of another: two counters and partials.
-      const int g = static_cast<int>(id) / kGroup, lo = max(w0, g * kGroup);
-      e = g == w0 / kGroup ? 1 : 0;
-      n = min(w1, (g + 1) * kGroup - 1) - lo + 1;
-      from = 2 * static_cast<int64_t>(lo);
-      into = 2 * all_warps + 2 * g + e;  // partials of groups follow those of workers
-      group_cnt = a.cnt + static_cast<int64_t>(a.S) * a.H + 2 * g + e;
+  for (int round = 0; round < 2; ++round) {
+    __syncthreads();
+    if (*abort_flag) return;
+    bool groups = false;
+#pragma unroll 1
+    for (int k = 0; k < 2 * WARPS; ++k) {
+      const Left x = left[k >> 1][k & 1];
+      if (x.state != 2) continue;
+      const bool many = x.w1 - x.w0 >= kFlat;
+      const int of = (k >> 1) * gridDim.x + blockIdx.x;  // the worker whose piece it is
+      Join j;
+      j.s = x.s;
+      j.h = x.h;
+      j.into = -1;
+      if (round == 0 && many) {
+        const int g = of / kGroup, lo = max(x.w0, g * kGroup);
+        j.first = 2 * static_cast<int64_t>(lo);
+        j.e = lo == x.w0 ? 1 : 0;
+        j.n = arrivals_of(x, of);
+        j.into = 2 * all_warps + 2 * g + j.e;  // partials of groups follow those of workers
+        groups = true;
+      } else {
+        j.first = round == 0 ? 2 * static_cast<int64_t>(x.w0) : 2 * all_warps + 2 * (x.w0 / kGroup);
+        j.e = 1;
+        j.n = round == 0 ? x.w1 - x.w0 + 1 : x.w1 / kGroup - x.w0 / kGroup + 1;
+      }
+#pragma unroll 1
+      for (int col = (warp + k) % WARPS; col < a.g; col += WARPS) join_query<T, D>(a, j, col, lane);
     }
+    if (!groups) return;
+    __syncthreads();
 #pragma unroll 1
-    while (last_of(group_cnt ? group_cnt : cnt, n, lane)) {
-      join<T, D>(a, from, e, n, into, x.x, x.y, lane);
-      if (!group_cnt) break;
-      group_cnt = nullptr;
-      from = 2 * all_warps + 2 * (w0 / kGroup);
-      into = -1;
-      e = 1;
-      n = w1 / kGroup - w0 / kGroup + 1;
+    for (int side = 0; side < 2; ++side) {
+      const Left x = left[warp][side];
+      if (x.state != 2) continue;
+      bool last = false;
+      if (x.w1 - x.w0 >= kFlat)
+        last = last_of(a.cnt + static_cast<int64_t>(x.s) * a.H + x.h, x.w1 / kGroup - x.w0 / kGroup + 1, lane);
+      __syncwarp();
+      if (lane == 0 && !last) left[warp][side].state = 0;
     }
   }
 }
@@ -873,7 +882,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
 cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
   const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>);
-  constexpr uint32_t smem = WARPS * (warp_smem<F, STAGES>() + 32) + 16;  // + the abort flag and what is owed
+  constexpr uint32_t smem = WARPS * (warp_smem<F, STAGES>() + 2 * sizeof(Left)) + 16;  // + the abort flag
   int occ = 0;
   cudaError_t e = kernel_prep(fn, WARPS * 32, smem, &occ);
   if (e != cudaSuccess) return e;
