@@ -1446,6 +1446,7 @@ int rope_args(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* s
   a->H = static_cast<int32_t>(H);
   a->D = static_cast<int32_t>(D);
   a->interleaved = interleaved;
+  if (!pa::rope_fits(*a, elem_bytes(dt))) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 
@@ -1496,6 +1497,7 @@ int pa_cache_append_q4(const pa_tensor* k_new, const pa_tensor* v_new, const pa_
   a.k_cache = static_cast<unsigned char*>(k_cache->data);
   a.v_cache = static_cast<unsigned char*>(v_cache->data);
   a.B = static_cast<int32_t>(z.B);
+  while ((1 << a.log2_B) < z.B) ++a.log2_B;
   a.num_slots = z.nb * z.B;
   a.status = g_dev[dev].status;
   if (pa::launch_rope_append(dt, true, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
@@ -1516,7 +1518,7 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
   PA_TRY(check_i32(slot_mapping, 1));
   const int64_t T = k_out->shape[0];
   if (v_out->shape[0] != T || slot_mapping->shape[0] != T) return PA_ERR_SHAPE;
-  if (T > INT32_MAX || z.H > INT32_MAX / 4) return PA_ERR_UNSUPPORTED;
+  if (T * 2 * z.H > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (T == 0) return PA_OK;
   int dev;
   PA_TRY(current_device(&dev));
@@ -1534,6 +1536,7 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
   a.H = static_cast<int32_t>(z.H);
   a.D = static_cast<int32_t>(z.D);
   a.B = static_cast<int32_t>(z.B);
+  while ((1 << a.log2_B) < z.B) ++a.log2_B;
   a.status = g_dev[dev].status;
   if (pa::launch_read_q4(dt, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
   g_launches.fetch_add(1);

@@ -223,8 +223,11 @@ struct RopeArgs {
   unsigned char *k_cache, *v_cache;
   int64_t num_slots;
   int32_t T, H, Hq, D, B, R, P, interleaved;
+  int32_t log2_B;                 // 4-bit caches
+  int32_t V, at_once, warps_q, warps_k;  // set by the launcher: vectors of a row, rows of a warp, warps of a token's rows
   int32_t* status;
 };
+bool rope_fits(const RopeArgs& a, int elem);  // whether one launch holds that many rows
 cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stream);
 
 struct ReadQ4Args {
@@ -233,7 +236,8 @@ struct ReadQ4Args {
   void *k_out, *v_out;                     // [T, H, D]
   int64_t ko_row, vo_row;
   int64_t num_slots;
-  int32_t T, H, D, B;
+  int32_t T, H, D, B, log2_B;
+  int32_t warps_k;                         // set by the launcher: warps of a token's rows of one cache
   int32_t* status;
 };
 cudaError_t launch_read_q4(int dtype, ReadQ4Args a, cudaStream_t stream);

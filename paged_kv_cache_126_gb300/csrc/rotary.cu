@@ -97,41 +97,50 @@ __device__ __forceinline__ uint4 shfl4(const uint4& u, int lane) {
 // codes for this lane; step and offset of the group, the same in its four lanes.
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* params) {
   constexpr float kTop = 65024.f;  // the top code is at most kTop (1 + 2^-10): finite in fp16
-  bool finite = true;
-  float v[8], lo = INFINITY, hi = -INFINITY;
+  float lo = x[0], hi = x[0], none = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    finite = finite && fabsf(x[i]) < INFINITY;  // false for NaN too
-    v[i] = fminf(fmaxf(x[i], -kTop), kTop);
-    lo = fminf(lo, v[i]);
-    hi = fmaxf(hi, v[i]);
+    none = fmaf(x[i], 0.f, none);  // NaN once an element is not finite
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(kAll, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(kAll, hi, o));
-    finite = __shfl_xor_sync(kAll, static_cast<int>(finite), o) && finite;
+    none += __shfl_xor_sync(kAll, none, o);
   }
+  const bool finite = none == 0.f;
+  // an element beyond +-kTop is coded like +-kTop: as 0 or 15
+  lo = fminf(fmaxf(lo, -kTop), kTop);
+  hi = fminf(fmaxf(hi, -kTop), kTop);
   const __half off = __float2half_rn(lo);
   const float offf = __half2float(off);
   const __half step = __float2half_rn(__fmul_rn(__fsub_rn(hi, offf), 1.0f / 15.0f));
   const float stepf = __half2float(step);
-  // round((x - off) / step) by a product with 1 / step: the product is within 2^-21 * 15 of the quotient, so
-  // where it is further than 2^-15 from a border between two codes both round alike; a lane with a
-  // value nearer than that divides.
+  // round((x - off) / step) by a product with 1 / (15 step), which the multiplier clamps to [0, 1]: five roundings
+  // leave it within 15 * 5 * 2^-24 < 2^-17 of the quotient, so where it is further than 2^-15 from a border
+  // between two codes both round alike; a lane with a value nearer than that divides.
   const bool coded = finite && stepf > 0.f;
-  const float inv = coded ? __frcp_rn(stepf) : 0.f;
+  const float inv = coded ? __fmul_rn(__frcp_rn(stepf), 1.0f / 15.0f) : 0.f;
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded addend
   float half_way = 0.f, n[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(v[i], offf), inv), 0.f), 15.f);
-    n[i] = __fsub_rn(__fadd_rn(q, kRound), kRound);
-    half_way = fmaxf(half_way, fabsf(__fsub_rn(q, n[i])));
+    const float t = __saturatef(__fmul_rn(__fsub_rn(x[i], offf), inv));
+    n[i] = __fsub_rn(fmaf(t, 15.f, kRound), kRound);
+    half_way = fmaxf(half_way, fabsf(fmaf(t, 15.f, -n[i])));
   }
   if (half_way > 0.5f - 0x1p-15f) {
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {  // rare: one division's code, and selects so that x and n stay in registers
+      float v = x[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[i], offf), stepf)), 0.f), 15.f);
+      for (int i = 1; i < 8; ++i) v = i == k ? x[i] : v;
+      v = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v, offf), stepf)), 0.f), 15.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = i == k ? v : n[i];
+    }
   }
   // four codes as one number below 2^16, exact in fp32
   const float a = fmaf(fmaf(fmaf(n[3], 16.f, n[2]), 16.f, n[1]), 16.f, n[0]) + 8388608.f;
@@ -142,21 +151,21 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* par
 }
 
 template <typename T, bool Q4>
-__global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(256, 4) rope_append_kernel(const RopeArgs a) {
   constexpr int N = Vec<T>::N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int V = a.D / N, at_once = 32 / V;
+  const int V = a.V, at_once = a.at_once;
   const int sub = lane / V, vec = lane - sub * V;
   const int rv = a.R / N;           // rotated vectors of a row
   const int per = at_once * kSteps;
-  const int cq = a.q ? (a.Hq + per - 1) / per : 0, ck = (a.H + per - 1) / per;  // warps of a token's queries, keys
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int jobs = cq + 2 * ck;
-  if (job >= static_cast<int64_t>(a.T) * jobs) return;
+  const unsigned job = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const unsigned jobs = a.warps_q + 2 * a.warps_k;  // of a token
+  if (job >= a.T * jobs) return;
   const int t = static_cast<int>(job / jobs);
-  const int part = static_cast<int>(job - static_cast<int64_t>(t) * jobs);
+  const int part = static_cast<int>(job - t * jobs);
+  const int cq = a.warps_q, ck = a.warps_k;
   const bool is_q = part < cq, is_k = !is_q && part < cq + ck;
   const int h0 = (is_q ? part : is_k ? part - cq : part - cq - ck) * per + sub;  // first of this lane's rows
   const int heads = is_q ? a.Hq : a.H;
@@ -189,7 +198,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
   float c[N] = {}, s[N] = {};
   if (rot) {
     const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.cs_row;
-    if (!a.interleaved) {  // (c, s) of this vector's elements; the second half of a pair takes its partner with + s
+    if (!a.interleaved) {  // the first of a pair takes its partner with - sin, the second with + sin
       row += (first ? vec : vec - rv / 2) * N;
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
@@ -197,6 +206,8 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
         c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
         s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = first ? -s[i] : s[i];
     } else {
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
   // the lane that holds the partner vector (half-split pairs)
   const int partner = rot && !a.interleaved ? (first ? lane + rv / 2 : lane - rv / 2) : lane;
 
-  const int64_t frame = slot / a.B;
+  const int64_t frame = Q4 ? slot >> a.log2_B : 0;
   const int W = a.D / 2 + a.D / 8;
   unsigned char* dst;  // of this lane's first row, and its distance to the next
   int64_t dist;
@@ -234,10 +245,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
         Vec<T>::unpack(shfl4(u[i], partner), y);
         if (rot) {
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const float p = __fmul_rn(x[j], c[j]), o = __fmul_rn(y[j], s[j]);
-            x[j] = first ? __fsub_rn(p, o) : __fadd_rn(p, o);
-          }
+          for (int j = 0; j < N; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(y[j], s[j]));
         }
       } else if (rot) {
 #pragma unroll
@@ -292,21 +300,22 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const ReadQ4Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int V = a.D / 8, at_once = 32 / V, sub = lane / V, vec = lane - sub * V;
-  const int W = a.D / 2 + a.D / 8, per = at_once * kSteps, chunks = (a.H + per - 1) / per;
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (job >= static_cast<int64_t>(a.T) * 2 * chunks) return;
+  const int at_once = a.D == 128 ? 2 : 4, sub = a.D == 128 ? lane >> 4 : lane >> 3, vec = a.D == 128 ? lane & 15 : lane & 7;
+  const int W = a.D / 2 + a.D / 8, per = at_once * kSteps;
+  const unsigned chunks = a.warps_k;
+  const unsigned job = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (job >= a.T * 2 * chunks) return;
   const int t = static_cast<int>(job / (2 * chunks));
-  const int part = static_cast<int>(job - static_cast<int64_t>(t) * 2 * chunks);
-  const bool is_v = part >= chunks;
-  const int h0 = (is_v ? part - chunks : part) * per + sub;
+  const int part = static_cast<int>(job - t * 2 * chunks);
+  const bool is_v = part >= static_cast<int>(chunks);
+  const int h0 = (is_v ? part - static_cast<int>(chunks) : part) * per + sub;
   const int32_t slot = a.slots[t];
   if (slot < 0) return;
   if (slot >= a.num_slots) {
     if (lane == 0) atomicOr(a.status, kDevBadSlot);
     return;
   }
-  const int64_t frame = slot / a.B;
+  const int64_t frame = slot >> a.log2_B;
   const unsigned char* src = (is_v ? a.v_cache : a.k_cache) + ((frame * a.H + h0) * a.B + (slot - frame * a.B)) * W;
   uint32_t word[kSteps], params[kSteps];
 #pragma unroll
@@ -348,11 +357,20 @@ cudaError_t launch_pdl(const void* fn, int64_t grid, void** args, cudaStream_t s
 
 }  // namespace
 
+// warps that the rows of a token are split into
+static int64_t warps_of(int64_t heads, int at_once) { return (heads + at_once * kSteps - 1) / (at_once * kSteps); }
+
+bool rope_fits(const RopeArgs& a, int elem) {
+  const int at_once = 32 / (a.D * elem / 16);
+  return a.T * ((a.q ? warps_of(a.Hq, at_once) : 0) + 2 * warps_of(a.H, at_once)) <= INT32_MAX;
+}
+
 cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stream) {
-  const int at_once = 32 / (a.D * (dtype == PA_F32 ? 4 : 2) / 16), per = at_once * kSteps;
-  const int64_t jobs = (a.q ? (a.Hq + per - 1) / per : 0) + 2 * static_cast<int64_t>((a.H + per - 1) / per);
-  const int64_t grid = (a.T * jobs + 7) / 8;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  a.V = a.D * (dtype == PA_F32 ? 4 : 2) / 16;
+  a.at_once = 32 / a.V;
+  a.warps_q = a.q ? static_cast<int>(warps_of(a.Hq, a.at_once)) : 0;
+  a.warps_k = static_cast<int>(warps_of(a.H, a.at_once));
+  const int64_t grid = (static_cast<int64_t>(a.T) * (a.warps_q + 2 * a.warps_k) + 7) / 8;
   void* args[1] = {&a};
   const void* fn = nullptr;
   if (q4)
@@ -366,9 +384,8 @@ cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stre
 }
 
 cudaError_t launch_read_q4(int dtype, ReadQ4Args a, cudaStream_t stream) {
-  const int per = 32 / (a.D / 8) * kSteps;
-  const int64_t grid = (static_cast<int64_t>(a.T) * 2 * ((a.H + per - 1) / per) + 7) / 8;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  a.warps_k = static_cast<int>(warps_of(a.H, 32 / (a.D / 8)));
+  const int64_t grid = (static_cast<int64_t>(a.T) * 2 * a.warps_k + 7) / 8;
   void* args[1] = {&a};
   const void* fn = dtype == PA_F16 ? reinterpret_cast<const void*>(&read_q4_kernel<__half>)
                                    : reinterpret_cast<const void*>(&read_q4_kernel<__nv_bfloat16>);

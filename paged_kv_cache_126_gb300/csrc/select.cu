@@ -175,7 +175,7 @@ __device__ __forceinline__ bool scored(const SelectArgs& a, int blocks) { return
 constexpr int kScoreWarps = 4;
 
 template <typename T, int D, int kQueries>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries == 2 ? 4 : 3) score_kernel(const SelectArgs a) {
   constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 4, kUnit = kRows * kAhead;
   __shared__ float4 q_parts[kScoreWarps][kQueries][4][kRowLanes];  // positive part (two vectors a lane), negative part
   pdl_begin();
