@@ -18,7 +18,7 @@ cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorM
   if (a.g <= 4 && !one)
     return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwinColumns, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
   if (a.g <= 8) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 2, 4, 2>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

@@ -50,10 +50,11 @@ struct RowFormat {
     x.slot[1] = p.frame[1] >= 0 ? p.frame[1] * a.B + p.row + (a.B >= 16 ? 8 : 0) : -1;
     return x;
   }
+  __device__ __forceinline__ static int issuer(int part) { return part; }
   __device__ __forceinline__ static void load(const GatherArgs&, const CUtensorMap* map, const Place& x, int h, int lane,
-                                              int part, uint32_t dst, uint32_t bar) {
+                                              int part, uint32_t dst, uint32_t bar, uint32_t more) {
     if (lane != part) return;
-    dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * kHalfTile);
+    dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * kHalfTile + more);
     if (x.slot[0] >= 0) tma_load_4d(dst, map, 0, x.slot[0], 0, h, bar);
     if (x.slot[1] >= 0) tma_load_4d(dst + kHalfTile, map, 0, x.slot[1], 0, h, bar);
   }
@@ -62,7 +63,7 @@ struct RowFormat {
   __device__ __forceinline__ static void read_q(const T* q, int c, bool on, float (&x)[D / 4]) {
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-      const float2 y = unpack2<T>(on ? __ldg(reinterpret_cast<const uint32_t*>(q + 8 * i + 2 * c)) : 0u);
+      const float2 y = unpack2<T>(on ? *reinterpret_cast<const uint32_t*>(q + 8 * i + 2 * c) : 0u);
       x[2 * i] = y.x;
       x[2 * i + 1] = y.y;
     }
@@ -137,9 +138,9 @@ cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorM
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 3, 4, 2>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 3, 4, 2>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, gk::kTwoParts, true, 3, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, true, 2, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, true, 2, 4, 2>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, true, 2, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

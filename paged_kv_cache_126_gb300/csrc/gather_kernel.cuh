@@ -105,6 +105,11 @@ __device__ __forceinline__ uint32_t lds(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr));
   return w;
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 // four rows of a two-dimensional tensor, one after the other
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int r0, int r1, int r2, int r3, uint32_t bar) {
   asm volatile(
@@ -277,21 +282,23 @@ struct Q4Format {
       x.row[i] = p.frame[i] >= 0 ? static_cast<int>((static_cast<int64_t>(p.frame[i]) * a.H + h) << per) + (p.row >> 4) : 0;
     return x;
   }
-  // All lanes: the keys (or values) of a tile whose parts were planned by lanes part .. part + kLoads - 1.
+  // All lanes: the keys (or values) of a tile whose parts were planned by lanes part .. part + kLoads - 1.  The barrier
+  // expects `more` bytes besides; lane issuer(part) is the one that arrives.
+  __device__ __forceinline__ static int issuer(int) { return 0; }
   __device__ __forceinline__ static void load(const GatherArgs& a, const CUtensorMap* map, const Place& x, int, int lane,
-                                              int part, uint32_t dst, uint32_t bar) {
+                                              int part, uint32_t dst, uint32_t bar, uint32_t more) {
     const int r0 = __shfl_sync(kAll, x.row[0], part), r1 = __shfl_sync(kAll, x.row[0], part + 1);
     const int r2 = __shfl_sync(kAll, x.row[0], part + 2), r3 = __shfl_sync(kAll, x.row[0], part + 3);
     if (a.B >= 16) {
       if (lane == 0) {
-        dk::mbar_arrive_expect_tx(bar, kLoads * kTile);
+        dk::mbar_arrive_expect_tx(bar, kLoads * kTile + more);
         tma_gather4(dst, map, r0, r1, r2, r3, bar);
       }
     } else {
       const int s0 = __shfl_sync(kAll, x.row[1], part), s1 = __shfl_sync(kAll, x.row[1], part + 1);
       const int s2 = __shfl_sync(kAll, x.row[1], part + 2), s3 = __shfl_sync(kAll, x.row[1], part + 3);
       if (lane == 0) {
-        dk::mbar_arrive_expect_tx(bar, kLoads * kTile);
+        dk::mbar_arrive_expect_tx(bar, kLoads * kTile + more);
         tma_gather4(dst, map, r0, s0, r1, s1, bar);
         tma_gather4(dst + 2 * kTile, map, r2, s2, r3, s3, bar);
       }
@@ -314,7 +321,7 @@ struct Q4Format {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (on) u = __ldg(reinterpret_cast<const uint4*>(q + c * (D / 4)) + i);
+      if (on) u = reinterpret_cast<const uint4*>(q + c * (D / 4))[i];
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -503,9 +510,13 @@ __device__ __forceinline__ int arrivals_of(const Left& x, int w) {
   return x.w1 - x.w0 < kFlat ? x.w1 - x.w0 + 1 : min(x.w1, (g + 1) * kGroup - 1) - max(x.w0, g * kGroup) + 1;
 }
 
-template <class F, int STAGES>
+template <class F, int NT>
+__host__ __device__ constexpr uint32_t stage_bytes() {  // a tile's keys, its values, and the queries of a (s, h) that begins with it
+  return 2 * F::kLoads * F::kTile + 8 * NT * F::D * sizeof(typename F::In);
+}
+template <class F, int NT, int STAGES>
 __host__ __device__ constexpr uint32_t warp_smem() {
-  return STAGES * F::kLoads * 2 * F::kTile + STAGES * 32;  // stages, then metas (4 bytes a part) and two mbarriers each
+  return STAGES * (stage_bytes<F, NT>() + 32);  // stages, then metas (4 bytes a part) and two mbarriers each
 }
 
 template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
@@ -521,11 +532,11 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int LOADS = F::kLoads;
   static_assert(LOADS <= 4, "a stage's metas are 16 bytes");
-  constexpr uint32_t kKeys = LOADS * F::kTile, kStage = 2 * kKeys;  // the tile's keys, then its values
+  constexpr uint32_t kKeys = LOADS * F::kTile, kStage = stage_bytes<F, NT>();
   const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * kStage);
   const uint32_t metas = dk::smem_u32(smem) + WARPS * (STAGES * kStage) + warp * STAGES * 32;  // [stage][4]
   const uint32_t bars = metas + STAGES * 16;  // [stage][2]: keys, values
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + WARPS * warp_smem<F, STAGES>());
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + WARPS * warp_smem<F, NT, STAGES>());
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
     for (int i = 0; i < 2 * STAGES; ++i) dk::mbar_init(bars + 8 * i, 1);
@@ -593,10 +604,16 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     const int sub = lane - (part & 31);
     if (static_cast<unsigned>(sub) < LOADS)
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 16 + sub * 4), "r"(plan_meta) : "memory");
-    F::load(a, &maps.k, place, ahead.h, lane, part & 31, stages + issue_st * kStage, bars + 16 * issue_st);
+    // the first tile of a (s, h), or of this warp's part of it, brings the queries along
+    const uint32_t dst = stages + issue_st * kStage, bar = bars + 16 * issue_st;
+    const bool first = ahead.t == 0 || issued == 0;
+    const uint32_t q_bytes = a.g * D * sizeof(T);
+    F::load(a, &maps.k, place, ahead.h, lane, part & 31, dst, bar, first ? q_bytes : 0);
+    if (first && lane == F::issuer(part & 31))
+      bulk_load(dst + 2 * kKeys, static_cast<const T*>(a.q) + ahead.s * a.q_row + static_cast<int64_t>(ahead.h) * a.g * D, q_bytes, bar);
   };
   auto issue_values = [&]() {  // of the same tile, and on to the next
-    F::load(a, &maps.v, place, ahead.h, lane, (ahead.t * LOADS) & 31, stages + issue_st * kStage + kKeys, bars + 16 * issue_st + 8);
+    F::load(a, &maps.v, place, ahead.h, lane, (ahead.t * LOADS) & 31, stages + issue_st * kStage + kKeys, bars + 16 * issue_st + 8, 0);
     if (++issue_st == STAGES) issue_st = 0;
     ++issued;
     if (++ahead.t == ahead.tiles && issued < count) {
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
-  Left(*left)[2] = reinterpret_cast<Left(*)[2]>(smem + WARPS * warp_smem<F, STAGES>() + 16);  // side 0: begun before
+  Left(*left)[2] = reinterpret_cast<Left(*)[2]>(smem + WARPS * warp_smem<F, NT, STAGES>() + 16);  // side 0: begun before
   if (lane < 2) left[warp][lane].state = 0;
   __syncwarp();
   bool stuck = false;
@@ -638,10 +655,15 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
     const int first_t = cur.t;
     bool poison = false;
+    if (!__all_sync(kAll, dk::mbar_wait(bars + 16 * st, phase, abort_flag, a.status))) {
+      drain(i, false);
+      stuck = true;
+      break;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = PARTS == kTwinColumns ? (r & 3) : 8 * n + r;
-      const T* q = static_cast<const T*>(a.q) + cur.s * a.q_row + (static_cast<int64_t>(cur.h) * a.g + col) * D;
+      const T* q = reinterpret_cast<const T*>(smem + warp * (STAGES * kStage) + st * kStage + 2 * kKeys) + col * D;
       float x[D / 4], top = 0.f;
       F::read_q(q, c, col < a.g, x);
 #pragma unroll
@@ -882,7 +904,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
 cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
   const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>);
-  constexpr uint32_t smem = WARPS * (warp_smem<F, STAGES>() + 2 * sizeof(Left)) + 16;  // + the abort flag
+  constexpr uint32_t smem = WARPS * (warp_smem<F, NT, STAGES>() + 2 * sizeof(Left)) + 16;  // + the abort flag
   int occ = 0;
   cudaError_t e = kernel_prep(fn, WARPS * 32, smem, &occ);
   if (e != cudaSuccess) return e;
