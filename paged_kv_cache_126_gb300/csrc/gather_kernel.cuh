@@ -40,7 +40,7 @@ namespace pa {
 namespace gk {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kMinKeys = 64;     // fewest keys a warp is given
+constexpr int kMinKeys = 64;     // fewest keys that a (s, h) is cut into
 constexpr int kGroup = 16;       // pieces of one (s, h) are joined in groups of this many workers
 constexpr int kFlat = 24;        // where there are fewer pieces than this they are joined at once
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
@@ -555,7 +555,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   total *= a.H;
   constexpr int kMinTiles = kMinKeys / (16 * LOADS);
   const int64_t all_warps = static_cast<int64_t>(gridDim.x) * WARPS;
-  const int64_t workers = min(all_warps, (total + kMinTiles - 1) / kMinTiles);
+  const int64_t pairs = static_cast<int64_t>(a.S) * a.H;
+  int64_t workers = min(all_warps, max(pairs, (total + kMinTiles - 1) / kMinTiles));
+  // a multiple of the (s, h) where that leaves few warps idle: sequences of one length are then cut at their ends
+  if (workers / pairs * pairs * 10 >= workers * 9) workers = workers / pairs * pairs;
   const int64_t id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
   if (blockIdx.x >= workers) return;
   const int64_t b0 = min(id, workers) * total / workers, b1 = min(id + 1, workers) * total / workers;

@@ -6,7 +6,8 @@
 // The bounds and the scores read memory once and compute little: both give consecutive ranges
 // of their (sequence, frame, head) units to resident warps, found from the lengths on the
 // device, and keep several 16-byte loads a lane in flight.  The selection holds a list's
-// ranks in registers and finds the K-th by counting, two bits of it at a time.
+// ranks in registers, finds the K-th's neighbourhood with one histogram over the scores' range, and
+// orders the few that share its bin.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -305,14 +306,55 @@ __device__ __forceinline__ uint32_t rank_of(const SelectArgs& a, float score, in
   return max(u & 0x80000000u ? ~u : u | 0x80000000u, 1u);  // 0 is no frame's, not even one with a NaN score
 }
 
+__device__ __forceinline__ float score_of(uint32_t rank) {
+  return __uint_as_float(rank & 0x80000000u ? rank & 0x7fffffffu : ~rank);
+}
+
+// Sum over the block of a value per thread before this one, and over all threads (64-bit: two counts side by side).
+template <int kWarpsOf>
+__device__ __forceinline__ uint64_t block_before(uint64_t own, uint64_t* total, uint64_t (&sums)[kWarpsOf]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kAll, upto, o);
+    if (lane >= o) upto += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  uint64_t all = lane < kWarpsOf ? sums[lane] : 0, before = 0;
+#pragma unroll
+  for (int o = 1; o < kWarpsOf; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kAll, all, o);
+    if (lane >= o) all += y;
+  }
+  before = __shfl_sync(kAll, all, (warp + 31) & 31);
+  *total = __shfl_sync(kAll, all, kWarpsOf - 1);
+  return upto - own + (warp ? before : 0);
+}
+
 // One block per (sequence, head).  Thread t holds the ranks of frames t * R .. t * R + R - 1 in registers, so
 // that thread order is frame order; lists longer than kThreads * R frames (LONG) are read again for each
-// count.  The K-th largest rank is found from its top bits down: the largest T such that at least K
-// ranks are >= T, two bits a step, three counts packed into one sum.
+// count.
+//
+// The kept frames are above all others.  The scores of the rest are put into bins, four a thread, that split their
+// range evenly (a subtraction and a product, both monotonic, so a higher bin holds higher scores only); the
+// bin with the last place is found by a scan from the top, all above it are taken, and the
+// scores in it, a handful, are ordered by comparing each with each.  Where that does not hold (scores that are
+// not finite or all the same, more than kTies of them in the bin, more kept frames than places, LONG), the
+// K-th largest rank is found from its top bits down instead: the largest T such that at least K ranks
+// are >= T, two bits a step, three counts packed into one sum.  That alone took 15 us for 256 lists of up
+// to 2048 frames, all of it counting.
 template <int kThreads, int R, bool LONG>
 __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
-  constexpr int kWarpsOf = kThreads / 32;
+  constexpr int kWarpsOf = kThreads / 32, kBins = 4 * kThreads, kTies = kThreads;
   __shared__ uint64_t sums[2][kWarpsOf];
+  __shared__ int4 bins[LONG ? 1 : kThreads];     // bin b at word kBins - 1 - b: a thread's four from the top down
+  __shared__ uint2 tied[LONG ? 1 : kTies];       // (rank, frame) of the bin with the last place
+  __shared__ uint8_t tied_in[LONG ? 1 : kTies];  // whether it is taken
+  __shared__ int edge_bin, edge_need, n_tied;
+  __shared__ uint32_t least[kWarpsOf], most[kWarpsOf];
   pdl_begin();
   const int h = blockIdx.x % a.H, s = blockIdx.x / a.H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -330,11 +372,100 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
   const float* scores = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks;
   const int mine = LONG ? (blocks + kThreads - 1) / kThreads : R;  // frames of a thread
   const int j0 = threadIdx.x * mine;
+  constexpr uint32_t kKept = 0xffffffffu;
   uint32_t held[R];
-  if (!LONG) {
+  if constexpr (!LONG) {
 #pragma unroll
     for (int i = 0; i < R; ++i) held[i] = j0 + i < blocks ? rank_of(a, scores[j0 + i], j0 + i, blocks) : 0;
+    // ---- one histogram ----
+    uint32_t lo = kKept, hi = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (held[i] != 0 && held[i] != kKept) {
+        lo = min(lo, held[i]);
+        hi = max(hi, held[i]);
+      }
+    lo = __reduce_min_sync(kAll, lo);
+    hi = __reduce_max_sync(kAll, hi);
+    if (lane == 0) {
+      least[warp] = lo;
+      most[warp] = hi;
+    }
+    bins[threadIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) n_tied = 0;
+    __syncthreads();
+    lo = __reduce_min_sync(kAll, lane < kWarpsOf ? least[lane] : kKept);
+    hi = __reduce_max_sync(kAll, lane < kWarpsOf ? most[lane] : 0);
+    const float low = score_of(lo), span = score_of(hi) - low;
+    const int kept = min(a.keep_first, blocks) + max(0, min(a.keep_last, blocks - a.keep_first));
+    const int places = a.K - kept;  // for the others
+    const float scale = kBins / span;
+    if (lo < hi && span < INFINITY && scale < INFINITY && places > 0) {  // not so for NaN
+      int* words = reinterpret_cast<int*>(bins);
+      int word[R];  // of each frame's bin; -1: taken in any case, kBins: no frame
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        word[i] = held[i] == 0 ? kBins : held[i] == kKept ? -1 : max(0, kBins - 1 - static_cast<int>((score_of(held[i]) - low) * scale));
+        if (word[i] >= 0 && word[i] < kBins) atomicAdd(words + word[i], 1);
+      }
+      __syncthreads();
+      const int4 c = bins[threadIdx.x];
+      uint64_t all;
+      int left = places - static_cast<int>(block_before<kWarpsOf>(c.x + c.y + c.z + c.w, &all, sums[0]));
+      if (left > 0 && left <= c.x + c.y + c.z + c.w) {
+        int i = 0;
+        if (c.x < left) left -= c.x, ++i;
+        if (i == 1 && c.y < left) left -= c.y, ++i;
+        if (i == 2 && c.z < left) left -= c.z, ++i;
+        edge_bin = 4 * static_cast<int>(threadIdx.x) + i;
+        edge_need = left;
+      }
+      __syncthreads();
+      const int edge = edge_bin, need = edge_need;
+      uint32_t take = 0;
+      uint32_t slot = 0;  // which of this thread's frames are in the edge's bin, and where in `tied` they are
+      int first_slot = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        take |= static_cast<uint32_t>(word[i] < edge) << i;
+        slot |= static_cast<uint32_t>(word[i] == edge) << i;
+      }
+      if (slot) {
+        first_slot = atomicAdd(&n_tied, __popc(slot));
+        int at = first_slot;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (slot >> i & 1) {
+            if (at < kTies) tied[at] = make_uint2(held[i], j0 + i);
+            ++at;
+          }
+      }
+      __syncthreads();
+      const int ties = n_tied;
+      if (ties <= kTies) {
+        if (static_cast<int>(threadIdx.x) < ties) {
+          const uint2 own = tied[threadIdx.x];
+          int above = 0;
+          for (int k = 0; k < ties; ++k) {
+            const uint2 x = tied[k];
+            above += x.x > own.x || (x.x == own.x && x.y < own.y);
+          }
+          tied_in[threadIdx.x] = above < need;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (slot >> i & 1) take |= static_cast<uint32_t>(tied_in[first_slot++]) << i;
+        uint64_t total;
+        int at = static_cast<int>(block_before<kWarpsOf>(__popc(take), &total, sums[1]));
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (take >> i & 1) sel[at++] = j0 + i;
+        return;
+      }
+    }
   }
+  // ---- bit by bit ----
   // calls f(rank, position) for each of this thread's frames; ranks of frames are above 0
   auto each = [&](auto f) {
     if (LONG) {
@@ -345,6 +476,7 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
     }
   };
   uint32_t T = 0;
+  __syncthreads();
   for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
     const uint32_t step = 1u << shift;
     uint32_t c1 = 0, c2 = 0, c3 = 0;
@@ -356,19 +488,16 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
     c1 = __reduce_add_sync(kAll, c1);
     c2 = __reduce_add_sync(kAll, c2);
     c3 = __reduce_add_sync(kAll, c3);
-    if (kWarpsOf > 1) {
-      // 21 bits a count: tables have at most 2^20 columns
-      if (lane == 0) sums[turn][warp] = c1 | static_cast<uint64_t>(c2) << 21 | static_cast<uint64_t>(c3) << 42;
-      __syncthreads();
-      const uint64_t w = lane < kWarpsOf ? sums[turn][lane] : 0;
-      c1 = __reduce_add_sync(kAll, static_cast<uint32_t>(w) & 0x1fffff);
-      c2 = __reduce_add_sync(kAll, static_cast<uint32_t>(w >> 21) & 0x1fffff);
-      c3 = __reduce_add_sync(kAll, static_cast<uint32_t>(w >> 42));
-    }
-    const uint32_t K = a.K;
-    const uint32_t most = c3 >= K ? c3 : c2 >= K ? c2 : c1 >= K ? c1 : 0;
+    // 21 bits a count: tables have at most 2^20 columns
+    if (lane == 0) sums[turn][warp] = c1 | static_cast<uint64_t>(c2) << 21 | static_cast<uint64_t>(c3) << 42;
+    __syncthreads();
+    const uint64_t w = lane < kWarpsOf ? sums[turn][lane] : 0;
+    c1 = __reduce_add_sync(kAll, static_cast<uint32_t>(w) & 0x1fffff);
+    c2 = __reduce_add_sync(kAll, static_cast<uint32_t>(w >> 21) & 0x1fffff);
+    c3 = __reduce_add_sync(kAll, static_cast<uint32_t>(w >> 42));
+    const uint32_t K = a.K, hits = c3 >= K ? c3 : c2 >= K ? c2 : c1 >= K ? c1 : 0;
     T += c3 >= K ? 3 * step : c2 >= K ? 2 * step : c1 >= K ? step : 0;
-    if (most == K) {  // exactly K ranks from T on: they are the ranks above T - 1, whatever its other digits
+    if (hits == K) {  // exactly K ranks from T on: they are the ranks above T - 1, whatever its other digits
       --T;
       break;
     }
@@ -379,24 +508,8 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
     above += r > T;
     equal += r == T;
   });
-  uint64_t upto = above | static_cast<uint64_t>(equal) << 32;
-  const uint64_t own = upto;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(kAll, upto, o);
-    if (lane >= o) upto += y;
-  }
-  uint64_t before = upto - own, total = __shfl_sync(kAll, upto, 31);
-  if (kWarpsOf > 1) {
-    __syncthreads();
-    if (lane == 31) sums[0][warp] = upto;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < kWarpsOf; ++w) {
-      if (w < warp) before += sums[0][w];
-      total += sums[0][w];
-    }
-  }
+  uint64_t total;
+  const uint64_t before = block_before<kWarpsOf>(above | static_cast<uint64_t>(equal) << 32, &total, sums[0]);
   const uint32_t need = a.K - static_cast<uint32_t>(total);
   uint32_t a0 = static_cast<uint32_t>(before), e0 = static_cast<uint32_t>(before >> 32);
   each([&](uint32_t r, int j) {
@@ -465,6 +578,7 @@ cudaError_t launch_select_blocks(int dtype, SelectArgs a, int num_sms, cudaStrea
   const int64_t lists = static_cast<int64_t>(a.S) * a.H;
   ++*launched;
   if (n <= 1024) return launch_pdl(ptr(top_kernel<128, 8, false>), lists, 128, args, stream);
+  if (n <= 2048) return launch_pdl(ptr(top_kernel<256, 8, false>), lists, 256, args, stream);
   if (n <= 4096) return launch_pdl(ptr(top_kernel<512, 8, false>), lists, 512, args, stream);
   if (n <= 16384) return launch_pdl(ptr(top_kernel<1024, 16, false>), lists, 1024, args, stream);
   return launch_pdl(ptr(top_kernel<1024, 16, true>), lists, 1024, args, stream);
