@@ -176,7 +176,7 @@ __device__ __forceinline__ bool scored(const SelectArgs& a, int blocks) { return
 constexpr int kScoreWarps = 4;
 
 template <typename T, int D, int kQueries>
-__global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries == 2 ? 4 : 3) score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries == 2 ? 3 : 2) score_kernel(const SelectArgs a) {
   constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 4, kUnit = kRows * kAhead;
   __shared__ float4 q_parts[kScoreWarps][kQueries][4][kRowLanes];  // positive part (two vectors a lane), negative part
   pdl_begin();
@@ -199,11 +199,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries
   int h = static_cast<int>(rest / units), unit = static_cast<int>(rest % units);
   int blocks = (a.context_lens[s] + a.B - 1) / a.B;
   float4 (*qs)[4][kRowLanes] = q_parts[threadIdx.x >> 5];
-  auto load_q = [&](int g0) {
+  auto load_q_of = [&](const T* base, int g0) {  // base: the head's first query
     __syncwarp();
     for (int g = sub; g < kQueries; g += kRows) {
       // a query behind the group's last is its last again: the largest score stays
-      const T* q = static_cast<const T*>(a.q) + s * a.q_row + (static_cast<int64_t>(h) * a.g + min(g0 + g, a.g - 1)) * D;
+      const T* q = base + min(g0 + g, a.g - 1) * D;
       float f[8];
       unpack8<T>(__ldg(reinterpret_cast<const uint4*>(q) + vec), f);
 #pragma unroll
@@ -214,10 +214,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries
     }
     __syncwarp();
   };
+  auto load_q = [&](int g0) { load_q_of(static_cast<const T*>(a.q) + s * a.q_row + static_cast<int64_t>(h) * a.g * D, g0); };
   bool fresh = true;
   int known = -1;   // which 32 positions `frame` is of
   int frame = -1;
-  for (int64_t x = x0; x < x1; ++x) {
+  uint4 lo[kAhead], hi[kAhead];
+  uint32_t good;    // whether each frame of the unit has a good id
+  auto load = [&]() {
     const int j0 = unit * kUnit;
     if (fresh || (j0 >> 5) != known) {
       known = j0 >> 5;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries
         }
       }
     }
-    uint4 lo[kAhead], hi[kAhead];
+    good = __ballot_sync(kAll, frame >= 0) >> (j0 & 31);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int j = j0 + i * kRows + sub;
@@ -243,17 +246,39 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries
         hi[i] = __ldg(b + kRowLanes);
       }
     }
+  };
+  load();
+  for (int64_t x = x0; x < x1; ++x) {
     if (fresh && a.g <= kQueries) load_q(0);
+    // this unit's numbers, and the next one's on their way while they are used
+    const int j0 = unit * kUnit, its_blocks = blocks;
+    const uint32_t its_good = good;
+    float* out = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks;
+    const T* its_q = static_cast<const T*>(a.q) + s * a.q_row + static_cast<int64_t>(h) * a.g * D;
+    uint4 l[kAhead], u[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) l[i] = lo[i], u[i] = hi[i];
     fresh = false;
+    if (++unit == units) {
+      unit = 0;
+      fresh = true;
+      if (++h == a.H && x + 1 < x1) {
+        h = 0;
+        do units = count(++s);
+        while (units == 0);
+        blocks = (a.context_lens[s] + a.B - 1) / a.B;
+      }
+    }
+    if (x + 1 < x1) load();
     float best = -INFINITY;
     for (int g0 = 0; g0 < a.g; g0 += kQueries) {
-      if (a.g > kQueries) load_q(g0);
+      if (a.g > kQueries) load_q_of(its_q, g0);
       float y[kQueries][kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         float l8[8], h8[8];
-        unpack8<T>(lo[i], l8);
-        unpack8<T>(hi[i], h8);
+        unpack8<T>(l[i], l8);
+        unpack8<T>(u[i], h8);
 #pragma unroll
         for (int g = 0; g < kQueries; ++g) {
           float z[2];
@@ -281,19 +306,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 5 : kQueries
       }
     }
     const int at = j0 + (lane & 3) * kRows + sub;  // frame (b1, b0) = step 2 b1 + b0
-    const int its = __shfl_sync(kAll, frame, at & 31);
-    if ((vec & ~3) == 0 && at < blocks)
-      a.scores[(static_cast<int64_t>(s) * a.H + h) * a.max_blocks + at] = its < 0 ? -INFINITY : best;
-    if (++unit == units) {
-      unit = 0;
-      fresh = true;
-      if (++h == a.H && x + 1 < x1) {
-        h = 0;
-        do units = count(++s);
-        while (units == 0);
-        blocks = (a.context_lens[s] + a.B - 1) / a.B;
-      }
-    }
+    if ((vec & ~3) == 0 && at < its_blocks) out[at] = its_good >> (at - j0) & 1 ? best : -INFINITY;
   }
 }
 
