@@ -131,6 +131,47 @@ def test_selection_long_context(pa):
     assert np.array_equal(sel.cpu().numpy(), selection_reference(q, b, tables, lens, 8, 100, 1, 1))
 
 
+@pytest.mark.parametrize("L,K", [(15000, 33), (30000, 700), (90000, 5), (160000, 64), (160000, 1)])
+def test_selection_list_sizes(pa, L, K):
+    """Lists for each number of threads, and one longer than the registers hold."""
+    q, kc, vc, tables, lens = make([L, 400], 1, 2, 64, 8, "f16", K, poison=False)
+    b = with_bounds(pa, q, kc, tables, lens)
+    sel = torch.empty(2, 1, K, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(q, b, tables, lens, 8, sel, keep_first=1, keep_last=0)
+    assert np.array_equal(sel.cpu().numpy(), selection_reference(q, b, tables, lens, 8, K, 1, 0))
+
+
+def test_selection_scores_that_crowd(pa):
+    """Nearly all scores in one corner of their range, many of them equal, and the last place among those."""
+    q, kc, vc, tables, lens = make([8 * 1000], 1, 1, 64, 8, "bf16", 3, poison=False)
+    b = torch.zeros(kc.shape[0], 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q.fill_(1.0)
+    f = tables[0].long()
+    b[f, 0, 1, 0] = (torch.arange(1000, device="cuda") % 5).to(torch.bfloat16) * 2.0 ** -20
+    b[f[17], 0, 1, 0] = 1e30
+    b[f[23], 0, 1, 0] = -1e30
+    for K in (1, 2, 150, 201, 202, 400, 999):
+        sel = torch.empty(1, 1, K, dtype=torch.int32, device="cuda")
+        pa.pa_select_blocks(q, b, tables, lens, 8, sel, keep_first=0, keep_last=0)
+        assert np.array_equal(sel.cpu().numpy(), selection_reference(q, b, tables, lens, 8, K, 0, 0)), K
+
+
+def test_selection_nan_scores_stay_inside(pa):
+    """Non-finite scores rank somewhere: the list still holds distinct frames of the sequence."""
+    q, kc, vc, tables, lens = make([8 * 500, 8 * 90], 2, 2, 64, 8, "f16", 4, poison=False)
+    b = with_bounds(pa, q, kc, tables, lens)
+    b[tables[0, ::3].long()] = float("nan")
+    b[tables[0, 1::3].long()] = float("inf")
+    b[tables[1, :90].long()] = float("nan")
+    sel = torch.full((2, 2, 40), -9, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(q, b, tables, lens, 8, sel)
+    assert pa.pa_get_device_status() == 0
+    for s, n in enumerate((500, 90)):
+        for h in range(2):
+            x = sel[s, h].tolist()
+            assert x == sorted(set(x)) and 0 <= x[0] and x[-1] < n and x[0] == 0 and x[-1] == n - 1
+
+
 def test_selection_bad_indexes(pa):
     q, kc, vc, tables, lens = make([320, 320, 320], 2, 2, 64, 16, "f16", 7)
     b = with_bounds(pa, q, kc, tables, lens)
@@ -208,6 +249,16 @@ def test_selected_decode_any_order(pa, dtype):
         sel[2, 1, 4:] = 0                                   # behind the end: not read
         sel[3, :, 0] = n[3] - 1
         check_selected(pa, case, sel.cuda(), 0.09, dtype)
+
+
+@pytest.mark.parametrize("g", [1, 4, 16])
+def test_selected_decode_long_lists(pa, g):
+    """Lists cut into many pieces (joined in groups) beside short ones."""
+    case = make([64 * 500, 64 * 3, 0], 1, g, 64, 64, "bf16", g)
+    sel = torch.full((3, 1, 500), -1, dtype=torch.int32)
+    sel[0, 0] = torch.randperm(500, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    sel[1, 0, :2] = torch.tensor([2, 0])
+    check_selected(pa, case, sel.cuda(), 0.125, "bf16")
 
 
 def test_every_frame_selected_is_pa_decode(pa):
