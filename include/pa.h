@@ -367,7 +367,8 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
  * softmax in fp32, the weights carried as two fp16 parts for fp16 outputs (for bf16
  * outputs one part where g > 4), one rounding to the output dtype.  bf16 queries are
  * scaled by a power of two per head to fp16 range; an element below 2^-14 of its head's
- * largest loses bits of weight below 2^-25 of that largest.
+ * largest loses bits of weight below 2^-25 of that largest.  PA_ERR_UNSUPPORTED where
+ * S * H * ceil(max_blocks * B / 64) passes int32.
  */
 int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
                  const pa_tensor* block_tables, const pa_tensor* context_lens, float scale,
@@ -429,6 +430,7 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
  *                 twice counts twice.  An entry outside [0, ceil(L_s/B)) sets
  *                 PA_DEV_BAD_BLOCK and zeroes the output rows of that head.
  * Lists without a frame give zero rows.  Slots that hold no token may hold any bits.
+ * PA_ERR_UNSUPPORTED where S * H * min(K, max_blocks) * max(B / 16, 1) passes int32.
  * Arithmetic as for pa_decode_q4, the weights carried as two parts of the cache dtype.
  */
 int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,

@@ -228,7 +228,8 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
     // an allocation would end the capture with an error
     if (cap != cudaStreamCaptureStatusNone) return PA_ERR_SCRATCH_LIMIT;
     if (w.ptr && w.cnt_bytes < cnt) cnt = std::max(cnt, 2 * w.cnt_bytes);
-    const size_t bytes = std::max(std::max(kSchedBytes + cnt + rest_bytes, static_cast<size_t>(1) << 20), 2 * w.bytes);
+    // whole 2 MB pages: what a process that watches its free memory sees of it
+    const size_t bytes = std::max(std::max(kSchedBytes + cnt + rest_bytes, static_cast<size_t>(2) << 20), 2 * w.bytes);
     try {
       g_ws_old.reserve(g_ws_old.size() + 1);
     } catch (...) {
@@ -1582,6 +1583,11 @@ int gather_args(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v
   return PA_OK;
 }
 
+// Tiles are numbered in int32 over the whole batch.
+bool tiles_fit(const pa::GatherArgs& a, int64_t most_of_one) {
+  return static_cast<int64_t>(a.S) * a.H * std::max<int64_t>(most_of_one, 1) <= INT32_MAX;
+}
+
 // Workspace of a gathered decode on `workers` warps: an arrival counter per (sequence, head) and two per group
 // of 16 workers, and as many partials as workers and groups have sides.
 int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, pa::GatherArgs* a) {
@@ -1642,6 +1648,7 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
   pa::GatherArgs a;
   PA_TRY(gather_args(q, k_cache, v_cache, block_tables, context_lens, out, scale, z.nb, z.H, z.B, z.D, &a));
   if (a.S == 0) return PA_OK;
+  if (!tiles_fit(a, (static_cast<int64_t>(a.max_blocks) * a.B + 63) / 64)) return PA_ERR_UNSUPPORTED;
   int dev;
   PA_TRY(current_device(&dev));
   a.status = g_dev[dev].status;
@@ -1680,6 +1687,7 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
   a.sel_seq = selected->stride[0];
   a.sel_head = selected->stride[1];
   a.K = static_cast<int32_t>(selected->shape[2]);
+  if (!tiles_fit(a, std::min<int64_t>(a.K, a.max_blocks) * std::max<int64_t>(B / 16, 1))) return PA_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   PA_TRY(make_rows8_map(&tk, k_cache->data, q->dtype, nb * B, H, D));
   PA_TRY(make_rows8_map(&tv, v_cache->data, q->dtype, nb * B, H, D));

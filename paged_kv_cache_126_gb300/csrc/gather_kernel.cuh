@@ -222,6 +222,19 @@ __device__ __forceinline__ TilePlan plan_tiles(const GatherArgs& a, const Cursor
   return p;
 }
 
+// How a batch's tiles are cut: worker w has the tiles floor(w total / workers) .. floor((w + 1) total / workers) - 1.
+struct Cut {
+  int total, workers, per, rest;  // total = per * workers + rest; workers^2 < 2^31
+  __device__ __forceinline__ int start(int w) const { return w * per + static_cast<int>(static_cast<unsigned>(w * rest) / workers); }
+  // the worker of tile x: a division in fp32 is off by at most one
+  __device__ __forceinline__ int owner(int x) const {
+    int w = min(workers - 1, static_cast<int>((x + 0.5f) * (static_cast<float>(workers) / total)));
+    if (start(w) > x) --w;
+    if (w + 1 < workers && start(w + 1) <= x) ++w;
+    return w;
+  }
+};
+
 // ---- formats: how a tile is loaded and multiplied ------------------------------------------------
 // 4-bit rows of D / 2 bytes of codes and D / 8 bytes of (step, offset) pairs.  A code n is made fp16 by
 // putting it into the mantissa of 1024 (low bits) or 64 (bits 4..7): 1024 + n and 64 + n are exact, so is
@@ -546,27 +559,33 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // this warp's range [b0, b1) of the batch's tiles
-  int64_t total = 0;
+  int total = 0;
   int n = 0;  // tiles of sequence s0 + lane
   for (int s0 = 0; s0 < a.S; s0 += 32) {
     n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     total += __reduce_add_sync(kAll, n);
   }
-  total *= a.H;
-  constexpr int kMinTiles = kMinKeys / (16 * LOADS);
-  const int64_t all_warps = static_cast<int64_t>(gridDim.x) * WARPS;
-  const int64_t pairs = static_cast<int64_t>(a.S) * a.H;
-  int64_t workers = min(all_warps, max(pairs, (total + kMinTiles - 1) / kMinTiles));
+  total *= a.H;  // the host has checked that all this stays in int32
+  // A join costs as much as about 128 keys: shorter (s, h) are left whole.  Fewer keys a worker where the pieces can
+  // still be joined at once.
+  const int pairs = a.S * a.H, all_warps = gridDim.x * WARPS;
+  const int tiles = total / pairs;  // of a (s, h), on average
+  const int min_keys = tiles * (16 * LOADS) <= 128 ? 128 : tiles * (16 * LOADS) <= kFlat * (kMinKeys / 2) ? kMinKeys / 2 : kMinKeys;
+  Cut cut;
+  cut.workers = min(all_warps, max(pairs, total / max(1, min_keys / (16 * LOADS))));
   // a multiple of the (s, h) where that leaves few warps idle: sequences of one length are then cut at their ends
-  if (workers / pairs * pairs * 10 >= workers * 9) workers = workers / pairs * pairs;
-  const int64_t id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
-  if (blockIdx.x >= workers) return;
-  const int64_t b0 = min(id, workers) * total / workers, b1 = min(id + 1, workers) * total / workers;
-  const int count = static_cast<int>(b1 - b0);  // 0: no worker
+  if (cut.workers / pairs * pairs * 10 >= cut.workers * 9) cut.workers = cut.workers / pairs * pairs;
+  const int id = warp * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
+  if (blockIdx.x >= cut.workers) return;
+  cut.total = total;
+  cut.per = total / cut.workers;
+  cut.rest = total - cut.per * cut.workers;
+  const int b0 = cut.start(min(id, cut.workers));
+  const int count = cut.start(min(id + 1, cut.workers)) - b0;  // 0: no worker
 
   Cursor cur;
   cur.s = cur.h = cur.t = 0;
-  int64_t before = 0;
+  int before = 0;
   for (int s0 = 0; s0 < a.S && count > 0; s0 += 32) {
     if (a.S > 32) n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     int upto = n;
@@ -575,17 +594,17 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       const int y = __shfl_up_sync(kAll, upto, o);
       if (lane >= o) upto += y;
     }
-    const unsigned past = __ballot_sync(kAll, before + static_cast<int64_t>(upto) * a.H > b0);
+    const unsigned past = __ballot_sync(kAll, before + upto * a.H > b0);
     if (past) {
       const int f = __ffs(past) - 1;
       const int nf = __shfl_sync(kAll, n, f), uf = __shfl_sync(kAll, upto, f);
-      const int64_t rest = b0 - before - static_cast<int64_t>(uf - nf) * a.H;
+      const int rest = b0 - before - (uf - nf) * a.H;
       cur.s = s0 + f;
-      cur.h = static_cast<int>(rest / nf);
-      cur.t = static_cast<int>(rest - static_cast<int64_t>(cur.h) * nf);
+      cur.h = rest / nf;
+      cur.t = rest - cur.h * nf;
       break;
     }
-    before += static_cast<int64_t>(__shfl_sync(kAll, upto, 31)) * a.H;
+    before += __shfl_sync(kAll, upto, 31) * a.H;
   }
   enter_seq<SEL, LOADS>(a, cur);
 
@@ -820,7 +839,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
           }
         }
       const bool whole = first_t == 0 && cur.t == cur.tiles;
-      const int64_t slot = 2 * id + (first_t == 0 ? 1 : 0);
+      const int64_t slot = 2 * static_cast<int64_t>(id) + (first_t == 0 ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -844,13 +863,13 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         }
       if (!whole) {
         // pieces are the workers w0 .. w1: the first's second partial, the others' first
-        const int64_t p0 = b0 + i - cur.t, p1 = p0 + cur.tiles;  // the tiles of (s, h)
+        const int p0 = b0 + i - cur.t;  // the first tile of (s, h)
         Left x;
         x.s = cur.s;
         x.h = cur.h;
-        x.w0 = static_cast<int>(((p0 + 1) * workers - 1) / total);
-        x.w1 = static_cast<int>((p1 * workers - 1) / total);
-        x.state = last_of(arrivals(a, x, static_cast<int>(id)), arrivals_of(x, static_cast<int>(id)), lane) ? 2 : 1;
+        x.w0 = cut.owner(p0);
+        x.w1 = cut.owner(p0 + cur.tiles - 1);
+        x.state = last_of(arrivals(a, x, id), arrivals_of(x, id), lane) ? 2 : 1;
         if (lane == 0) left[warp][first_t == 0 ? 1 : 0] = x;
       }
     }
@@ -881,7 +900,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         j.into = 2 * all_warps + 2 * g + j.e;  // partials of groups follow those of workers
         groups = true;
       } else {
-        j.first = round == 0 ? 2 * static_cast<int64_t>(x.w0) : 2 * all_warps + 2 * (x.w0 / kGroup);
+        j.first = round == 0 ? 2 * static_cast<int64_t>(x.w0) : 2 * static_cast<int64_t>(all_warps) + 2 * (x.w0 / kGroup);
         j.e = 1;
         j.n = round == 0 ? x.w1 - x.w0 + 1 : x.w1 / kGroup - x.w0 / kGroup + 1;
       }

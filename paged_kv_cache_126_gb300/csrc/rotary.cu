@@ -29,6 +29,9 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSteps = 4;  // row steps a warp loads at once
+// Small blocks: a block's place is free again as soon as its four warps are done (128 threads: 36.9 us for 16 chunks
+// of 512 tokens with 32 query and 8 key heads in bf16, 256 threads: 39.6).
+constexpr int kThreads = 128;
 
 template <typename T>
 struct Vec;
@@ -151,7 +154,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* par
 }
 
 template <typename T, bool Q4>
-__global__ void __launch_bounds__(256, 4) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) rope_append_kernel(const RopeArgs a) {
   constexpr int N = Vec<T>::N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -296,7 +299,7 @@ __device__ __forceinline__ void values8(uint32_t word, uint32_t params, uint32_t
 
 // A warp per token, cache and kSteps * 32 / V heads; a lane reads a word of codes and writes 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(256) read_q4_kernel(const ReadQ4Args a) {
+__global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const ReadQ4Args a) {
 cudaError_t launch_pdl(const void* fn, int64_t grid, void** args, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -370,7 +373,7 @@ cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stre
   a.at_once = 32 / a.V;
   a.warps_q = a.q ? static_cast<int>(warps_of(a.Hq, a.at_once)) : 0;
   a.warps_k = static_cast<int>(warps_of(a.H, a.at_once));
-  const int64_t grid = (static_cast<int64_t>(a.T) * (a.warps_q + 2 * a.warps_k) + 7) / 8;
+  const int64_t grid = (static_cast<int64_t>(a.T) * (a.warps_q + 2 * a.warps_k) + kThreads / 32 - 1) / (kThreads / 32);
   void* args[1] = {&a};
   const void* fn = nullptr;
   if (q4)
@@ -385,7 +388,7 @@ cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stre
 
 cudaError_t launch_read_q4(int dtype, ReadQ4Args a, cudaStream_t stream) {
   a.warps_k = static_cast<int>(warps_of(a.H, 32 / (a.D / 8)));
-  const int64_t grid = (static_cast<int64_t>(a.T) * 2 * a.warps_k + 7) / 8;
+  const int64_t grid = (static_cast<int64_t>(a.T) * 2 * a.warps_k + kThreads / 32 - 1) / (kThreads / 32);
   void* args[1] = {&a};
   const void* fn = dtype == PA_F16 ? reinterpret_cast<const void*>(&read_q4_kernel<__half>)
                                    : reinterpret_cast<const void*>(&read_q4_kernel<__nv_bfloat16>);
