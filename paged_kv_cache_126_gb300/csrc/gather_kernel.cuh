@@ -569,10 +569,13 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   // A join costs as much as about 128 keys: shorter (s, h) are left whole.  Fewer keys a worker where the pieces can
   // still be joined at once.
   const int pairs = a.S * a.H, all_warps = gridDim.x * WARPS;
-  const int tiles = total / pairs;  // of a (s, h), on average
+  const int tiles = min(total / pairs, 1 << 20);  // of a (s, h), on average
   const int min_keys = tiles * (16 * LOADS) <= 128 ? 128 : tiles * (16 * LOADS) <= kFlat * (kMinKeys / 2) ? kMinKeys / 2 : kMinKeys;
   Cut cut;
   cut.workers = min(all_warps, max(pairs, total / max(1, min_keys / (16 * LOADS))));
+  // no more workers than the longest range needs: fewer pieces in the same time
+  const int longest = (total + cut.workers - 1) / cut.workers;
+  cut.workers = (total + longest - 1) / longest;
   // a multiple of the (s, h) where that leaves few warps idle: sequences of one length are then cut at their ends
   if (cut.workers / pairs * pairs * 10 >= cut.workers * 9) cut.workers = cut.workers / pairs * pairs;
   const int id = warp * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
