@@ -49,13 +49,15 @@ def quantise_q4(x: np.ndarray) -> np.ndarray:
                            np.ascontiguousarray(par).view(np.uint8).reshape(*x.shape[:-1], D // 8)], axis=-1)
 
 
-def values_q4(rows: np.ndarray) -> np.ndarray:
-    """The numbers (float64, each exact in fp16) that 4-bit rows [..., 5 D / 8] stand for."""
+def values_q4(rows: np.ndarray, rounded: bool = True) -> np.ndarray:
+    """The numbers (float64, each exact in fp16) that 4-bit rows [..., 5 D / 8] stand for; step * n + offset itself
+    where not `rounded`."""
     D = rows.shape[-1] // 5 * 8
     code = np.stack([rows[..., : D // 2] & 15, rows[..., : D // 2] >> 4], axis=-1).reshape(*rows.shape[:-1], D // GROUP, GROUP)
     par = np.ascontiguousarray(rows[..., D // 2:]).view(np.float16).reshape(*rows.shape[:-1], D // GROUP, 2).astype(np.float64)
     with np.errstate(invalid="ignore", over="ignore"):
-        x = (code * par[..., :1] + par[..., 1:]).astype(np.float16).astype(np.float64)
+        x = code * par[..., :1] + par[..., 1:]
+        x = x.astype(np.float16).astype(np.float64) if rounded else x
     return x.reshape(*rows.shape[:-1], D)
 
 

@@ -1720,6 +1720,7 @@ int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, con
     PA_TRY(check_i32(first_tokens, 1));
     if (first_tokens->shape[0] != S) return PA_ERR_SHAPE;
   }
+  if (S * H > INT32_MAX || S * H * block_tables->shape[1] > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (S == 0) return PA_OK;
   int dev;
   PA_TRY(current_device(&dev));
@@ -1759,7 +1760,8 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
   const int64_t S = q->shape[0];
   PA_TRY(check_tables(block_tables, context_lens, S, B));
   PA_TRY(check_selected(selected, S, H));
-  if (S * H * g > INT32_MAX || block_tables->shape[1] > 1 << 20) return PA_ERR_UNSUPPORTED;
+  if (S * H * g > INT32_MAX || block_tables->shape[1] > 1 << 20 || S * H * block_tables->shape[1] > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
   if (S == 0) return PA_OK;
   int dev;
   PA_TRY(current_device(&dev));

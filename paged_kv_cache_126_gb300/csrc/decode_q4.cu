@@ -10,8 +10,8 @@ namespace {
 template <typename T, int D>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {
-  using F = gk::Q4Format<T, D>;
-  constexpr bool one = F::kScaleQ;  // bf16
+  constexpr bool one = !std::is_same<T, __half>::value;  // bf16
+  using F = gk::Q4Format<T, D, one>;
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;

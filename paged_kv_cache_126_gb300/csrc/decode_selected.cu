@@ -33,6 +33,7 @@ struct RowFormat {
   using M = T;
   static constexpr int D = D_;
   static constexpr bool kScaleQ = false;
+  static constexpr int kLift = 0, kCodeScale = 0, kSums = 0;
   static constexpr int kSecond = 8;
   static constexpr uint32_t kHalfTile = 8 * D * 2, kTile = 2 * kHalfTile;
   __device__ __forceinline__ static int key_of(int r) { return r; }
@@ -68,7 +69,7 @@ struct RowFormat {
       x[2 * i + 1] = y.y;
     }
   }
-  __device__ __forceinline__ static void load_q(const float (&q)[D / 4], uint32_t (&f)[D / 16][2]) {
+  __device__ __forceinline__ static void load_q(const float (&q)[D / 4], int, uint32_t (&f)[D / 16][2]) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       f[k][0] = pack2<M>(q[4 * k], q[4 * k + 1]);

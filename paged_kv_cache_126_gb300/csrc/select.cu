@@ -32,10 +32,10 @@ __device__ __forceinline__ void pdl_begin() {
 }
 
 // Where unit x lies when sequence s has count(s) * per units: its sequence, and the unit's number in it.
-// Every lane of the warp calls it; x < the total.
+// Every lane of the warp calls it; x < the total.  Units are numbered in int32 over the whole batch.
 template <typename Count>
-__device__ __forceinline__ int find_unit(int S, int per, int64_t x, int lane, Count count, int64_t* rest) {
-  int64_t before = 0;
+__device__ __forceinline__ int find_unit(int S, int per, int x, int lane, Count count, int* rest) {
+  int before = 0;
   for (int s0 = 0; s0 < S; s0 += 32) {
     const int n = s0 + lane < S ? count(s0 + lane) : 0;
     int upto = n;
@@ -44,21 +44,26 @@ __device__ __forceinline__ int find_unit(int S, int per, int64_t x, int lane, Co
       const int y = __shfl_up_sync(kAll, upto, o);
       if (lane >= o) upto += y;
     }
-    const unsigned past = __ballot_sync(kAll, before + static_cast<int64_t>(upto) * per > x);
+    const unsigned past = __ballot_sync(kAll, before + upto * per > x);
     if (past) {
       const int f = __ffs(past) - 1;
-      *rest = x - before - static_cast<int64_t>(__shfl_sync(kAll, upto, f) - __shfl_sync(kAll, n, f)) * per;
+      *rest = x - before - (__shfl_sync(kAll, upto, f) - __shfl_sync(kAll, n, f)) * per;
       return s0 + f;
     }
-    before += static_cast<int64_t>(__shfl_sync(kAll, upto, 31)) * per;
+    before += __shfl_sync(kAll, upto, 31) * per;
   }
   return -1;
 }
 template <typename Count>
-__device__ __forceinline__ int64_t all_units(int S, int per, int lane, Count count) {
-  int64_t total = 0;
+__device__ __forceinline__ int all_units(int S, int per, int lane, Count count) {
+  int total = 0;
   for (int s0 = 0; s0 < S; s0 += 32) total += __reduce_add_sync(kAll, s0 + lane < S ? count(s0 + lane) : 0);
   return total * per;
+}
+// First unit of worker w where `total` units are cut evenly among `workers` (< 2^15 of them).
+__device__ __forceinline__ int first_unit(int total, int workers, int w) {
+  const int per = total / workers;
+  return w * per + static_cast<int>(static_cast<unsigned>(w * (total - per * workers)) / workers);
 }
 
 template <typename T2>
@@ -78,23 +83,23 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
     const int L = a.context_lens[s], first = a.first ? a.first[s] : 0;
     return bad_len(L, a.max_blocks, a.B) || first < 0 || first >= L ? 0 : (L + a.B - 1) / a.B - first / a.B;
   };
-  const int64_t total = all_units(a.S, a.H, lane, count);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  const int64_t id = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const int total = all_units(a.S, a.H, lane, count);
+  const int warps = gridDim.x * 8;
+  const int id = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   if (id < a.S) {  // bad lengths are reported by one warp each
     for (int64_t s = id; s < a.S; s += warps)
       if (lane == 0 && (bad_len(a.context_lens[s], a.max_blocks, a.B) || (a.first && a.first[s] < 0)))
         atomicOr(a.status, kDevBadLen);
   }
-  const int64_t workers = min(warps, total);
+  const int workers = min(warps, total);
   if (id >= workers) return;
-  const int64_t x0 = id * total / workers, x1 = (id + 1) * total / workers;
-  int64_t rest;
+  const int x0 = first_unit(total, workers, id), x1 = first_unit(total, workers, id + 1);
+  int rest;
   int s = find_unit(a.S, a.H, x0, lane, count, &rest);
-  int left = count(s) - static_cast<int>(rest / a.H), h = static_cast<int>(rest % a.H);
+  int left = count(s) - rest / a.H, h = rest % a.H;
   int L = a.context_lens[s];
   int j = (L + a.B - 1) / a.B - left;
-  for (int64_t x = x0; x < x1; ++x) {
+  for (int x = x0; x < x1; ++x) {
     const int frame = a.block_tables[s * a.bt_row + j];
     if (frame < 0 || frame >= a.num_blocks) {
       if (lane == 0) atomicOr(a.status, kDevBadBlock);
@@ -187,16 +192,16 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries
     const int blocks = bad_len(L, a.max_blocks, a.B) ? 0 : (L + a.B - 1) / a.B;
     return scored(a, blocks) ? (blocks + kUnit - 1) / kUnit : 0;
   };
-  const int64_t total = all_units(a.S, a.H, lane, count);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kScoreWarps;
-  const int64_t id = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-  const int64_t workers = min(warps, total);
+  const int total = all_units(a.S, a.H, lane, count);
+  const int warps = gridDim.x * kScoreWarps;
+  const int id = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const int workers = min(warps, total);
   if (id >= workers) return;
-  const int64_t x0 = id * total / workers, x1 = (id + 1) * total / workers;
-  int64_t rest;
+  const int x0 = first_unit(total, workers, id), x1 = first_unit(total, workers, id + 1);
+  int rest;
   int s = find_unit(a.S, a.H, x0, lane, count, &rest);
   int units = count(s);
-  int h = static_cast<int>(rest / units), unit = static_cast<int>(rest % units);
+  int h = rest / units, unit = rest % units;
   int blocks = (a.context_lens[s] + a.B - 1) / a.B;
   float4 (*qs)[4][kRowLanes] = q_parts[threadIdx.x >> 5];
   auto load_q_of = [&](const T* base, int g0) {  // base: the head's first query
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries
     }
   };
   load();
-  for (int64_t x = x0; x < x1; ++x) {
+  for (int x = x0; x < x1; ++x) {
     if (fresh && a.g <= kQueries) load_q(0);
     // this unit's numbers, and the next one's on their way while they are used
     const int j0 = unit * kUnit, its_blocks = blocks;

@@ -113,7 +113,9 @@ def test_4_bit_loop_with_forks(pa):
         k, v = lp.rows(n, H), lp.rows(n, H)
         pos = np.arange(n, dtype=np.int32)
         pa.pa_cache_append_q4(k.cuda(), v.cuda(), dev(slots), kc, vc, dev(pos), lp.cs)
-        lp.dense[seq] = [list(values_q4(quantise_q4(rotate(k.float().numpy(), lp.table, pos, False)))), list(values_q4(quantise_q4(v.float().numpy())))]
+        # with bf16 queries a key enters its score as step * n + offset, not rounded to fp16
+        lp.dense[seq] = [list(values_q4(quantise_q4(rotate(k.float().numpy(), lp.table, pos, False)), rounded=False)),
+                         list(values_q4(quantise_q4(v.float().numpy())))]
     seqs = [0, 1]
     for step in range(6):
         if step == 2:
@@ -128,7 +130,7 @@ def test_4_bit_loop_with_forks(pa):
         k, v, q = lp.rows(len(seqs), H), lp.rows(len(seqs), H), lp.rows(len(seqs), H * g)
         qd = q.cuda()
         pa.pa_cache_append_q4(k.cuda(), v.cuda(), dev(slots), kc, vc, dev(pos), lp.cs, q=qd, q_out=qd)
-        kq = values_q4(quantise_q4(rotate(k.float().numpy(), lp.table, pos, False)))
+        kq = values_q4(quantise_q4(rotate(k.float().numpy(), lp.table, pos, False)), rounded=False)
         vq = values_q4(quantise_q4(v.float().numpy()))
         for i, s in enumerate(seqs):
             lp.dense[s][0].append(kq[i])

@@ -115,9 +115,11 @@ def decode_case(lens, H, g, D, B, dtype, seed, poison=True, q_scale=1.0, width=N
 
 
 def decode_reference(q, kc, vc, tables, lens, B, scale, s):
+    """With bf16 queries a key enters its score as step * n + offset, not rounded to fp16."""
     n = int(lens[s])
     f = tables[s, : -(-n // B)].long()
-    k, v = (values_q4(c[f].numpy()).transpose(0, 2, 1, 3).reshape(-1, c.shape[1], c.shape[3] // 5 * 8)[:n] for c in (kc, vc))
+    k, v = (values_q4(c[f].numpy(), rounded=c is vc or q.dtype == torch.float16).transpose(0, 2, 1, 3)
+            .reshape(-1, c.shape[1], c.shape[3] // 5 * 8)[:n] for c in (kc, vc))
     return attend(host64(q[s]), k, v, scale), k, v
 
 
