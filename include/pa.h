@@ -54,7 +54,8 @@ enum pa_dtype { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_I32 = 3, PA_U8 = 4 };
 #define PA_ERR_CUDA          -9   /* a CUDA runtime call or launch failed */
 #define PA_ERR_UNSUPPORTED  -10   /* head_dim / dtype / size outside the built kernels */
 #define PA_ERR_CAPACITY     -11   /* caller-provided output buffer too small */
-#define PA_ERR_SCRATCH_LIMIT -12  /* pa_decode_static: scratch need exceeds its fixed array */
+#define PA_ERR_SCRATCH_LIMIT -12  /* pa_decode_static: scratch need exceeds its fixed array; under
+                                     stream capture: the stream's workspace is too small */
 #define PA_ERR_HOST_MEMORY  -13   /* a host allocation failed (no exception crosses this ABI) */
 
 /* ---- sticky device status bits (pa_get_device_status) ------------------------------ */
@@ -138,7 +139,7 @@ int pa_copy_blocks(const pa_tensor* k_cache, const pa_tensor* v_cache,
  * grid through an atomic counter.  Counter and split partials live in a
  * workspace the library owns: one per (device, stream), allocated (cudaMalloc)
  * and zeroed on the first call with that pair and grown on the first call that
- * needs more (keep such calls outside CUDA-graph capture), freed by
+ * needs more (under CUDA-graph capture such a call returns PA_ERR_SCRATCH_LIMIT), freed by
  * pa_shutdown().  Calls on one stream run in order; calls on different streams
  * use different workspaces.
  * Supported: dtype f32/f16/bf16; D in {64, 128, 256} (f32: {64, 128});
@@ -299,7 +300,8 @@ int pa_decode_static(const pa_tensor* q, const pa_tensor* k_cache, const pa_tens
  * These calls share query heads among key heads: q and out hold Hq = g * H heads, query
  * head j reads key head j / g, 1 <= g <= 16.  dtype fp16 or bf16 where not said
  * otherwise, D in {64, 128}, block sizes B in {8, 16, 32, 64, 128, 256}; else
- * PA_ERR_UNSUPPORTED.
+ * PA_ERR_UNSUPPORTED.  No output may overlap an input or another output, save where it is
+ * said.
  * Decode workspaces: as for pa_decode, one per (device, stream).  A CUDA graph keeps the
  * workspace of the stream it was captured on, also when later calls need a larger one
  * (the older buffer stays until pa_shutdown); two graphs captured on one stream share it,
@@ -417,7 +419,8 @@ int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, con
  *                 than K frames.
  * Bounds and queries must be finite (a NaN or infinite score ranks somewhere, no more is
  * said).  A bad length or frame id sets its status bit; a bad L_s selects nothing, a frame
- * with a bad id ranks last.  Uses the (device, stream) workspace for the scores.
+ * with a bad id ranks last.  Uses the (device, stream) workspace for the scores,
+ * 4 * S * H * max_blocks bytes.
  */
 int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tensor* block_tables,
                      const pa_tensor* context_lens, int32_t block_size, int32_t keep_first,

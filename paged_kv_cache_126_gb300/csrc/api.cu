@@ -222,11 +222,18 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
   }
   Workspace& w = *wp;
   size_t cnt = std::max(round256(cnt_need), std::max(w.cnt_bytes, kMinCntBytes));
-  if (!w.ptr || w.cnt_bytes < cnt || w.bytes < kSchedBytes + cnt + rest_bytes) {
+  const bool small = !w.ptr || w.cnt_bytes < cnt || w.bytes < kSchedBytes + cnt + rest_bytes;
+  if (small || !w.zeroed) {
+    // Under capture an allocation would end the capture with an error, and counters zeroed by the graph would not be
+    // zero for a call made before its first replay.
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
-    // an allocation would end the capture with an error
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+      cudaGetLastError();
+      return PA_ERR_CUDA;
+    }
     if (cap != cudaStreamCaptureStatusNone) return PA_ERR_SCRATCH_LIMIT;
+  }
+  if (small) {
     if (w.ptr && w.cnt_bytes < cnt) cnt = std::max(cnt, 2 * w.cnt_bytes);
     // whole 2 MB pages: what a process that watches its free memory sees of it
     const size_t bytes = std::max(std::max(kSchedBytes + cnt + rest_bytes, static_cast<size_t>(2) << 20), 2 * w.bytes);
@@ -378,7 +385,7 @@ const char* pa_strerror(int code) {
     case PA_ERR_UNSUPPORTED: return "size or dtype outside the built kernels";
     case PA_ERR_HOST_MEMORY: return "host memory allocation failed";
     case PA_ERR_CAPACITY: return "output buffer too small";
-    case PA_ERR_SCRATCH_LIMIT: return "problem needs more scratch than the fixed 16 MiB array of pa_decode_static";
+    case PA_ERR_SCRATCH_LIMIT: return "more scratch needed than is there (the fixed array of pa_decode_static; a stream's workspace under capture)";
     default: return "unknown code";
   }
 }
@@ -639,7 +646,8 @@ int pa_decode_split(const pa_tensor* q, const pa_tensor* k_cache, const pa_tenso
 
 int pa_copy_blocks(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* pairs, pa_stream stream) {
   PA_TRY(check_cache(k_cache, v_cache, true));
-  if (!pairs) return PA_ERR_INVALID;
+  if (!v_cache || !pairs) return PA_ERR_INVALID;
+  if (v_cache->dtype == PA_U8) PA_TRY(check_cache(v_cache, nullptr, true));
   PA_TRY(check_i32(pairs, 2));
   if (pairs->shape[1] != 2 || (pairs->shape[0] > 1 && pairs->stride[0] != 2)) return PA_ERR_SHAPE;
   const int64_t n = pairs->shape[0];

@@ -884,6 +884,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (more) issue_values();
       if (++st == STAGES) st = 0, phase ^= 1;
     }
+    if (stuck) break;  // nothing of this piece is written or counted
 
     {
       // ---- the end of a piece of (s, h) ----
