@@ -24,6 +24,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Bound by memory as it is read here, in pieces of one head's row (256 bytes, H rows apart): 64 of 1024 frames
+// of 16 tokens for 4 x 32 heads (67 MB) take 19.5 us, 2048 of up to 65,536 tokens for 32 x 8 heads (184 MB) 43 us,
+// 38 of them streaming at 4.8 TB/s.  Two to six stages, 4 to 16 warps an SM, boxes of 128- or 256-byte
+// rows and every L2 promotion gave the same within 3 %.
+//
 // 16-bit rows.  A half tile, 8 keys, is one TMA box [D / 64 column groups][8 rows][64 elements] with the
 // 128-byte swizzle: row y of a column group keeps its 16-byte chunk x at x ^ y, so that the eight row
 // addresses of an ldmatrix fall into different banks.
@@ -132,6 +137,7 @@ struct RowFormat {
 
 namespace {
 
+// Weights in two parts of the cache's type, in the second copy of the queries where four or fewer share a head.
 template <typename T, int D>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {

