@@ -17,15 +17,17 @@
 // since a row is loaded by one warp before any of it is stored, q_out may be q.
 //
 // Bound by memory: 16 chunks of 512 tokens, 32 query and 8 key heads of 128 in bf16 (206 MB) take
-// 37.0 us, 5.55 TB/s; into the 4-bit cache 46 us, where the codes of keys and values take as many
-// instructions as a fourth of that; read back (44 MB) 9.5 us.  A decode step of 64 tokens (3.2 MB) takes
-// 2.6 us, a launch.  Two steps a warp (44 us), eight (42 us) and one warp a token (50 us, 21 us for the
-// step) were slower.
+// 32.6 us, 6.3 TB/s; into the 4-bit cache (178 MB) 36.6 us, where the codes of keys and values take more instructions
+// than all queries; read back (44 MB) 9.4 us.  A decode step of 64 tokens (3.2 MB) takes 2.8 us, a launch.
+// 34.8 and 41.8 us without two fp32 numbers an instruction; 37.0 and 44.7 where a block's four warps were parts of one token,
+// whose kind and rows were then each lane's to compute.  Two steps a warp (44 us), six (34.3 us) and warps that
+// stay and load their next rows meanwhile (51 us) were slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -35,9 +37,10 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSteps = 4;  // row steps a warp loads at once
-// Small blocks: a block's place is free again as soon as its four warps are done (128 threads: 36.9 us for 16 chunks
-// of 512 tokens with 32 query and 8 key heads in bf16, 256 threads: 39.6).
+// Small blocks: a block's place is free again as soon as its four warps are done (36.9 us where 256 threads took 39.6).
+// Nine blocks an SM, 56 registers: 32.6 us for 16 chunks of 512 tokens; eight 33.7, ten (spills) 33.5.
 constexpr int kThreads = 128;
+constexpr int kBlocks = 9;
 
 template <typename T>
 struct Vec;
@@ -102,17 +105,50 @@ __device__ __forceinline__ uint4 shfl4(const uint4& u, int lane) {
                     __shfl_sync(kAll, u.w, lane));
 }
 
+// Two fp32 numbers in one register pair: one instruction for both, each rounded as by itself.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ float2 both(uint64_t p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+  return p;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+  return p;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
+  return p;
+}
+
 // Eight consecutive elements of one 4-bit row (element 0 at a multiple of 8): the word of
 // codes for this lane; step and offset of the group, the same in its four lanes.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* params) {
+__device__ __forceinline__ uint32_t quantise8(const float* x, uint32_t* params) {
   constexpr float kTop = 65024.f;  // the top code is at most kTop (1 + 2^-10): finite in fp16
-  float lo = x[0], hi = x[0], none = 0.f;
+  float lo = x[0], hi = x[0];
+  uint64_t p[4], none2 = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    none = fmaf(x[i], 0.f, none);  // NaN once an element is not finite
+  for (int i = 0; i < 4; ++i) {
+    p[i] = pair(x[2 * i], x[2 * i + 1]);
+    none2 = fma2(p[i], 0, none2);  // NaN once an element is not finite
+  }
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
   }
+  float none = both(none2).x + both(none2).y;
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(kAll, lo, o));
@@ -121,62 +157,76 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* par
   }
   const bool finite = none == 0.f;
   // an element beyond +-kTop is coded like +-kTop: as 0 or 15
-  lo = fminf(fmaxf(lo, -kTop), kTop);
-  hi = fminf(fmaxf(hi, -kTop), kTop);
-  const __half off = __float2half_rn(lo);
+  const float bottom = fminf(fmaxf(lo, -kTop), kTop), top = fminf(fmaxf(hi, -kTop), kTop);
+  const __half off = __float2half_rn(bottom);
   const float offf = __half2float(off);
-  const __half step = __float2half_rn(__fmul_rn(__fsub_rn(hi, offf), 1.0f / 15.0f));
+  const __half step = __float2half_rn(__fmul_rn(__fsub_rn(top, offf), 1.0f / 15.0f));
   const float stepf = __half2float(step);
-  // round((x - off) / step) by a product with 1 / (15 step), which the multiplier clamps to [0, 1]: five roundings
-  // leave it within 15 * 5 * 2^-24 < 2^-17 of the quotient, so where it is further than 2^-15 from a border
-  // between two codes both round alike; a lane with a value nearer than that divides.
+  // round((x - off) / step) by a product with 1 / step: four roundings and 2^-23 of the reciprocal leave it within
+  // 15.5 * 6 * 2^-24 < 2^-17 of the quotient, so where it is further than 2^-16 from a border between two codes both
+  // round alike.  Nearer ones (16-bit rows have many that lie on a border: a seventh of the steps of bf16 values)
+  // are compared with it: the rest of n steps is exact, and a quotient that is not on the border does not
+  // round to it, for step and border have 16 bits together.  The same path serves groups whose ends are not coded
+  // as 0 and 15 by themselves.
   const bool coded = finite && stepf > 0.f;
-  const float inv = coded ? __fmul_rn(__frcp_rn(stepf), 1.0f / 15.0f) : 0.f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(stepf));
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded addend
-  float half_way = 0.f, n[8];
+  const uint64_t noff2 = pair(-offf, -offf), inv2 = pair(inv, inv), round2 = pair(kRound, kRound), back2 = pair(-kRound, -kRound);
+  const uint64_t minus2 = pair(-1.f, -1.f);
+  float half_way = 0.f;
+  uint64_t n2[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __saturatef(__fmul_rn(__fsub_rn(x[i], offf), inv));
-    n[i] = __fsub_rn(fmaf(t, 15.f, kRound), kRound);
-    half_way = fmaxf(half_way, fabsf(fmaf(t, 15.f, -n[i])));
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = mul2(add2(p[i], noff2), inv2);
+    n2[i] = add2(add2(t, round2), back2);
+    const float2 d = both(fma2(n2[i], minus2, t));
+    half_way = fmaxf(half_way, fmaxf(fabsf(d.x), fabsf(d.y)));
   }
-  if (half_way > 0.5f - 0x1p-15f) {
-#pragma unroll 1
-    for (int k = 0; k < 8; ++k) {  // rare: one division's code, and selects so that x and n stay in registers
-      float v = x[0];
+  const bool inside = fmaf(lo - offf, inv, 0.5f) > 0x1p-10f && fmaf(hi - offf, inv, -15.5f) < -0x1p-10f;
+  if (!(half_way <= 0.5f - 0x1p-16f) || !inside || !coded) {
+    const float half = 0.5f * stepf;
 #pragma unroll
-      for (int i = 1; i < 8; ++i) v = i == k ? x[i] : v;
-      v = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v, offf), stepf)), 0.f), 15.f);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = both(n2[i]);
+      float n[2] = {f.x, f.y};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = i == k ? v : n[i];
+      for (int k = 0; k < 2; ++k) {
+        n[k] = fminf(fmaxf(n[k], 0.f), 15.f);
+        const float rest = fmaf(-n[k], stepf, __fsub_rn(x[2 * i + k], offf));
+        const bool odd = __float_as_uint(n[k] + kRound) & 1u;
+        if (rest > half || (rest == half && odd)) n[k] += 1.f;
+        else if (rest < -half || (rest == -half && odd)) n[k] -= 1.f;
+        n[k] = coded ? fminf(fmaxf(n[k], 0.f), 15.f) : 0.f;
+      }
+      n2[i] = pair(n[0], n[1]);
     }
   }
   // four codes as one number below 2^16, exact in fp32
-  const float a = fmaf(fmaf(fmaf(n[3], 16.f, n[2]), 16.f, n[1]), 16.f, n[0]) + 8388608.f;
-  const float b = fmaf(fmaf(fmaf(n[7], 16.f, n[6]), 16.f, n[5]), 16.f, n[4]) + 8388608.f;
+  const uint64_t s256 = pair(256.f, 256.f);
+  const float2 a = both(fma2(n2[1], s256, n2[0])), b = both(fma2(n2[3], s256, n2[2]));
+  const float wa = fmaf(a.y, 16.f, a.x) + 8388608.f, wb = fmaf(b.y, 16.f, b.x) + 8388608.f;
   const uint32_t st = finite ? __half_as_ushort(step) : 0x7fffu, of = finite ? __half_as_ushort(off) : 0x7fffu;
   *params = st | (of << 16);
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+  return __byte_perm(__float_as_uint(wa), __float_as_uint(wb), 0x5410);
 }
 
 template <typename T, bool Q4>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const RopeArgs a) {
   constexpr int N = Vec<T>::N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int V = a.V, at_once = a.at_once;
-  const int sub = lane / V, vec = lane - sub * V;
+  const int sub = (lane * a.per_V) >> 16, vec = lane - sub * V;  // lane / V
   const int rv = a.R / N;           // rotated vectors of a row
-  const int per = at_once * kSteps;
-  const unsigned job = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const unsigned jobs = a.warps_q + 2 * a.warps_k;  // of a token
-  if (job >= a.T * jobs) return;
-  const int t = static_cast<int>(job / jobs);
-  const int part = static_cast<int>(job - t * jobs);
+  // the kind and the rows are the block's, so that what follows from them is computed once for all lanes
+  const int part = blockIdx.x;
+  const int t = static_cast<int>((blockIdx.z * gridDim.y + blockIdx.y) * (kThreads / 32) + (threadIdx.x >> 5));
+  if (t >= a.T) return;
   const int cq = a.warps_q, ck = a.warps_k;
   const bool is_q = part < cq, is_k = !is_q && part < cq + ck;
-  const int h0 = (is_q ? part : is_k ? part - cq : part - cq - ck) * per + sub;  // first of this lane's rows
+  const int h0 = (is_q ? part : is_k ? part - cq : part - cq - ck) * at_once * kSteps + sub;  // first of this lane's rows
   const int heads = is_q ? a.Hq : a.H;
   const T* src = is_q ? static_cast<const T*>(a.q) + t * a.q_row
                  : is_k ? static_cast<const T*>(a.k_new) + t * a.k_row
@@ -242,43 +292,57 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) rope_append_kernel(
     dst = (is_k ? a.k_cache : a.v_cache) + ((frame * a.H + h0) * a.B + (slot - frame * a.B)) * W;
     dist = static_cast<int64_t>(at_once) * a.B * W;
   }
+  const auto steps = [&](auto turned_, auto coded_) {
+    constexpr bool turned = decltype(turned_)::value, coded = decltype(coded_)::value;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const bool live = sub < at_once && h0 + i * at_once < heads;
-    if (!__any_sync(kAll, live)) break;
-    float x[N];
-    if (turn || (Q4 && !is_q)) Vec<T>::unpack(u[i], x);
-    if (turn) {
-      if (!a.interleaved) {
-        float y[N];
-        Vec<T>::unpack(shfl4(u[i], partner), y);
-        if (rot) {
+    for (int i = 0; i < kSteps; ++i) {
+      const bool live = sub < at_once && h0 + i * at_once < heads;
+      if (!__any_sync(kAll, live)) break;
+      float x[N];
+      if constexpr (turned || coded) Vec<T>::unpack(u[i], x);
+      if constexpr (turned) {
+        if (!a.interleaved) {
+          float y[N];
+          Vec<T>::unpack(shfl4(u[i], partner), y);
+          if (rot) {
 #pragma unroll
-          for (int j = 0; j < N; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(y[j], s[j]));
-        }
-      } else if (rot) {
+            for (int j = 0; j < N; j += 2) {
+              const float2 z = both(add2(mul2(pair(x[j], x[j + 1]), pair(c[j], c[j + 1])), mul2(pair(y[j], y[j + 1]), pair(s[j], s[j + 1]))));
+              x[j] = z.x, x[j + 1] = z.y;
+            }
+          }
+        } else if (rot) {
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          const float x1 = x[2 * j], x2 = x[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(x1, c[j]), __fmul_rn(x2, s[j]));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(x2, c[j]), __fmul_rn(x1, s[j]));
+          for (int j = 0; j < N / 2; ++j) {
+            const float x1 = x[2 * j], x2 = x[2 * j + 1];
+            x[2 * j] = __fsub_rn(__fmul_rn(x1, c[j]), __fmul_rn(x2, s[j]));
+            x[2 * j + 1] = __fadd_rn(__fmul_rn(x2, c[j]), __fmul_rn(x1, s[j]));
+          }
         }
       }
-    }
-    if constexpr (Q4) {
-      if (!is_q) {
+      if constexpr (coded) {
         uint32_t params;
         const uint32_t word = quantise8(x, &params);  // groups are four lanes of one row
         if (live) {
           *reinterpret_cast<uint32_t*>(dst + vec * 4) = word;
           if ((vec & 3) == 0) *reinterpret_cast<uint32_t*>(dst + a.D / 2 + vec) = params;
         }
-        dst += dist;
-        continue;
+      } else if (live) {
+        if constexpr (turned) *reinterpret_cast<uint4*>(dst) = rot ? Vec<T>::pack(x) : u[i];
+        else *reinterpret_cast<uint4*>(dst) = u[i];
       }
+      dst += dist;
     }
-    if (live) *reinterpret_cast<uint4*>(dst) = rot ? Vec<T>::pack(x) : u[i];
-    dst += dist;
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  if constexpr (Q4) {
+    if (is_q) steps(yes, no);
+    else if (turn) steps(yes, yes);
+    else steps(no, yes);
+  } else {
+    if (turn) steps(yes, no);
+    else steps(no, no);
   }
 }
 
@@ -351,9 +415,9 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
   }
 }
 
-cudaError_t launch_pdl(const void* fn, int64_t grid, void** args, cudaStream_t stream) {
+cudaError_t launch_pdl(const void* fn, dim3 grid, void** args, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -379,7 +443,9 @@ cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stre
   a.at_once = 32 / a.V;
   a.warps_q = a.q ? static_cast<int>(warps_of(a.Hq, a.at_once)) : 0;
   a.warps_k = static_cast<int>(warps_of(a.H, a.at_once));
-  const int64_t grid = (static_cast<int64_t>(a.T) * (a.warps_q + 2 * a.warps_k) + kThreads / 32 - 1) / (kThreads / 32);
+  a.per_V = 65536 / a.V + 1;
+  const int tokens = (a.T + kThreads / 32 - 1) / (kThreads / 32), rows = tokens < 65535 ? tokens : 65535;
+  const dim3 grid(a.warps_q + 2 * a.warps_k, rows, (tokens + rows - 1) / rows);
   void* args[1] = {&a};
   const void* fn = nullptr;
   if (q4)
@@ -398,7 +464,7 @@ cudaError_t launch_read_q4(int dtype, ReadQ4Args a, cudaStream_t stream) {
   void* args[1] = {&a};
   const void* fn = dtype == PA_F16 ? reinterpret_cast<const void*>(&read_q4_kernel<__half>)
                                    : reinterpret_cast<const void*>(&read_q4_kernel<__nv_bfloat16>);
-  return launch_pdl(fn, grid, args, stream);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), args, stream);
 }
 
 }  // namespace pa

@@ -74,6 +74,31 @@ def test_corner_groups(pa):
     assert torch.isnan(ko[3, 0, :32]).all() and torch.isfinite(ko[3, 0, 32:]).all() and torch.isnan(ko[4, 0, 32:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_borders_between_codes(pa, dtype):
+    """Elements on a border between two codes and next to it, and ranges far below their offset's rounding: each code
+    is that of the division."""
+    g = torch.Generator().manual_seed(41)
+    n, D, B = 4096, 128, 16
+    step = (torch.rand(n, 1, generator=g) + 0.5) * 2.0 ** torch.randint(-22, 11, (n, 1), generator=g)
+    step = step.half().float()
+    border = torch.randint(0, 31, (n, D), generator=g).float() * 0.5
+    border[:, 0::32], border[:, 1::32] = 0.0, 15.0  # the range is 15 steps
+    x = (step * border).to(TD[dtype])
+    near = x.view(torch.int16) + torch.randint(-1, 2, (n, D), generator=g).to(torch.int16)
+    near[:, 0::32], near[:, 1::32] = x.view(torch.int16)[:, 0::32], x.view(torch.int16)[:, 1::32]
+    x[n // 2:] = near.clamp(min=0).view(TD[dtype])[n // 2:]
+    x = x - (torch.randint(0, 3, (n, 1), generator=g) * 7.0 * step).to(TD[dtype])
+    far = (torch.randn(n, D, generator=g) * 0.02 + 1000 * torch.randn(n, 1, generator=g)).to(TD[dtype])
+    x, far = (t.reshape(n // 2, 2, D) for t in (x, far))
+    slots = torch.arange(n // 2, dtype=torch.int32).cuda()
+    kc, vc = (torch.zeros(n // 2 // B, 2, B, 5 * D // 8, dtype=torch.uint8, device="cuda") for _ in range(2))
+    pa.pa_cache_append_q4(x.cuda(), far.cuda(), slots, kc, vc)
+    for cache, rows_ in ((kc, x), (vc, far)):
+        got = cache.transpose(1, 2).flatten(0, 1).cpu().numpy()
+        assert np.array_equal(got, quantise_q4(rows_.float().numpy()))
+
+
 def test_read_padding_and_bad_slots(pa):
     kc, vc = (torch.randint(0, 200, (2, 1, 8, 40), device="cuda").to(torch.uint8) for _ in range(2))
     slots = torch.tensor([-1, 16, 3, 3], dtype=torch.int32, device="cuda")
