@@ -18,7 +18,7 @@
 //
 // Bound by memory: 16 chunks of 512 tokens, 32 query and 8 key heads of 128 in bf16 (206 MB) take
 // 32.6 us, 6.3 TB/s; into the 4-bit cache (178 MB) 36.6 us, where the codes of keys and values take more instructions
-// than all queries; read back (44 MB) 9.4 us.  A decode step of 64 tokens (3.2 MB) takes 2.8 us, a launch.
+// than all queries; read back (44 MB) 9.4 us.  A decode step of 64 tokens (3.2 MB) takes 2.6 us, a launch.
 // 34.8 and 41.8 us without two fp32 numbers an instruction; 37.0 and 44.7 where a block's four warps were parts of one token,
 // whose kind and rows were then each lane's to compute.  Two steps a warp (44 us), six (34.3 us) and warps that
 // stay and load their next rows meanwhile (51 us) were slower.
@@ -31,6 +31,7 @@
 
 #include "pa.h"
 #include "pa_internal.h"
+#include "pair32.cuh"
 
 namespace pa {
 namespace {
@@ -103,33 +104,6 @@ struct Vec<__nv_bfloat16> {
 __device__ __forceinline__ uint4 shfl4(const uint4& u, int lane) {
   return make_uint4(__shfl_sync(kAll, u.x, lane), __shfl_sync(kAll, u.y, lane), __shfl_sync(kAll, u.z, lane),
                     __shfl_sync(kAll, u.w, lane));
-}
-
-// Two fp32 numbers in one register pair: one instruction for both, each rounded as by itself.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
-  return p;
-}
-__device__ __forceinline__ float2 both(uint64_t p) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
-  return f;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t p;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
-  return p;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t p;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
-  return p;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t p;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
-  return p;
 }
 
 // Eight consecutive elements of one 4-bit row (element 0 at a multiple of 8): the word of

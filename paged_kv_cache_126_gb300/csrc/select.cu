@@ -5,13 +5,13 @@
 //
 // The bounds and the scores read memory once and compute little: both give consecutive ranges
 // of their (sequence, frame, head) units to resident warps, found from the lengths on the
-// device, and keep several 16-byte loads a lane in flight.  The selection holds a list's
+// device, and keep several 16-byte loads or copies a lane in flight.  The selection holds a list's
 // ranks in registers, finds the K-th's neighbourhood with one histogram over the scores' range, and
 // orders the few that share its bin.
 //
 // Measured: bounds of 16 prompts of 4096 tokens, 8 heads of 128 in bf16, frames of 32 (143 MB): 27.1 us, 5.25 TB/s;
-// of the tail frames of 64 sequences 4.5 us.  Selection of 64 from 1024 frames for 4 x 32 heads (67 MB of bounds):
-// 20.9 us, of which the scores 16; for 32 sequences of 100 to 65,536 tokens with 8 heads of 4 queries (43 MB): 20.8 us,
+// of the tail frames of 64 sequences 4.5 us.  Selection of 64 from 1024 frames for 4 x 32 heads (67 MB of bounds, in
+// 512-byte pieces): 18.6 us; for 32 sequences of 100 to 65,536 tokens with 8 heads of 4 queries (43 MB): 20.3 us,
 // bound by the instructions of four queries a row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -21,6 +21,7 @@
 
 #include "pa.h"
 #include "pa_internal.h"
+#include "pair32.cuh"
 
 namespace pa {
 namespace {
@@ -158,13 +159,19 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 
 // ---- scores -----------------------------------------------------------------------------------------
 // A unit is kRows * kAhead consecutive frames of one (sequence, head): a bounds row is D / 8 lanes, kRows
-// frames lie side by side in a warp and kAhead deep, all loaded before the first is used.  With q split
+// frames lie side by side in a warp and kAhead deep.  Lanes copy their own 16 bytes of the next units to
+// shared memory while they use this one's, so that what is on its way takes no registers and no barrier.  With q split
 // into its positive and negative part (in shared memory) one product is zero and the other exact,
-// so x_d = max(q_d min_d, q_d max_d) comes from a product and a fused multiply-add.  The order of
-// the sum (neighbours first) is a tree: eight elements in a lane, then lanes by xor 1, 2, 4, ...; the
-// four frames of a lane are reduced together, each lane passing on half of what it holds, which adds
-// the same pairs.  kQueries queries at a time; more queries read the rows of the unit again from
-// registers and their own numbers from the cache.
+// so x_d = max(q_d min_d, q_d max_d) comes from a product and a fused multiply-add, for two elements in one
+// instruction.  The order of the sum is a tree: eight elements in a lane (neighbours, their sums, the two
+// halves), then lanes by xor 1, 2, 4, ...; the four frames of a lane are reduced together, each lane passing on half
+// of what it holds, which adds the same pairs.  kQueries queries at a time; more queries read the unit's rows again from
+// shared memory and their own numbers from the cache.
+//
+// Units on their way and blocks an SM, both kernels of a selection, 4 x 32 heads of 1024 frames and 32 x 8 heads of up to
+// 2048: one query 4 and 3 (18.6, 16.7 us; 3 and 4: 18.3, 19.8, where the selection's blocks no longer fit beside
+// them and start late; through registers 20.8, 18.1); two 5 and 2 (21.3, 18.7; 3 and 3 20.8, 19.6); four 2 and 3
+// (22.4, 20.3; 4 and 2 25.2, 22.0; through registers 24.8, 21.0; one element an instruction 25.3, 24.6).
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -185,12 +192,33 @@ __device__ __forceinline__ bool scored(const SelectArgs& a, int blocks) { return
 
 constexpr int kScoreWarps = 4;
 
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {  // zeros where not live
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+
+// Where a warp is in the batch's units: a head's unit of a sequence that has `units` of them.
+struct ScoreAt {
+  int s, h, unit, units, blocks;
+};
+
+template <int D, int kQueries>
+struct ScoreSmem {
+  static constexpr int kRowLanes = D / 8, kAhead = 4;
+  static constexpr int kStages = kQueries == 1 ? 4 : kQueries == 2 ? 5 : 2;
+  static constexpr int kBlocks = kQueries == 2 ? 2 : 3;  // an SM
+  uint4 rows[kScoreWarps][kStages][kAhead][2][32];  // each lane's 16 bytes of minima and of maxima
+  // positive part of the queries (two vectors a lane), negative part, in pairs (e, e + 4)
+  float4 q[kScoreWarps][kQueries][4][kRowLanes];
+};
+
 template <typename T, int D, int kQueries>
-__global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries == 2 ? 3 : 2) score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 3) score_kernel(const SelectArgs a) {
   constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 4, kUnit = kRows * kAhead;
-  __shared__ float4 q_parts[kScoreWarps][kQueries][4][kRowLanes];  // positive part (two vectors a lane), negative part
+  constexpr int kStages = ScoreSmem<D, kQueries>::kStages;
+  extern __shared__ __align__(16) unsigned char smem[];
+  ScoreSmem<D, kQueries>& sm = *reinterpret_cast<ScoreSmem<D, kQueries>*>(smem);
   pdl_begin();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kRowLanes, vec = lane % kRowLanes;
   auto count = [&](int s) {
     const int L = a.context_lens[s];
@@ -199,17 +227,29 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries
   };
   const int total = all_units(a.S, a.H, lane, count);
   const int warps = gridDim.x * kScoreWarps;
-  const int id = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const int id = warp * gridDim.x + blockIdx.x;
   const int workers = min(warps, total);
   if (id >= workers) return;
   const int x0 = first_unit(total, workers, id), x1 = first_unit(total, workers, id + 1);
   int rest;
-  int s = find_unit(a.S, a.H, x0, lane, count, &rest);
-  int units = count(s);
-  int h = rest / units, unit = rest % units;
-  int blocks = (a.context_lens[s] + a.B - 1) / a.B;
-  float4 (*qs)[4][kRowLanes] = q_parts[threadIdx.x >> 5];
-  auto load_q_of = [&](const T* base, int g0) {  // base: the head's first query
+  ScoreAt now;
+  now.s = find_unit(a.S, a.H, x0, lane, count, &rest);
+  now.units = count(now.s);
+  now.h = rest / now.units, now.unit = rest % now.units;
+  now.blocks = (a.context_lens[now.s] + a.B - 1) / a.B;
+  ScoreAt then = now;  // of the next copies
+  auto advance = [&](ScoreAt& at) {  // not behind the last unit
+    if (++at.unit < at.units) return;
+    at.unit = 0;
+    if (++at.h == a.H) {
+      at.h = 0;
+      do at.units = count(++at.s);
+      while (at.units == 0);
+      at.blocks = (a.context_lens[at.s] + a.B - 1) / a.B;
+    }
+  };
+  float4 (*qs)[4][kRowLanes] = sm.q[warp];
+  auto load_q = [&](const T* base, int g0) {  // base: the head's first query
     __syncwarp();
     for (int g = sub; g < kQueries; g += kRows) {
       // a query behind the group's last is its last again: the largest score stays
@@ -218,88 +258,79 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries
       unpack8<T>(__ldg(reinterpret_cast<const uint4*>(q) + vec), f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        qs[g][i][vec] = make_float4(fmaxf(f[4 * i], 0.f), fmaxf(f[4 * i + 1], 0.f), fmaxf(f[4 * i + 2], 0.f), fmaxf(f[4 * i + 3], 0.f));
-        qs[g][2 + i][vec] = make_float4(fminf(f[4 * i], 0.f), fminf(f[4 * i + 1], 0.f), fminf(f[4 * i + 2], 0.f), fminf(f[4 * i + 3], 0.f));
+        qs[g][i][vec] = make_float4(fmaxf(f[2 * i], 0.f), fmaxf(f[2 * i + 4], 0.f), fmaxf(f[2 * i + 1], 0.f), fmaxf(f[2 * i + 5], 0.f));
+        qs[g][2 + i][vec] = make_float4(fminf(f[2 * i], 0.f), fminf(f[2 * i + 4], 0.f), fminf(f[2 * i + 1], 0.f), fminf(f[2 * i + 5], 0.f));
       }
     }
     __syncwarp();
   };
-  auto load_q = [&](int g0) { load_q_of(static_cast<const T*>(a.q) + s * a.q_row + static_cast<int64_t>(h) * a.g * D, g0); };
-  bool fresh = true;
-  int known = -1;   // which 32 positions `frame` is of
-  int frame = -1;
-  uint4 lo[kAhead], hi[kAhead];
-  uint32_t good;    // whether each frame of the unit has a good id
-  auto load = [&]() {
-    const int j0 = unit * kUnit;
-    if (fresh || (j0 >> 5) != known) {
-      known = j0 >> 5;
-      const int j = known * 32 + lane;
-      frame = -1;
-      if (j < blocks) {
-        frame = a.block_tables[s * a.bt_row + j];
-        if (frame < 0 || frame >= a.num_blocks) {
-          atomicOr(a.status, kDevBadBlock);
-          frame = -1;
-        }
-      }
-    }
-    good = __ballot_sync(kAll, frame >= 0) >> (j0 & 31);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i * kRows + sub;
-      const int f = __shfl_sync(kAll, frame, j & 31);
-      const uint4* b = static_cast<const uint4*>(a.bounds) + (static_cast<int64_t>(max(f, 0)) * a.H + h) * 2 * kRowLanes + vec;
-      lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-      if (j < blocks) {
-        lo[i] = __ldg(b);
-        hi[i] = __ldg(b + kRowLanes);
-      }
-    }
+  // 32 of the sequence's block ids, a lane each, read a unit before they are used
+  int frame;
+  auto read_ids = [&]() {
+    const int j = (then.unit * kUnit & ~31) + lane;
+    frame = j < then.blocks ? a.block_tables[then.s * a.bt_row + j] : -1;
   };
-  load();
-  for (int x = x0; x < x1; ++x) {
-    if (fresh && a.g <= kQueries) load_q(0);
-    // this unit's numbers, and the next one's on their way while they are used
-    const int j0 = unit * kUnit, its_blocks = blocks;
-    const uint32_t its_good = good;
-    float* out = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks;
-    const T* its_q = static_cast<const T*>(a.q) + s * a.q_row + static_cast<int64_t>(h) * a.g * D;
-    uint4 l[kAhead], u[kAhead];
+  // copies of the next unit's rows, and whether each of its frames has a good id
+  auto copy = [&](int x, int stage) {
+    uint32_t good = 0;
+    if (x < x1) {
+      const int j0 = then.unit * kUnit;
+      if ((j0 & ~31) + lane < then.blocks && (frame < 0 || frame >= a.num_blocks)) {
+        atomicOr(a.status, kDevBadBlock);
+        frame = -1;
+      }
+      good = __ballot_sync(kAll, frame >= 0) >> (j0 & 31);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) l[i] = lo[i], u[i] = hi[i];
-    fresh = false;
-    if (++unit == units) {
-      unit = 0;
-      fresh = true;
-      if (++h == a.H && x + 1 < x1) {
-        h = 0;
-        do units = count(++s);
-        while (units == 0);
-        blocks = (a.context_lens[s] + a.B - 1) / a.B;
+      for (int i = 0; i < kAhead; ++i) {
+        const int f = __shfl_sync(kAll, frame, (j0 + i * kRows + sub) & 31);
+        const uint4* b = static_cast<const uint4*>(a.bounds) + (static_cast<int64_t>(max(f, 0)) * a.H + then.h) * 2 * kRowLanes + vec;
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.rows[warp][stage][i][0][lane]));
+        copy16(to, b, f >= 0);
+        copy16(to + 32 * 16, b + kRowLanes, f >= 0);
+      }
+      if (x + 1 < x1) {
+        advance(then);
+        if (then.unit == 0 || (then.unit * kUnit & 31) == 0) read_ids();
       }
     }
-    if (x + 1 < x1) load();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return good;
+  };
+  read_ids();
+  uint32_t goods[kStages - 1];
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) goods[k] = copy(x0 + k, k);
+  int stage = 0, ahead = kStages - 1;
+  bool fresh = true;
+  for (int x = x0; x < x1; ++x) {
+    const T* its_q = static_cast<const T*>(a.q) + now.s * a.q_row + static_cast<int64_t>(now.h) * a.g * D;
+    if (fresh && a.g <= kQueries) load_q(its_q, 0);
+    const uint32_t good = goods[0];
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) goods[k] = goods[k + 1];
+    goods[kStages - 2] = copy(x + kStages - 1, ahead);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");  // a lane reads what it has copied itself
+    const uint4 (*rows)[2][32] = sm.rows[warp][stage];
     float best = -INFINITY;
     for (int g0 = 0; g0 < a.g; g0 += kQueries) {
-      if (a.g > kQueries) load_q_of(its_q, g0);
+      if (a.g > kQueries) load_q(its_q, g0);
       float y[kQueries][kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         float l8[8], h8[8];
-        unpack8<T>(l[i], l8);
-        unpack8<T>(u[i], h8);
+        unpack8<T>(rows[i][0][lane], l8);
+        unpack8<T>(rows[i][1][lane], h8);
 #pragma unroll
         for (int g = 0; g < kQueries; ++g) {
-          float z[2];
+          uint64_t t[4];  // elements (e, e + 4)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 p = qs[g][e][vec], n = qs[g][2 + e][vec];
-            const float t0 = fmaf(n.x, l8[4 * e], __fmul_rn(p.x, h8[4 * e])), t1 = fmaf(n.y, l8[4 * e + 1], __fmul_rn(p.y, h8[4 * e + 1]));
-            const float t2 = fmaf(n.z, l8[4 * e + 2], __fmul_rn(p.z, h8[4 * e + 2])), t3 = fmaf(n.w, l8[4 * e + 3], __fmul_rn(p.w, h8[4 * e + 3]));
-            z[e] = __fadd_rn(__fadd_rn(t0, t1), __fadd_rn(t2, t3));
+          for (int e = 0; e < 4; e += 2) {
+            const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(&qs[g][e / 2][vec]), n = *reinterpret_cast<const ulonglong2*>(&qs[g][2 + e / 2][vec]);
+            t[e] = fma2(n.x, pair(l8[e], l8[e + 4]), mul2(p.x, pair(h8[e], h8[e + 4])));
+            t[e + 1] = fma2(n.y, pair(l8[e + 1], l8[e + 5]), mul2(p.y, pair(h8[e + 1], h8[e + 5])));
           }
-          y[g][i] = __fadd_rn(z[0], z[1]);
+          const float2 z = both(add2(add2(t[0], t[1]), add2(t[2], t[3])));
+          y[g][i] = __fadd_rn(z.x, z.y);
         }
       }
 #pragma unroll
@@ -315,8 +346,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kQueries == 1 ? 4 : kQueries
         best = fmaxf(best, z);
       }
     }
-    const int at = j0 + (lane & 3) * kRows + sub;  // frame (b1, b0) = step 2 b1 + b0
-    if ((vec & ~3) == 0 && at < its_blocks) out[at] = its_good >> (at - j0) & 1 ? best : -INFINITY;
+    const int at = (lane & 3) * kRows + sub;  // frame (b1, b0) = step 2 b1 + b0
+    const int j = now.unit * kUnit + at;
+    if ((vec & ~3) == 0 && j < now.blocks)
+      a.scores[(static_cast<int64_t>(now.s) * a.H + now.h) * a.max_blocks + j] = good >> at & 1 ? best : -INFINITY;
+    if (x + 1 < x1) advance(now);
+    fresh = now.unit == 0;
+    stage = stage + 1 < kStages ? stage + 1 : 0;
+    ahead = ahead + 1 < kStages ? ahead + 1 : 0;
   }
 }
 
@@ -545,10 +582,11 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
   });
 }
 
-cudaError_t launch_pdl(const void* fn, int64_t grid, int threads, void** args, cudaStream_t stream) {
+cudaError_t launch_pdl(const void* fn, int64_t grid, int threads, void** args, cudaStream_t stream, int smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -561,15 +599,16 @@ cudaError_t launch_pdl(const void* fn, int64_t grid, int threads, void** args, c
 template <typename F>
 const void* ptr(F* f) { return reinterpret_cast<const void*>(f); }
 
-// as many blocks as are resident, and no more than there can be units
-cudaError_t launch_resident(const void* fn, int threads, int64_t units, int num_sms, void** args, cudaStream_t stream) {
+// as many blocks as are resident, at most `most` an SM, and no more than there can be units
+cudaError_t launch_resident(const void* fn, int threads, int64_t units, int num_sms, void** args, cudaStream_t stream, int smem = 0,
+                            int most = 32) {
   int occ = 0;
-  cudaError_t e = kernel_prep(fn, threads, 0, &occ);
+  cudaError_t e = kernel_prep(fn, threads, smem, &occ);
   if (e != cudaSuccess) return e;
   if (occ < 1) return cudaErrorInvalidConfiguration;
-  int64_t grid = static_cast<int64_t>(num_sms) * occ;
+  int64_t grid = static_cast<int64_t>(num_sms) * (occ < most ? occ : most);
   if (units < grid) grid = units < 1 ? 1 : units;
-  return launch_pdl(fn, grid, threads, args, stream);
+  return launch_pdl(fn, grid, threads, args, stream, smem);
 }
 
 }  // namespace
@@ -581,18 +620,26 @@ cudaError_t launch_block_bounds(int dtype, BoundsArgs a, int num_sms, cudaStream
   return launch_resident(fn, 256, static_cast<int64_t>(a.S) * a.H * (a.max_blocks < 1 ? 1 : a.max_blocks), num_sms, args, stream);
 }
 
+template <typename T, int D, int kQueries>
+static const void* score_kernel_of(int* smem, int* blocks) {
+  *blocks = ScoreSmem<D, kQueries>::kBlocks;
+  *smem = sizeof(ScoreSmem<D, kQueries>);
+  return ptr(score_kernel<T, D, kQueries>);
+}
+
 template <typename T>
-static const void* score_fn(int D, int g) {
-  if (D == 128) return g == 1 ? ptr(score_kernel<T, 128, 1>) : g == 2 ? ptr(score_kernel<T, 128, 2>) : ptr(score_kernel<T, 128, 4>);
-  return g == 1 ? ptr(score_kernel<T, 64, 1>) : g == 2 ? ptr(score_kernel<T, 64, 2>) : ptr(score_kernel<T, 64, 4>);
+static const void* score_fn(int D, int g, int* smem, int* blocks) {
+  if (D == 128) return g == 1 ? score_kernel_of<T, 128, 1>(smem, blocks) : g == 2 ? score_kernel_of<T, 128, 2>(smem, blocks) : score_kernel_of<T, 128, 4>(smem, blocks);
+  return g == 1 ? score_kernel_of<T, 64, 1>(smem, blocks) : g == 2 ? score_kernel_of<T, 64, 2>(smem, blocks) : score_kernel_of<T, 64, 4>(smem, blocks);
 }
 
 cudaError_t launch_select_blocks(int dtype, SelectArgs a, int num_sms, cudaStream_t stream, int* launched) {
   void* args[1] = {&a};
   *launched = 0;
   if (a.max_blocks > a.K) {
-    const void* fn = dtype == PA_F16 ? score_fn<__half>(a.D, a.g) : score_fn<__nv_bfloat16>(a.D, a.g);
-    const cudaError_t e = launch_resident(fn, kScoreWarps * 32, static_cast<int64_t>(a.S) * a.H * ((a.max_blocks + 7) / 8), num_sms, args, stream);
+    int smem, blocks;
+    const void* fn = dtype == PA_F16 ? score_fn<__half>(a.D, a.g, &smem, &blocks) : score_fn<__nv_bfloat16>(a.D, a.g, &smem, &blocks);
+    const cudaError_t e = launch_resident(fn, kScoreWarps * 32, static_cast<int64_t>(a.S) * a.H * ((a.max_blocks + 7) / 8), num_sms, args, stream, smem, blocks);
     if (e != cudaSuccess) return e;
     ++*launched;
   }
