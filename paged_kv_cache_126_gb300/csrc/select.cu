@@ -9,7 +9,7 @@
 // ranks in registers, finds the K-th's neighbourhood with one histogram over the scores' range, and
 // orders the few that share its bin.
 //
-// Measured: bounds of 16 prompts of 4096 tokens, 8 heads of 128 in bf16, frames of 32 (143 MB): 27.1 us, 5.25 TB/s;
+// Measured: bounds of 16 prompts of 4096 tokens, 8 heads of 128 in bf16, frames of 32 (143 MB): 25.9 us, 5.5 TB/s;
 // of the tail frames of 64 sequences 4.5 us.  Selection of 64 from 1024 frames for 4 x 32 heads (67 MB of bounds, in
 // 512-byte pieces): 18.6 us; for 32 sequences of 100 to 65,536 tokens with 8 heads of 4 queries (43 MB): 20.3 us,
 // bound by the instructions of four queries a row.
@@ -78,9 +78,12 @@ template <typename T2>
 __device__ __forceinline__ T2 pair_of(uint32_t x) { return *reinterpret_cast<const T2*>(&x); }
 
 // ---- bounds -----------------------------------------------------------------------------------------
-// A unit is one frame of one head: its rows, 32 * 8 / D at a time, as 16-byte vectors.
+// A unit is one frame of one head: its rows, 32 * 8 / D at a time, as 16-byte vectors.  More units than warps: 25.9 us for
+// the prompts where a range each took 27.2; the units of a step spread over all SMs: 4.5 us, by blocks 5.2.
+constexpr int kBoundsWarps = 8;
+
 template <typename T2, int D>
-__global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
+__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsArgs a) {
   constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kAhead = 8;
   pdl_begin();
   const int lane = threadIdx.x & 31;
@@ -90,22 +93,26 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
     return bad_len(L, a.max_blocks, a.B) || first < 0 || first >= L ? 0 : (L + a.B - 1) / a.B - first / a.B;
   };
   const int total = all_units(a.S, a.H, lane, count);
-  const int warps = gridDim.x * 8;
+  const int warps = gridDim.x * kBoundsWarps;
   const int id = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   if (id < a.S) {  // bad lengths are reported by one warp each
     for (int64_t s = id; s < a.S; s += warps)
       if (lane == 0 && (bad_len(a.context_lens[s], a.max_blocks, a.B) || (a.first && a.first[s] < 0)))
         atomicOr(a.status, kDevBadLen);
   }
-  const int workers = min(warps, total);
-  if (id >= workers) return;
-  const int x0 = first_unit(total, workers, id), x1 = first_unit(total, workers, id + 1);
+  int x0, x1;
+  if (total <= warps) {  // one each, over all SMs
+    x0 = id, x1 = min(id + 1, total);
+  } else {  // a range a block, its warps on neighbouring heads of a frame: together they read whole rows of tokens
+    x0 = first_unit(total, gridDim.x, blockIdx.x) + (threadIdx.x >> 5), x1 = first_unit(total, gridDim.x, blockIdx.x + 1);
+  }
+  if (x0 >= x1) return;
   int rest;
   int s = find_unit(a.S, a.H, x0, lane, count, &rest);
   int left = count(s) - rest / a.H, h = rest % a.H;
   int L = a.context_lens[s];
   int j = (L + a.B - 1) / a.B - left;
-  for (int x = x0; x < x1; ++x) {
+  for (int x = x0; x < x1; x += kBoundsWarps) {
     const int frame = a.block_tables[s * a.bt_row + j];
     if (frame < 0 || frame >= a.num_blocks) {
       if (lane == 0) atomicOr(a.status, kDevBadBlock);
@@ -144,10 +151,10 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
             make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
-    if (++h == a.H) {
-      h = 0;
+    if (x + kBoundsWarps >= x1) break;
+    for (h += kBoundsWarps; h >= a.H; h -= a.H) {
       ++j;
-      if (--left == 0 && x + 1 < x1) {
+      if (--left == 0) {
         do left = count(++s);
         while (left == 0);
         L = a.context_lens[s];
@@ -617,7 +624,7 @@ cudaError_t launch_block_bounds(int dtype, BoundsArgs a, int num_sms, cudaStream
   const void* fn = dtype == PA_F16 ? (a.D == 128 ? ptr(block_bounds_kernel<__half2, 128>) : ptr(block_bounds_kernel<__half2, 64>))
                                    : (a.D == 128 ? ptr(block_bounds_kernel<__nv_bfloat162, 128>) : ptr(block_bounds_kernel<__nv_bfloat162, 64>));
   void* args[1] = {&a};
-  return launch_resident(fn, 256, static_cast<int64_t>(a.S) * a.H * (a.max_blocks < 1 ? 1 : a.max_blocks), num_sms, args, stream);
+  return launch_resident(fn, kBoundsWarps * 32, static_cast<int64_t>(a.S) * a.H * (a.max_blocks < 1 ? 1 : a.max_blocks), num_sms, args, stream);
 }
 
 template <typename T, int D, int kQueries>

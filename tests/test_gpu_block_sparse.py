@@ -54,6 +54,20 @@ def test_bounds(pa, dtype, H, D, B):
     assert pa.pa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("H,most", [(5, 700), (1, 4000), (11, 300)])
+def test_bounds_more_units_than_warps(pa, H, most):
+    """Sequences of no, few and many frames: a warp's next frame is heads or several sequences further on."""
+    g = torch.Generator().manual_seed(H)
+    lens = [0, 1, 0, 0, 8, 9] + torch.randint(0, most, (90,), generator=g).tolist() + [3, 0, 0, 17, 0]
+    q, kc, vc, tables, lens = make(lens, H, 1, 64, 8, "f16", H)
+    old = torch.full((kc.shape[0], H, 2, 64), 3.0, dtype=torch.float16, device="cuda")
+    for first in (torch.zeros(len(lens), dtype=torch.int32), (torch.rand(len(lens), generator=g) * 0.3 * lens.cpu()).to(torch.int32)):
+        got = old.clone()
+        pa.pa_block_bounds(kc, tables, lens, first.cuda(), got)
+        assert torch.equal(got, bounds_reference(kc, tables, lens, first.tolist(), old))
+    assert pa.pa_get_device_status() == 0
+
+
 def test_bounds_bad_indexes(pa):
     q, kc, vc, tables, lens = make([100, 50, 40, 30], 2, 1, 64, 16, "f16", 1)
     old = torch.zeros(kc.shape[0], 2, 2, 64, dtype=torch.float16, device="cuda")
