@@ -364,14 +364,12 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
 /*
  * pa_decode_q4 -- pa_decode over the 4-bit cache.  q, out [S, Hq, D]; block_tables,
  * context_lens, scale, empty sequences and status bits as for pa_decode.  Slots that hold no token
- * of a sequence may hold any bits.  fp16 queries: keys and values are the numbers the codes
- * stand for, exact in fp16.  bf16 queries: a key enters its score as step * n + offset
- * without the rounding to fp16 (in a score at most a share of 2^-11 of each product, less
- * than a bf16 output resolves).  q.k and the weighted sums of values run on the tensor
- * cores with fp32 accumulation, softmax in fp32, the weights carried as two fp16 parts for
- * fp16 outputs and as one for bf16, one rounding to the output dtype.  bf16 queries are
- * scaled by a power of two per head to fp16 range; an element below 2^-24 of its head's
- * largest loses bits of weight below 2^-35 of that largest.  PA_ERR_UNSUPPORTED where
+ * of a sequence may hold any bits.  Keys and values are the numbers the codes stand for,
+ * exact in fp16, whatever the queries' type.  q.k and the weighted sums of values run on
+ * the tensor cores with fp32 accumulation, softmax in fp32, the weights carried as two fp16
+ * parts for fp16 outputs and as one for bf16, one rounding to the output dtype.  bf16
+ * queries are scaled by a power of two per head to fp16 range; an element below 2^-31 of its
+ * head's largest loses bits of weight below 2^-39 of that largest.  PA_ERR_UNSUPPORTED where
  * S * H * ceil(max_blocks * B / 64) passes int32.
  */
 int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,

@@ -7,17 +7,16 @@ namespace {
 
 // Weights go to the tensor cores as two fp16 parts where the output is fp16 (one part alone would add an
 // error as large as the output's own rounding); a bf16 output rounds 8 times coarser than one part, so it
-// has one, and keys that are not rounded (LINEAR, see gather_kernel.cuh).
+// has one.
 //
 // 12 warps an SM, three on each scheduler, with one stage of 64 keys: 64 sequences of 512 to 2048 tokens, 32 heads
-// of 128 in fp16 (421 MB) take 98.6 us, 4.3 TB/s; 4 x 16384 in bf16 (336 MB) 66.1 us, 5.1 TB/s, 70.7 with
-// rounded keys.  16 warps (128 registers, spills) 98.8 and 73 us, 10 and 8 warps 105 and 101 us; tiles of 16 keys
+// of 128 in fp16 (421 MB) take 98.7 us, 4.3 TB/s; 4 x 16384 in bf16 (336 MB) 71.0 us, 4.7 TB/s.  16 warps (128 registers, spills) 98.8 and 73 us, 10 and 8 warps 105 and 101 us; tiles of 16 keys
 // with 16 warps 108, of 32 keys with 12 warps 98 us.
 template <typename T, int D>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {
   constexpr bool one = !std::is_same<T, __half>::value;  // bf16
-  using F = gk::Q4Format<T, D, one>;
+  using F = gk::Q4Format<T, D>;
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;

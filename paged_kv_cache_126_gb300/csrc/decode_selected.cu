@@ -38,7 +38,6 @@ struct RowFormat {
   using M = T;
   static constexpr int D = D_;
   static constexpr bool kScaleQ = false;
-  static constexpr int kLift = 0, kCodeScale = 0, kSums = 0;
   static constexpr int kSecond = 8;
   static constexpr uint32_t kHalfTile = 8 * D * 2, kTile = 2 * kHalfTile;
   __device__ __forceinline__ static int key_of(int r) { return r; }

@@ -241,22 +241,12 @@ struct Cut {
 // the difference, and one fused multiply-add with (step, offset) gives the number that the code
 // stands for.  Two codes of a 32-bit word at a time: five logic operations and eight half2
 // operations for eight codes.  Both kinds run at half rate (2 clocks a warp and scheduler), so the
-// 16 + 10 clocks of eight codes, not memory, bound the decode: 71 % of the copy bandwidth for
+// 16 + 10 clocks of eight codes, not memory, bound the decode: 70 % of the copy bandwidth for
 // 4 x 16384 tokens.
-//
-// LINEAR (bf16 outputs): keys skip that.  The masked codes are fp16 as they are, n * 2^-24 (bits 0..3) and n * 2^-20
-// (bits 4..7, their queries scaled by 2^-4): subnormal, exact, and multiplied at full rate.  A score
-// step of the tensor core holds 32 elements of one group, so that
-//     q . k = sum over groups of step * (q . n) + offset * (sum of q)
-// takes one fp32 multiply-add a group and value, and one more score step whose operands are the offsets and the
-// queries' sums (in two parts).  The key's rounding to fp16 is left out: against the codes' numbers a
-// score is off by what that rounding would be, a share of 2^-11 of each product at most, which moves an
-// output by about 2^-12 of its size, a 16th of a bf16 output's own rounding (for fp16 outputs it would
-// be half as much again as theirs, so they keep the exact numbers).
 //
 // Rows of the score tile are keys in an order that spreads the reads over the banks (rows are 80 bytes, 20 banks):
 // keys 0,12,2,14,4,8,6,10,1,13,3,15,5,9,7,11 for the 16-byte reads of K (rows r and r + 1 together)
-// and the 8-byte reads of V (rows 2c); 0..15 for the 4-byte reads of LINEAR and the same of V.
+// and the 8-byte reads of V (rows 2c).
 // (w & mask) | magic in one instruction
 __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
   uint32_t y;
@@ -276,22 +266,19 @@ __device__ __forceinline__ void codes8(uint32_t w, __half2 step, __half2 off, ui
   x[3] = as_u32(__hfma2(y3, step, off));
 }
 
-template <typename T, int D_, bool LINEAR>
+template <typename T, int D_>
 struct Q4Format {
   using In = T;          // queries and outputs
   using M = __half;      // operands of the tensor cores
   static constexpr int D = D_;
-  static constexpr bool kScaleQ = LINEAR || !std::is_same<T, __half>::value;  // queries to fp16 range:
-  static constexpr int kLift = LINEAR ? 14 : 0;       // their largest to 2^kLift .. 2^(kLift + 1),
-  static constexpr int kCodeScale = LINEAR ? 24 : 0;  // and codes count as 2^-kCodeScale
-  static constexpr int kSums = LINEAR ? 1 : 0;        // an operand of the queries' sums behind the queries
+  static constexpr bool kScaleQ = !std::is_same<T, __half>::value;  // queries to fp16 range, by head
   static constexpr int kRow = D / 2 + D / 8;
   static constexpr uint32_t kHalfTile = 8 * kRow, kTile = 16 * kRow;
   static constexpr int kWordsK = D / 32, kWordsV = D / 64;  // words of codes a lane reads of a key
 
   // key of score row r; that of row r + 8 is kSecond further on
-  static constexpr int kSecond = LINEAR ? 8 : 1;
-  __device__ __forceinline__ static int key_of(int r) { return LINEAR ? r : (r & 1) ? ((r + 3) & 7) + 8 : r; }
+  static constexpr int kSecond = 1;
+  __device__ __forceinline__ static int key_of(int r) { return (r & 1) ? ((r + 3) & 7) + 8 : r; }
 
   // The caches as rows of 16 tokens of one head (of 8 where a frame holds 8): four rows a copy.
   struct Maps {
@@ -334,12 +321,12 @@ struct Q4Format {
     }
   }
 
-  // The elements of a query that load_q takes in lane column c: a run of D / 4, or 8 of each group.
+  // The elements of a query that load_q takes in lane column c: a run of D / 4.
   __device__ __forceinline__ static void read_q(const T* q, int c, bool on, float (&x)[D / 4]) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (on) u = *reinterpret_cast<const uint4*>(q + (LINEAR ? 32 * i + 8 * c : c * (D / 4) + 8 * i));
+      if (on) u = *reinterpret_cast<const uint4*>(q + c * (D / 4) + 8 * i);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -349,72 +336,24 @@ struct Q4Format {
       }
     }
   }
-  // B operands for the D / 16 score steps of lane (r, c), and of the sums for the offsets' step: the four groups' sums
-  // rounded (columns 0, 1 of the step's lanes), then what the rounding left over (2, 3).
-  __device__ __forceinline__ static void load_q(const float (&q)[D / 4], int c, uint32_t (&f)[D / 16 + kSums][2]) {
-    constexpr float k = LINEAR ? 0x1p-4f : 1.f;
+  // B operands for the D / 16 score steps of lane (r, c)
+  __device__ __forceinline__ static void load_q(const float (&q)[D / 4], int, uint32_t (&f)[D / 16][2]) {
 #pragma unroll
     for (int w = 0; w < kWordsK; ++w) {
       const float* e = q + 8 * w;
       f[2 * w][0] = pack2<M>(e[0], e[4]);
-      f[2 * w][1] = pack2<M>(e[1] * k, e[5] * k);
+      f[2 * w][1] = pack2<M>(e[1], e[5]);
       f[2 * w + 1][0] = pack2<M>(e[2], e[6]);
-      f[2 * w + 1][1] = pack2<M>(e[3] * k, e[7] * k);
-    }
-    if constexpr (LINEAR) {
-      float sum[4] = {};
-#pragma unroll
-      for (int w = 0; w < kWordsK; ++w) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[w] += q[8 * w + i];
-        sum[w] += __shfl_xor_sync(kAll, sum[w], 1);
-        sum[w] += __shfl_xor_sync(kAll, sum[w], 2);
-        sum[w] *= 0x1p-24f;
-      }
-      const float s0 = c & 1 ? sum[2] : sum[0], s1 = c & 1 ? sum[3] : sum[1];
-      const uint32_t hi = pack2<M>(s0, s1);
-      const float2 back = unpack2<M>(hi);
-      f[D / 16][0] = c < 2 ? hi : pack2<M>(s0 - back.x, s1 - back.y);
-      f[D / 16][1] = 0;
+      f[2 * w + 1][1] = pack2<M>(e[3], e[7]);
     }
   }
 
   template <int NT>
   __device__ __forceinline__ static void scores(uint32_t kst, int r, int c,
-                                                const uint32_t (&qf)[NT][D / 16 + kSums][2], float (&acc)[NT][4]) {
+                                                const uint32_t (&qf)[NT][D / 16][2], float (&acc)[NT][4]) {
     const uint32_t row0 = kst + key_of(r) * kRow, row1 = row0 + kSecond * kRow;
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    if constexpr (LINEAR) {
-      uint32_t p0[kWordsK], p1[kWordsK];  // the groups' (step, offset) of the two keys
-      lds(row0 + D / 2, p0);
-      lds(row1 + D / 2, p1);
-      uint32_t a0 = prmt(p0[0], p0[1], 0x7632), a1 = prmt(p1[0], p1[1], 0x7632);
-      if (c & 1) {
-        a0 = D == 128 ? prmt(p0[kWordsK - 2], p0[kWordsK - 1], 0x7632) : 0;
-        a1 = D == 128 ? prmt(p1[kWordsK - 2], p1[kWordsK - 1], 0x7632) : 0;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mma(acc[n], a0, a1, 0, 0, qf[n][D / 16][0], 0, M());
-#pragma unroll
-      for (int g = 0; g < kWordsK; ++g) {
-        const uint32_t w0 = lds(row0 + 16 * g + 4 * c), w1 = lds(row1 + 16 * g + 4 * c);
-        const uint32_t u0 = w0 >> 8, u1 = w1 >> 8;
-        const float s0 = unpack2<M>(p0[g]).x, s1 = unpack2<M>(p1[g]).x;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float y[4] = {};
-          mma(y, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[n][2 * g][0], qf[n][2 * g][1], M());
-          mma(y, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u, qf[n][2 * g + 1][0],
-              qf[n][2 * g + 1][1], M());
-          acc[n][0] = fmaf(s0, y[0], acc[n][0]);
-          acc[n][1] = fmaf(s0, y[1], acc[n][1]);
-          acc[n][2] = fmaf(s1, y[2], acc[n][2]);
-          acc[n][3] = fmaf(s1, y[3], acc[n][3]);
-        }
-      }
-      return;
-    }
     uint32_t w0[kWordsK], w1[kWordsK];
     lds(row0 + c * (D / 8), w0);
     lds(row1 + c * (D / 8), w1);
@@ -716,7 +655,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   }
   __syncwarp();
 
-  uint32_t qf[NT][D / 16 + F::kSums][2];
+  uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
   Left(*left)[2] = reinterpret_cast<Left(*)[2]>(smem + WARPS * warp_smem<F, NT, STAGES>() + 16);  // side 0: begun before
@@ -759,14 +698,15 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (F::kScaleQ) {
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        // by 2^(kLift - e) with top in [2^e, 2^(e+1)); zero, subnormal and non-finite heads stay as they are
+        // by 2^(14 - e) with top in [2^e, 2^(e+1)): 8 bits of an element down to 2^-31 of top are exact in fp16; zero,
+        // subnormal and non-finite heads stay as they are
         const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         const bool in = top > 0.f && e > -112 && e < 100;
-        const int lift = in ? F::kLift - e : 0;
+        const int lift = in ? 14 - e : 0;
         const float up = __uint_as_float(static_cast<uint32_t>(127 + lift) << 23);
 #pragma unroll
         for (int j = 0; j < D / 4; ++j) x[j] *= up;
-        back *= __uint_as_float(static_cast<uint32_t>(127 + F::kCodeScale - lift) << 23);
+        back *= __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
       }
       F::load_q(x, c, qf[n]);
       f[n][0] = __shfl_sync(kAll, back, 8 * c);       // column 2c is lane row 2c

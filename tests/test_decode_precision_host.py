@@ -1,0 +1,35 @@
+"""The cases of test_gpu_decode_precision.py tell right from wrong: a mistake planted in the plain form leaves their
+tolerance (CPU)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle.operators import attend, values_q4
+from tests._operators_common import TD
+from tests._precision_cases import fine_tolerance, outlying_query, single_products
+
+
+def rounded(x, dtype):
+    return torch.from_numpy(x).to(TD[dtype]).double().numpy()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [1, 4, 8, 16])
+def test_keys_that_are_not_rounded_are_seen(D, g):
+    q, k4, v4 = single_products(2, g, D, 300, D + g)
+    k, v = values_q4(k4), values_q4(v4)
+    tol = fine_tolerance(q, k, v, 1.0, "bf16", 2.0 ** -11)
+    assert (np.abs(rounded(attend(q, k, v, 1.0), "bf16") - attend(q, k, v, 1.0)) <= tol).all()
+    wrong = attend(q, values_q4(k4, rounded=False), v, 1.0)
+    assert (np.abs(wrong - attend(q, k, v, 1.0)) > tol).any()
+
+
+def test_offsets_behind_an_outlying_query_are_seen():
+    q, k4, v4 = outlying_query(2, 4, 128, 300, 1)
+    k, v = values_q4(k4), values_q4(v4)
+    s = k[:, 0] @ q[0]
+    assert np.abs(s).max() > 8                     # the small elements decide the softmax
+    tol = fine_tolerance(q, k, v, 1.0, "bf16", 2.0 ** -11)
+    wrong = attend(np.where(q > 1, q, 0), k, v, 1.0)
+    assert (np.abs(wrong - attend(q, k, v, 1.0)) > tol).any()

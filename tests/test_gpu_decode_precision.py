@@ -1,0 +1,47 @@
+"""Decode over the 4-bit cache and over selected frames where one rounding decides: each case's scores are exact in fp32
+(GPU).  test_decode_precision_host.py shows that the tolerances see the mistakes they are for."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle.operators import attend, values_q4
+from tests._operators_common import TD, host64
+from tests._precision_cases import fine_tolerance, outlying_query, paged_rows, single_products
+
+pytestmark = pytest.mark.gpu
+
+
+def decode_q4(pa, q, k4, v4, scale, dtype, B=16):
+    """pa_decode_q4 of q [Hq, D] over rows [N, H, W] of one sequence -> [Hq, D] in 64 bits."""
+    (kc, t), (vc, _) = (paged_rows(torch.from_numpy(x), B, 1) for x in (k4, v4))
+    kc, vc = (c.transpose(1, 2).contiguous().cuda() for c in (kc, vc))
+    qd = torch.from_numpy(q).to(TD[dtype])[None].cuda()
+    assert np.array_equal(host64(qd[0]), q)
+    out = torch.full_like(qd, float("nan"))
+    lens = torch.tensor([len(k4)], dtype=torch.int32).cuda()
+    pa.pa_decode_q4(qd, kc, vc, t.cuda(), lens, scale, out)
+    assert pa.pa_get_device_status() == 0
+    return host64(out[0])
+
+
+def close(got, q, k, v, scale, dtype, weight_step, weight_tiny=0.0):
+    err, tol = np.abs(got - attend(q, k, v, scale)), fine_tolerance(q, k, v, scale, dtype, weight_step, weight_tiny)
+    assert (err <= tol).all(), (float((err / tol).max()), float(err.max()))
+
+
+# ---- the 4-bit cache's numbers ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [1, 4, 8, 16])
+def test_keys_are_the_numbers_that_codes_stand_for(pa, dtype, D, g):
+    q, k4, v4 = single_products(2, g, D, 300, D + g)
+    close(decode_q4(pa, q, k4, v4, 1.0, dtype), q, values_q4(k4), values_q4(v4), 1.0, dtype, 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22,
+          2.0 ** -25)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [1, 4, 8, 16])
+def test_small_queries_beside_an_outlying_one(pa, D, g):
+    q, k4, v4 = outlying_query(2, g, D, 300, 1)
+    close(decode_q4(pa, q, k4, v4, 1.0, "bf16"), q, values_q4(k4), values_q4(v4), 1.0, "bf16", 2.0 ** -11, 2.0 ** -25)
