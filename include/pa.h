@@ -367,8 +367,7 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
  * of a sequence may hold any bits.  Keys and values are the numbers the codes stand for,
  * exact in fp16, whatever the queries' type.  q.k and the weighted sums of values run on
  * the tensor cores with fp32 accumulation, softmax in fp32, the weights carried as two fp16
- * parts for fp16 outputs and as one for bf16, one rounding to the output dtype.  bf16
- * queries are scaled by a power of two per head to fp16 range; an element below 2^-31 of its
+ * parts, one rounding to the output dtype.  bf16 queries are scaled by a power of two per head to fp16 range; an element below 2^-31 of its
  * head's largest loses bits of weight below 2^-39 of that largest.  PA_ERR_UNSUPPORTED where
  * S * H * ceil(max_blocks * B / 64) passes int32.
  */

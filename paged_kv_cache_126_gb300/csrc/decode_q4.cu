@@ -5,25 +5,22 @@
 namespace pa {
 namespace {
 
-// Weights go to the tensor cores as two fp16 parts where the output is fp16 (one part alone would add an
-// error as large as the output's own rounding); a bf16 output rounds 8 times coarser than one part, so it
-// has one.
+// Weights go to the tensor cores as two fp16 parts: one alone, off by 2^-12 of a weight, would add an error as large as a
+// fp16 output's own rounding, and several times what fp32 sums leave to a bf16 output that the values cancel to near zero.
 //
 // 12 warps an SM, three on each scheduler, with one stage of 64 keys: 64 sequences of 512 to 2048 tokens, 32 heads
-// of 128 in fp16 (421 MB) take 98.7 us, 4.3 TB/s; 4 x 16384 in bf16 (336 MB) 71.0 us, 4.7 TB/s.  16 warps (128 registers, spills) 98.8 and 73 us, 10 and 8 warps 105 and 101 us; tiles of 16 keys
-// with 16 warps 108, of 32 keys with 12 warps 98 us.
+// of 128 in fp16 (421 MB) take 99.0 us, 4.2 TB/s; 4 x 16384 in bf16 (336 MB) 75.1 us, 4.5 TB/s.  16 warps (128 registers,
+// spills) 98.8 us for the first, 10 and 8 warps 105 and 101 us; tiles of 16 keys with 16 warps 108, of 32 keys with 12 warps 98 us.
 template <typename T, int D>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {
-  constexpr bool one = !std::is_same<T, __half>::value;  // bf16
   using F = gk::Q4Format<T, D>;
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4 && !one)
-    return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwinColumns, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, one ? gk::kOnePart : gk::kTwoParts, false, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, false, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

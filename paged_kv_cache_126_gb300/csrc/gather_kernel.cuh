@@ -47,7 +47,8 @@ constexpr int kGroup = 16;       // pieces of one (s, h) are joined in groups of
 constexpr int kFlat = 24;        // up to this many pieces are joined at once
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
 
-enum Parts { kOnePart = 0, kTwinColumns = 1, kTwoParts = 2 };
+// How the second part of the weights gets to the tensor cores: in the second copy of the queries, or as another operand.
+enum Parts { kTwinColumns, kTwoParts };
 
 // ---- instructions -----------------------------------------------------------------------------
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -241,7 +242,7 @@ struct Cut {
 // the difference, and one fused multiply-add with (step, offset) gives the number that the code
 // stands for.  Two codes of a 32-bit word at a time: five logic operations and eight half2
 // operations for eight codes.  Both kinds run at half rate (2 clocks a warp and scheduler), so the
-// 16 + 10 clocks of eight codes, not memory, bound the decode: 70 % of the copy bandwidth for
+// 16 + 10 clocks of eight codes, not memory, bound the decode: 66 % of the copy bandwidth for
 // 4 x 16384 tokens.
 //
 // Rows of the score tile are keys in an order that spreads the reads over the banks (rows are 80 bytes, 20 banks):
@@ -810,12 +811,11 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t hi = pack2<M>(w[2 * j], w[2 * j + 1]);
-              if (PARTS != kOnePart) {  // what the rounding leaves over: `rest` is 1 in the lanes that carry it, else 0
-                const float2 back = unpack2<M>(hi);
-                const uint32_t lo = pack2<M>(fmaf(-rest, back.x, w[2 * j]), fmaf(-rest, back.y, w[2 * j + 1]));
-                if (PARTS == kTwoParts) p[kB - 1][n][j] = transpose8(lo);
-                if (PARTS == kTwinColumns) hi = lo;
-              }
+              // what the rounding leaves over: `rest` is 1 in the lanes that carry it, else 0
+              const float2 back = unpack2<M>(hi);
+              const uint32_t lo = pack2<M>(fmaf(-rest, back.x, w[2 * j]), fmaf(-rest, back.y, w[2 * j + 1]));
+              if (PARTS == kTwoParts) p[kB - 1][n][j] = transpose8(lo);
+              if (PARTS == kTwinColumns) hi = lo;
               p[0][n][j] = transpose8(hi);
             }
           }

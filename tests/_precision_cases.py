@@ -72,6 +72,37 @@ def outlying_query(H, g, D, N, seed):
     return q, k, v
 
 
+def uneven_weights(H, D, part, seed):
+    """64 keys whose weights all round the same way to type `part`, seen from the sign of their values: what that
+    rounding leaves over adds up, while the weighted values cancel.  A score is the sum of elements 0 and 32 of its key,
+    a multiple of 2^-10.  -> keys and values [64, H, D], exact in bf16 and in constant groups of 32."""
+    rng = np.random.default_rng(seed)
+    j = np.arange(1, 1024)
+    w = np.exp(-j / 1024.0)
+    left = (w - torch.from_numpy(w).to(part).double().numpy()) / w
+    eps = torch.finfo(part).eps
+    up, down = j[left > 0.2 * eps], j[left < -0.2 * eps]
+    pairs = []
+    for a in rng.permutation(up):
+        b = down[np.abs(down - a).argmin()]
+        if abs(int(b) - int(a)) <= 40 and all(abs(b - p[1]) > 0 for p in pairs):
+            pairs.append((int(a), int(b)))
+        if len(pairs) == 31:
+            break
+    assert len(pairs) == 31
+    at, sign = [0, 0], [0.0, 0.0]                     # the largest score, twice
+    for a, b in pairs:
+        at += [a, b]
+        sign += [1.0, -1.0]
+    at, sign = np.array(at), np.array(sign)
+    order = np.concatenate([[0], 1 + rng.permutation(63)])
+    k, v = np.zeros((64, H, D)), np.zeros((64, H, D))
+    k[:, :, :32] = -(at[order] // 32 / 32.0)[:, None, None]
+    k[:, :, 32:64] = -(at[order] % 32 / 1024.0)[:, None, None]
+    v[:] = sign[order][:, None, None]
+    return k, v
+
+
 def paged_rows(rows, B, seed):
     """Rows [N, H, W] of one sequence in shuffled frames of B: (cache as [frames, B, H, W], table [1, frames])."""
     n = -(-len(rows) // B)

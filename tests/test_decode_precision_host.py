@@ -7,7 +7,7 @@ import torch
 
 from oracle.operators import attend, values_q4
 from tests._operators_common import TD
-from tests._precision_cases import fine_tolerance, outlying_query, single_products
+from tests._precision_cases import fine_tolerance, outlying_query, single_products, uneven_weights
 
 
 def rounded(x, dtype):
@@ -33,3 +33,17 @@ def test_offsets_behind_an_outlying_query_are_seen():
     tol = fine_tolerance(q, k, v, 1.0, "bf16", 2.0 ** -11)
     wrong = attend(np.where(q > 1, q, 0), k, v, 1.0)
     assert (np.abs(wrong - attend(q, k, v, 1.0)) > tol).any()
+
+
+@pytest.mark.parametrize("part,dtype,step", [("f16", "f16", 2.0 ** -22), ("f16", "bf16", 2.0 ** -22), ("bf16", "bf16", 2.0 ** -16)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_without_their_second_part_are_seen(part, dtype, step, D):
+    k, v = uneven_weights(1, D, TD[part], D)
+    q = np.zeros((1, D))
+    q[0, [0, 32]] = 1.0
+    ref, tol = attend(q, k, v, 1.0), fine_tolerance(q, k, v, 1.0, dtype, step)
+    w = np.exp(k[:, 0] @ q[0])
+    wrong = rounded(w, part) @ v[:, 0] / w.sum()
+    assert (np.abs(wrong - ref[0]) > 2 * tol[0]).all()
+    both = (rounded(w, part) + rounded(w - rounded(w, part), part)) @ v[:, 0] / w.sum()
+    assert (np.abs(rounded(both, dtype) - ref[0]) <= tol[0]).all()

@@ -5,9 +5,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.operators import attend, values_q4
+from oracle.operators import attend, quantise_q4, values_q4
 from tests._operators_common import TD, host64
-from tests._precision_cases import fine_tolerance, outlying_query, paged_rows, single_products
+from tests._precision_cases import fine_tolerance, outlying_query, paged_rows, single_products, uneven_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -25,6 +25,19 @@ def decode_q4(pa, q, k4, v4, scale, dtype, B=16):
     return host64(out[0])
 
 
+def decode_selected(pa, q, k, v, scale, dtype, B=16):
+    """pa_decode_selected of q [Hq, D] over all frames of one sequence's rows [N, H, D] -> [Hq, D] in 64 bits."""
+    (kc, t), (vc, _) = (paged_rows(torch.from_numpy(x).to(TD[dtype]), B, 1) for x in (k, v))
+    qd = torch.from_numpy(q).to(TD[dtype])[None].cuda()
+    assert np.array_equal(host64(qd[0]), q)
+    out = torch.full_like(qd, float("nan"))
+    lens = torch.tensor([len(k)], dtype=torch.int32).cuda()
+    sel = torch.arange(t.shape[1], dtype=torch.int32).repeat(1, k.shape[1], 1).cuda()
+    pa.pa_decode_selected(qd, kc.cuda(), vc.cuda(), t.cuda(), lens, sel, scale, out)
+    assert pa.pa_get_device_status() == 0
+    return host64(out[0])
+
+
 def close(got, q, k, v, scale, dtype, weight_step, weight_tiny=0.0):
     err, tol = np.abs(got - attend(q, k, v, scale)), fine_tolerance(q, k, v, scale, dtype, weight_step, weight_tiny)
     assert (err <= tol).all(), (float((err / tol).max()), float(err.max()))
@@ -36,12 +49,30 @@ def close(got, q, k, v, scale, dtype, weight_step, weight_tiny=0.0):
 @pytest.mark.parametrize("g", [1, 4, 8, 16])
 def test_keys_are_the_numbers_that_codes_stand_for(pa, dtype, D, g):
     q, k4, v4 = single_products(2, g, D, 300, D + g)
-    close(decode_q4(pa, q, k4, v4, 1.0, dtype), q, values_q4(k4), values_q4(v4), 1.0, dtype, 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22,
-          2.0 ** -25)
+    close(decode_q4(pa, q, k4, v4, 1.0, dtype), q, values_q4(k4), values_q4(v4), 1.0, dtype, 2.0 ** -22, 2.0 ** -25)
 
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("g", [1, 4, 8, 16])
 def test_small_queries_beside_an_outlying_one(pa, D, g):
     q, k4, v4 = outlying_query(2, g, D, 300, 1)
-    close(decode_q4(pa, q, k4, v4, 1.0, "bf16"), q, values_q4(k4), values_q4(v4), 1.0, "bf16", 2.0 ** -11, 2.0 ** -25)
+    close(decode_q4(pa, q, k4, v4, 1.0, "bf16"), q, values_q4(k4), values_q4(v4), 1.0, "bf16", 2.0 ** -22, 2.0 ** -25)
+
+
+# ---- the weights -------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("call", ["q4", "selected"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [1, 4, 8, 16])
+def test_weights_keep_their_second_part(pa, call, dtype, D, g):
+    part = "f16" if call == "q4" else dtype
+    k, v = uneven_weights(2, D, TD[part], D + g)
+    q = np.zeros((2 * g, D))
+    q[:, [0, 32]] = 1.0
+    if call == "q4":
+        k4, v4 = (quantise_q4(x.astype(np.float32)) for x in (k, v))
+        assert np.array_equal(values_q4(k4), k) and np.array_equal(values_q4(v4), v)
+        got = decode_q4(pa, q, k4, v4, 1.0, dtype)
+    else:
+        got = decode_selected(pa, q, k, v, 1.0, dtype)
+    close(got, q, k, v, 1.0, dtype, 2.0 ** (-22 if part == "f16" else -16))
