@@ -3,7 +3,7 @@
 //
 // For each sequence s and key head h, with the g query heads that share it:
 //     out = sum_j w_j v_j / sum_j w_j,   w_j = exp2(q . k_j * scale * log2(e) - m),
-// in one pass, m being a running maximum that moves only when a score passes it by 2^8.
+// in one pass, m being a running maximum (less 7) that moves only when a score passes it by 2^8.
 //
 // Work.  A tile is up to four parts of 16 keys of one (s, h): its keys are one copy, its values another,
 // and each is loaded again as soon as the warp has read it.  All tiles of the batch, numbered by
@@ -46,6 +46,9 @@ constexpr int kMinKeys = 64;     // fewest keys that a (s, h) is cut into
 constexpr int kGroup = 16;       // pieces of one (s, h) are joined in groups of this many workers
 constexpr int kFlat = 24;        // up to this many pieces are joined at once
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
+// Weights are 2^kRoom times what they stand for: at most 2^15, which fp16 holds, and as many more of a long context's small
+// ones are above its least number, 2^-24.  (Many keys 2^-24 below one sink were off by half of themselves.)
+constexpr float kRoom = 7.f;
 
 // How the second part of the weights gets to the tensor cores: in the second copy of the queries, or as another operand.
 enum Parts { kTwinColumns, kTwoParts };
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
             for (int u = 1; u < LOADS; ++u) top[n][j] = fmaxf(top[n][j], fmaxf(x[u][n][j], x[u][n][j + 2]));
             over = fmaxf(over, top[n][j] - m[n][j]);
           }
-        if (__any_sync(kAll, over > kSlack)) {
+        if (__any_sync(kAll, over > kSlack + kRoom)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
               float t = top[n][j];
 #pragma unroll
               for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, s));
-              const float now = fmaxf(m[n][j], t);
+              const float now = fmaxf(m[n][j], t - kRoom);
               const float less = m[n][j] == now ? 1.f : dk::ex2(m[n][j] - now);
               m[n][j] = now;
               l[n][j] *= less;

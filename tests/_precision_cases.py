@@ -103,6 +103,15 @@ def uneven_weights(H, D, part, seed):
     return k, v
 
 
+def one_sink(H, D, N):
+    """One key far above all others, its value zero: the output is what the others' small weights leave, each
+    0.69 * 2^-24 of the sink's.  -> keys and values [N, H, D] in constant groups of 32."""
+    k, v = np.full((N, H, D), -17.0), np.ones((N, H, D))
+    k[N // 2], v[N // 2] = 0.0, 0.0
+    k[:, :, 32:] = 0.0
+    return k, v
+
+
 def paged_rows(rows, B, seed):
     """Rows [N, H, W] of one sequence in shuffled frames of B: (cache as [frames, B, H, W], table [1, frames])."""
     n = -(-len(rows) // B)

@@ -7,7 +7,7 @@ import torch
 
 from oracle.operators import attend, values_q4
 from tests._operators_common import TD
-from tests._precision_cases import fine_tolerance, outlying_query, single_products, uneven_weights
+from tests._precision_cases import fine_tolerance, one_sink, outlying_query, single_products, uneven_weights
 
 
 def rounded(x, dtype):
@@ -47,3 +47,14 @@ def test_weights_without_their_second_part_are_seen(part, dtype, step, D):
     assert (np.abs(wrong - ref[0]) > 2 * tol[0]).all()
     both = (rounded(w, part) + rounded(w - rounded(w, part), part)) @ v[:, 0] / w.sum()
     assert (np.abs(rounded(both, dtype) - ref[0]) <= tol[0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_small_weights_in_few_bits_are_seen(dtype):
+    k, v = one_sink(1, 64, 1000)
+    q = np.zeros((1, 64))
+    q[0, 0] = 1.0
+    ref, tol = attend(q, k, v, 1.0), fine_tolerance(q, k, v, 1.0, dtype, 2.0 ** -22, 2.0 ** -32)
+    w = np.exp(k[:, 0] @ q[0])
+    both = rounded(w, "f16") + rounded(w - rounded(w, "f16"), "f16")
+    assert (np.abs(both @ v[:, 0] / w.sum() - ref[0]) > 10 * tol[0]).all()
