@@ -49,6 +49,7 @@ constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running 
 // Weights are 2^kRoom times what they stand for: at most 2^15, which fp16 holds, and as many more of a long context's small
 // ones are above its least number, 2^-24.  (Many keys 2^-24 below one sink were off by half of themselves.)
 constexpr float kRoom = 7.f;
+constexpr float kLeast = -3.402823466e38f;  // a running maximum of no score yet: finite, so that a score of -inf weighs nothing
 
 // How the second part of the weights gets to the tensor cores: in the second copy of the queries, or as another operand.
 enum Parts { kTwinColumns, kTwoParts };
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       F::load_q(x, c, qf[n]);
       f[n][0] = __shfl_sync(kAll, back, 8 * c);       // column 2c is lane row 2c
       f[n][1] = __shfl_sync(kAll, back, 8 * c + 4);
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kLeast;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle.operators import attend, quantise_q4, values_q4
-from tests._operators_common import TD, host64
+from tests._operators_common import TD, attention_tolerance, host64
 from tests._precision_cases import fine_tolerance, one_sink, outlying_query, paged_rows, single_products, uneven_weights
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,25 @@ def test_small_weights_beside_a_sink(pa, call, dtype, N, g):
     q[:, 0] = 1.0
     bf16 = call == "selected" and dtype == "bf16"     # no least number to speak of
     close(decode(pa, call, q, k, v, 1.0, dtype), q, k, v, 1.0, dtype, 2.0 ** (-16 if bf16 else -22), 0.0 if bf16 else 2.0 ** -32)
+
+
+# ---- infinities ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("g", [1, 4, 8, 16])
+def test_scores_of_minus_infinity_weigh_nothing(pa, dtype, g):
+    """The keys of a sequence's first tokens score -inf, over more than a tile; then all of them do."""
+    for first, N in ((1, 20), (20, 40), (40, 3000), (0, 20)):
+        gen = torch.Generator().manual_seed(first + g)
+        k, v = (torch.randn(N, 2, 64, generator=gen).to(TD[dtype]).double().numpy() for _ in range(2))
+        q = torch.randn(2 * g, 64, generator=gen).to(TD[dtype]).double().numpy()
+        q[:, 3] = 1.0
+        k[:first, :, 3] = -np.inf
+        with np.errstate(invalid="ignore"):
+            ref = attend(q, k, v, 0.125)
+        rest = attend(q, k[first:], v[first:], 0.125)
+        assert np.allclose(ref, rest, rtol=1e-12, atol=0)
+        tol = attention_tolerance(rest, TD[dtype], q, k[first:], v[first:], 0.125, 2.0 ** (-22 if dtype == "f16" else -16))
+        err = np.abs(decode_selected(pa, q, k, v, 0.125, dtype) - rest)
+        assert (err <= tol).all(), (first, N, float(err.max()))
+    k[:, :, 3] = -np.inf
+    assert not decode_selected(pa, q, k, v, 0.125, dtype).any()   # as pa_decode leaves it
