@@ -703,11 +703,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (F::kScaleQ) {
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        // by 2^(14 - e) with top in [2^e, 2^(e+1)): 8 bits of an element down to 2^-31 of top are exact in fp16; zero,
-        // subnormal and non-finite heads stay as they are
+        // by 2^(14 - e) with top in [2^e, 2^(e+1)), at most 2^126: 8 bits of an element down to 2^-31 of top are exact in fp16;
+        // zero and non-finite heads stay as they are
         const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        const bool in = top > 0.f && e > -112 && e < 100;
-        const int lift = in ? 14 - e : 0;
+        const int lift = top > 0.f && e < 128 ? min(14 - e, 126) : 0;
         const float up = __uint_as_float(static_cast<uint32_t>(127 + lift) << 23);
 #pragma unroll
         for (int j = 0; j < D / 4; ++j) x[j] *= up;

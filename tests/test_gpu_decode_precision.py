@@ -113,3 +113,17 @@ def test_scores_of_minus_infinity_weigh_nothing(pa, dtype, g):
         assert (err <= tol).all(), (first, N, float(err.max()))
     k[:, :, 3] = -np.inf
     assert not decode_selected(pa, q, k, v, 0.125, dtype).any()   # as pa_decode leaves it
+
+
+# ---- the range of the queries ------------------------------------------------------------------------------
+@pytest.mark.parametrize("power", [120, 110, 99, 16, -100, -112, -120, -126])
+@pytest.mark.parametrize("g", [1, 8])
+def test_queries_over_the_whole_range_of_bf16(pa, power, g):
+    """The same softmax whatever power of two the queries carry and the scale takes back: the same bits."""
+    gen = torch.Generator().manual_seed(g)
+    k4, v4 = (quantise_q4(torch.randn(200, 2, 64, generator=gen).numpy()) for _ in range(2))
+    q = torch.rand(2 * g, 64, generator=gen).add(1.0).bfloat16().double().numpy() * np.where(np.arange(64) % 2, -1.0, 1.0)
+    plain = decode_q4(pa, q, k4, v4, 2.0 ** -3, "bf16")
+    assert np.array_equal(decode_q4(pa, q * 2.0 ** power, k4, v4, 2.0 ** (-3 - power), "bf16"), plain)
+    ref = attend(q, values_q4(k4), values_q4(v4), 2.0 ** -3)
+    assert (np.abs(plain - ref) <= attention_tolerance(ref, torch.bfloat16, q, values_q4(k4), values_q4(v4), 2.0 ** -3, 2.0 ** -22)).all()
