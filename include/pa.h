@@ -21,6 +21,10 @@
  *     decode the affected output rows are written as zeros) and a bit is set in a
  *     sticky per-device status word that pa_get_device_status() reads.  No kernel
  *     traps or asserts.
+ *   - Device calls may come from several threads, onto one stream too: a call's
+ *     launches are enqueued together, and its kernels meet no other call's numbers in
+ *     the workspace of their stream.  Two exceptions: pa_decode_static (one array for
+ *     all callers, see there) and pa_step_decode (one thread a stream).
  *   - Cache layout [MW "The Architecture at a Glance"]: k_cache and v_cache are
  *     separate contiguous tensors [num_blocks, block_size, num_heads, head_dim];
  *     token i of a sequence sits at frame table[i / block_size], offset

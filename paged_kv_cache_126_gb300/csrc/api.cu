@@ -200,23 +200,35 @@ constexpr size_t kSchedBytes = 256;
 constexpr size_t kMinCntBytes = 64 * 1024;
 
 struct Workspace {
+  std::mutex mu;  // held by a call from the workspace it is given to its last launch
   void* ptr = nullptr;
   size_t bytes = 0;
   size_t cnt_bytes = 0;  // size of the arrival-counter region
   bool zeroed = false;   // the counter regions hold zeros
 };
-std::mutex g_ws_mu;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+// Locks are taken in this order: g_ws_mu (the map), a workspace's own, g_old_mu (the list of old buffers).
+std::mutex g_ws_mu, g_old_mu;
+std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;  // entries stay until the process ends
 std::vector<std::pair<int, void*>> g_ws_old;  // (device, buffer) that captured graphs may still use
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Returns the workspace base and the size of its arrival-counter region (>= cnt_need).
-int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, void** out, size_t* cnt_bytes) {
-  std::lock_guard<std::mutex> lk(g_ws_mu);
+// A call's use of its stream's workspace.  What its kernels pass to one another there must not meet another call's on the
+// same stream, so the workspace is held until the call has enqueued all of them: a second thread's call waits.
+struct Scratch {
+  unsigned char* ptr = nullptr;
+  size_t cnt_bytes = 0;  // size of the arrival-counter region (>= what was asked for)
+  std::unique_lock<std::mutex> held;
+};
+
+int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, Scratch* out) {
   Workspace* wp = nullptr;
   try {  // no C++ exception crosses the C ABI
-    wp = &g_ws[{dev, stream}];
+    {
+      std::lock_guard<std::mutex> lk(g_ws_mu);
+      wp = &g_ws[{dev, stream}];
+    }
+    out->held = std::unique_lock<std::mutex>(wp->mu);
   } catch (...) {
     return PA_ERR_HOST_MEMORY;
   }
@@ -237,6 +249,7 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
     if (w.ptr && w.cnt_bytes < cnt) cnt = std::max(cnt, 2 * w.cnt_bytes);
     // whole 2 MB pages: what a process that watches its free memory sees of it
     const size_t bytes = std::max(std::max(kSchedBytes + cnt + rest_bytes, static_cast<size_t>(2) << 20), 2 * w.bytes);
+    std::lock_guard<std::mutex> lk(g_old_mu);
     try {
       g_ws_old.reserve(g_ws_old.size() + 1);
     } catch (...) {
@@ -257,8 +270,8 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
     if (cudaMemsetAsync(w.ptr, 0, kSchedBytes + w.cnt_bytes, stream) != cudaSuccess) return PA_ERR_CUDA;
     w.zeroed = true;
   }
-  *out = w.ptr;
-  *cnt_bytes = w.cnt_bytes;
+  out->ptr = static_cast<unsigned char*>(w.ptr);
+  out->cnt_bytes = w.cnt_bytes;
   return PA_OK;
 }
 
@@ -407,7 +420,10 @@ int pa_get_device_status(pa_stream stream, int32_t* status_out) {
     // mark every workspace of this device unknown, so its next use zeroes them.
     std::lock_guard<std::mutex> lk(g_ws_mu);
     for (auto& kv : g_ws)
-      if (kv.first.first == dev) kv.second.zeroed = false;
+      if (kv.first.first == dev) {
+        std::lock_guard<std::mutex> held(kv.second.mu);
+        kv.second.zeroed = false;
+      }
   }
   *status_out = v;
   return PA_OK;
@@ -443,17 +459,22 @@ int pa_shutdown(void) {
   int prev = -1;
   cudaGetDevice(&prev);
   for (auto& kv : g_ws) {
-    if (kv.second.ptr) {
+    Workspace& w = kv.second;
+    std::lock_guard<std::mutex> held(w.mu);
+    if (w.ptr) {
       cudaSetDevice(kv.first.first);
-      cudaFree(kv.second.ptr);
+      cudaFree(w.ptr);
     }
+    w.ptr = nullptr;
+    w.bytes = w.cnt_bytes = 0;
+    w.zeroed = false;
   }
+  std::lock_guard<std::mutex> old_lk(g_old_mu);
   for (auto& old : g_ws_old) {
     cudaSetDevice(old.first);
     cudaFree(old.second);
   }
   g_ws_old.clear();
-  g_ws.clear();
   if (prev >= 0) cudaSetDevice(prev);
   return PA_OK;
 }
@@ -628,12 +649,11 @@ int pa_decode_split(const pa_tensor* q, const pa_tensor* k_cache, const pa_tenso
   a.status = g_dev[dev].status;
   const size_t items = static_cast<size_t>(S * groups * NP);
   const size_t rest = NP > 1 ? items * hg * (2 + static_cast<size_t>(D)) * sizeof(float) : 0;
-  void* ws = nullptr;
-  size_t cnt_bytes = 0;
-  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, rest, &ws, &cnt_bytes));
-  a.sched = static_cast<int32_t*>(ws);
+  Scratch ws;
+  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, rest, &ws));
+  a.sched = reinterpret_cast<int32_t*>(ws.ptr);
   if (NP > 1) {
-    float* base = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kSchedBytes + cnt_bytes);
+    float* base = reinterpret_cast<float*>(ws.ptr + kSchedBytes + ws.cnt_bytes);
     a.ws_ml = base;
     a.ws_o = base + items * hg * 2;
   }
@@ -768,18 +788,16 @@ int decode_shared(int dev, const pa_tensor* q, const pa_tensor* k_cache, const p
   const int64_t slot_bytes = H * (D + 2) * static_cast<int64_t>(sizeof(float));
   part_cap = std::max<int64_t>(2 * S, std::min<int64_t>(part_cap, (static_cast<int64_t>(1) << 32) / slot_bytes));
   a.part_cap = static_cast<int32_t>(part_cap);
+  Scratch ws;  // held over both launches
   {
     const size_t o_bytes = static_cast<size_t>(part_cap * H * D) * sizeof(float);
     const size_t ml_bytes = static_cast<size_t>(part_cap * H * 2) * sizeof(float);
     const size_t lcp_bytes = static_cast<size_t>(S) * sizeof(int32_t);
     // arrival counters: parts finished per (sequence, head), for the in-kernel merges
     const size_t cnt_need = static_cast<size_t>(S * H) * sizeof(int32_t);
-    void* ws = nullptr;
-    size_t cnt_bytes = 0;
-    PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), cnt_need, o_bytes + ml_bytes + lcp_bytes, &ws,
-                     &cnt_bytes));
-    unsigned char* w = static_cast<unsigned char*>(ws);
-    unsigned char* rest = w + kSchedBytes + cnt_bytes;
+    PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), cnt_need, o_bytes + ml_bytes + lcp_bytes, &ws));
+    unsigned char* w = ws.ptr;
+    unsigned char* rest = w + kSchedBytes + ws.cnt_bytes;
     a.sched = reinterpret_cast<int32_t*>(w);
     a.ws_cnt = reinterpret_cast<int32_t*>(w + kSchedBytes);
     a.ws_o = reinterpret_cast<float*>(rest);
@@ -996,10 +1014,9 @@ int pa_decode_ex(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
     }
     if (rc == kTooManySeqs) return PA_ERR_UNSUPPORTED;
     PA_TRY(rc);
-    void* ws = nullptr;
-    size_t cnt_bytes = 0;
-    PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), pl.cnt_need, pl.o_bytes + pl.ml_bytes, &ws, &cnt_bytes));
-    place_scratch(&pl, static_cast<unsigned char*>(ws), cnt_bytes);
+    Scratch ws;
+    PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), pl.cnt_need, pl.o_bytes + pl.ml_bytes, &ws));
+    place_scratch(&pl, ws.ptr, ws.cnt_bytes);
     if (dispatch_decode(pl.a, pl.c, pl.tk, pl.tv, static_cast<cudaStream_t>(stream), false, nullptr) != cudaSuccess)
       return PA_ERR_CUDA;
     g_launches.fetch_add(1);
@@ -1073,10 +1090,9 @@ int pa_prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_
   PA_TRY(make_sw128_map(&tq, q->data, dt, T, H, D, q->stride[0], 128));
   PA_TRY(make_frame_map(&tk, k_cache->data, dt, nb * B, H, D, static_cast<int>(B)));
   PA_TRY(make_frame_map(&tv, v_cache->data, dt, nb * B, H, D, static_cast<int>(B)));
-  void* ws = nullptr;
-  size_t cnt_bytes = 0;
-  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, 0, &ws, &cnt_bytes));
-  a.sched = static_cast<int32_t*>(ws);
+  Scratch ws;
+  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, 0, &ws));
+  a.sched = reinterpret_cast<int32_t*>(ws.ptr);
   const int grid = g_dev[dev].num_sms;
   for (int64_t s0 = 0; s0 < S; s0 += chunk) {
     const int64_t n = std::min(chunk, S - s0);
@@ -1598,16 +1614,12 @@ bool tiles_fit(const pa::GatherArgs& a, int64_t most_of_one) {
 
 // Workspace of a gathered decode on `workers` warps: an arrival counter per (sequence, head) and two per group
 // of 16 workers, and as many partials as workers and groups have sides.
-int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, pa::GatherArgs* a) {
+int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, Scratch* ws, pa::GatherArgs* a) {
   const size_t groups = 2 * (static_cast<size_t>(workers) / 16 + 1);
   const size_t slots = (2 * static_cast<size_t>(workers) + groups) * a->g;
-  void* ws = nullptr;
-  size_t cnt_bytes = 0;
-  PA_TRY(workspace(dev, stream, (static_cast<size_t>(a->S) * a->H + groups) * sizeof(int32_t), slots * (D + 2) * sizeof(float),
-                   &ws, &cnt_bytes));
-  unsigned char* base = static_cast<unsigned char*>(ws);
-  a->cnt = reinterpret_cast<int32_t*>(base + kSchedBytes);
-  a->ws_o = reinterpret_cast<float*>(base + kSchedBytes + cnt_bytes);
+  PA_TRY(workspace(dev, stream, (static_cast<size_t>(a->S) * a->H + groups) * sizeof(int32_t), slots * (D + 2) * sizeof(float), ws));
+  a->cnt = reinterpret_cast<int32_t*>(ws->ptr + kSchedBytes);
+  a->ws_o = reinterpret_cast<float*>(ws->ptr + kSchedBytes + ws->cnt_bytes);
   a->ws_ml = a->ws_o + slots * D;
   return PA_OK;
 }
@@ -1667,7 +1679,8 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
   PA_TRY(make_q4_map(&tk, k_cache->data, z.nb, z.H, z.B, z.D));
   PA_TRY(make_q4_map(&tv, v_cache->data, z.nb, z.H, z.B, z.D));
   if (pa::launch_decode_q4(q->dtype, D, a, tk, tv, sms, st, &workers) != cudaSuccess) return PA_ERR_CUDA;
-  PA_TRY(gather_scratch(dev, st, z.D, workers, &a));
+  Scratch ws;
+  PA_TRY(gather_scratch(dev, st, z.D, workers, &ws, &a));
   if (pa::launch_decode_q4(q->dtype, D, a, tk, tv, sms, st, nullptr) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(1);
@@ -1703,7 +1716,8 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
   int workers = 0;
   if (pa::launch_decode_selected(q->dtype, static_cast<int>(D), a, tk, tv, g_dev[dev].num_sms, st, &workers) != cudaSuccess)
     return PA_ERR_CUDA;
-  PA_TRY(gather_scratch(dev, st, D, workers, &a));
+  Scratch ws;
+  PA_TRY(gather_scratch(dev, st, D, workers, &ws, &a));
   if (pa::launch_decode_selected(q->dtype, static_cast<int>(D), a, tk, tv, g_dev[dev].num_sms, st, nullptr) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(1);
@@ -1795,11 +1809,10 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
   a.keep_first = keep_first;
   a.keep_last = keep_last;
   a.status = g_dev[dev].status;
-  void* ws = nullptr;
-  size_t cnt_bytes = 0;
+  Scratch ws;  // held over both launches
   const size_t scores = static_cast<size_t>(S * H) * std::max<int64_t>(a.max_blocks, 1) * sizeof(float);
-  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, scores, &ws, &cnt_bytes));
-  a.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kSchedBytes + cnt_bytes);
+  PA_TRY(workspace(dev, static_cast<cudaStream_t>(stream), 0, scores, &ws));
+  a.scores = reinterpret_cast<float*>(ws.ptr + kSchedBytes + ws.cnt_bytes);
   int launched = 0;
   if (pa::launch_select_blocks(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream), &launched) != cudaSuccess)
     return PA_ERR_CUDA;
