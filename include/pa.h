@@ -446,8 +446,10 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
 
 /* Synchronises `stream` (and then the device), returns the current device's sticky
  * PA_DEV_* bits in *status_out and clears them.  When PA_DEV_TIMEOUT was set, the
- * scheduler and arrival counters of every workspace of this device are re-zeroed on
- * their next use (a block that gave up may have left them non-zero). */
+ * scheduler and arrival counters of every workspace of this device are zeroed before it
+ * returns (a block that gave up may have left them non-zero), also of those that only
+ * captured graphs still use; PA_ERR_CUDA, with *status_out written, where that fails.  A
+ * graph must not be replayed between a timeout and this call. */
 int pa_get_device_status(pa_stream stream, int32_t* status_out);
 
 /* Human-readable name of a return code (static storage). */
@@ -610,6 +612,12 @@ int pa_bm_num_seqs(const pa_bm* bm, int32_t* n_out);
  * next pa_get_device_status.  Takes about two seconds; the context stays usable.
  * Errors: PA_ERR_INVALID (result_out NULL), PA_ERR_CUDA. */
 int pa_selftest_wait_timeout(int64_t* result_out, pa_stream stream);
+
+/* Self-test of what pa_get_device_status does about a timeout: synchronises the device, leaves
+ * the counters of all its workspaces non-zero, as blocks that gave up may, and sets
+ * PA_DEV_TIMEOUT.  No launch may follow before pa_get_device_status.
+ * Errors: PA_ERR_CUDA, PA_ERR_HOST_MEMORY. */
+int pa_selftest_raise_counters(void);
 
 /* Snapshot of the whole manager into caller buffers (parity checks against a reference
  * manager, debugging, inspection), the state the "Reference Implementation" of

@@ -43,6 +43,7 @@ from ._binding import (  # noqa: F401
     pa_decode_selected,
     pa_step_decode,
     pa_get_device_status,
+    pa_selftest_raise_counters,
     pa_selftest_wait_timeout,
     pa_launch_count,
     pa_shutdown,

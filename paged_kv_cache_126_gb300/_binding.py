@@ -121,6 +121,7 @@ def _load():
         "pa_bm_usage": ([vp, C.POINTER(PaBmUsage)], C.c_int),
         "pa_bm_export": ([vp, i64p, i32p, i64p, i32p, i32p, i32p, C.c_int32, C.c_int64, i32p, i64p, i32p], C.c_int),
         "pa_selftest_wait_timeout": ([i64p, vp], C.c_int),
+        "pa_selftest_raise_counters": ([], C.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -141,7 +142,7 @@ EXPORTED = (
     "pa_bm_fork_many", "pa_bm_free_many", "pa_step_decode", "pa_bm_usage", "pa_selftest_wait_timeout",
     "pa_bm_export",
     "pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",
-    "pa_select_blocks", "pa_decode_selected",
+    "pa_select_blocks", "pa_decode_selected", "pa_selftest_raise_counters",
 )
 
 
@@ -409,6 +410,12 @@ def pa_selftest_wait_timeout(stream=None) -> list:
     _check(LIB.pa_selftest_wait_timeout(res.ctypes.data_as(C.POINTER(C.c_int64)), C.c_void_p(s.cuda_stream)),
            "pa_selftest_wait_timeout")
     return res.tolist()
+
+
+def pa_selftest_raise_counters() -> None:
+    """``pa_selftest_raise_counters``: leave the device's workspace counters as after a timeout, for a test of
+    ``pa_get_device_status``, which has to follow."""
+    _check(LIB.pa_selftest_raise_counters(), "pa_selftest_raise_counters")
 
 
 def pa_launch_count() -> int:

@@ -209,7 +209,12 @@ struct Workspace {
 // Locks are taken in this order: g_ws_mu (the map), a workspace's own, g_old_mu (the list of old buffers).
 std::mutex g_ws_mu, g_old_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;  // entries stay until the process ends
-std::vector<std::pair<int, void*>> g_ws_old;  // (device, buffer) that captured graphs may still use
+struct OldBuffer {
+  int dev;
+  void* ptr;
+  size_t cnt_bytes;
+};
+std::vector<OldBuffer> g_ws_old;  // buffers that captured graphs may still use
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -260,7 +265,7 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
       cudaGetLastError();
       return PA_ERR_CUDA;
     }
-    if (w.ptr) g_ws_old.emplace_back(dev, w.ptr);
+    if (w.ptr) g_ws_old.push_back({dev, w.ptr, w.cnt_bytes});
     w.ptr = p;
     w.bytes = bytes;
     w.cnt_bytes = cnt;
@@ -273,6 +278,32 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
   out->ptr = static_cast<unsigned char*>(w.ptr);
   out->cnt_bytes = w.cnt_bytes;
   return PA_OK;
+}
+
+// Sets every byte of the counters of a device's workspaces, the old buffers' among them, once everything enqueued
+// on the device has run; calls that use one wait meanwhile.
+int set_counters(int dev, int byte) {
+  std::lock_guard<std::mutex> lk(g_ws_mu);
+  std::vector<std::unique_lock<std::mutex>> held;
+  try {
+    for (auto& kv : g_ws)
+      if (kv.first.first == dev) held.emplace_back(kv.second.mu);
+  } catch (...) {
+    return PA_ERR_HOST_MEMORY;
+  }
+  std::lock_guard<std::mutex> old_lk(g_old_mu);
+  bool ok = cudaDeviceSynchronize() == cudaSuccess;
+  for (auto& kv : g_ws) {
+    Workspace& w = kv.second;
+    if (kv.first.first != dev || !w.ptr) continue;
+    const bool set = cudaMemset(w.ptr, byte, kSchedBytes + w.cnt_bytes) == cudaSuccess;
+    w.zeroed = set;  // if not: zeroed by its next call
+    ok = ok && set;
+  }
+  for (const OldBuffer& old : g_ws_old)
+    if (old.dev == dev) ok = cudaMemset(old.ptr, byte, kSchedBytes + old.cnt_bytes) == cudaSuccess && ok;
+  ok = cudaDeviceSynchronize() == cudaSuccess && ok;
+  return ok ? PA_OK : PA_ERR_CUDA;
 }
 
 // ---- validation helpers ---------------------------------------------------------------------
@@ -415,15 +446,10 @@ int pa_get_device_status(pa_stream stream, int32_t* status_out) {
   if (cudaMemset(g_dev[dev].status, 0, sizeof(v)) != cudaSuccess) return PA_ERR_CUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return PA_ERR_CUDA;
   if (v & PA_DEV_TIMEOUT) {
-    // A block that gave up a wait may have left scheduler or arrival counters
-    // non-zero.  Nothing of this library runs on the device now (synchronised above):
-    // mark every workspace of this device unknown, so its next use zeroes them.
-    std::lock_guard<std::mutex> lk(g_ws_mu);
-    for (auto& kv : g_ws)
-      if (kv.first.first == dev) {
-        std::lock_guard<std::mutex> held(kv.second.mu);
-        kv.second.zeroed = false;
-      }
+    // A block that gave up a wait may have left scheduler or arrival counters non-zero.  A captured graph goes on
+    // using its buffer without a call of this library, so they are zeroed here and now, in old buffers too.
+    *status_out = v;
+    return set_counters(dev, 0);
   }
   *status_out = v;
   return PA_OK;
@@ -453,6 +479,14 @@ int pa_selftest_wait_timeout(int64_t* result_out, pa_stream stream) {
   return PA_OK;
 }
 
+int pa_selftest_raise_counters(void) {
+  int dev;
+  PA_TRY(current_device(&dev));
+  PA_TRY(set_counters(dev, 1));
+  const int32_t v = PA_DEV_TIMEOUT;
+  return cudaMemcpy(g_dev[dev].status, &v, sizeof(v), cudaMemcpyHostToDevice) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 int pa_shutdown(void) {
   release_step_stages();
   std::lock_guard<std::mutex> lk(g_ws_mu);
@@ -471,8 +505,8 @@ int pa_shutdown(void) {
   }
   std::lock_guard<std::mutex> old_lk(g_old_mu);
   for (auto& old : g_ws_old) {
-    cudaSetDevice(old.first);
-    cudaFree(old.second);
+    cudaSetDevice(old.dev);
+    cudaFree(old.ptr);
   }
   g_ws_old.clear();
   if (prev >= 0) cudaSetDevice(prev);
