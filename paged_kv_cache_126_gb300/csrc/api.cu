@@ -191,11 +191,10 @@ int make_half_rows_map(CUtensorMap* map, void* base, int dtype, int64_t rows, in
 // Layout: [0, 256) scheduler counters | arrival counters, one per (sequence, head) |
 // per-launch offsets and split partials.  Both counter regions must hold zeros
 // when a launch starts; every decode launch leaves them zero.  They are zeroed when
-// first allocated.  A buffer keeps its address and its layout for good: a CUDA graph
-// captured from a call goes on using the buffer that the call was given, and its counters
-// stay where they were.  A call that needs more gets a new, larger buffer, and the old one
-// waits for pa_shutdown (each is at least twice the one before, so all old ones together
-// are smaller than the one in use).
+// first allocated or grown into.  Once a call under capture was given a buffer, that keeps its address and its
+// layout for good: the graph goes on using it, and its counters stay where they were.  A call
+// that needs more then gets another buffer, twice as large where there is room (so that all old ones together stay
+// smaller than the one in use), and the old one waits for pa_shutdown.  A buffer of no graph is freed instead.
 constexpr size_t kSchedBytes = 256;
 constexpr size_t kMinCntBytes = 64 * 1024;
 
@@ -205,6 +204,7 @@ struct Workspace {
   size_t bytes = 0;
   size_t cnt_bytes = 0;  // size of the arrival-counter region
   bool zeroed = false;   // the counter regions hold zeros
+  bool captured = false; // a graph may use it
 };
 // Locks are taken in this order: g_ws_mu (the map), a workspace's own, g_old_mu (the list of old buffers).
 std::mutex g_ws_mu, g_old_mu;
@@ -238,43 +238,77 @@ int workspace(int dev, cudaStream_t stream, size_t cnt_need, size_t rest_bytes, 
     return PA_ERR_HOST_MEMORY;
   }
   Workspace& w = *wp;
-  size_t cnt = std::max(round256(cnt_need), std::max(w.cnt_bytes, kMinCntBytes));
-  const bool small = !w.ptr || w.cnt_bytes < cnt || w.bytes < kSchedBytes + cnt + rest_bytes;
-  if (small || !w.zeroed) {
-    // Under capture an allocation would end the capture with an error, and counters zeroed by the graph would not be
-    // zero for a call made before its first replay.
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
-      cudaGetLastError();
-      return PA_ERR_CUDA;
-    }
-    if (cap != cudaStreamCaptureStatusNone) return PA_ERR_SCRATCH_LIMIT;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {  // the legacy stream beside a capture: the launch will tell
+    cudaGetLastError();
+    status = cudaStreamCaptureStatusNone;
   }
-  if (small) {
-    if (w.ptr && w.cnt_bytes < cnt) cnt = std::max(cnt, 2 * w.cnt_bytes);
+  const bool capturing = status != cudaStreamCaptureStatusNone;
+  const size_t cnt = std::max(round256(cnt_need), std::max(w.cnt_bytes, kMinCntBytes));
+  const size_t need = kSchedBytes + cnt + rest_bytes;
+  const bool fits = w.ptr && w.bytes >= need;
+  if (capturing) {
+    // Under capture an allocation would end the capture with an error, and zeros of a memset that only the graph
+    // does would not be there for a call made before its first replay.
+    if (!fits || !w.zeroed) return PA_ERR_SCRATCH_LIMIT;
+    // Counters where other calls have partials: zeroed by the graph itself, before each use.
+    if (cnt > w.cnt_bytes && cudaMemsetAsync(static_cast<unsigned char*>(w.ptr) + kSchedBytes + w.cnt_bytes, 0, cnt - w.cnt_bytes,
+                                             stream) != cudaSuccess)
+      return PA_ERR_CUDA;
+    w.captured = true;
+    out->ptr = static_cast<unsigned char*>(w.ptr);
+    out->cnt_bytes = cnt;
+    return PA_OK;
+  }
+  if (!fits || (w.captured && cnt > w.cnt_bytes)) {
     // whole 2 MB pages: what a process that watches its free memory sees of it
-    const size_t bytes = std::max(std::max(kSchedBytes + cnt + rest_bytes, static_cast<size_t>(2) << 20), 2 * w.bytes);
-    std::lock_guard<std::mutex> lk(g_old_mu);
-    try {
-      g_ws_old.reserve(g_ws_old.size() + 1);
-    } catch (...) {
-      return PA_ERR_HOST_MEMORY;
+    const size_t bytes = std::max(need, static_cast<size_t>(2) << 20);
+    if (w.captured) {
+      std::lock_guard<std::mutex> lk(g_old_mu);
+      try {
+        g_ws_old.reserve(g_ws_old.size() + 1);
+      } catch (...) {
+        return PA_ERR_HOST_MEMORY;
+      }
+      void* p = nullptr;
+      size_t got = std::max(bytes, 2 * w.bytes);
+      if (cudaMalloc(&p, got) != cudaSuccess) {
+        cudaGetLastError();
+        got = bytes;
+        if (cudaMalloc(&p, got) != cudaSuccess) {
+          cudaGetLastError();
+          return PA_ERR_CUDA;
+        }
+      }
+      g_ws_old.push_back({dev, w.ptr, w.cnt_bytes});
+      w.ptr = p;
+      w.bytes = got;
+    } else {
+      if (w.ptr) {
+        // the old buffer may still be used by earlier launches on this stream
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return PA_ERR_CUDA;
+        cudaFree(w.ptr);
+        w.ptr = nullptr;
+        w.bytes = w.cnt_bytes = 0;
+      }
+      if (cudaMalloc(&w.ptr, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        w.ptr = nullptr;
+        return PA_ERR_CUDA;
+      }
+      w.bytes = bytes;
     }
-    void* p = nullptr;
-    if (cudaMalloc(&p, bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return PA_ERR_CUDA;
-    }
-    if (w.ptr) g_ws_old.push_back({dev, w.ptr, w.cnt_bytes});
-    w.ptr = p;
-    w.bytes = bytes;
     w.cnt_bytes = cnt;
-    w.zeroed = false;
+    w.zeroed = w.captured = false;
   }
+  unsigned char* counters = static_cast<unsigned char*>(w.ptr) + kSchedBytes;
   if (!w.zeroed) {
-    if (cudaMemsetAsync(w.ptr, 0, kSchedBytes + w.cnt_bytes, stream) != cudaSuccess) return PA_ERR_CUDA;
-    w.zeroed = true;
+    if (cudaMemsetAsync(w.ptr, 0, kSchedBytes + cnt, stream) != cudaSuccess) return PA_ERR_CUDA;
+  } else if (cnt > w.cnt_bytes) {
+    if (cudaMemsetAsync(counters + w.cnt_bytes, 0, cnt - w.cnt_bytes, stream) != cudaSuccess) return PA_ERR_CUDA;
   }
+  w.cnt_bytes = cnt;
+  w.zeroed = true;
   out->ptr = static_cast<unsigned char*>(w.ptr);
   out->cnt_bytes = w.cnt_bytes;
   return PA_OK;
@@ -501,7 +535,7 @@ int pa_shutdown(void) {
     }
     w.ptr = nullptr;
     w.bytes = w.cnt_bytes = 0;
-    w.zeroed = false;
+    w.zeroed = w.captured = false;
   }
   std::lock_guard<std::mutex> old_lk(g_old_mu);
   for (auto& old : g_ws_old) {
