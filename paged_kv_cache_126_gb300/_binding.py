@@ -3,8 +3,8 @@
 Every device operation runs in libpa's CUDA kernels; this module turns torch
 tensors into ``pa_tensor`` descriptors and return codes into exceptions.  The calls of
 the rotary, 4-bit and block-sparse operators take many tensors and are marshalled by the
-extension module ``_marshal`` instead of ctypes.  If ``libpa.so`` or ``_marshal.so`` is
-missing the import fails: there is no fallback path.
+extension module ``_marshal`` instead of ctypes, loaded by the first of them.  If ``libpa.so`` is missing the
+import fails, if ``_marshal.so`` is missing or of another torch these calls: there is no fallback path.
 """
 
 from __future__ import annotations
@@ -324,13 +324,25 @@ def _load_marshal():
     spec = importlib.util.spec_from_file_location("_marshal", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
+    if mod.torch_version != torch.__version__.split("+")[0]:
+        raise ImportError(f"{path} was built against torch {mod.torch_version}, this is {torch.__version__}; build it again "
+                          "(python paged_kv_cache_126_gb300/build.py)")
     for name in ("pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",
                  "pa_select_blocks", "pa_decode_selected"):
         mod.bind(name, C.cast(getattr(LIB, name), C.c_void_p).value)
     return mod
 
 
-_marshal = _load_marshal()
+class _Unloaded:
+    """Stands for ``_marshal`` until one of its functions is asked for."""
+
+    def __getattr__(self, name):
+        global _marshal
+        _marshal = _load_marshal()
+        return getattr(_marshal, name)
+
+
+_marshal = _Unloaded()
 
 
 def pa_cache_append_rope(k_new, v_new, slot_mapping, k_cache, v_cache, positions, cos_sin, q=None, q_out=None,

@@ -3,12 +3,13 @@
 Each source is compiled to an object in parallel (one -gencode, -lineinfo), then
 linked into ``paged_kv_cache_126_gb300/libpa.so``; ``csrc/marshal.cpp`` becomes
 ``paged_kv_cache_126_gb300/_marshal.so`` beside it.  A rebuild happens only when a
-source or header is newer than the libraries.
+source or header is newer than the libraries, or torch is another than _marshal was built against.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -21,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_TORCH = os.path.join(BUILD, "_marshal.torch")  # the torch version that _marshal.so was built against
 
 SOURCES = ["block_manager.cpp", "api.cu", "append.cu", "decode_f16.cu", "decode_bf16.cu", "decode_f32.cu",
            "prefill.cu", "decode_split.cu", "decode_shared.cu", "rotary.cu", "decode_q4.cu", "decode_selected.cu",
@@ -42,9 +44,21 @@ def _inputs():
     return files
 
 
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+
+        return torch.__version__
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL) or not os.path.exists(MARSHAL_TORCH):
         return True
+    with open(MARSHAL_TORCH) as f:
+        if f.read() != _torch_version():
+            return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
@@ -83,6 +97,8 @@ def _build_marshal() -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for marshal.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_TORCH, "w") as f:
+        f.write(_torch_version())
     return MARSHAL
 
 
