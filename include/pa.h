@@ -420,7 +420,8 @@ int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, con
  *                 than K frames.
  * Bounds and queries must be finite (a NaN or infinite score ranks somewhere, no more is
  * said).  A bad length or frame id sets its status bit; a bad L_s selects nothing, a frame
- * with a bad id ranks last.  Uses the (device, stream) workspace for the scores,
+ * with a bad id ranks last (kept ones and those of a list that takes all frames are listed;
+ * pa_decode_selected gives zero rows for them).  Uses the (device, stream) workspace for the scores,
  * 4 * S * H * max_blocks bytes.
  */
 int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tensor* block_tables,

@@ -434,6 +434,10 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
   const int blocks = (L + a.B - 1) / a.B;
   if (!scored(a, blocks)) {
     for (int j = threadIdx.x; j < a.K; j += kThreads) sel[j] = j < blocks ? j : -1;
+    for (int j = threadIdx.x; h == 0 && j < blocks; j += kThreads) {  // no score has looked at these
+      const int frame = a.block_tables[s * a.bt_row + j];
+      if (frame < 0 || frame >= a.num_blocks) atomicOr(a.status, kDevBadBlock);
+    }
     return;
   }
   const float* scores = a.scores + (static_cast<int64_t>(s) * a.H + h) * a.max_blocks;
