@@ -37,14 +37,13 @@
 
 #include "decode_kernel.cuh"
 #include "pa_internal.h"
+#include "ranges.h"
 
 namespace pa {
 namespace gk {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kMinKeys = 64;     // fewest keys that a (s, h) is cut into
 constexpr int kGroup = 16;       // pieces of one (s, h) are joined in groups of this many workers
-constexpr int kFlat = 24;        // up to this many pieces are joined at once
 constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running maximum
 // Weights are 2^kRoom times what they stand for: at most 2^15, which fp16 holds, and as many more of a long context's small
 // ones are above its least number, 2^-24.  (Many keys 2^-24 below one sink were off by half of themselves.)
@@ -138,7 +137,7 @@ __device__ __forceinline__ int checked_len(const GatherArgs& a, int s) {
 // Parts of 16 keys of a sequence or list (16 slots of a listed frame, or two frames of 8); at least one.
 template <bool SEL>
 __device__ __forceinline__ int parts_of(const GatherArgs& a, int L) {
-  if (!SEL) return max(1, (max(L, 0) + 15) >> 4);
+  if (!SEL) return parts16(L);
   const int n = min(a.K, (max(L, 0) + a.B - 1) >> a.log2_B);
   return max(1, a.B >= 16 ? n << (a.log2_B - 4) : (n + 1) >> 1);
 }
@@ -226,19 +225,6 @@ __device__ __forceinline__ TilePlan plan_tiles(const GatherArgs& a, const Cursor
   if (n1 == 0) p.frame[1] = -2;
   return p;
 }
-
-// How a batch's tiles are cut: worker w has the tiles floor(w total / workers) .. floor((w + 1) total / workers) - 1.
-struct Cut {
-  int total, workers, per, rest;  // total = per * workers + rest; workers^2 < 2^31
-  __device__ __forceinline__ int start(int w) const { return w * per + static_cast<int>(static_cast<unsigned>(w * rest) / workers); }
-  // the worker of tile x: a division in fp32 is off by at most one
-  __device__ __forceinline__ int owner(int x) const {
-    int w = min(workers - 1, static_cast<int>((x + 0.5f) * (static_cast<float>(workers) / total)));
-    if (start(w) > x) --w;
-    if (w + 1 < workers && start(w + 1) <= x) ++w;
-    return w;
-  }
-};
 
 // ---- formats: how a tile is loaded and multiplied ------------------------------------------------
 // 4-bit rows of D / 2 bytes of codes and D / 8 bytes of (step, offset) pairs.  A code n is made fp16 by
@@ -570,25 +556,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     total += __reduce_add_sync(kAll, n);
   }
   total *= a.H;  // the host has checked that all this stays in int32
-  // A join costs as much as about 128 keys: shorter (s, h) are left whole (64 keys of 8 heads: 7.6 us, cut in two
-  // 8.8).  Fewer keys a worker where the pieces can still be joined at once (512 keys of 8 heads in pieces of 32 keys
-  // 9.1 us, of 64 10.7; 4096 keys 17.3 and 15.8).
-  const int pairs = a.S * a.H, all_warps = gridDim.x * WARPS;
-  const int tiles = min(total / pairs, 1 << 20);  // of a (s, h), on average
-  const int min_keys = tiles * (16 * LOADS) <= 128 ? 128 : tiles * (16 * LOADS) <= kFlat * (kMinKeys / 2) ? kMinKeys / 2 : kMinKeys;
-  Cut cut;
-  cut.workers = min(all_warps, max(pairs, total / max(1, min_keys / (16 * LOADS))));
-  // no more workers than the longest range needs: fewer pieces in the same time (1 x 16000 tokens: 24 -> 18 us)
-  const int longest = (total + cut.workers - 1) / cut.workers;
-  cut.workers = (total + longest - 1) / longest;
-  // A multiple of the (s, h) where that leaves few warps idle: sequences of one length are then cut at their ends
-  // (64 listed frames for 4 x 32 heads: 22.7 -> 19.8 us).
-  if (cut.workers / pairs * pairs * 10 >= cut.workers * 9) cut.workers = cut.workers / pairs * pairs;
+  const int all_warps = gridDim.x * WARPS;
+  const Cut cut = cut_tiles(total, a.S * a.H, all_warps, 16 * LOADS);
   const int id = warp * gridDim.x + blockIdx.x;  // few workers: spread over the blocks
   if (blockIdx.x >= cut.workers) return;
-  cut.total = total;
-  cut.per = total / cut.workers;
-  cut.rest = total - cut.per * cut.workers;
   const int b0 = cut.start(min(id, cut.workers));
   const int count = cut.start(min(id + 1, cut.workers)) - b0;  // 0: no worker
 

@@ -22,6 +22,7 @@
 #include "pa.h"
 #include "pa_internal.h"
 #include "pair32.cuh"
+#include "ranges.h"
 
 namespace pa {
 namespace {
@@ -66,12 +67,6 @@ __device__ __forceinline__ int all_units(int S, int per, int lane, Count count) 
   for (int s0 = 0; s0 < S; s0 += 32) total += __reduce_add_sync(kAll, s0 + lane < S ? count(s0 + lane) : 0);
   return total * per;
 }
-// First unit of worker w where `total` units are cut evenly among `workers` (< 2^15 of them).
-__device__ __forceinline__ int first_unit(int total, int workers, int w) {
-  const int per = total / workers;
-  return w * per + static_cast<int>(static_cast<unsigned>(w * (total - per * workers)) / workers);
-}
-
 template <typename T2>
 __device__ __forceinline__ uint32_t bits(T2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 template <typename T2>
@@ -104,7 +99,10 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
   if (total <= warps) {  // one each, over all SMs
     x0 = id, x1 = min(id + 1, total);
   } else {  // a range a block, its warps on neighbouring heads of a frame: together they read whole rows of tokens
-    x0 = first_unit(total, gridDim.x, blockIdx.x) + (threadIdx.x >> 5), x1 = first_unit(total, gridDim.x, blockIdx.x + 1);
+    x0 = first_unit(total, gridDim.x, blockIdx.x), x1 = first_unit(total, gridDim.x, blockIdx.x + 1);
+    const int warp = threadIdx.x >> 5;
+    if (x1 - x0 <= warp) return;  // x0 + warp may pass int32
+    x0 += warp;
   }
   if (x0 >= x1) return;
   int rest;
@@ -151,7 +149,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
             make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
-    if (x + kBoundsWarps >= x1) break;
+    if (x1 - x <= kBoundsWarps) break;
     for (h += kBoundsWarps; h >= a.H; h -= a.H) {
       ++j;
       if (--left == 0) {
@@ -433,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) top_kernel(const SelectArgs a) {
   }
   const int blocks = (L + a.B - 1) / a.B;
   if (!scored(a, blocks)) {
-    for (int j = threadIdx.x; j < a.K; j += kThreads) sel[j] = j < blocks ? j : -1;
+    for (int64_t j = threadIdx.x; j < a.K; j += kThreads) sel[j] = j < blocks ? static_cast<int>(j) : -1;  // K may be INT32_MAX
     for (int j = threadIdx.x; h == 0 && j < blocks; j += kThreads) {  // no score has looked at these
       const int frame = a.block_tables[s * a.bt_row + j];
       if (frame < 0 || frame >= a.num_blocks) atomicOr(a.status, kDevBadBlock);
