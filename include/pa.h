@@ -415,7 +415,7 @@ int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, con
  *   q             [S, Hq, D];  bounds [num_blocks, H, 2, D] of the same dtype.
  *   block_tables, context_lens  as for pa_decode, at most 2^20 columns;  block_size = B of
  *                 the cache.
- *   selected      int32 [S, H, K], K >= 1, inner stride 1: positions in the sequence's
+ *   selected      int32 [S, H, K], K >= 1, inner stride 1, no two lists overlapping: positions in the sequence's
  *                 block table, ascending; -1 behind the last where the sequence has fewer
  *                 than K frames.
  * Bounds and queries must be finite (a NaN or infinite score ranks somewhere, no more is

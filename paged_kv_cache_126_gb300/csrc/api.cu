@@ -1850,6 +1850,7 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
   const int64_t S = q->shape[0];
   PA_TRY(check_tables(block_tables, context_lens, S, B));
   PA_TRY(check_selected(selected, S, H));
+  if (S > 1 && selected->stride[0] < (H - 1) * selected->stride[1] + selected->shape[2]) return PA_ERR_STRIDE;  // lists overlap
   if (S * H * g > INT32_MAX || block_tables->shape[1] > 1 << 20 || S * H * block_tables->shape[1] > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   if (S == 0) return PA_OK;
