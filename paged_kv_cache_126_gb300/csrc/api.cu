@@ -1641,9 +1641,8 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
 namespace {
 
 // Arguments that pa_decode_q4 and pa_decode_selected share, checked; *S = 0: nothing to do.
-int gather_args(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
-                const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* out, float scale,
-                int64_t nb, int64_t H, int64_t B, int64_t D, pa::GatherArgs* a) {
+int gather_args(const pa_tensor* q, const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* out,
+                float scale, int64_t nb, int64_t H, int64_t B, int64_t D, pa::GatherArgs* a) {
   std::memset(a, 0, sizeof(*a));
   if (!q || !out) return PA_ERR_INVALID;
   const int dt = q->dtype;
@@ -1659,8 +1658,6 @@ int gather_args(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v
   a->out = out->data;
   a->q_row = q->stride[0];
   a->out_row = out->stride[0];
-  a->k_cache = static_cast<const unsigned char*>(k_cache->data);
-  a->v_cache = static_cast<const unsigned char*>(v_cache->data);
   a->block_tables = static_cast<const int32_t*>(block_tables->data);
   a->bt_row = block_tables->stride[0];
   a->context_lens = static_cast<const int32_t*>(context_lens->data);
@@ -1734,7 +1731,7 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
   Q4Shape z;
   PA_TRY(check_q4_caches(k_cache, v_cache, &z));
   pa::GatherArgs a;
-  PA_TRY(gather_args(q, k_cache, v_cache, block_tables, context_lens, out, scale, z.nb, z.H, z.B, z.D, &a));
+  PA_TRY(gather_args(q, block_tables, context_lens, out, scale, z.nb, z.H, z.B, z.D, &a));
   if (a.S == 0) return PA_OK;
   if (!tiles_fit(a, (static_cast<int64_t>(a.max_blocks) * a.B + 63) / 64)) return PA_ERR_UNSUPPORTED;
   int dev;
@@ -1766,7 +1763,7 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
     return PA_ERR_UNSUPPORTED;
   if (!q || q->dtype != k_cache->dtype) return q ? PA_ERR_DTYPE : PA_ERR_INVALID;
   pa::GatherArgs a;
-  PA_TRY(gather_args(q, k_cache, v_cache, block_tables, context_lens, out, scale, nb, H, B, D, &a));
+  PA_TRY(gather_args(q, block_tables, context_lens, out, scale, nb, H, B, D, &a));
   PA_TRY(check_selected(selected, a.S, H));
   if (a.S == 0) return PA_OK;
   int dev;

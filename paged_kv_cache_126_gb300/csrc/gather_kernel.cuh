@@ -264,7 +264,7 @@ struct Q4Format {
   static constexpr int D = D_;
   static constexpr bool kScaleQ = !std::is_same<T, __half>::value;  // queries to fp16 range, by head
   static constexpr int kRow = D / 2 + D / 8;
-  static constexpr uint32_t kHalfTile = 8 * kRow, kTile = 16 * kRow;
+  static constexpr uint32_t kTile = 16 * kRow;
   static constexpr int kWordsK = D / 32, kWordsV = D / 64;  // words of codes a lane reads of a key
 
   // key of score row r; that of row r + 8 is kSecond further on

@@ -247,7 +247,6 @@ struct GatherArgs {
   const void* q;                // [S, g * H, D], row stride q_row elements
   void* out;
   int64_t q_row, out_row;
-  const unsigned char *k_cache, *v_cache;
   const int32_t* block_tables;  // [S, max_blocks], row stride bt_row
   int64_t bt_row;
   const int32_t* context_lens;  // [S]
