@@ -327,7 +327,8 @@ int pa_decode_static(const pa_tensor* q, const pa_tensor* k_cache, const pa_tens
  *   q, q_out    [T, Hq, D] (cache dtype) or both NULL; rows as for k_new, any Hq >= 1.
  *               q_out may be q itself.  A token whose slot is < 0 or out of range still
  *               has its query rotated.
- *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin) in fp32, rounded once.
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin) in fp32, each product and each sum
+ *   rounded by itself, then once to the cache's type.
  * D * element size must be a multiple of 16 and at most 512 bytes, else
  * PA_ERR_UNSUPPORTED.  Slots within one call must be distinct.
  */

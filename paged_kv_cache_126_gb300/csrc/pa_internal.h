@@ -224,6 +224,7 @@ struct RopeArgs {
   int64_t num_slots;
   int32_t T, H, Hq, D, B, R, P, interleaved;
   int32_t log2_B;                 // 4-bit caches
+  float minus_zero;               // set by the launcher: -0 (pair32.cuh)
   int32_t V, per_V, at_once, warps_q, warps_k;  // set by the launcher: vectors of a row, 2^16 / V, rows of a warp, warps of a token's rows
   int32_t* status;
 };

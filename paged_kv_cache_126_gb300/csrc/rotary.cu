@@ -17,9 +17,9 @@
 // since a row is loaded by one warp before any of it is stored, q_out may be q.
 //
 // Bound by memory: 16 chunks of 512 tokens, 32 query and 8 key heads of 128 in bf16 (206 MB) take
-// 32.6 us, 6.3 TB/s; into the 4-bit cache (178 MB) 36.6 us, where the codes of keys and values take more instructions
-// than all queries; read back (44 MB) 9.4 us.  A decode step of 64 tokens (3.2 MB) takes 2.6 us, a launch.
-// 34.8 and 41.8 us without two fp32 numbers an instruction; 37.0 and 44.7 where a block's four warps were parts of one token,
+// 33.1 us, 6.2 TB/s; into the 4-bit cache (178 MB) 37.2 us, where the codes of keys and values take more instructions
+// than all queries; read back (44 MB) 9.5 us.  A decode step of 64 tokens (3.2 MB) takes 2.6 us, a launch.
+// 34.8 and 41.8 us without two fp32 numbers an instruction (32.6 and 36.6 when its products were fused into its sums); 37.0 and 44.7 where a block's four warps were parts of one token,
 // whose kind and rows were then each lane's to compute.  Two steps a warp (44 us), six (34.3 us) and warps that
 // stay and load their next rows meanwhile (51 us) were slower.
 #include <cuda_bf16.h>
@@ -39,7 +39,8 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSteps = 4;  // row steps a warp loads at once
 // Small blocks: a block's place is free again as soon as its four warps are done (36.9 us where 256 threads took 39.6).
-// Nine blocks an SM, 56 registers (two of the 16-bit append's spilled): 32.6 us for 16 chunks of 512 tokens; eight 33.7, ten (more
+// Nine blocks an SM, 56 registers (one or two of the 16-bit append's spilled): 33.1 us for 16 chunks of 512 tokens; with fused
+// products nine 32.6, eight 33.7, ten (more
 // spills) 33.5.  The 4-bit append spills about 20 registers at nine and was not tried at fewer.
 constexpr int kThreads = 128;
 constexpr int kBlocks = 9;
@@ -153,7 +154,7 @@ __device__ __forceinline__ uint32_t quantise8(const float* x, uint32_t* params) 
   uint64_t n2[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t t = mul2(add2(p[i], noff2), inv2);
+    const uint64_t t = mul2(add2(p[i], noff2), inv2);  // (fused into the next sum or not: within the margin below)
     n2[i] = add2(add2(t, round2), back2);
     const float2 d = both(fma2(n2[i], minus2, t));
     half_way = fmaxf(half_way, fmaxf(fabsf(d.x), fabsf(d.y)));
@@ -280,9 +281,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
           float y[N];
           Vec<T>::unpack(shfl4(u[i], partner), y);
           if (rot) {
+            const uint64_t none2 = pair(a.minus_zero, a.minus_zero);
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
-              const float2 z = both(add2(mul2(pair(x[j], x[j + 1]), pair(c[j], c[j + 1])), mul2(pair(y[j], y[j + 1]), pair(s[j], s[j + 1]))));
+              const float2 z = both(add2(rounded2(pair(x[j], x[j + 1]), pair(c[j], c[j + 1]), none2), rounded2(pair(y[j], y[j + 1]), pair(s[j], s[j + 1]), none2)));
               x[j] = z.x, x[j + 1] = z.y;
             }
           }
@@ -419,6 +421,7 @@ cudaError_t launch_rope_append(int dtype, bool q4, RopeArgs a, cudaStream_t stre
   a.warps_q = a.q ? static_cast<int>(warps_of(a.Hq, a.at_once)) : 0;
   a.warps_k = static_cast<int>(warps_of(a.H, a.at_once));
   a.per_V = 65536 / a.V + 1;
+  a.minus_zero = -0.f;
   const int tokens = (a.T + kThreads / 32 - 1) / (kThreads / 32), rows = tokens < 65535 ? tokens : 65535;
   const dim3 grid(a.warps_q + 2 * a.warps_k, rows, (tokens + rows - 1) / rows);
   void* args[1] = {&a};
