@@ -8,9 +8,10 @@ namespace {
 // Weights go to the tensor cores as two fp16 parts: one alone, off by 2^-12 of a weight, would add an error as large as a
 // fp16 output's own rounding, and several times what fp32 sums leave to a bf16 output that the values cancel to near zero.
 //
-// 12 warps an SM, three on each scheduler, with one stage of 64 keys (168 registers, five or six of them spilled at D = 128): 64 sequences of 512 to 2048 tokens, 32 heads
-// of 128 in fp16 (421 MB) take 99.0 us, 4.2 TB/s; 4 x 16384 in bf16 (336 MB) 75.1 us, 4.5 TB/s.  16 warps (128 registers,
-// spills) 98.8 us for the first, 10 and 8 warps 105 and 101 us; tiles of 16 keys with 16 warps 108, of 32 keys with 12 warps 98 us.
+// 12 warps an SM, three on each scheduler, with one stage of 64 keys (168 registers, five or six of them spilled at
+// D = 128): 64 sequences of 512 to 2048 tokens, 32 heads of 128 in fp16 (421 MB) take 98.9 us, 4.3 TB/s; 4 x 16384 in bf16
+// (336 MB) 74.7 us, 4.5 TB/s.  16 warps (128 registers, spills) 98.8 us for the first, 10 and 8 warps 105 and 101 us; tiles of 16
+// keys with 16 warps 108, of 32 keys with 12 warps 98 us.
 template <typename T, int D>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {

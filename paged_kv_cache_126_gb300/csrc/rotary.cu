@@ -40,8 +40,8 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSteps = 4;  // row steps a warp loads at once
 // Small blocks: a block's place is free again as soon as its four warps are done (36.9 us where 256 threads took 39.6).
 // Nine blocks an SM, 56 registers (one or two of the 16-bit append's spilled): 33.1 us for 16 chunks of 512 tokens; with fused
-// products nine 32.6, eight 33.7, ten (more
-// spills) 33.5.  The 4-bit append spills about 20 registers at nine and was not tried at fewer.
+// products nine 32.6, eight 33.7, ten (more spills) 33.5.  The 4-bit append spills about 20 registers at nine and was not
+// tried at fewer.
 constexpr int kThreads = 128;
 constexpr int kBlocks = 9;
 
