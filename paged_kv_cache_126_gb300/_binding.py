@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes as C
 import importlib.util
 import os
+import re
 
 import numpy as np
 import torch
@@ -324,7 +325,8 @@ def _load_marshal():
     spec = importlib.util.spec_from_file_location("_marshal", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
-    if mod.torch_version != torch.__version__.split("+")[0]:
+    release = re.match(r"[\d.]*\d", torch.__version__)[0]  # without what marks a nightly or a local build
+    if ".".join(release.split(".")[:3]) != mod.torch_version:
         raise ImportError(f"{path} was built against torch {mod.torch_version}, this is {torch.__version__}; build it again "
                           "(python paged_kv_cache_126_gb300/build.py)")
     for name in ("pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",

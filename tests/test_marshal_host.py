@@ -44,6 +44,17 @@ def test_another_torch_is_refused(pa):
     assert res.returncode == 0, res.stdout + res.stderr
 
 
+@pytest.mark.parametrize("suffix", ["", "+cu130", "a0+gitabc123", ".dev20260101+cu130", "rc2"])
+def test_the_same_release_under_other_names_is_taken(pa, monkeypatch, suffix):
+    import torch
+
+    import paged_kv_cache_126_gb300._binding as b
+
+    release = b._load_marshal().torch_version
+    monkeypatch.setattr(torch, "__version__", release + suffix)
+    assert b._load_marshal().torch_version == release
+
+
 def test_another_torch_is_rebuilt_for(pa, tmp_path, monkeypatch):
     mod = _build_module()
     assert not mod.is_stale()
