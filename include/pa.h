@@ -372,8 +372,9 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
  * of a sequence may hold any bits.  Keys and values are the numbers the codes stand for,
  * exact in fp16, whatever the queries' type.  q.k and the weighted sums of values run on
  * the tensor cores with fp32 accumulation, softmax in fp32, the weights carried as two fp16
- * parts, one rounding to the output dtype.  bf16 queries are scaled by a power of two per head to fp16 range; an element below 2^-31 of its
- * head's largest loses bits of weight below 2^-39 of that largest.  PA_ERR_UNSUPPORTED where
+ * parts, one rounding to the output dtype.  bf16 queries are scaled by a power of two per
+ * head to fp16 range; an element below 2^-31 of its head's largest loses bits of weight
+ * below 2^-39 of that largest.  PA_ERR_UNSUPPORTED where
  * S * H * ceil(max_blocks * B / 64) passes int32.
  */
 int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
@@ -396,7 +397,8 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
  *                 token are left as they were.
  * PA_ERR_UNSUPPORTED where S * H * max_blocks passes int32 (here and in pa_select_blocks).
  * first_tokens[s] >= L_s: nothing for s.  first_tokens[s] < 0 or a bad L_s:
- * PA_DEV_BAD_LEN, nothing for s.  A NaN key element counts for neither bound unless the
+ * PA_DEV_BAD_LEN, nothing for s.  Sequences that share a frame must hold the same tokens of
+ * it, as forks do until copy-on-write.  A NaN key element counts for neither bound unless the
  * frame holds no other.
  */
 int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, const pa_tensor* context_lens,
@@ -416,14 +418,14 @@ int pa_block_bounds(const pa_tensor* k_cache, const pa_tensor* block_tables, con
  *   q             [S, Hq, D];  bounds [num_blocks, H, 2, D] of the same dtype.
  *   block_tables, context_lens  as for pa_decode, at most 2^20 columns;  block_size = B of
  *                 the cache.
- *   selected      int32 [S, H, K], K >= 1, inner stride 1, no two lists overlapping: positions in the sequence's
- *                 block table, ascending; -1 behind the last where the sequence has fewer
- *                 than K frames.
+ *   selected      int32 [S, H, K], K >= 1, inner stride 1, no two lists overlapping:
+ *                 positions in the sequence's block table, ascending; -1 behind the last
+ *                 where the sequence has fewer than K frames.
  * Bounds and queries must be finite (a NaN or infinite score ranks somewhere, no more is
  * said).  A bad length or frame id sets its status bit; a bad L_s selects nothing, a frame
  * with a bad id ranks last (kept ones and those of a list that takes all frames are listed;
- * pa_decode_selected gives zero rows for them).  Uses the (device, stream) workspace for the scores,
- * 4 * S * H * max_blocks bytes.
+ * pa_decode_selected gives zero rows for them).  Uses the (device, stream) workspace for
+ * the scores, 4 * S * H * max_blocks bytes.
  */
 int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tensor* block_tables,
                      const pa_tensor* context_lens, int32_t block_size, int32_t keep_first,
