@@ -448,6 +448,89 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
                        const pa_tensor* block_tables, const pa_tensor* context_lens,
                        const pa_tensor* selected, float scale, const pa_tensor* out, pa_stream stream);
 
+/* ===================================================================================
+ * Windows and the 8-bit cache: what bounds the cost of a long context
+ * ===================================================================================
+ * Heads, types, sizes and workspaces as for the calls above (q and out hold Hq = g * H heads,
+ * 1 <= g <= 16). */
+
+/*
+ * pa_decode_window -- pa_decode over the last `window` tokens of a sequence and its first `sinks`: token j of
+ * L_s is attended where j >= L_s - window or j < sinks.
+ *
+ *   q, out        [S, Hq, D];  k_cache, v_cache [num_blocks, B, H, D], same dtype.
+ *   block_tables, context_lens, scale, empty sequences and status bits as for pa_decode; only the
+ *                 entries of frames that hold an attended token are read, so that the others may be
+ *                 given up (any value).
+ *   window >= 1 (a window of at least L_s is every token), sinks >= 0, else PA_ERR_INVALID.
+ * Slots that hold no attended token may hold any bits.  Arithmetic as for pa_decode_selected.
+ * PA_ERR_UNSUPPORTED where S * H times a sequence's parts of 16 attended tokens (ceil(window / 16) + ceil(sinks / 16) + 1,
+ * or one more than max_blocks * B / 16) passes int32.
+ */
+int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                     const pa_tensor* block_tables, const pa_tensor* context_lens, int32_t window, int32_t sinks,
+                     float scale, const pa_tensor* out, pa_stream stream);
+
+/*
+ * pa_prefill_window -- pa_prefill where the query at position p attends j <= p with j > p - window or j < sinks,
+ * and query heads share key heads.
+ *
+ *   q, out        [T, Hq, 128] fp16/bf16;  the other arguments, arithmetic, errors and status bits as for
+ *                 pa_prefill.  Entries of frames that hold no token attended by a query of the call are not read.
+ *   window >= 1, sinks >= 0, scale > 0 and finite, else PA_ERR_INVALID.
+ */
+int pa_prefill_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                      const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* query_start,
+                      int32_t window, int32_t sinks, float scale, const pa_tensor* out, pa_stream stream);
+
+/* ---- the 8-bit cache: k_cache, v_cache PA_U8 [num_blocks, H, B, D], contiguous, and k_scale, v_scale
+ * PA_F32 [num_blocks, H], the step of each (frame, head), inner stride 1, row stride free.  A byte b, 1 .. 255, stands
+ * for (b - 128) * step.  Copy-on-write: pa_copy_blocks for the caches, and for the steps as frames
+ * [num_blocks, 1, 1, H] (H a multiple of 4, or rows allocated so). */
+
+/*
+ * pa_cache_append_q8 -- write each sequence's new tokens into its frames.
+ *
+ *   k_new, v_new  [T, H, D] fp16/bf16, rows as for pa_cache_append.  Rows query_start[s] .. query_start[s+1]-1 are the
+ *                 last tokens of sequence s, as for pa_prefill; query_start NULL: row s is the last token of sequence s
+ *                 (T = S; a sequence of no tokens has its row skipped).
+ *   block_tables  int32 [S, max_blocks]; context_lens int32 [S] = L_s, the new tokens included.  Only the entries
+ *                 of frames that hold a new token are read.  No frame may be written to for two sequences.
+ * A frame whose tokens are all new:
+ *     r = 127 / max |x| over its new tokens of that head (fp32), all but the 8 leading bits cleared;
+ *     step = 1 / r (fp32);  b = 128 + round-half-even(x * r).
+ * max |x| counts as at least 2^-60 and at most 2^60, elements beyond that as +-2^60.  A frame that holds earlier
+ * tokens: with r the number of 8 bits nearest to 1 / step, k the least integer >= 0 with max |x| * r <= 127 * 2^k:
+ *     r /= 2^k, step *= 2^k, and each earlier code n = b - 128 becomes round-half-even(n / 2^k).
+ * A NaN or an infinity among the new elements, or a step that no append leaves, makes the step NaN and the new codes 0:
+ * the frame's tokens of that head read as NaN until it is begun anew.  Slots behind the last token are left as
+ * they were.  A sequence with a bad length or query range sets PA_DEV_BAD_LEN and is skipped (ranges that hold more
+ * frames than T rows can: some of them are too), a bad frame id PA_DEV_BAD_BLOCK and the frame is skipped.
+ */
+int pa_cache_append_q8(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* block_tables,
+                       const pa_tensor* context_lens, const pa_tensor* query_start, const pa_tensor* k_cache,
+                       const pa_tensor* v_cache, const pa_tensor* k_scale, const pa_tensor* v_scale, pa_stream stream);
+
+/*
+ * pa_cache_read_q8 -- rows of the 8-bit cache as 16-bit rows (for pa_prefill over a cached prefix, inspection):
+ * k_out, v_out [T, H, D] = (b - 128) * step in fp32, rounded to their type, of the rows at slot_mapping [T].
+ * slot < 0: that output row is left as it was; slot >= num_blocks * B: PA_DEV_BAD_SLOT and the row is left as
+ * it was.  The same slot may be read often.
+ */
+int pa_cache_read_q8(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                     const pa_tensor* v_scale, const pa_tensor* slot_mapping, const pa_tensor* k_out,
+                     const pa_tensor* v_out, pa_stream stream);
+
+/*
+ * pa_decode_q8 -- pa_decode over the 8-bit cache, all tokens (window = 0, sinks = 0) or those of pa_decode_window
+ * (window >= 1, sinks >= 0; else PA_ERR_INVALID).  q, out [S, Hq, D] fp16/bf16; the rest as for pa_decode_window.
+ * Codes are exact in the tensor cores' fp16; steps multiply scores and weights in fp32.  Weights and bf16
+ * queries as for pa_decode_q4.
+ */
+int pa_decode_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                 const pa_tensor* v_scale, const pa_tensor* block_tables, const pa_tensor* context_lens,
+                 int32_t window, int32_t sinks, float scale, const pa_tensor* out, pa_stream stream);
+
 /* Synchronises `stream` (and then the device), returns the current device's sticky
  * PA_DEV_* bits in *status_out and clears them.  When PA_DEV_TIMEOUT was set, the
  * scheduler and arrival counters of every workspace of this device are zeroed before it

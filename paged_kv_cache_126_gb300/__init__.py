@@ -41,6 +41,11 @@ from ._binding import (  # noqa: F401
     pa_block_bounds,
     pa_select_blocks,
     pa_decode_selected,
+    pa_decode_window,
+    pa_prefill_window,
+    pa_cache_append_q8,
+    pa_cache_read_q8,
+    pa_decode_q8,
     pa_step_decode,
     pa_get_device_status,
     pa_selftest_raise_counters,

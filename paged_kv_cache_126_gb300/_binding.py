@@ -2,7 +2,7 @@
 
 Every device operation runs in libpa's CUDA kernels; this module turns torch
 tensors into ``pa_tensor`` descriptors and return codes into exceptions.  The calls of
-the rotary, 4-bit and block-sparse operators take many tensors and are marshalled by the
+the rotary, 4-bit, 8-bit, block-sparse and window operators take many tensors and are marshalled by the
 extension module ``_marshal`` instead of ctypes, loaded by the first of them.  If ``libpa.so`` is missing the
 import fails, if ``_marshal.so`` is missing or of another torch these calls: there is no fallback path.
 """
@@ -91,6 +91,11 @@ def _load():
         "pa_block_bounds": ([P, P, P, P, P, vp], C.c_int),
         "pa_select_blocks": ([P, P, P, P, C.c_int32, C.c_int32, C.c_int32, P, vp], C.c_int),
         "pa_decode_selected": ([P, P, P, P, P, P, C.c_float, P, vp], C.c_int),
+        "pa_decode_window": ([P, P, P, P, P, C.c_int32, C.c_int32, C.c_float, P, vp], C.c_int),
+        "pa_prefill_window": ([P, P, P, P, P, P, C.c_int32, C.c_int32, C.c_float, P, vp], C.c_int),
+        "pa_cache_append_q8": ([P, P, P, P, P, P, P, P, P, vp], C.c_int),
+        "pa_cache_read_q8": ([P, P, P, P, P, P, P, vp], C.c_int),
+        "pa_decode_q8": ([P, P, P, P, P, P, P, C.c_int32, C.c_int32, C.c_float, P, vp], C.c_int),
         "pa_get_device_status": ([vp, i32p], C.c_int),
         "pa_strerror": ([C.c_int], C.c_char_p),
         "pa_launch_count": ([], C.c_int64),
@@ -144,6 +149,7 @@ EXPORTED = (
     "pa_bm_export",
     "pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",
     "pa_select_blocks", "pa_decode_selected", "pa_selftest_raise_counters",
+    "pa_decode_window", "pa_prefill_window", "pa_cache_append_q8", "pa_cache_read_q8", "pa_decode_q8",
 )
 
 
@@ -330,7 +336,8 @@ def _load_marshal():
         raise ImportError(f"{path} was built against torch {mod.torch_version}, this is {torch.__version__}; build it again "
                           "(python paged_kv_cache_126_gb300/build.py)")
     for name in ("pa_cache_append_rope", "pa_cache_append_q4", "pa_cache_read_q4", "pa_decode_q4", "pa_block_bounds",
-                 "pa_select_blocks", "pa_decode_selected"):
+                 "pa_select_blocks", "pa_decode_selected", "pa_decode_window", "pa_prefill_window", "pa_cache_append_q8",
+                 "pa_cache_read_q8", "pa_decode_q8"):
         mod.bind(name, C.cast(getattr(LIB, name), C.c_void_p).value)
     return mod
 
@@ -405,6 +412,49 @@ def pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, selected
     rc = _marshal.pa_decode_selected(q, k_cache, v_cache, block_tables, context_lens, selected, scale, out, stream)
     if rc:
         _check(rc, "pa_decode_selected")
+    return out
+
+
+def pa_decode_window(q, k_cache, v_cache, block_tables, context_lens, window, scale, out, sinks=0, stream=None):
+    """``pa_decode_window``: decode attention over each sequence's last ``window`` and first ``sinks`` tokens into
+    ``out`` [S, Hq, D]."""
+    rc = _marshal.pa_decode_window(q, k_cache, v_cache, block_tables, context_lens, window, sinks, scale, out, stream)
+    if rc:
+        _check(rc, "pa_decode_window")
+    return out
+
+
+def pa_prefill_window(q, k_cache, v_cache, block_tables, context_lens, query_start, window, scale, out, sinks=0, stream=None):
+    """``pa_prefill_window``: attention of query chunks, each query over the last ``window`` tokens up to its own and the
+    sequence's first ``sinks``, into ``out`` [T, Hq, 128]."""
+    rc = _marshal.pa_prefill_window(q, k_cache, v_cache, block_tables, context_lens, query_start, window, sinks, scale, out, stream)
+    if rc:
+        _check(rc, "pa_prefill_window")
+    return out
+
+
+def pa_cache_append_q8(k_new, v_new, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale, query_start=None,
+                       stream=None) -> None:
+    """``pa_cache_append_q8``: rows query_start[s] .. query_start[s + 1] - 1 (None: row s) into the 8-bit caches, uint8
+    [num_blocks, H, B, D], as the last tokens of sequence s; steps float32 [num_blocks, H] (see include/pa.h)."""
+    rc = _marshal.pa_cache_append_q8(k_new, v_new, block_tables, context_lens, query_start, k_cache, v_cache, k_scale, v_scale, stream)
+    if rc:
+        _check(rc, "pa_cache_append_q8")
+
+
+def pa_cache_read_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, stream=None) -> None:
+    """``pa_cache_read_q8``: the 8-bit rows at slot_mapping [T] as 16-bit rows [T, H, D]."""
+    rc = _marshal.pa_cache_read_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, stream)
+    if rc:
+        _check(rc, "pa_cache_read_q8")
+
+
+def pa_decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, window=0, sinks=0, stream=None):
+    """``pa_decode_q8``: decode attention over the 8-bit caches into ``out`` [S, Hq, D]: over every token, or where ``window``
+    is not 0 over the last ``window`` and the first ``sinks``."""
+    rc = _marshal.pa_decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, window, sinks, scale, out, stream)
+    if rc:
+        _check(rc, "pa_decode_q8")
     return out
 
 

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -402,6 +403,15 @@ int check_i32(const pa_tensor* t, int ndim) {
     int _rc = (x);                 \
     if (_rc != PA_OK) return _rc;  \
   } while (0)
+
+// q or out [N, Hq, D] with Hq a multiple of H, at most 16 query heads a key head; *g = Hq / H.
+int check_grouped_rows(const pa_tensor* t, int dtype, int64_t H, int64_t D, int64_t* g) {
+  if (!t) return PA_ERR_INVALID;
+  if (t->ndim != 3 || t->shape[1] < H || t->shape[1] % H != 0) return PA_ERR_SHAPE;
+  PA_TRY(check_rows(t, dtype, t->shape[1], D));
+  *g = t->shape[1] / H;
+  return *g > 16 ? PA_ERR_UNSUPPORTED : PA_OK;
+}
 
 int round_up(int64_t x, int64_t m) { return static_cast<int>(((x + m - 1) / m) * m); }
 
@@ -1098,17 +1108,30 @@ int pa_decode(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_c
   return pa_decode_ex(q, k_cache, v_cache, block_tables, context_lens, scale, out, nullptr, stream);
 }
 
-int pa_prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* block_tables,
-               const pa_tensor* context_lens, const pa_tensor* query_start, float scale, const pa_tensor* out,
-               pa_stream stream) {
-  const Range range("pa_prefill");
+}  // extern "C"
+
+namespace {
+
+// pa_prefill (window 0, Hq = H) and pa_prefill_window.
+int prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* block_tables,
+            const pa_tensor* context_lens, const pa_tensor* query_start, int32_t window, int32_t sinks, float scale,
+            const pa_tensor* out, pa_stream stream) {
   PA_TRY(check_cache(k_cache, v_cache));
   const int dt = k_cache->dtype;
   if (dt != PA_F16 && dt != PA_BF16) return PA_ERR_UNSUPPORTED;
   const int64_t nb = k_cache->shape[0], B = k_cache->shape[1], H = k_cache->shape[2], D = k_cache->shape[3];
   if (D != 128 || !(B == 8 || B == 16 || B == 32 || B == 64 || B == 128)) return PA_ERR_UNSUPPORTED;
-  PA_TRY(check_rows(q, dt, H, D));
-  PA_TRY(check_rows(out, dt, H, D));
+  int64_t g = 1;
+  if (window > 0) {
+    PA_TRY(check_cache(v_cache, nullptr));
+    int64_t go = 0;
+    PA_TRY(check_grouped_rows(q, dt, H, D, &g));
+    PA_TRY(check_grouped_rows(out, dt, H, D, &go));
+    if (go != g) return PA_ERR_SHAPE;
+  } else {
+    PA_TRY(check_rows(q, dt, H, D));
+    PA_TRY(check_rows(out, dt, H, D));
+  }
   if (!block_tables || !context_lens || !query_start) return PA_ERR_INVALID;
   PA_TRY(check_i32(block_tables, 2));
   PA_TRY(check_i32(context_lens, 1));
@@ -1146,7 +1169,10 @@ int pa_prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_
   a.context_lens = static_cast<const int32_t*>(context_lens->data);
   a.query_start = static_cast<const int32_t*>(query_start->data);
   a.S = static_cast<int32_t>(S);
-  a.H = static_cast<int32_t>(H);
+  a.H = static_cast<int32_t>(H * g);
+  a.window = window;
+  a.sinks = sinks;
+  a.g = static_cast<int32_t>(g);
   a.B = static_cast<int32_t>(B);
   a.num_blocks = static_cast<int32_t>(nb);
   a.max_blocks = static_cast<int32_t>(max_blocks);
@@ -1155,7 +1181,7 @@ int pa_prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_
   a.status = g_dev[dev].status;
 
   CUtensorMap tq, tk, tv;
-  PA_TRY(make_sw128_map(&tq, q->data, dt, T, H, D, q->stride[0], 128));
+  PA_TRY(make_sw128_map(&tq, q->data, dt, T, H * g, D, q->stride[0], 128));
   PA_TRY(make_frame_map(&tk, k_cache->data, dt, nb * B, H, D, static_cast<int>(B)));
   PA_TRY(make_frame_map(&tv, v_cache->data, dt, nb * B, H, D, static_cast<int>(B)));
   Scratch ws;
@@ -1170,12 +1196,34 @@ int pa_prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_
     r.query_start = a.query_start + s0;
     r.S = static_cast<int32_t>(n);
     r.unit_cap = static_cast<int32_t>(n + tile_cap);
-    const cudaError_t e = dt == PA_F16 ? pa::launch_prefill_f16(r, tq, tk, tv, grid, static_cast<cudaStream_t>(stream))
-                                       : pa::launch_prefill_bf16(r, tq, tk, tv, grid, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = window > 0     ? pa::launch_prefill_window(dt, r, tq, tk, tv, grid, st)
+                          : dt == PA_F16 ? pa::launch_prefill_f16(r, tq, tk, tv, grid, st)
+                                         : pa::launch_prefill_bf16(r, tq, tk, tv, grid, st);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     g_launches.fetch_add(1);
   }
   return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* block_tables,
+               const pa_tensor* context_lens, const pa_tensor* query_start, float scale, const pa_tensor* out,
+               pa_stream stream) {
+  const Range range("pa_prefill");
+  return prefill(q, k_cache, v_cache, block_tables, context_lens, query_start, 0, 0, scale, out, stream);
+}
+
+int pa_prefill_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                      const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* query_start,
+                      int32_t window, int32_t sinks, float scale, const pa_tensor* out, pa_stream stream) {
+  const Range range("pa_prefill_window");
+  // the kernel masks scores before they are scaled
+  if (window < 1 || sinks < 0 || !(scale > 0.f) || scale > FLT_MAX) return PA_ERR_INVALID;
+  return prefill(q, k_cache, v_cache, block_tables, context_lens, query_start, window, sinks, scale, out, stream);
 }
 
 }  // extern "C"
@@ -1454,15 +1502,6 @@ int check_q4_caches(const pa_tensor* k, const pa_tensor* v, Q4Shape* z) {
   return PA_OK;
 }
 
-// q or out [N, Hq, D] with Hq a multiple of H, at most 16 query heads a key head; *g = Hq / H.
-int check_grouped_rows(const pa_tensor* t, int dtype, int64_t H, int64_t D, int64_t* g) {
-  if (!t) return PA_ERR_INVALID;
-  if (t->ndim != 3 || t->shape[1] < H || t->shape[1] % H != 0) return PA_ERR_SHAPE;
-  PA_TRY(check_rows(t, dtype, t->shape[1], D));
-  *g = t->shape[1] / H;
-  return *g > 16 ? PA_ERR_UNSUPPORTED : PA_OK;
-}
-
 // block_tables [S, max_blocks] and context_lens [S] of a call over blocks of B tokens.
 int check_tables(const pa_tensor* block_tables, const pa_tensor* context_lens, int64_t S, int64_t B) {
   if (!block_tables || !context_lens) return PA_ERR_INVALID;
@@ -1640,7 +1679,7 @@ int pa_cache_read_q4(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
 
 namespace {
 
-// Arguments that pa_decode_q4 and pa_decode_selected share, checked; *S = 0: nothing to do.
+// Arguments that the gathered decodes share, checked; S = 0: nothing to do.
 int gather_args(const pa_tensor* q, const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* out,
                 float scale, int64_t nb, int64_t H, int64_t B, int64_t D, pa::GatherArgs* a) {
   std::memset(a, 0, sizeof(*a));
@@ -1677,6 +1716,17 @@ bool tiles_fit(const pa::GatherArgs& a, int64_t most_of_one) {
   return static_cast<int64_t>(a.S) * a.H * std::max<int64_t>(most_of_one, 1) <= INT32_MAX;
 }
 
+// The last `window` and first `sinks` tokens, into a; `least`: the smallest window allowed.  Also whether their tiles of `keys` keys fit.
+int window_args(int32_t window, int32_t sinks, int32_t least, int64_t keys, pa::GatherArgs* a) {
+  if (window < least || sinks < 0 || (window == 0 && sinks != 0)) return PA_ERR_INVALID;
+  a->window = window;
+  a->sinks = sinks;
+  int64_t parts = (static_cast<int64_t>(a->max_blocks) * a->B + 15) / 16;
+  // sinks and a window each begin and end inside a part
+  if (window > 0) parts = std::min(parts + 1, (static_cast<int64_t>(window) + 15) / 16 + (static_cast<int64_t>(sinks) + 15) / 16 + 1);
+  return tiles_fit(*a, (16 * parts + keys - 1) / keys) ? PA_OK : PA_ERR_UNSUPPORTED;
+}
+
 // Workspace of a gathered decode on `workers` warps: an arrival counter per (sequence, head) and two per group
 // of 16 workers, and as many partials as workers and groups have sides.
 int gather_scratch(int dev, cudaStream_t stream, int64_t D, int workers, Scratch* ws, pa::GatherArgs* a) {
@@ -1702,6 +1752,20 @@ int make_q4_map(CUtensorMap* map, void* base, int64_t nb, int64_t H, int64_t B, 
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PA_OK : PA_ERR_UNSUPPORTED;
+}
+
+// View {D bytes, B rows, num_blocks * H} of an 8-bit cache, box {D, min(B, 16), 1}, swizzled as wide as a row.
+int make_q8_map(CUtensorMap* map, void* base, int64_t nb, int64_t H, int64_t B, int64_t D) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return PA_ERR_CUDA;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(B), static_cast<cuuint64_t>(nb * H)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(B * D)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(std::min<int64_t>(B, 16)), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
@@ -1747,6 +1811,38 @@ int pa_decode_q4(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
   Scratch ws;
   PA_TRY(gather_scratch(dev, st, z.D, workers, &ws, &a));
   if (pa::launch_decode_q4(q->dtype, D, a, tk, tv, sms, st, nullptr) != cudaSuccess)
+    return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                     const pa_tensor* block_tables, const pa_tensor* context_lens, int32_t window, int32_t sinks,
+                     float scale, const pa_tensor* out, pa_stream stream) {
+  const Range range("pa_decode_window");
+  PA_TRY(check_cache(k_cache, v_cache));
+  PA_TRY(check_cache(v_cache, nullptr));
+  const int64_t nb = k_cache->shape[0], B = k_cache->shape[1], H = k_cache->shape[2], D = k_cache->shape[3];
+  if (k_cache->dtype == PA_F32 || !(D == 64 || D == 128) || B < 8 || B > 256 || (B & (B - 1)) != 0)
+    return PA_ERR_UNSUPPORTED;
+  if (!q || q->dtype != k_cache->dtype) return q ? PA_ERR_DTYPE : PA_ERR_INVALID;
+  pa::GatherArgs a;
+  PA_TRY(gather_args(q, block_tables, context_lens, out, scale, nb, H, B, D, &a));
+  PA_TRY(window_args(window, sinks, 1, 16, &a));
+  if (a.S == 0) return PA_OK;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.status = g_dev[dev].status;
+  CUtensorMap tk, tv;
+  PA_TRY(make_rows8_map(&tk, k_cache->data, q->dtype, nb * B, H, D));
+  PA_TRY(make_rows8_map(&tv, v_cache->data, q->dtype, nb * B, H, D));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int workers = 0;
+  if (pa::launch_decode_window(q->dtype, static_cast<int>(D), a, tk, tv, g_dev[dev].num_sms, st, &workers) != cudaSuccess)
+    return PA_ERR_CUDA;
+  Scratch ws;
+  PA_TRY(gather_scratch(dev, st, D, workers, &ws, &a));
+  if (pa::launch_decode_window(q->dtype, static_cast<int>(D), a, tk, tv, g_dev[dev].num_sms, st, nullptr) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(1);
   return PA_OK;
@@ -1883,6 +1979,170 @@ int pa_select_blocks(const pa_tensor* q, const pa_tensor* bounds, const pa_tenso
   if (pa::launch_select_blocks(dt, a, g_dev[dev].num_sms, static_cast<cudaStream_t>(stream), &launched) != cudaSuccess)
     return PA_ERR_CUDA;
   g_launches.fetch_add(launched);
+  return PA_OK;
+}
+
+}  // extern "C"
+
+// ---- the 8-bit cache -------------------------------------------------------------------------------
+namespace {
+
+// Caches PA_U8 [num_blocks, H, B, D] and steps PA_F32 [num_blocks, H], rows apart as far as the caller likes.
+struct Q8Shape {
+  int64_t nb, H, B, D;
+};
+int check_q8_caches(const pa_tensor* k, const pa_tensor* v, const pa_tensor* ks, const pa_tensor* vs, Q8Shape* z) {
+  if (!k || !v || !v->data || !ks || !vs) return PA_ERR_INVALID;
+  if (k->dtype != PA_U8 || v->dtype != PA_U8) return PA_ERR_DTYPE;
+  PA_TRY(check_cache(k, v, true));
+  PA_TRY(check_cache(v, nullptr, true));
+  z->nb = k->shape[0];
+  z->H = k->shape[1];
+  z->B = k->shape[2];
+  z->D = k->shape[3];
+  if (!(z->D == 64 || z->D == 128) || z->B < 8 || z->B > 256 || (z->B & (z->B - 1)) != 0) return PA_ERR_UNSUPPORTED;
+  if (z->nb * z->B > INT32_MAX || z->nb * z->H > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  for (const pa_tensor* t : {ks, vs}) {
+    if (t->dtype != PA_F32) return PA_ERR_DTYPE;
+    if (t->ndim != 2 || t->shape[0] != z->nb || t->shape[1] != z->H) return PA_ERR_SHAPE;
+    if (!t->data) return PA_ERR_INVALID;
+    if (t->stride[1] != 1 || (z->nb > 1 && t->stride[0] < z->H)) return PA_ERR_STRIDE;
+    if ((reinterpret_cast<uintptr_t>(t->data) & 3u) != 0) return PA_ERR_ALIGN;
+  }
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_cache_append_q8(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* block_tables,
+                       const pa_tensor* context_lens, const pa_tensor* query_start, const pa_tensor* k_cache,
+                       const pa_tensor* v_cache, const pa_tensor* k_scale, const pa_tensor* v_scale, pa_stream stream) {
+  const Range range("pa_cache_append_q8");
+  Q8Shape z;
+  PA_TRY(check_q8_caches(k_cache, v_cache, k_scale, v_scale, &z));
+  if (!k_new || !context_lens) return PA_ERR_INVALID;
+  const int dt = k_new->dtype;
+  if (dt != PA_F16 && dt != PA_BF16) return PA_ERR_DTYPE;
+  PA_TRY(check_rows(k_new, dt, z.H, z.D));
+  PA_TRY(check_rows(v_new, dt, z.H, z.D));
+  const int64_t T = k_new->shape[0], S = context_lens->shape[0];
+  if (v_new->shape[0] != T) return PA_ERR_SHAPE;
+  PA_TRY(check_tables(block_tables, context_lens, S, z.B));
+  if (query_start) {
+    PA_TRY(check_i32(query_start, 1));
+    if (query_start->shape[0] != S + 1) return PA_ERR_SHAPE;
+  } else if (T != S) {
+    return PA_ERR_SHAPE;
+  }
+  if (T > INT32_MAX || z.H > INT32_MAX / 4) return PA_ERR_UNSUPPORTED;
+  if (T == 0 || S == 0) return PA_OK;
+  pa::Append8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.k_new = k_new->data;
+  a.v_new = v_new->data;
+  a.k_row = k_new->stride[0];
+  a.v_row = v_new->stride[0];
+  a.block_tables = static_cast<const int32_t*>(block_tables->data);
+  a.bt_row = block_tables->stride[0];
+  a.context_lens = static_cast<const int32_t*>(context_lens->data);
+  a.query_start = query_start ? static_cast<const int32_t*>(query_start->data) : nullptr;
+  a.k_cache = static_cast<unsigned char*>(k_cache->data);
+  a.v_cache = static_cast<unsigned char*>(v_cache->data);
+  a.k_scale = static_cast<float*>(k_scale->data);
+  a.v_scale = static_cast<float*>(v_scale->data);
+  a.ks_row = k_scale->stride[0];
+  a.vs_row = v_scale->stride[0];
+  a.T = static_cast<int32_t>(T);
+  a.S = static_cast<int32_t>(S);
+  a.H = static_cast<int32_t>(z.H);
+  a.D = static_cast<int32_t>(z.D);
+  a.B = static_cast<int32_t>(z.B);
+  while ((1 << a.log2_B) < z.B) ++a.log2_B;
+  a.num_blocks = static_cast<int32_t>(z.nb);
+  a.max_blocks = static_cast<int32_t>(block_tables->shape[1]);
+  if (!pa::append8_fits(&a)) return PA_ERR_UNSUPPORTED;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.status = g_dev[dev].status;
+  if (pa::launch_append8(dt, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_cache_read_q8(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                     const pa_tensor* v_scale, const pa_tensor* slot_mapping, const pa_tensor* k_out,
+                     const pa_tensor* v_out, pa_stream stream) {
+  const Range range("pa_cache_read_q8");
+  Q8Shape z;
+  PA_TRY(check_q8_caches(k_cache, v_cache, k_scale, v_scale, &z));
+  if (!k_out || !v_out || !slot_mapping) return PA_ERR_INVALID;
+  const int dt = k_out->dtype;
+  if (dt != PA_F16 && dt != PA_BF16) return PA_ERR_DTYPE;
+  PA_TRY(check_rows(k_out, dt, z.H, z.D));
+  PA_TRY(check_rows(v_out, dt, z.H, z.D));
+  PA_TRY(check_i32(slot_mapping, 1));
+  const int64_t T = k_out->shape[0];
+  if (v_out->shape[0] != T || slot_mapping->shape[0] != T) return PA_ERR_SHAPE;
+  if (T > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (T == 0) return PA_OK;
+  pa::Read8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.k_cache = static_cast<const unsigned char*>(k_cache->data);
+  a.v_cache = static_cast<const unsigned char*>(v_cache->data);
+  a.k_scale = static_cast<const float*>(k_scale->data);
+  a.v_scale = static_cast<const float*>(v_scale->data);
+  a.ks_row = k_scale->stride[0];
+  a.vs_row = v_scale->stride[0];
+  a.slots = static_cast<const int32_t*>(slot_mapping->data);
+  a.k_out = k_out->data;
+  a.v_out = v_out->data;
+  a.ko_row = k_out->stride[0];
+  a.vo_row = v_out->stride[0];
+  a.num_slots = z.nb * z.B;
+  a.T = static_cast<int32_t>(T);
+  a.H = static_cast<int32_t>(z.H);
+  a.D = static_cast<int32_t>(z.D);
+  a.B = static_cast<int32_t>(z.B);
+  while ((1 << a.log2_B) < z.B) ++a.log2_B;
+  if (!pa::read8_fits(&a)) return PA_ERR_UNSUPPORTED;
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.status = g_dev[dev].status;
+  if (pa::launch_read8(dt, a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+int pa_decode_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                 const pa_tensor* v_scale, const pa_tensor* block_tables, const pa_tensor* context_lens,
+                 int32_t window, int32_t sinks, float scale, const pa_tensor* out, pa_stream stream) {
+  const Range range("pa_decode_q8");
+  Q8Shape z;
+  PA_TRY(check_q8_caches(k_cache, v_cache, k_scale, v_scale, &z));
+  pa::GatherArgs a;
+  PA_TRY(gather_args(q, block_tables, context_lens, out, scale, z.nb, z.H, z.B, z.D, &a));
+  PA_TRY(window_args(window, sinks, 0, 64, &a));
+  if (a.S == 0) return PA_OK;
+  a.k_step = static_cast<const float*>(k_scale->data);
+  a.v_step = static_cast<const float*>(v_scale->data);
+  a.ks_row = k_scale->stride[0];
+  a.vs_row = v_scale->stride[0];
+  int dev;
+  PA_TRY(current_device(&dev));
+  a.status = g_dev[dev].status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int workers = 0;
+  const int D = static_cast<int>(z.D), sms = g_dev[dev].num_sms;
+  CUtensorMap tk, tv;
+  PA_TRY(make_q8_map(&tk, k_cache->data, z.nb, z.H, z.B, z.D));
+  PA_TRY(make_q8_map(&tv, v_cache->data, z.nb, z.H, z.B, z.D));
+  if (pa::launch_decode_q8(q->dtype, D, a, tk, tv, sms, st, &workers) != cudaSuccess) return PA_ERR_CUDA;
+  Scratch ws;
+  PA_TRY(gather_scratch(dev, st, z.D, workers, &ws, &a));
+  if (pa::launch_decode_q8(q->dtype, D, a, tk, tv, sms, st, nullptr) != cudaSuccess) return PA_ERR_CUDA;
+  g_launches.fetch_add(1);
   return PA_OK;
 }
 

@@ -19,9 +19,9 @@ cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorM
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, false, 1, 4, 3>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, gk::kTwoParts, false, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, gk::kEvery, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, gk::kEvery, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, gk::kEvery, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

@@ -48,7 +48,11 @@ constexpr float kSlack = 8.f;    // how far (log2) a score may pass the running 
 // Weights are 2^kRoom times what they stand for: at most 2^15, which fp16 holds, and as many more of a long context's small
 // ones are above its least number, 2^-24.  (Many keys 2^-24 below one sink were off by half of themselves.)
 constexpr float kRoom = 7.f;
+constexpr float kLeastStep = 0x1p-126f;
 constexpr float kLeast = -3.402823466e38f;  // a running maximum of no score yet: finite, so that a score of -inf weighs nothing
+
+// Which keys of a sequence: every one, those of listed frames, or its last `window` and first `sinks`.
+enum Keys { kEvery, kListed, kWindow };
 
 // How the second part of the weights gets to the tensor cores: in the second copy of the queries, or as another operand.
 enum Parts { kTwinColumns, kTwoParts };
@@ -135,50 +139,53 @@ __device__ __forceinline__ int checked_len(const GatherArgs& a, int s) {
 }
 
 // Parts of 16 keys of a sequence or list (16 slots of a listed frame, or two frames of 8); at least one.
-template <bool SEL>
+template <int KEYS>
 __device__ __forceinline__ int parts_of(const GatherArgs& a, int L) {
-  if (!SEL) return parts16(L);
+  if (KEYS == kEvery) return parts16(L);
+  if (KEYS == kWindow) return sight_of(max(L, 0), a.window, a.sinks).parts;
   const int n = min(a.K, (max(L, 0) + a.B - 1) >> a.log2_B);
   return max(1, a.B >= 16 ? n << (a.log2_B - 4) : (n + 1) >> 1);
 }
-template <bool SEL, int LOADS>
+template <int KEYS, int LOADS>
 __device__ __forceinline__ int tiles_of(const GatherArgs& a, int L) {
-  return (parts_of<SEL>(a, L) + LOADS - 1) / LOADS;
+  return (parts_of<KEYS>(a, L) + LOADS - 1) / LOADS;
 }
 
-template <bool SEL, int LOADS>
+template <int KEYS, int LOADS>
 __device__ __forceinline__ void enter_seq(const GatherArgs& a, Cursor& c) {
   const int L = checked_len(a, c.s);
   if (L < 0) atomicOr(a.status, kDevBadLen);
   c.L = max(L, 0);
   c.blocks = (c.L + a.B - 1) >> a.log2_B;
-  c.parts = parts_of<SEL>(a, L);
+  c.parts = parts_of<KEYS>(a, L);
   c.tiles = (c.parts + LOADS - 1) / LOADS;
 }
 
 // To the next (s, h).
-template <bool SEL, int LOADS>
+template <int KEYS, int LOADS>
 __device__ __forceinline__ void next_head(const GatherArgs& a, Cursor& c) {
   c.t = 0;
   if (++c.h < a.H) return;
   c.h = 0;
-  if (++c.s < a.S) enter_seq<SEL, LOADS>(a, c);
+  if (++c.s < a.S) enter_seq<KEYS, LOADS>(a, c);
 }
 
 // A part of a tile as the producer sees it: 16 keys, two halves of 8, each inside one frame.
 struct TilePlan {
   int frame[2];   // < 0: nothing to load
   int row;        // first key's row in its frame (both halves of one frame: row, row + 8)
-  int meta;       // keys of the halves (0..8 each) | 1 << 16 for a bad frame id
+  // Of each half: keys up to its n-th (0..8), in bits 0.. and 8..; | 1 << 16 for a bad frame id; windows: but for the first
+  // so many (0..7), in bits 20.. and 24..
+  int meta;
 };
 
-// Where the list of (s, h) ends, as far as it has been read (SEL).
+// Where the list of (s, h) ends, as far as it has been read (kListed).
 struct List {
   int seen;    // entries read so far
   bool ended;
 };
 
-// Table position and frame of entry j of (s, h), one entry per lane: frame -1 bad, -2 none.  `list`: for SEL,
+// Table position and frame of entry j of (s, h), one entry per lane: frame -1 bad, -2 none.  `list`: for kListed,
 // entries [0, list.seen) have been read; j - lane is at or behind that.
 __device__ __forceinline__ int checked_frame(const GatherArgs& a, const Cursor& c, int e) {
   int frame = e >= 0 && e < c.blocks ? a.block_tables[c.s * a.bt_row + e] : -1;
@@ -190,18 +197,38 @@ __device__ __forceinline__ int checked_frame(const GatherArgs& a, const Cursor& 
 }
 
 // Plans of the 32 parts t0 .. t0 + 31 of (s, h), one per lane.
-template <bool SEL>
+template <int KEYS>
 __device__ __forceinline__ TilePlan plan_tiles(const GatherArgs& a, const Cursor& c, int t0, int lane, List& list) {
   TilePlan p;
   const bool pairs = a.B < 16;             // a part is two frames of 8
+  if (KEYS == kWindow) {
+    const Sight x = sight_of(c.L, a.window, a.sinks);
+    const int t = t0 + lane;
+    const bool sink = t < x.sink_parts;
+    const int base = t < c.parts ? x.base(t) : 0;
+    const int end = t < c.parts ? (sink ? x.sinks : c.L) - base : 0, begin = sink ? 0 : max(0, x.start - base);
+    int n0 = min(8, end), n1 = min(8, max(0, end - 8));
+    int from0 = min(8, begin), from1 = min(8, max(0, begin - 8));
+    if (from0 >= n0) n0 = from0 = 0;  // no key: a frame of this half alone is not looked up
+    if (from1 >= n1) n1 = from1 = 0;
+    const int e = base >> a.log2_B;
+    p.row = pairs ? 0 : base & (a.B - 1);
+    p.frame[0] = (pairs ? n0 : n0 + n1) > 0 ? checked_frame(a, c, e) : -2;
+    p.frame[1] = pairs ? (n1 > 0 ? checked_frame(a, c, e + 1) : -2) : p.frame[0];
+    const bool bad = p.frame[0] == -1 || p.frame[1] == -1;
+    if (n0 == 0 || p.frame[0] < 0) n0 = from0 = 0, p.frame[0] = -2;
+    if (n1 == 0 || p.frame[1] < 0) n1 = from1 = 0, p.frame[1] = -2;
+    p.meta = n0 | (n1 << 8) | (bad ? 1 << 16 : 0) | (from0 << 20) | (from1 << 24);
+    return p;
+  }
   const int per = a.log2_B - 4;            // log2(parts of a frame)
   const int t = t0 + lane;
   const int j = pairs ? 2 * t : t >> per;  // first entry of this lane's part
   p.row = pairs ? 0 : (t & ((1 << per) - 1)) << 4;
   int e[2] = {j, j + 1};
-  const int n = SEL ? min(a.K, c.blocks) : c.blocks;
+  const int n = KEYS == kListed ? min(a.K, c.blocks) : c.blocks;
   bool have[2] = {t < c.parts && j < n, t < c.parts && pairs && j + 1 < n};
-  if (SEL) {
+  if (KEYS == kListed) {
     const int32_t* entries = a.selected + c.s * a.sel_seq + c.h * a.sel_head;
     const int j0 = pairs ? 2 * t0 : t0 >> per;
     for (int b = list.seen; b < j0 && !list.ended; b += 32)  // entries of other warps' tiles
@@ -263,6 +290,7 @@ struct Q4Format {
   using M = __half;      // operands of the tensor cores
   static constexpr int D = D_;
   static constexpr bool kScaleQ = !std::is_same<T, __half>::value;  // queries to fp16 range, by head
+  static constexpr bool kSteps = false;  // whether keys and values are multiples of a step that each (frame, head) has
   static constexpr int kRow = D / 2 + D / 8;
   static constexpr uint32_t kTile = 16 * kRow;
   static constexpr int kWordsK = D / 32, kWordsV = D / 64;  // words of codes a lane reads of a key
@@ -517,12 +545,14 @@ template <class F, int NT>
 __host__ __device__ constexpr uint32_t stage_bytes() {  // a tile's keys, its values, and the queries of a (s, h) that begins with it
   return 2 * F::kLoads * F::kTile + 8 * NT * F::D * sizeof(typename F::In);
 }
+// Stages, then metas (4 bytes a part) and two mbarriers each; where there are steps, for each part its keys' (two halves) and its
+// values', those of a stage's next tile beside those in use.
 template <class F, int NT, int STAGES>
 __host__ __device__ constexpr uint32_t warp_smem() {
-  return STAGES * (stage_bytes<F, NT>() + 32);  // stages, then metas (4 bytes a part) and two mbarriers each
+  return STAGES * (stage_bytes<F, NT>() + 32 + (F::kSteps ? 2 * F::kLoads * 16 : 0));
 }
 
-template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
+template <class F, int NT, int PARTS, int KEYS, int STAGES, int WARPS, int BLOCKS>
 __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     gather_kernel(const GatherArgs a, const __grid_constant__ typename F::Maps maps) {
   using T = typename F::In;
@@ -539,6 +569,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   const uint32_t stages = dk::smem_u32(smem) + warp * (STAGES * kStage);
   const uint32_t metas = dk::smem_u32(smem) + WARPS * (STAGES * kStage) + warp * STAGES * 32;  // [stage][4]
   const uint32_t bars = metas + STAGES * 16;  // [stage][2]: keys, values
+  const uint32_t steps = dk::smem_u32(smem) + WARPS * (STAGES * (kStage + 32)) + warp * STAGES * (2 * LOADS * 16);  // [2][stage][part]
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + WARPS * warp_smem<F, NT, STAGES>());
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
@@ -552,7 +583,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   int total = 0;
   int n = 0;  // tiles of sequence s0 + lane
   for (int s0 = 0; s0 < a.S; s0 += 32) {
-    n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
+    n = s0 + lane < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     total += __reduce_add_sync(kAll, n);
   }
   total *= a.H;  // the host has checked that all this stays in int32
@@ -567,7 +598,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   cur.s = cur.h = cur.t = 0;
   int before = 0;
   for (int s0 = 0; s0 < a.S && count > 0; s0 += 32) {
-    if (a.S > 32) n = s0 + lane < a.S ? tiles_of<SEL, LOADS>(a, checked_len(a, s0 + lane)) : 0;
+    if (a.S > 32) n = s0 + lane < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s0 + lane)) : 0;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -586,7 +617,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     }
     before += __shfl_sync(kAll, upto, 31) * a.H;
   }
-  enter_seq<SEL, LOADS>(a, cur);
+  enter_seq<KEYS, LOADS>(a, cur);
 
   // The producer's place.  Lane i plans the parts i, i + 32, ... of a (s, h) and issues their copies itself.
   Cursor ahead = cur;
@@ -594,18 +625,31 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   int planned = -1;  // first part of the window of 32 that the lanes have planned; -1: none
   typename F::Place place;
   int plan_meta = 0;
-  int issued = 0, issue_st = 0;
+  float4 plan_steps = make_float4(0.f, 0.f, 0.f, 0.f);  // of the halves' keys, of their values
+  int issued = 0, issue_st = 0, issue_phase = 0;
   auto issue_keys = [&]() {
     const int part = ahead.t * LOADS;
     if ((part & ~31) != planned) {
       planned = part & ~31;
-      const TilePlan p = plan_tiles<SEL>(a, ahead, planned, lane, list);
+      const TilePlan p = plan_tiles<KEYS>(a, ahead, planned, lane, list);
       place = F::place(a, p, ahead.h);
       plan_meta = p.meta;
+      if constexpr (F::kSteps) {
+        const int64_t f0 = p.frame[0], f1 = p.frame[1];
+        plan_steps.x = f0 >= 0 ? a.k_step[f0 * a.ks_row + ahead.h] : 0.f;
+        plan_steps.y = f1 >= 0 ? a.k_step[f1 * a.ks_row + ahead.h] : 0.f;
+        plan_steps.z = f0 >= 0 ? a.v_step[f0 * a.vs_row + ahead.h] : 0.f;
+        plan_steps.w = f1 >= 0 ? a.v_step[f1 * a.vs_row + ahead.h] : 0.f;
+      }
     }
     const int sub = lane - (part & 31);
-    if (static_cast<unsigned>(sub) < LOADS)
+    if (static_cast<unsigned>(sub) < LOADS) {
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 16 + sub * 4), "r"(plan_meta) : "memory");
+      if constexpr (F::kSteps)
+        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(steps + ((issue_phase * STAGES + issue_st) * LOADS + sub) * 16),
+                     "f"(plan_steps.x), "f"(plan_steps.y), "f"(plan_steps.z), "f"(plan_steps.w)
+                     : "memory");
+    }
     // the first tile of a (s, h), or of this warp's part of it, brings the queries along
     const uint32_t dst = stages + issue_st * kStage, bar = bars + 16 * issue_st;
     const bool first = ahead.t == 0 || issued == 0;
@@ -616,10 +660,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   };
   auto issue_values = [&]() {  // of the same tile, and on to the next
     F::load(a, &maps.v, place, ahead.h, lane, (ahead.t * LOADS) & 31, stages + issue_st * kStage + kKeys, bars + 16 * issue_st + 8, 0);
-    if (++issue_st == STAGES) issue_st = 0;
+    if (++issue_st == STAGES) issue_st = 0, issue_phase ^= 1;
     ++issued;
     if (++ahead.t == ahead.tiles && issued < count) {
-      next_head<SEL, LOADS>(a, ahead);
+      next_head<KEYS, LOADS>(a, ahead);
       planned = -1;
       list.seen = 0;
       list.ended = false;
@@ -634,6 +678,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   uint32_t qf[NT][D / 16][2];
   float o[D / 16][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];
+  float unit = kLeastStep, per_unit = 1.f / kLeastStep;  // kSteps: values are summed in multiples of `unit`
   Left(*left)[2] = reinterpret_cast<Left(*)[2]>(smem + WARPS * warp_smem<F, NT, STAGES>() + 16);  // side 0: begun before
   if (lane < 2) left[warp][lane].state = 0;
   __syncwarp();
@@ -688,6 +733,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       f[n][1] = __shfl_sync(kAll, back, 8 * c + 4);
       m[n][0] = m[n][1] = kLeast;
       l[n][0] = l[n][1] = 0.f;
+      unit = kLeastStep;
+      per_unit = 1.f / kLeastStep;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
     }
@@ -707,11 +754,21 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         full = full == 0x0808 ? meta[u] : full;  // 0x0808: every slot of every part holds a key
         any |= meta[u];
       }
-      if (any >> 16) poison = true;
+      if (any & (1 << 16)) poison = true;
       float x[LOADS][NT][4];
       if (any & 0xffff) {
 #pragma unroll
-        for (int u = 0; u < LOADS; ++u) F::template scores<NT>(kst + u * F::kTile, r, c, qf, x[u]);
+        for (int u = 0; u < LOADS; ++u) {
+          F::template scores<NT>(kst + u * F::kTile, r, c, qf, x[u]);
+          if constexpr (F::kSteps) {
+            uint32_t w[2];
+            lds(steps + ((phase * STAGES + st) * LOADS + u) * 16, w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[u][n][j] *= __uint_as_float(w[j >> 1]);
+          }
+        }
       }
       __syncwarp();
       const bool more = issued < count;
@@ -729,7 +786,12 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 #pragma unroll
           for (int u = 0; u < LOADS; ++u) {
             const int n0 = meta[u] & 255, n1 = (meta[u] >> 8) & 255;
-            const bool in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1, in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
+            bool in0 = k0 < 8 ? k0 < n0 : k0 - 8 < n1, in1 = k1 < 8 ? k1 < n0 : k1 - 8 < n1;
+            if (KEYS == kWindow) {
+              const int from0 = (meta[u] >> 20) & 15, from1 = (meta[u] >> 24) & 15;
+              in0 = in0 && (k0 < 8 ? k0 >= from0 : k0 - 8 >= from1);
+              in1 = in1 && (k1 < 8 ? k1 >= from0 : k1 - 8 >= from1);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -772,6 +834,35 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         break;
       }
       if (any & 0xffff) {
+        float step[LOADS][2];  // of the values, in units
+        if constexpr (F::kSteps) {
+          float top = 0.f;
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) {
+            uint32_t w[2];
+            lds(steps + ((phase * STAGES + st) * LOADS + u) * 16 + 8, w);
+            step[u][0] = __uint_as_float(w[0]);
+            step[u][1] = __uint_as_float(w[1]);
+            top = fmaxf(top, fmaxf(step[u][0], step[u][1]));
+          }
+          if (top > unit) {  // (a step that is NaN is none)
+            const float now = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + 0x800000u);  // the power of two above
+            const float less = unit / now;
+            unit = now;
+            per_unit = 1.f / now;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][n][j] *= less;
+          }
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) {
+            step[u][0] *= per_unit;
+            step[u][1] *= per_unit;
+          }
+        }
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
           uint32_t p[kB][NT][2];
@@ -782,6 +873,12 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
             for (int j = 0; j < 4; ++j) w[j] = dk::ex2(x[u][n][j] - m[n][j & 1]);
             l[n][0] += w[0] + w[2];
             l[n][1] += w[1] + w[3];
+            if constexpr (F::kSteps) {
+              w[0] *= step[u][0];
+              w[1] *= step[u][0];
+              w[2] *= step[u][1];
+              w[3] *= step[u][1];
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t hi = pack2<M>(w[2 * j], w[2 * j + 1]);
@@ -793,7 +890,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
               p[0][n][j] = transpose8(hi);
             }
           }
-          F::template values<NT, kB>(vst + u * F::kTile, r, c, full != 0x0808 ? meta[u] & 0xffff : 0x0808, p, o);
+          F::template values<NT, kB>(vst + u * F::kTile, r, c, full != 0x0808 ? meta[u] & (KEYS == kWindow ? 0xff0ffff : 0xffff) : 0x0808, p, o);
         }
       }
       __syncwarp();
@@ -828,6 +925,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
           if (col >= a.g || (PARTS == kTwinColumns && c >= 2)) continue;
           float inv = 1.f;
           if (whole) inv = poison || !(l[n][j] != 0.f) ? 0.f : 1.f / l[n][j];
+          if (F::kSteps) inv *= unit;
           float y[D / 16][2];
 #pragma unroll
           for (int t = 0; t < D / 16; ++t)
@@ -853,7 +951,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         if (lane == 0) left[warp][first_t == 0 ? 1 : 0] = x;
       }
     }
-    if (i < count) next_head<SEL, LOADS>(a, cur);
+    if (i < count) next_head<KEYS, LOADS>(a, cur);
   }
 
   // The joins that fall to this block, a query a warp at a time; then those of groups.
@@ -903,9 +1001,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 }
 
 // Launches, or only reports the launch's warps where `query` is not null.
-template <class F, int NT, int PARTS, bool SEL, int STAGES, int WARPS, int BLOCKS>
+template <class F, int NT, int PARTS, int KEYS, int STAGES, int WARPS, int BLOCKS>
 cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sms, cudaStream_t stream, int* query) {
-  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>);
+  const void* fn = reinterpret_cast<const void*>(&gather_kernel<F, NT, PARTS, KEYS, STAGES, WARPS, BLOCKS>);
   constexpr uint32_t smem = WARPS * (warp_smem<F, NT, STAGES>() + 2 * sizeof(Left)) + 16;  // + the abort flag
   int occ = 0;
   cudaError_t e = kernel_prep(fn, WARPS * 32, smem, &occ);
@@ -926,7 +1024,7 @@ cudaError_t launch(const GatherArgs& a, const typename F::Maps& maps, int num_sm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, SEL, STAGES, WARPS, BLOCKS>, a, maps);
+  return cudaLaunchKernelEx(&cfg, gather_kernel<F, NT, PARTS, KEYS, STAGES, WARPS, BLOCKS>, a, maps);
 }
 
 }  // namespace gk

@@ -26,6 +26,11 @@ decltype(&pa_decode_q4) g_decode_q4;
 decltype(&pa_block_bounds) g_block_bounds;
 decltype(&pa_select_blocks) g_select_blocks;
 decltype(&pa_decode_selected) g_decode_selected;
+decltype(&pa_decode_window) g_decode_window;
+decltype(&pa_prefill_window) g_prefill_window;
+decltype(&pa_cache_append_q8) g_append_q8;
+decltype(&pa_cache_read_q8) g_read_q8;
+decltype(&pa_decode_q8) g_decode_q8;
 
 struct Function {
   const char* name;
@@ -35,7 +40,9 @@ Function g_functions[] = {
     {"pa_cache_append_rope", &g_append_rope}, {"pa_cache_append_q4", &g_append_q4},
     {"pa_cache_read_q4", &g_read_q4},         {"pa_decode_q4", &g_decode_q4},
     {"pa_block_bounds", &g_block_bounds},     {"pa_select_blocks", &g_select_blocks},
-    {"pa_decode_selected", &g_decode_selected},
+    {"pa_decode_selected", &g_decode_selected}, {"pa_decode_window", &g_decode_window},
+    {"pa_prefill_window", &g_prefill_window}, {"pa_cache_append_q8", &g_append_q8},
+    {"pa_cache_read_q8", &g_read_q8},         {"pa_decode_q8", &g_decode_q8},
 };
 
 // One call's arguments.  Every method returns false with a Python exception set.
@@ -240,6 +247,85 @@ PyObject* py_decode_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+PyObject* py_decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  // q, k_cache, v_cache, block_tables, context_lens, window, sinks, scale, out, stream
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const pa_tensor *t[5], *out;
+    int32_t v[2];
+    float scale;
+    pa_stream st;
+    if (!count_is(n, 10)) return nullptr;
+    for (int i = 0; i < 5; ++i)
+      if (!c.tensor(a[i], &t[i])) return nullptr;
+    if (!c.number(a[5], &v[0]) || !c.number(a[6], &v[1]) || !c.real(a[7], &scale) || !c.tensor(a[8], &out) || !c.stream(a[9], &st))
+      return nullptr;
+    return run([&] { return g_decode_window(t[0], t[1], t[2], t[3], t[4], v[0], v[1], scale, out, st); });
+  });
+}
+
+PyObject* py_prefill_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  // q, k_cache, v_cache, block_tables, context_lens, query_start, window, sinks, scale, out, stream
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const pa_tensor *t[6], *out;
+    int32_t v[2];
+    float scale;
+    pa_stream st;
+    if (!count_is(n, 11)) return nullptr;
+    for (int i = 0; i < 6; ++i)
+      if (!c.tensor(a[i], &t[i])) return nullptr;
+    if (!c.number(a[6], &v[0]) || !c.number(a[7], &v[1]) || !c.real(a[8], &scale) || !c.tensor(a[9], &out) || !c.stream(a[10], &st))
+      return nullptr;
+    return run([&] { return g_prefill_window(t[0], t[1], t[2], t[3], t[4], t[5], v[0], v[1], scale, out, st); });
+  });
+}
+
+PyObject* py_append_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  // k_new, v_new, block_tables, context_lens, query_start, k_cache, v_cache, k_scale, v_scale, stream
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const pa_tensor* t[9];
+    pa_stream st;
+    if (!count_is(n, 10)) return nullptr;
+    for (int i = 0; i < 9; ++i)
+      if (!c.tensor(a[i], &t[i], i == 4)) return nullptr;
+    if (!c.stream(a[9], &st)) return nullptr;
+    return run([&] { return g_append_q8(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], t[8], st); });
+  });
+}
+
+PyObject* py_read_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  // k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, stream
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const pa_tensor* t[7];
+    pa_stream st;
+    if (!count_is(n, 8)) return nullptr;
+    for (int i = 0; i < 7; ++i)
+      if (!c.tensor(a[i], &t[i])) return nullptr;
+    if (!c.stream(a[7], &st)) return nullptr;
+    return run([&] { return g_read_q8(t[0], t[1], t[2], t[3], t[4], t[5], t[6], st); });
+  });
+}
+
+PyObject* py_decode_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  // q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, window, sinks, scale, out, stream
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const pa_tensor *t[7], *out;
+    int32_t v[2];
+    float scale;
+    pa_stream st;
+    if (!count_is(n, 12)) return nullptr;
+    for (int i = 0; i < 7; ++i)
+      if (!c.tensor(a[i], &t[i])) return nullptr;
+    if (!c.number(a[7], &v[0]) || !c.number(a[8], &v[1]) || !c.real(a[9], &scale) || !c.tensor(a[10], &out) || !c.stream(a[11], &st))
+      return nullptr;
+    return run([&] { return g_decode_q8(t[0], t[1], t[2], t[3], t[4], t[5], t[6], v[0], v[1], scale, out, st); });
+  });
+}
+
 // bind(name, address): where a function of libpa is
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 2)) return nullptr;
@@ -266,6 +352,11 @@ PyMethodDef g_methods[] = {
     {"pa_block_bounds", FAST(py_block_bounds)},
     {"pa_select_blocks", FAST(py_select_blocks)},
     {"pa_decode_selected", FAST(py_decode_selected)},
+    {"pa_decode_window", FAST(py_decode_window)},
+    {"pa_prefill_window", FAST(py_prefill_window)},
+    {"pa_cache_append_q8", FAST(py_append_q8)},
+    {"pa_cache_read_q8", FAST(py_read_q8)},
+    {"pa_decode_q8", FAST(py_decode_q8)},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

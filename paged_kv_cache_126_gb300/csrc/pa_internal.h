@@ -173,6 +173,9 @@ struct PrefillArgs {
   const int32_t* query_start;   // [S + 1] q rows of sequence s: query_start[s] .. query_start[s+1]-1
   int32_t S, H, B, num_blocks, max_blocks, T;
   int32_t unit_cap;             // room for (sequence, tile pair) units in shared memory
+  // windows: H counts the query heads, g of them to a key head; a query sees the last `window` keys up to its own and the
+  // first `sinks`
+  int32_t window, sinks, g;
   float qk_scale_log2;
   int32_t* sched;               // [2] work counter, retired blocks (zero between launches)
   int32_t* status;
@@ -181,6 +184,8 @@ cudaError_t launch_prefill_f16(const PrefillArgs&, const CUtensorMap& tq, const 
                                const CUtensorMap& tv, int grid, cudaStream_t);
 cudaError_t launch_prefill_bf16(const PrefillArgs&, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int grid, cudaStream_t);
+cudaError_t launch_prefill_window(int dtype, const PrefillArgs&, const CUtensorMap& tq, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, int grid, cudaStream_t);
 size_t prefill_smem_bytes(int S, int unit_cap);
 
 // Decode over the split cache layout (k [nb, H, D/x, B, x], v [nb, H, D, B]).
@@ -243,7 +248,40 @@ struct ReadQ4Args {
 };
 cudaError_t launch_read_q4(int dtype, ReadQ4Args a, cudaStream_t stream);
 
-// ---- decode over gathered tiles of 16 keys: the 4-bit cache, and listed frames ---------------
+// ---- the 8-bit cache (quant8.cu) ---------------------------------------------------------------
+struct Append8Args {
+  const void *k_new, *v_new;      // [T, H, D]
+  int64_t k_row, v_row;           // elements between token rows
+  const int32_t* block_tables;    // [S, max_blocks], row stride bt_row
+  int64_t bt_row;
+  const int32_t* context_lens;    // [S], the new tokens included
+  const int32_t* query_start;     // [S + 1] rows of sequence s; null: row s (T = S)
+  unsigned char *k_cache, *v_cache;  // [num_blocks, H, B, D]
+  float *k_scale, *v_scale;       // [num_blocks, H], row strides ks_row, vs_row
+  int64_t ks_row, vs_row;
+  int32_t T, S, H, D, B, log2_B, num_blocks, max_blocks;
+  int32_t units, blocks_unit, log2_slabs;  // set by append8_fits: most frames written to, blocks of each, log2 of a frame's warps
+  int32_t* status;
+};
+bool append8_fits(Append8Args* a);  // whether one launch holds the call
+cudaError_t launch_append8(int dtype, const Append8Args& a, cudaStream_t stream);
+
+struct Read8Args {
+  const unsigned char *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  int64_t ks_row, vs_row;
+  const int32_t* slots;           // [T]
+  void *k_out, *v_out;            // [T, H, D]
+  int64_t ko_row, vo_row;
+  int64_t num_slots;
+  int32_t T, H, D, B, log2_B;
+  int32_t chunks;                 // set by read8_fits: warps of a token's rows of one cache
+  int32_t* status;
+};
+bool read8_fits(Read8Args* a);
+cudaError_t launch_read8(int dtype, const Read8Args& a, cudaStream_t stream);
+
+// ---- decode over gathered tiles of 16 keys: the 4-bit and 8-bit caches, listed frames, windows ---------------
 struct GatherArgs {
   const void* q;                // [S, g * H, D], row stride q_row elements
   void* out;
@@ -254,6 +292,9 @@ struct GatherArgs {
   const int32_t* selected;      // [S, H, K]; null: every frame
   int64_t sel_seq, sel_head;    // elements between sequences, heads of `selected`
   int32_t K;
+  int32_t window, sinks;        // the last and first tokens seen; window 0: every token
+  const float *k_step, *v_step; // 8-bit caches: [num_blocks, H], row strides ks_row, vs_row
+  int64_t ks_row, vs_row;
   int32_t S, H, g, B, log2_B, num_blocks, max_blocks;
   float qk_scale_log2;          // scale * log2(e)
   int32_t* cnt;                 // [S * H] partials finished per (sequence, head), zero between launches
@@ -264,6 +305,10 @@ struct GatherArgs {
 // workers: not null: only report the launch's warps (each may leave two partials)
 cudaError_t launch_decode_q4(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                              int num_sms, cudaStream_t stream, int* workers);
+cudaError_t launch_decode_q8(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int num_sms, cudaStream_t stream, int* workers);
+cudaError_t launch_decode_window(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 int num_sms, cudaStream_t stream, int* workers);
 cudaError_t launch_decode_selected(int dtype, int D, const GatherArgs& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int num_sms, cudaStream_t stream, int* workers);
 

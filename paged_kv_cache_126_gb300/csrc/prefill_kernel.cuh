@@ -31,6 +31,11 @@
 //     lazily raised reference max, P (operand type; bf16 as high part + remainder)
 //     back to TMEM, O rescaled in TMEM
 //     when the reference max moves; normalised rows are written to `out`.
+//   * WINDOW: query i attends the keys j <= p with j > p - window or j < sinks, and query heads share
+//     key heads in groups of g.  An item walks the key tiles that hold sinks, then those from its first query's
+//     window on (a step of the walk is not the tile's number then); frames of a tile that none of its
+//     queries sees are zero-filled and not looked up.  A row may see nothing of its first tiles: its
+//     reference max is -inf until it does, and its weights 0.
 //   * Every wait is a bounded mbarrier wait; one that gives up sets PA_DEV_TIMEOUT
 //     and makes the block's later waits no-ops; before the TMEM is freed the MMA
 //     lane waits (bounded) for its own MMAs and the producer for its copies.
@@ -293,6 +298,8 @@ __device__ __forceinline__ int upper_seq(const int32_t* off, int S, int x) {
 struct PItem {
   int s, h;
   int nkv;       // key tiles the item walks (those of slot 1)
+  // WINDOW: step j is tile j, from step `sink_tiles` on tile j + skip; keys below `start` but for the sinks are seen by no row
+  int sink_tiles, skip, start;
   int qrow0[2];  // first q row of the slot's tile (global row index)
   int nrows[2];  // valid rows of the slot's tile, 0 when the slot is unused
   int pos0[2];   // position of the slot's first row
@@ -307,6 +314,7 @@ __device__ __forceinline__ bool seq_bad(int qs, int qe, int L, const PrefillArgs
 }
 
 // Tiles of pair p (counted from the end of the chunk) of a sequence.
+template <bool WINDOW>
 __device__ __forceinline__ void pair_tiles(const PrefillArgs& a, int s, int p, PItem& it) {
   const int qs = a.query_start[s], qe = a.query_start[s + 1];
   const int n = qe - qs;
@@ -328,10 +336,19 @@ __device__ __forceinline__ void pair_tiles(const PrefillArgs& a, int s, int p, P
       it.nkv_q[q] = (it.pos0[q] + it.nrows[q] - 1 + kBN) / kBN;
     }
   }
+  if (WINDOW) {
+    it.start = max(0, (it.nrows[0] > 0 ? it.pos0[0] : it.pos0[1]) + 1 - a.window);
+    if (a.sinks >= it.start) it.start = 0;
+    it.sink_tiles = min((a.sinks >> 7) + ((a.sinks & 127) != 0), it.start / kBN);
+    it.skip = it.start / kBN - it.sink_tiles;
+    if (it.nkv_q[0] > 0) it.nkv_q[0] -= it.skip;
+    if (it.nkv_q[1] > 0) it.nkv_q[1] -= it.skip;
+  }
   it.nkv = it.nkv_q[1];
 }
 
 // Item -> (unit of rank item / H in the longest-first order, head item % H).
+template <bool WINDOW>
 __device__ __forceinline__ PItem locate(const PrefillArgs& a, const int32_t* offu, const int32_t* order,
                                         int item) {
   PItem it;
@@ -339,11 +356,11 @@ __device__ __forceinline__ PItem locate(const PrefillArgs& a, const int32_t* off
   it.h = item - r * a.H;
   const int u = order[r];
   it.s = upper_seq(offu, a.S, u);
-  pair_tiles(a, it.s, u - offu[it.s], it);
+  pair_tiles<WINDOW>(a, it.s, u - offu[it.s], it);
   return it;
 }
 
-template <typename T>
+template <typename T, bool WINDOW>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const PrefillArgs a) {
@@ -404,7 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = bad ? 0 : qe - qs;
     const int ntiles = (n + kBM - 1) / kBM;
     offu[s + 1] = (ntiles + 1) / 2;
-    if (n > 0) atomicMax(max_nkv, (L + kBN - 1) / kBN);  // the last tile sees the whole context
+    int most = (L + kBN - 1) / kBN;  // the last tile sees the whole context
+    if (WINDOW) most = min(most, a.window / kBN + a.sinks / kBN + 5);  // (two tiles of queries, and ends inside a tile)
+    if (n > 0) atomicMax(max_nkv, most);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -434,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= n_units) return -1;
       PItem t;
       const int s = upper_seq(offu, a.S, u);
-      pair_tiles(a, s, u - offu[s], t);
+      pair_tiles<WINDOW>(a, s, u - offu[s], t);
       return min(31, static_cast<int>((static_cast<long long>(t.nkv) * 32) / (mx + 1)));
     };
     const unsigned lt = (1u << lane) - 1u;
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++ni;
       if (done) break;
-      const PItem it = locate(a, offu, order, item);
+      const PItem it = locate<WINDOW>(a, offu, order, item);
       if (it.nkv == 0) continue;
       // Q tiles of the used slots (two 64-column halves each)
       int ok = 1;
@@ -511,11 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* table = a.block_tables + static_cast<int64_t>(it.s) * a.bt_row;
       const int Lv = a.context_lens[it.s];
       const int oob_group = a.num_blocks * (B / 8);  // any frame past the cache: zero fill
-      // first 8-row group (in the frame view) of the frame lane f copies in tile j
+      const int head = WINDOW ? it.h / a.g : it.h;  // of the caches
+      // first 8-row group (in the frame view) of the frame lane f copies in step j
       auto frame_group = [&](int j) -> int {
-        const int lb = j * fpt + lane;
+        const int lb = (WINDOW && j >= it.sink_tiles ? j + it.skip : j) * fpt + lane;
         int g = oob_group;
-        if (lane < fpt && lb * B < Lv) {
+        if (lane < fpt && lb * B < Lv && (!WINDOW || lb * B < a.sinks || lb * B > it.start - B)) {
           const int fr = __ldg(table + lb);
           if (fr >= 0 && fr < a.num_blocks) g = fr * (B / 8);
           else atomicOr(a.status, kDevBadBlock);
@@ -531,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         w = __shfl_sync(kFull, w, 0);
         if (!w) return false;
-        if (lane < fpt) tma_load_5d(sb + ring + st * kTile + lane * B * 256, map, g, it.h, BAR(full_bar + st));
+        if (lane < fpt) tma_load_5d(sb + ring + st * kTile + lane * B * 256, map, g, head, BAR(full_bar + st));
         return true;
       };
       int g = frame_group(0);
@@ -610,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(BAR(BI_EMPTY + sl));
         ++ni;
         if (item < 0) break;
-        const PItem it = locate(a, offu, order, item);
+        const PItem it = locate<WINDOW>(a, offu, order, item);
         if (it.nkv == 0) continue;
         const int n0 = it.nkv_q[0], n1 = it.nkv_q[1];
         bool ok = wait(BQ_FULL, qi & 1);
@@ -721,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(BAR(BI_EMPTY + sl));
       ++ni;
       if (item < 0) break;
-      const PItem it = locate(a, offu, order, item);
+      const PItem it = locate<WINDOW>(a, offu, order, item);
       const int n0 = it.nkv_q[0], n1 = it.nkv_q[1];
       if (n1 == 0) continue;
       // rows past the chunk end attend everything they are shown (not stored)
@@ -742,8 +762,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys of this half a row may see: 64 half + (0 .. nv-1).  Rows of a warp are
         // consecutive positions, so a 32-key chunk is (warp-uniformly) fully visible,
         // fully masked (weight 0, not loaded) or split by the diagonal.
-        const int nvalid = max(0, min(kBN, pos[q] - j * kBN + 1));
-        const int nv = max(0, min(64, nvalid - 64 * half));
+        const int tile = WINDOW && j >= it.sink_tiles ? j + it.skip : j;
+        const int nvalid = max(0, min(kBN, pos[q] - tile * kBN + 1));
+        int nv = max(0, min(64, nvalid - 64 * half));
+        int from = 0, sinks = 0;  // WINDOW: of those, sinks .. from - 1 are hidden
+        if (WINDOW) {
+          const int base = tile * kBN + 64 * half;
+          from = max(0, min(64, max(0, pos[q] + 1 - a.window) - base));
+          sinks = max(0, min(64, a.sinks - base));
+          if (sinks >= from) from = 0;
+          if (sinks == 0 && from >= nv) nv = 0;
+        }
         const int wmin = __reduce_min_sync(kFull, nv), wmax = __reduce_max_sync(kFull, nv);
         uint32_t sr[2][32];
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -761,6 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (cc * 32 + i >= nv) cur[i] = __float_as_uint(-INFINITY);
+            }
+            if (WINDOW && __any_sync(kFull, from > cc * 32)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (cc * 32 + i >= sinks && cc * 32 + i < from) cur[i] = __float_as_uint(-INFINITY);
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
@@ -783,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool spec = kSplitP && __all_sync(kFull, m_ref[q] > -INFINITY && mine * sl2 <= m_ref[q] + 8.f);
         uint64_t sum2[2];  // packed fp32 pairs of partial row sums
         auto weights = [&](float mref) {
+          if (WINDOW && mref == -INFINITY) mref = 0.f;  // nothing seen yet: every score is -inf
           const uint64_t nm2 = f2(-mref, -mref);
           sum2[0] = sum2[1] = 0ull;
 #pragma unroll
@@ -904,11 +939,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <typename T>
+template <typename T, bool WINDOW>
 cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    int grid, cudaStream_t stream) {
   const size_t smem = smem_bytes(a.S, a.unit_cap);
-  auto kern = prefill_kernel<T>;
+  auto kern = prefill_kernel<T, WINDOW>;
   cudaError_t e = kernel_prep(reinterpret_cast<const void*>(kern), kThreads, smem, nullptr);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, a);

@@ -1,0 +1,326 @@
+// Append into the 8-bit cache [num_blocks, H, B, D], and its rows read back in 16 bits.
+//
+// A byte b stands for (b - 128) * step, one step for each (frame, head).  A frame that begins with the call's tokens takes
+//     r = 127 / max |x|, cut to 8 leading bits;  step = 1 / r;  b = 128 + round-half-even(x r).
+// x has at most 11 bits, so x r has at most 19 and is exact in fp32: the rounding to a whole number is the only one, and a code
+// follows from the formula alone.  A frame that holds earlier tokens keeps its r, or halves it as often as the new
+// tokens need to fit, and each earlier code n becomes round-half-even(n / 2^k).  Halvings are exact, and there are
+// few of them: an earlier token is off by less than (1/2 + 1/4 + ...) final steps, however often the frame grows (a step that followed each new maximum
+// would round every earlier code again at every one).
+//
+// A warp takes 16 rows of one frame and head, all in registers: their maximum, then their codes, one pass over the data.
+// Frames of more than 16 tokens are as many warps of one block, which exchange their maxima.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pa.h"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 128;
+constexpr float kLeast = 0x1p-60f, kMost = 0x1p60f;  // what a frame's largest element counts as: every product of r and x stays in fp32's range
+
+template <typename T>
+struct Bits;
+template <>
+struct Bits<__half> {
+  static constexpr uint32_t kInf = 0x7c00;
+  static constexpr bool kPastMost = false;  // whether an element may be above kMost
+  __device__ __forceinline__ static float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+  __device__ __forceinline__ static float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
+  __device__ __forceinline__ static uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Bits<__nv_bfloat16> {
+  static constexpr uint32_t kInf = 0x7f80;
+  static constexpr bool kPastMost = true;
+  __device__ __forceinline__ static float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  __device__ __forceinline__ static float value(uint32_t bits) { return __uint_as_float(bits << 16); }
+  __device__ __forceinline__ static uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// The codes of four elements as bytes: x r + 128 rounded in the low bits of 1.5 * 2^23.
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b, float r) {
+  constexpr float kRound = 12582912.f + 128.f;  // even, as 128 is: ties go to even codes
+  const uint32_t c0 = __float_as_uint(fmaf(a.x, r, kRound)), c1 = __float_as_uint(fmaf(a.y, r, kRound));
+  const uint32_t c2 = __float_as_uint(fmaf(b.x, r, kRound)), c3 = __float_as_uint(fmaf(b.y, r, kRound));
+  return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
+}
+// The same of four earlier codes times 2^-k = p.
+__device__ __forceinline__ uint32_t halved4(uint32_t w, float p) {
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = static_cast<float>((w >> (8 * i)) & 255u) - 128.f;
+  return codes4(make_float2(f[0], f[1]), make_float2(f[2], f[3]), p);
+}
+
+// The call's frames in order of sequences: which one is the u-th, found by each warp for itself.
+struct Unit {
+  int s, L, first, row0;  // sequence, its tokens, its first new one and that token's row of k_new
+  int j;                  // position in its table; < 0: there are not so many
+};
+__device__ __forceinline__ int new_tokens(const Append8Args& a, int s, int* L, int* row0) {
+  *L = a.context_lens[s];
+  *row0 = a.query_start ? a.query_start[s] : s;
+  const int end = a.query_start ? a.query_start[s + 1] : s + min(max(*L, 0), 1);
+  const bool bad = *row0 < 0 || end < *row0 || end > a.T || *L < end - *row0 ||
+                   static_cast<int64_t>(*L) > (static_cast<int64_t>(a.max_blocks) << a.log2_B);
+  return bad ? -1 : end - *row0;
+}
+__device__ __forceinline__ Unit find_unit(const Append8Args& a, int u, int lane, bool report) {
+  Unit x;
+  x.j = -1;
+  int before = 0;
+  for (int s0 = 0; s0 < a.S; s0 += 32) {
+    int L = 0, row0 = 0, n = 0;
+    if (s0 + lane < a.S) n = new_tokens(a, s0 + lane, &L, &row0);
+    if (report && n < 0) atomicOr(a.status, kDevBadLen);
+    const int count = n > 0 ? ((L - 1) >> a.log2_B) - ((L - n) >> a.log2_B) + 1 : 0;
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned past = __ballot_sync(kAll, before + upto > u);
+    if (past && x.j < 0) {
+      const int f = __ffs(past) - 1;
+      x.s = s0 + f;
+      x.L = __shfl_sync(kAll, L, f);
+      x.first = x.L - __shfl_sync(kAll, n, f);
+      x.row0 = __shfl_sync(kAll, row0, f);
+      x.j = (x.first >> a.log2_B) + u - (before + __shfl_sync(kAll, upto - count, f));
+      if (!report) return x;
+    }
+    before = min(before + __shfl_sync(kAll, upto, 31), 1 << 29);  // (ranges that overlap: no sum passes int32)
+  }
+  if (report && before > a.units && lane == 0) atomicOr(a.status, kDevBadLen);
+  return x;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(512) append8_kernel(const Append8Args a) {
+  constexpr int V = D / 8, kRows = 32 / V, kSteps = 16 / kRows;  // lanes of a row, rows a step, steps of 16 rows
+  __shared__ uint32_t maxima[16];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / V, vec = lane % V;
+  const int u = blockIdx.x / a.blocks_unit, part = blockIdx.x - u * a.blocks_unit;
+  const Unit x = find_unit(a, u, lane, blockIdx.x == 0);
+  if (x.j < 0) return;  // (the whole block)
+  const int item = part * (blockDim.x >> (5 + a.log2_slabs)) + (warp >> a.log2_slabs), slab = warp & ((1 << a.log2_slabs) - 1);
+  const bool is_v = item >= a.H;
+  const int h = is_v ? item - a.H : item;
+  bool live = h < a.H;
+  const int begin = x.j << a.log2_B;  // the frame's first token
+  const int at = slab * 16 + sub;      // this lane's first row of it
+  const int past = min(a.B, x.L - begin), from = max(0, x.first - begin);  // its rows from .. past - 1 are new
+  const int frame = live ? a.block_tables[x.s * a.bt_row + x.j] : 0;
+
+  uint4 w[kSteps];
+  const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + (x.row0 + static_cast<int64_t>(begin) + at - x.first) * (is_v ? a.v_row : a.k_row) +
+                 static_cast<int64_t>(h) * D + vec * 8;
+  const int64_t step_row = kRows * (is_v ? a.v_row : a.k_row);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int row = at + i * kRows;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (live && row >= from && row < past) w[i] = *reinterpret_cast<const uint4*>(src + i * step_row);
+  }
+  if (live && (frame < 0 || frame >= a.num_blocks)) {
+    if (lane == 0) atomicOr(a.status, kDevBadBlock);
+    live = false;
+  }
+  float* step_at = (is_v ? a.v_scale : a.k_scale) + (live ? frame * (is_v ? a.vs_row : a.ks_row) + h : 0);
+  const float was = live && from > 0 ? *step_at : 0.f;
+
+  // the largest magnitude, as the bits of T: those of an infinity or more once an element is not finite
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                   __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+  }
+  uint32_t top = __reduce_max_sync(kAll, max(top2 & 0xffffu, top2 >> 16));
+  if (a.log2_slabs > 0) {
+    if (lane == 0) maxima[warp] = top;
+    __syncthreads();  // (also: each warp has the old step before one writes the new)
+    for (int i = 0; i < 1 << a.log2_slabs; ++i) top = max(top, maxima[(warp & ~((1 << a.log2_slabs) - 1)) + i]);
+  }
+  if (!live) return;
+
+  float r = 0.f, step = __uint_as_float(0x7fffffffu);
+  int halvings = 0;
+  const float largest = fminf(fmaxf(Bits<T>::value(top), kLeast), kMost);
+  // an earlier step that no append leaves is as good as NaN
+  const bool sound = top < Bits<T>::kInf && (from == 0 || (was >= 0x1p-67f && was <= 0x1p60f));
+  if (sound && from == 0) {
+    r = __uint_as_float(__float_as_uint(__fdiv_rn(127.f, largest)) & 0xffff0000u);
+    step = __frcp_rn(r);
+  } else if (sound) {
+    const uint32_t inv = __float_as_uint(__frcp_rn(was));
+    r = __uint_as_float((inv + 0x7fffu + ((inv >> 16) & 1u)) & 0xffff0000u);  // to 8 bits: the r that step is one over
+    const float over = largest * r;
+    halvings = max(0, static_cast<int>(__float_as_uint(over) >> 23) - 133);  // over / 2^halvings is below 128
+    if (__uint_as_float(__float_as_uint(over) - (static_cast<uint32_t>(halvings) << 23)) > 127.f) ++halvings;
+    r = __uint_as_float(__float_as_uint(r) - (static_cast<uint32_t>(halvings) << 23));
+    step = __uint_as_float(__float_as_uint(was) + (static_cast<uint32_t>(halvings) << 23));
+  }
+  unsigned char* dst = (is_v ? a.v_cache : a.k_cache) + ((static_cast<int64_t>(frame) * a.H + h) * a.B + at) * D + vec * 8;
+  if (Bits<T>::kPastMost && sound && Bits<T>::value(top) > kMost) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(&w[i]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Bits<T>::unpack(p[k]);
+        p[k] = Bits<T>::pack(fminf(fmaxf(f.x, -kMost), kMost), fminf(fmaxf(f.y, -kMost), kMost));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int row = at + i * kRows;
+    if (row >= from && row < past) {
+      uint2 y = make_uint2(0x80808080u, 0x80808080u);
+      if (sound) {
+        y.x = codes4(Bits<T>::unpack(w[i].x), Bits<T>::unpack(w[i].y), r);
+        y.y = codes4(Bits<T>::unpack(w[i].z), Bits<T>::unpack(w[i].w), r);
+      }
+      *reinterpret_cast<uint2*>(dst + i * kRows * D) = y;
+    }
+  }
+  if (halvings > 0) {
+    const float p = __uint_as_float(static_cast<uint32_t>(127 - min(halvings, 30)) << 23);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (at + i * kRows >= from) continue;
+      uint2 y = *reinterpret_cast<const uint2*>(dst + i * kRows * D);
+      y.x = halved4(y.x, p);
+      y.y = halved4(y.y, p);
+      *reinterpret_cast<uint2*>(dst + i * kRows * D) = y;
+    }
+  }
+  if (slab == 0 && lane == 0 && (from == 0 || halvings > 0 || !sound)) *step_at = step;
+}
+
+// A warp per token, cache and kSteps * 32 / V heads; a lane reads 8 bytes and writes 16.
+constexpr int kReadSteps = 4;
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Args a) {
+  constexpr int V = D / 8, kAtOnce = 32 / V;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, sub = lane / V, vec = lane % V;
+  const unsigned job = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), chunks = a.chunks;
+  if (job >= 2 * chunks * a.T) return;
+  const int t = static_cast<int>(job / (2 * chunks));
+  int part = static_cast<int>(job - t * 2 * chunks);
+  const bool is_v = part >= static_cast<int>(chunks);
+  if (is_v) part -= chunks;
+  const int h0 = part * kAtOnce * kReadSteps + sub;
+  const int32_t slot = a.slots[t];
+  if (slot < 0) return;
+  if (slot >= a.num_slots) {
+    if (lane == 0) atomicOr(a.status, kDevBadSlot);
+    return;
+  }
+  const int frame = slot >> a.log2_B;
+  const unsigned char* src = (is_v ? a.v_cache : a.k_cache) + ((static_cast<int64_t>(frame) * a.H + h0) * a.B + (slot & (a.B - 1))) * D + vec * 8;
+  const float* steps = (is_v ? a.v_scale : a.k_scale) + frame * (is_v ? a.vs_row : a.ks_row) + h0;
+  T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + t * (is_v ? a.vo_row : a.ko_row) + static_cast<int64_t>(h0) * D + vec * 8;
+  uint2 w[kReadSteps];
+  float step[kReadSteps];
+#pragma unroll
+  for (int i = 0; i < kReadSteps; ++i) {
+    if (h0 + i * kAtOnce >= a.H) continue;
+    w[i] = *reinterpret_cast<const uint2*>(src + static_cast<int64_t>(i * kAtOnce) * a.B * D);
+    step[i] = steps[i * kAtOnce];
+  }
+#pragma unroll
+  for (int i = 0; i < kReadSteps; ++i) {
+    if (h0 + i * kAtOnce >= a.H) continue;
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // 2^23 + byte, exactly
+      const uint32_t v = k < 2 ? w[i].x : w[i].y;
+      const float f0 = __uint_as_float(__byte_perm(v, 0x4b000000u, k & 1 ? 0x7442 : 0x7440)) - 8388736.f;
+      const float f1 = __uint_as_float(__byte_perm(v, 0x4b000000u, k & 1 ? 0x7443 : 0x7441)) - 8388736.f;
+      y[k] = Bits<T>::pack(f0 * step[i], f1 * step[i]);
+    }
+    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i * kAtOnce) * D) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned threads, void** args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+
+// Warps of a block; 16 rows each, and a frame's in one block.
+static int64_t append8_threads(int64_t B) { return B / 16 * 32 > kThreads ? B / 16 * 32 : kThreads; }
+
+bool append8_fits(Append8Args* a) {
+  a->log2_slabs = a->B > 16 ? a->log2_B - 4 : 0;
+  const int64_t items = append8_threads(a->B) / 32 >> a->log2_slabs;
+  const int64_t blocks = (2 * static_cast<int64_t>(a->H) + items - 1) / items;
+  // frames that hold a new token: every one holds at least one, all but two of a sequence B
+  const int64_t units = a->T < a->T / a->B + 2 * static_cast<int64_t>(a->S) ? a->T : a->T / a->B + 2 * static_cast<int64_t>(a->S);
+  if (units > 1 << 25 || units * blocks > INT32_MAX) return false;
+  a->units = static_cast<int32_t>(units);
+  a->blocks_unit = static_cast<int32_t>(blocks);
+  return true;
+}
+
+cudaError_t launch_append8(int dtype, const Append8Args& a, cudaStream_t stream) {
+  void* args[1] = {const_cast<Append8Args*>(&a)};
+  const void* fn = dtype == PA_F16 ? (a.D == 128 ? reinterpret_cast<const void*>(&append8_kernel<__half, 128>)
+                                                 : reinterpret_cast<const void*>(&append8_kernel<__half, 64>))
+                                   : (a.D == 128 ? reinterpret_cast<const void*>(&append8_kernel<__nv_bfloat16, 128>)
+                                                 : reinterpret_cast<const void*>(&append8_kernel<__nv_bfloat16, 64>));
+  return launch_pdl(fn, static_cast<unsigned>(a.units) * a.blocks_unit, static_cast<unsigned>(append8_threads(a.B)), args, stream);
+}
+
+bool read8_fits(Read8Args* a) {
+  const int64_t per = 32 / (a->D / 8) * kReadSteps, chunks = (a->H + per - 1) / per;
+  a->chunks = static_cast<int32_t>(chunks);
+  return 2 * chunks * a->T <= INT32_MAX;
+}
+
+cudaError_t launch_read8(int dtype, const Read8Args& a, cudaStream_t stream) {
+  void* args[1] = {const_cast<Read8Args*>(&a)};
+  const void* fn = dtype == PA_F16 ? (a.D == 128 ? reinterpret_cast<const void*>(&read8_kernel<__half, 128>)
+                                                 : reinterpret_cast<const void*>(&read8_kernel<__half, 64>))
+                                   : (a.D == 128 ? reinterpret_cast<const void*>(&read8_kernel<__nv_bfloat16, 128>)
+                                                 : reinterpret_cast<const void*>(&read8_kernel<__nv_bfloat16, 64>));
+  const int64_t jobs = 2 * static_cast<int64_t>(a.chunks) * a.T;
+  return launch_pdl(fn, static_cast<unsigned>((jobs + kThreads / 32 - 1) / (kThreads / 32)), kThreads, args, stream);
+}
+
+}  // namespace pa

@@ -13,6 +13,25 @@ namespace pa {
 // Parts of 16 keys of L >= 0 tokens; at least one.
 PA_RANGES int parts16(int L) { return ((L > 1 ? L - 1 : 0) >> 4) + 1; }
 
+// What a query behind L >= 0 tokens sees of them through a window and some sinks: the tokens 0 .. sinks - 1 and start .. L - 1, in
+// parts of 16 that begin at multiples of 16.  Sinks that reach the window are part of it: start is 0 then, sinks too.
+struct Sight {
+  int start, sinks;        // sinks < start, or both 0
+  int sink_parts, parts;   // of the sinks; of all, at least one
+  PA_RANGES int base(int part) const {  // first token of a part
+    return part < sink_parts ? 16 * part : (start & ~15) + 16 * (part - sink_parts);
+  }
+};
+PA_RANGES Sight sight_of(int L, int window, int sinks) {
+  Sight x;
+  x.start = L > window ? L - window : 0;
+  if (sinks >= x.start) x.start = 0;
+  x.sinks = x.start ? sinks : 0;
+  x.sink_parts = x.sinks ? parts16(x.sinks) : 0;
+  x.parts = x.sink_parts + parts16(L - (x.start & ~15));
+  return x;
+}
+
 // First unit of worker w (0 .. workers) where `total` units are cut evenly among `workers` (< 2^15 of them).
 PA_RANGES int first_unit(int total, int workers, int w) {
   const int per = total / workers;
