@@ -154,6 +154,10 @@ struct Q8Format {
 
 namespace {
 
+// Bound by memory while it streams.  8 warps an SM, two on each scheduler, one stage of 64 keys (206 registers at D = 128): 64 sequences of
+// 512 to 2048 tokens, 32 heads of 128 in fp16 (674 MB) take 111.4 us, 6.05 TB/s; 4 x 16384 in bf16 (538 MB) 85.8 us, 6.27 TB/s, of which
+// about 4 us pass before the first keys are there and 5 behind the last.  12 warps 118.8 and 94.0 us, 10 warps 114.7 and 90.7 us, 6
+// warps with two stages 132 and 100 us; tiles of 32 keys with 12 warps and two stages 134.6 and 104 us.
 template <typename T, int D, int KEYS>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {
@@ -161,8 +165,8 @@ cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorM
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, KEYS, 1, 4, 3>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, KEYS, 1, 4, 3>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, KEYS, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, KEYS, 1, 4, 2>(a, maps, num_sms, stream, workers);
   return gk::launch<F, 2, gk::kTwoParts, KEYS, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 

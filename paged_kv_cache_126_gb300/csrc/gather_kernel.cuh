@@ -627,6 +627,15 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   int plan_meta = 0;
   float4 plan_steps = make_float4(0.f, 0.f, 0.f, 0.f);  // of the halves' keys, of their values
   int issued = 0, issue_st = 0, issue_phase = 0;
+  auto note = [&](int part) {  // what the consumer needs to know of a tile
+    const int sub = lane - part;
+    if (static_cast<unsigned>(sub) >= LOADS) return;
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 16 + sub * 4), "r"(plan_meta) : "memory");
+    if constexpr (F::kSteps)
+      asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(steps + ((issue_phase * STAGES + issue_st) * LOADS + sub) * 16),
+                   "f"(plan_steps.x), "f"(plan_steps.y), "f"(plan_steps.z), "f"(plan_steps.w)
+                   : "memory");
+  };
   auto issue_keys = [&]() {
     const int part = ahead.t * LOADS;
     if ((part & ~31) != planned) {
@@ -642,14 +651,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         plan_steps.w = f1 >= 0 ? a.v_step[f1 * a.vs_row + ahead.h] : 0.f;
       }
     }
-    const int sub = lane - (part & 31);
-    if (static_cast<unsigned>(sub) < LOADS) {
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + issue_st * 16 + sub * 4), "r"(plan_meta) : "memory");
-      if constexpr (F::kSteps)
-        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(steps + ((issue_phase * STAGES + issue_st) * LOADS + sub) * 16),
-                     "f"(plan_steps.x), "f"(plan_steps.y), "f"(plan_steps.z), "f"(plan_steps.w)
-                     : "memory");
-    }
+    if constexpr (!F::kSteps) note(part & 31);  // (steps may still be on their way: noted behind both copies)
     // the first tile of a (s, h), or of this warp's part of it, brings the queries along
     const uint32_t dst = stages + issue_st * kStage, bar = bars + 16 * issue_st;
     const bool first = ahead.t == 0 || issued == 0;
@@ -660,6 +662,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   };
   auto issue_values = [&]() {  // of the same tile, and on to the next
     F::load(a, &maps.v, place, ahead.h, lane, (ahead.t * LOADS) & 31, stages + issue_st * kStage + kKeys, bars + 16 * issue_st + 8, 0);
+    if constexpr (F::kSteps) note((ahead.t * LOADS) & 31);
     if (++issue_st == STAGES) issue_st = 0, issue_phase ^= 1;
     ++issued;
     if (++ahead.t == ahead.tiles && issued < count) {
