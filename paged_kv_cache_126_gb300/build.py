@@ -26,7 +26,8 @@ MARSHAL_TORCH = os.path.join(BUILD, "_marshal.torch")  # the torch version that 
 
 SOURCES = ["block_manager.cpp", "api.cu", "append.cu", "decode_f16.cu", "decode_bf16.cu", "decode_f32.cu",
            "prefill.cu", "decode_split.cu", "decode_shared.cu", "rotary.cu", "decode_q4.cu", "decode_selected.cu",
-           "select.cu", "quant8.cu", "decode_q8.cu", "decode_window.cu", "prefill_window.cu"]
+           "select.cu", "quant8.cu", "decode_q8.cu", "decode_window.cu", "prefill_window_f16.cu",
+           "prefill_window_bf16.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -1147,7 +1147,7 @@ int prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cac
   // their unit offsets and order in shared memory: a batch larger than that runs as
   // launches over consecutive ranges of sequences (q and out stay whole: query_start
   // entries index all of q).
-  const int64_t tile_cap = (T + 255) / 256 + 1;
+  const int64_t tile_cap = window > 0 ? (T + 127) / 128 + 1 : (T + 255) / 256 + 1;  // (a window's units may be single tiles)
   auto fits = [&](int64_t n) {
     return n + tile_cap <= INT32_MAX &&
            pa::prefill_smem_bytes(static_cast<int>(n), static_cast<int>(n + tile_cap)) <= 227 * 1024;
@@ -1197,9 +1197,9 @@ int prefill(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cac
     r.S = static_cast<int32_t>(n);
     r.unit_cap = static_cast<int32_t>(n + tile_cap);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = window > 0     ? pa::launch_prefill_window(dt, r, tq, tk, tv, grid, st)
-                          : dt == PA_F16 ? pa::launch_prefill_f16(r, tq, tk, tv, grid, st)
-                                         : pa::launch_prefill_bf16(r, tq, tk, tv, grid, st);
+    const auto launch = dt == PA_F16 ? (window > 0 ? pa::launch_prefill_window_f16 : pa::launch_prefill_f16)
+                                     : (window > 0 ? pa::launch_prefill_window_bf16 : pa::launch_prefill_bf16);
+    const cudaError_t e = launch(r, tq, tk, tv, grid, st);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     g_launches.fetch_add(1);
   }

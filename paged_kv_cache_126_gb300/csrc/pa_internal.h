@@ -184,8 +184,10 @@ cudaError_t launch_prefill_f16(const PrefillArgs&, const CUtensorMap& tq, const 
                                const CUtensorMap& tv, int grid, cudaStream_t);
 cudaError_t launch_prefill_bf16(const PrefillArgs&, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int grid, cudaStream_t);
-cudaError_t launch_prefill_window(int dtype, const PrefillArgs&, const CUtensorMap& tq, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int grid, cudaStream_t);
+cudaError_t launch_prefill_window_f16(const PrefillArgs&, const CUtensorMap& tq, const CUtensorMap& tk,
+                                      const CUtensorMap& tv, int grid, cudaStream_t);
+cudaError_t launch_prefill_window_bf16(const PrefillArgs&, const CUtensorMap& tq, const CUtensorMap& tk,
+                                       const CUtensorMap& tv, int grid, cudaStream_t);
 size_t prefill_smem_bytes(int S, int unit_cap);
 
 // Decode over the split cache layout (k [nb, H, D/x, B, x], v [nb, H, D, B]).

@@ -32,10 +32,15 @@
 //     back to TMEM, O rescaled in TMEM
 //     when the reference max moves; normalised rows are written to `out`.
 //   * WINDOW: query i attends the keys j <= p with j > p - window or j < sinks, and query heads share
-//     key heads in groups of g.  An item walks the key tiles that hold sinks, then those from its first query's
-//     window on (a step of the walk is not the tile's number then); frames of a tile that none of its
-//     queries sees are zero-filled and not looked up.  A row may see nothing of its first tiles: its
-//     reference max is -inf until it does, and its weights 0.
+//     key heads in groups of g.  An item's keys are the frames that hold sinks and then those from its first
+//     query's window on, as one list: a key tile is any 128 / B entries of it (sinks take a few entries of the first
+//     tile, not a tile of their own, and no tile is lost to where the window begins).  What the two slots are:
+//       kRows   two tiles of one head, as above;
+//       kHeads  one tile of two heads of a key head, where g is even: both see the same keys, so that no slot
+//               walks tiles of the other's window or stands empty behind an odd tile;
+//       kSplit  one tile of one head, every other key tile to each slot, joined at the end: where there are no more
+//               tiles than thread blocks (512 queries of 32 heads over windows of 1024: 45.6 -> 24.9 us).
+//     A row may see nothing of its first tiles: its reference max is -inf until it does, and its weights 0.
 //   * Every wait is a bounded mbarrier wait; one that gives up sets PA_DEV_TIMEOUT
 //     and makes the block's later waits no-ops; before the TMEM is freed the MMA
 //     lane waits (bounded) for its own MMAs and the producer for its copies.
@@ -294,16 +299,18 @@ __device__ __forceinline__ int upper_seq(const int32_t* off, int S, int x) {
 // A unit is a pair of consecutive 128-query tiles of one sequence: slot 1 holds the
 // later tile, slot 0 the one before it (absent when the chunk has an odd tile count
 // and this is its first pair).  A work item is (unit, head); both tiles share every
-// K/V tile.
+// K/V tile.  (kHeads, kSplit: a unit is one tile.)
+enum Slots { kCausal, kRows, kHeads, kSplit };  // (kCausal: pa_prefill)
 struct PItem {
-  int s, h;
-  int nkv;       // key tiles the item walks (those of slot 1)
-  // WINDOW: step j is tile j, from step `sink_tiles` on tile j + skip; keys below `start` but for the sinks are seen by no row
-  int sink_tiles, skip, start;
+  int s, h;      // kHeads: slot 0's head, slot 1's is the next
+  int nkv;       // key tiles the item walks (kRows: those of slot 1)
   int qrow0[2];  // first q row of the slot's tile (global row index)
   int nrows[2];  // valid rows of the slot's tile, 0 when the slot is unused
   int pos0[2];   // position of the slot's first row
   int nkv_q[2];  // key tiles the slot visits, 0 when unused
+  // WINDOW: entry e of the list is frame e where e < sink_frames, else frame e + skip_frames; key i of the list is at position i,
+  // or i + shift
+  int sink_frames, skip_frames, shift;
 };
 
 // A sequence is skipped (and flagged) unless 0 <= qs <= qe <= T, n = qe - qs <= L and
@@ -314,7 +321,6 @@ __device__ __forceinline__ bool seq_bad(int qs, int qe, int L, const PrefillArgs
 }
 
 // Tiles of pair p (counted from the end of the chunk) of a sequence.
-template <bool WINDOW>
 __device__ __forceinline__ void pair_tiles(const PrefillArgs& a, int s, int p, PItem& it) {
   const int qs = a.query_start[s], qe = a.query_start[s + 1];
   const int n = qe - qs;
@@ -336,37 +342,68 @@ __device__ __forceinline__ void pair_tiles(const PrefillArgs& a, int s, int p, P
       it.nkv_q[q] = (it.pos0[q] + it.nrows[q] - 1 + kBN) / kBN;
     }
   }
-  if (WINDOW) {
-    it.start = max(0, (it.nrows[0] > 0 ? it.pos0[0] : it.pos0[1]) + 1 - a.window);
-    if (a.sinks >= it.start) it.start = 0;
-    it.sink_tiles = min((a.sinks >> 7) + ((a.sinks & 127) != 0), it.start / kBN);
-    it.skip = it.start / kBN - it.sink_tiles;
-    if (it.nkv_q[0] > 0) it.nkv_q[0] -= it.skip;
-    if (it.nkv_q[1] > 0) it.nkv_q[1] -= it.skip;
-  }
   it.nkv = it.nkv_q[1];
 }
 
-// Item -> (unit of rank item / H in the longest-first order, head item % H).
-template <bool WINDOW>
+// The slots of unit p (from the end of the chunk) of a sequence, and the list of its keys.
+template <int SLOTS>
+__device__ __forceinline__ void window_tiles(const PrefillArgs& a, int s, int p, PItem& it) {
+  const int qs = a.query_start[s], qe = a.query_start[s + 1];
+  const int n = qe - qs, L = a.context_lens[s];
+  const int ntiles = seq_bad(qs, qe, L, a) || n <= 0 ? 0 : (n + kBM - 1) / kBM;
+  int end[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int qt = SLOTS == kRows ? ntiles - 1 - 2 * p - (1 - q) : ntiles - 1 - p;
+    const bool on = qt >= 0;
+    it.qrow0[q] = qs + (on ? qt * kBM : 0);
+    it.nrows[q] = on ? min(kBM, n - qt * kBM) : 0;
+    it.pos0[q] = on ? L - n + qt * kBM : 0;
+    end[q] = it.pos0[q] + it.nrows[q];  // one past its last query
+  }
+  int start = max(0, (it.nrows[0] > 0 ? it.pos0[0] : it.pos0[1]) + 1 - a.window);
+  if (a.sinks >= start) start = 0;
+  start &= ~(a.B - 1);
+  const int sink_frames = start > 0 && a.sinks > 0 ? (a.sinks - 1) / a.B + 1 : 0;
+  it.shift = start - sink_frames * a.B;
+  it.sink_frames = sink_frames;
+  it.skip_frames = it.shift / a.B;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) it.nkv_q[q] = it.nrows[q] > 0 ? (end[q] - it.shift + kBN - 1) / kBN : 0;
+  it.nkv = it.nkv_q[1];
+  if (SLOTS == kSplit) {
+    it.nkv_q[0] = (it.nkv + 1) / 2;
+    it.nkv_q[1] = it.nkv / 2;
+  }
+}
+
+// Item -> (unit of rank item / H in the longest-first order, head item % H); kHeads: pairs of heads.
+template <int SLOTS>
 __device__ __forceinline__ PItem locate(const PrefillArgs& a, const int32_t* offu, const int32_t* order,
                                         int item) {
   PItem it;
-  const int r = item / a.H;
-  it.h = item - r * a.H;
+  const int heads = SLOTS == kHeads ? a.H >> 1 : a.H;
+  const int r = item / heads;
+  it.h = item - r * heads;
   const int u = order[r];
   it.s = upper_seq(offu, a.S, u);
-  pair_tiles<WINDOW>(a, it.s, u - offu[it.s], it);
+  if (SLOTS != kCausal) {
+    if (SLOTS == kHeads) it.h *= 2;
+    window_tiles<SLOTS>(a, it.s, u - offu[it.s], it);
+  } else {
+    pair_tiles(a, it.s, u - offu[it.s], it);
+  }
   return it;
 }
 
-template <typename T, bool WINDOW>
+template <typename T, int SLOTS>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const PrefillArgs a) {
   // bf16 weights keep 8 significant bits: each weight goes to the value product as a
   // high part and the remainder (two products into the same accumulator), which
   // leaves 2^-16 of it; fp16 weights (11 bits) go once.
+  constexpr bool WINDOW = SLOTS != kCausal;
   constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -420,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad && blockIdx.x == 0) atomicOr(a.status, kDevBadLen);
     const int n = bad ? 0 : qe - qs;
     const int ntiles = (n + kBM - 1) / kBM;
-    offu[s + 1] = (ntiles + 1) / 2;
+    offu[s + 1] = SLOTS == kHeads || SLOTS == kSplit ? ntiles : (ntiles + 1) / 2;
     int most = (L + kBN - 1) / kBN;  // the last tile sees the whole context
     if (WINDOW) most = min(most, a.window / kBN + a.sinks / kBN + 5);  // (two tiles of queries, and ends inside a tile)
     if (n > 0) atomicMax(max_nkv, most);
@@ -453,7 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= n_units) return -1;
       PItem t;
       const int s = upper_seq(offu, a.S, u);
-      pair_tiles<WINDOW>(a, s, u - offu[s], t);
+      if (WINDOW) window_tiles<SLOTS>(a, s, u - offu[s], t);
+      else pair_tiles(a, s, u - offu[s], t);
       return min(31, static_cast<int>((static_cast<long long>(t.nkv) * 32) / (mx + 1)));
     };
     const unsigned lt = (1u << lane) - 1u;
@@ -484,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const int total = n_units > a.unit_cap ? 0 : n_units * a.H;
+  const int total = n_units > a.unit_cap ? 0 : n_units * (SLOTS == kHeads ? a.H >> 1 : a.H);
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
@@ -507,19 +545,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++ni;
       if (done) break;
-      const PItem it = locate<WINDOW>(a, offu, order, item);
+      const PItem it = locate<SLOTS>(a, offu, order, item);
       if (it.nkv == 0) continue;
       // Q tiles of the used slots (two 64-column halves each)
       int ok = 1;
       if (lane == 0) {
         ok = mbar_wait(BAR(BQ_EMPTY), (qi & 1) ^ 1, abort_flag, a.status);
         if (ok) {
-          mbar_expect_tx(BAR(BQ_FULL), kTile * ((it.nrows[0] > 0) + (it.nrows[1] > 0)));
+          constexpr bool both = SLOTS != kSplit;  // (else slot 1's queries are slot 0's)
+          mbar_expect_tx(BAR(BQ_FULL), kTile * ((it.nrows[0] > 0) + (both && it.nrows[1] > 0)));
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            if (it.nrows[q] > 0) {
-              tma_load_3d(sb + kSmQ + q * kTile, &tmap_q, 0, it.h, it.qrow0[q], BAR(BQ_FULL));
-              tma_load_3d(sb + kSmQ + q * kTile + kHalf, &tmap_q, 64, it.h, it.qrow0[q], BAR(BQ_FULL));
+            if (it.nrows[q] > 0 && (q == 0 || both)) {
+              const int h = SLOTS == kHeads ? it.h + q : it.h;
+              tma_load_3d(sb + kSmQ + q * kTile, &tmap_q, 0, h, it.qrow0[q], BAR(BQ_FULL));
+              tma_load_3d(sb + kSmQ + q * kTile + kHalf, &tmap_q, 64, h, it.qrow0[q], BAR(BQ_FULL));
             }
           }
         }
@@ -531,11 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int Lv = a.context_lens[it.s];
       const int oob_group = a.num_blocks * (B / 8);  // any frame past the cache: zero fill
       const int head = WINDOW ? it.h / a.g : it.h;  // of the caches
-      // first 8-row group (in the frame view) of the frame lane f copies in step j
+      // first 8-row group (in the frame view) of the frame lane f copies in tile j
       auto frame_group = [&](int j) -> int {
-        const int lb = (WINDOW && j >= it.sink_tiles ? j + it.skip : j) * fpt + lane;
+        int lb = j * fpt + lane;
+        if (WINDOW && lb >= it.sink_frames) lb += it.skip_frames;
         int g = oob_group;
-        if (lane < fpt && lb * B < Lv && (!WINDOW || lb * B < a.sinks || lb * B > it.start - B)) {
+        if (lane < fpt && lb * B < Lv) {
           const int fr = __ldg(table + lb);
           if (fr >= 0 && fr < a.num_blocks) g = fr * (B / 8);
           else atomicOr(a.status, kDevBadBlock);
@@ -592,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st = t & 1;
 #pragma unroll
       for (int ks = 0; ks < kD / 16; ++ks) {
-        const uint64_t ad = sdesc(sb + kSmQ + q * kTile + (ks >> 2) * kHalf + (ks & 3) * 32, 0, 1024);
+        const uint64_t ad = sdesc(sb + kSmQ + (SLOTS == kSplit ? 0 : q * kTile) + (ks >> 2) * kHalf + (ks & 3) * 32, 0, 1024);
         const uint64_t bd = sdesc(sb + kSmK + st * kTile + (ks >> 2) * 1024 + (ks & 3) * 32, 0, 2048);
         mma(tmem + kTmemS + q * 128, ad, bd, id_qk, ks > 0 ? 1u : 0u);
       }
@@ -630,11 +671,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(BAR(BI_EMPTY + sl));
         ++ni;
         if (item < 0) break;
-        const PItem it = locate<WINDOW>(a, offu, order, item);
+        const PItem it = locate<SLOTS>(a, offu, order, item);
         if (it.nkv == 0) continue;
         const int n0 = it.nkv_q[0], n1 = it.nkv_q[1];
         bool ok = wait(BQ_FULL, qi & 1);
         ++qi;
+        if (SLOTS == kSplit) {
+          // slot q takes the tiles q, q + 2, ...: each is one slot's, and released after its one product
+          auto scores = [&](int q, int j) {  // of tile j
+            const int t = kt + j;
+            if (!wait(BK_FULL + (t & 1), (t >> 1) & 1)) return false;
+            qk(q, t);
+            commit(BAR(BK_EMPTY + (t & 1)));
+            if (j == it.nkv - 1) commit(BAR(BQ_EMPTY));
+            return true;
+          };
+          ok = ok && scores(0, 0) && (n1 == 0 || scores(1, 1));
+          for (int j = 0; j < it.nkv && ok; ++j) {
+            const int q = j & 1, t = kt + j;
+            ok = wait(BP_FULL + q, (q ? pc1 : pc0) & 1) && wait(BV_FULL + (t & 1), (t >> 1) & 1);
+            if (!ok) break;
+            pv(q, t, j < 2);
+            if (q) ++pc1; else ++pc0;
+            commit(BAR(BV_EMPTY + (t & 1)));
+            if (j + 2 >= it.nkv) commit(BAR(BO_FULL + q));
+            else ok = scores(q, j + 2);
+          }
+          kt += it.nkv;
+          if (!ok) break;
+          continue;
+        }
         ok = ok && wait(BK_FULL + (kt & 1), (kt >> 1) & 1);
         if (ok) {
           if (n0 > 0) qk(0, kt);
@@ -741,34 +807,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(BAR(BI_EMPTY + sl));
       ++ni;
       if (item < 0) break;
-      const PItem it = locate<WINDOW>(a, offu, order, item);
+      const PItem it = locate<SLOTS>(a, offu, order, item);
       const int n0 = it.nkv_q[0], n1 = it.nkv_q[1];
-      if (n1 == 0) continue;
+      if (it.nkv == 0) continue;
       // rows past the chunk end attend everything they are shown (not stored)
       int pos[2];
       float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < 2; ++q) pos[q] = row < it.nrows[q] ? it.pos0[q] + row : 0x3fffffff;
+      if (SLOTS == kSplit || SLOTS == kHeads) pos[1] = pos[0];
       bool ok = true;
       // per tile of slot q (slot 0 tile j, then slot 1 tile j): scores of this half's 64
       // keys -> weights, O rescaled if the reference moved
-      for (int j = 0; j < n1 && ok; ++j) {
+      for (int j = 0; j < (SLOTS == kSplit ? n0 : n1) && ok; ++j) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        if ((q == 0 && j >= n0) || !ok) continue;
+        if ((q == 0 && j >= n0) || (SLOTS == kSplit && q == 1 && j >= n1) || !ok) continue;
         if (!wait_all(BAR(BS_FULL + q), sc[q] & 1u)) { ok = false; continue; }
         ++sc[q];
         const uint32_t s_tmem = tmem + lane_base + kTmemS + q * 128;
         // keys of this half a row may see: 64 half + (0 .. nv-1).  Rows of a warp are
         // consecutive positions, so a 32-key chunk is (warp-uniformly) fully visible,
         // fully masked (weight 0, not loaded) or split by the diagonal.
-        const int tile = WINDOW && j >= it.sink_tiles ? j + it.skip : j;
-        const int nvalid = max(0, min(kBN, pos[q] - tile * kBN + 1));
+        const int tile = SLOTS == kSplit ? 2 * j + q : j;
+        const int last = WINDOW ? pos[q] - it.shift : pos[q];  // the last key a row sees, in the list
+        const int nvalid = max(0, min(kBN, last - tile * kBN + 1));
         int nv = max(0, min(64, nvalid - 64 * half));
         int from = 0, sinks = 0;  // WINDOW: of those, sinks .. from - 1 are hidden
         if (WINDOW) {
           const int base = tile * kBN + 64 * half;
-          from = max(0, min(64, max(0, pos[q] + 1 - a.window) - base));
+          from = max(0, min(64, max(it.sink_frames * B, last + 1 - a.window) - base));
           sinks = max(0, min(64, a.sinks - base));
           if (sinks >= from) from = 0;
           if (sinks == 0 && from >= nv) nv = 0;
@@ -897,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row sums, normalise this half's 64 dimensions, store
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        if ((q ? n1 : n0) == 0) continue;
+        if ((q ? n1 : n0) == 0 || (SLOTS == kSplit)) continue;
         if (ok && !wait_all(BAR(BO_FULL + q), oc[q] & 1u)) ok = false;
         ++oc[q];
         float other = 0.f;
@@ -908,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = row < it.nrows[q];
         const uint32_t o_tmem = tmem + lane_base + kTmemO + q * 128 + 64 * half;
         T* op = reinterpret_cast<T*>(a.out) + static_cast<int64_t>(it.qrow0[q] + row) * a.out_row +
-                static_cast<int64_t>(it.h) * kD + 64 * half;
+                static_cast<int64_t>(SLOTS == kHeads ? it.h + q : it.h) * kD + 64 * half;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t r[32];
@@ -929,6 +997,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (SLOTS == kSplit) {
+        // both slots hold parts of the same rows: joined by their references
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if ((q ? n1 : n0) == 0) continue;
+          if (ok && !wait_all(BAR(BO_FULL + q), oc[q] & 1u)) ok = false;
+          ++oc[q];
+          float other = 0.f;
+          if (ok && !exchange(l[q], other)) ok = false;
+          sum[q] = l[q] + other;
+        }
+        const float m = fmaxf(m_ref[0], m_ref[1]);
+        float f[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) f[q] = m_ref[q] == -INFINITY ? 0.f : ex2(m_ref[q] - m);
+        const float lt = sum[0] * f[0] + sum[1] * f[1];
+        const bool zero = !ok || !(lt > 0.f);
+        const float inv = zero ? 0.f : 1.f / lt;
+        f[0] *= inv;
+        f[1] *= inv;
+        T* op = reinterpret_cast<T*>(a.out) + static_cast<int64_t>(it.qrow0[0] + row) * a.out_row +
+                static_cast<int64_t>(it.h) * kD + 64 * half;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[2][16];
+          tmem_ld16_async(tmem + lane_base + kTmemO + 64 * half + c * 16, r[0]);
+          tmem_ld16_async(tmem + lane_base + kTmemO + 128 + 64 * half + c * 16, r[1]);
+          tmem_wait_ld();
+          tie16(r[0]);
+          tie16(r[1]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float y = __uint_as_float(r[0][i]) * f[0];
+            if (n1 > 0) y = fmaf(__uint_as_float(r[1][i]), f[1], y);  // (slot 1's columns are another item's where it has no tile)
+            r[0][i] = __float_as_uint(zero ? 0.f : y);
+          }
+          if (row < it.nrows[0]) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+              uint4 w4;
+              w4.x = pack2<T>(__uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1]));
+              w4.y = pack2<T>(__uint_as_float(r[0][i + 2]), __uint_as_float(r[0][i + 3]));
+              w4.z = pack2<T>(__uint_as_float(r[0][i + 4]), __uint_as_float(r[0][i + 5]));
+              w4.w = pack2<T>(__uint_as_float(r[0][i + 6]), __uint_as_float(r[0][i + 7]));
+              *reinterpret_cast<uint4*>(op + c * 16 + i) = w4;
+            }
+          }
+        }
+      }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       if (!ok) break;
     }
@@ -939,11 +1057,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <typename T, bool WINDOW>
+template <typename T, int SLOTS>
 cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    int grid, cudaStream_t stream) {
   const size_t smem = smem_bytes(a.S, a.unit_cap);
-  auto kern = prefill_kernel<T, WINDOW>;
+  auto kern = prefill_kernel<T, SLOTS>;
   cudaError_t e = kernel_prep(reinterpret_cast<const void*>(kern), kThreads, smem, nullptr);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, a);

@@ -242,6 +242,24 @@ def test_chunk_lengths(pa, dtype, H, g, B, window, sinks):
     check_chunk(pa, case, window, sinks, 128 ** -0.5, dtype, rows)
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 30), (128, 0), (150, 7), (300, 130), (100000, 9)])
+@pytest.mark.parametrize("dtype,H,g,B", [("f16", 16, 1, 16), ("bf16", 5, 3, 8), ("bf16", 4, 4, 32), ("f16", 3, 6, 128)])
+def test_chunk_of_many_heads(pa, dtype, H, g, B, window, sinks):
+    """More tiles than thread blocks: two tiles of a head a block, or a tile of two heads where they share a key head."""
+    fresh = [1, 0, 2, 130, 64, 257, 1, 300]
+    lens = [1, 0, 9, 130, 700, 500, 400, 1234]
+    case = chunk_case(lens, fresh, H, g, B, dtype, window, sinks, window + B, spare_rows=3)
+    check_chunk(pa, case, window, sinks, 128 ** -0.5, dtype, [0, 1, 2, 3, 131, 132, 133, 196, 197, 324, 325, 400, 453, 454, 455, 581, 582, 700, 754])
+
+
+@pytest.mark.parametrize("lens,fresh", [([5], [5]), ([128], [128]), ([129], [129]), ([256], [1]), ([257], [200]), ([384], [384]), ([513], [513])])
+def test_chunk_of_few_tiles(pa, lens, fresh):
+    """One tile a block, its key tiles to two slots in turn: one, two, odd and even numbers of them."""
+    for window, sinks in ((10 ** 6, 0), (200, 3), (1, 0), (130, 0)):
+        case = chunk_case(lens, fresh, 1, 2, 16, "bf16", window, sinks, lens[0] + window)
+        check_chunk(pa, case, window, sinks, 0.09, "bf16", list(range(0, fresh[0], 17)) + [fresh[0] - 1])
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_chunk_of_a_whole_prompt(pa, dtype):
     case = chunk_case([1500], [1500], 1, 2, 16, dtype, 200, 10, 3)
@@ -249,7 +267,8 @@ def test_chunk_of_a_whole_prompt(pa, dtype):
 
 
 def test_chunk_with_a_window_over_everything_is_prefill(pa):
-    q, kc, vc, tables, lens, start = (x.cuda() for x in chunk_case([300, 500], [300, 77], 4, 1, 16, "f16", 10 ** 6, 0, 4))
+    # more tiles than thread blocks and a query head a key head: the slots are those of pa_prefill
+    q, kc, vc, tables, lens, start = (x.cuda() for x in chunk_case([300, 500], [300, 77], 60, 1, 16, "f16", 10 ** 6, 0, 4))
     a, b = torch.empty_like(q), torch.empty_like(q)
     pa.pa_prefill_window(q, kc, vc, tables, lens, start, 2 ** 31 - 1, 0.1, a, sinks=2 ** 31 - 1)
     pa.pa_prefill(q, kc, vc, tables, lens, start, 0.1, b)
