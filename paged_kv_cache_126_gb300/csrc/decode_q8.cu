@@ -93,47 +93,66 @@ struct Q8Format {
     return D == 128 ? row * 128 + ((x ^ (row & 7)) << 4) : row * 64 + ((x ^ ((row >> 1) & 3)) << 4);
   }
 
+  // A step of all parts, then the next: products that follow one another do not wait for one another's sums (a part after the other:
+  // 1170 clocks of a warp alone).
   template <int NT>
-  __device__ __forceinline__ static void scores(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
-                                                float (&acc)[NT][4]) {
+  __device__ __forceinline__ static void scores_tile(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
+                                                     float (&acc)[kLoads][NT][4]) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[u][n][0] = acc[u][n][1] = acc[u][n][2] = acc[u][n][3] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-      uint32_t w0[4], w1[4];
-      lds(kst + chunk(r, c * (D / 64) + j), w0);
-      lds(kst + chunk(r + 8, c * (D / 64) + j), w1);
+      uint32_t w0[kLoads][4], w1[kLoads][4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a0 = codes2(w0[w], 0x4140), a1 = codes2(w1[w], 0x4140), a2 = codes2(w0[w], 0x4342), a3 = codes2(w1[w], 0x4342);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma(acc[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], M());
+      for (int u = 0; u < kLoads; ++u) {
+        lds(kst + u * kTile + chunk(r, c * (D / 64) + j), w0[u]);
+        lds(kst + u * kTile + chunk(r + 8, c * (D / 64) + j), w1[u]);
       }
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const uint32_t a0 = codes2(w0[u][w], 0x4140), a1 = codes2(w1[u][w], 0x4140);
+          const uint32_t a2 = codes2(w0[u][w], 0x4342), a3 = codes2(w1[u][w], 0x4342);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma(acc[u][n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1], M());
+        }
     }
   }
 
-  // Slots that hold no key hold some whole number, which the weight 0 takes out.
+  // Slots that hold no key hold some whole number, which the weight 0 takes out.  A part's codes are read while the part before
+  // is multiplied.
   template <int NT, int PARTS>
-  __device__ __forceinline__ static void values(uint32_t vst, int r, int c, int, const uint32_t (&p)[PARTS][NT][2],
-                                                float (&o)[D / 16][NT][4]) {
+  __device__ __forceinline__ static void values_tile(uint32_t vst, int r, int c, const uint32_t (&p)[kLoads][PARTS][NT][2],
+                                                     float (&o)[D / 16][NT][4]) {
     constexpr int W = D / 32;  // words of codes a lane reads of a key
-    uint32_t w[4][W];
+    uint32_t w[2][4][W];
+    auto read = [&](int u) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = 2 * c + (i & 1) + (i >> 1) * 8;
-      lds(vst + (D == 128 ? chunk(key, r) : chunk(key, r >> 1) + (r & 1) * 8), w[i]);
-    }
-#pragma unroll
-    for (int y = 0; y < W; ++y)
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {  // elements 4 y + 2 z and the next: of two keys, then of the two 8 further on
-        const uint32_t lo = prmt(w[0][y], w[1][y], z ? 0x7362 : 0x5140), hi = prmt(w[2][y], w[3][y], z ? 0x7362 : 0x5140);
-        const uint32_t a0 = codes2(lo, 0x4140), a1 = codes2(lo, 0x4342), a2 = codes2(hi, 0x4140), a3 = codes2(hi, 0x4342);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q) mma(o[2 * y + z][n], a0, a1, a2, a3, p[q][n][0], p[q][n][1], M());
+      for (int i = 0; i < 4; ++i) {
+        const int key = 2 * c + (i & 1) + (i >> 1) * 8;
+        lds(vst + u * kTile + (D == 128 ? chunk(key, r) : chunk(key, r >> 1) + (r & 1) * 8), w[u & 1][i]);
       }
+    };
+    read(0);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      if (u + 1 < kLoads) read(u + 1);
+      const uint32_t(&x)[4][W] = w[u & 1];
+#pragma unroll
+      for (int y = 0; y < W; ++y)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {  // elements 4 y + 2 z and the next: of two keys, then of the two 8 further on
+          const uint32_t lo = prmt(x[0][y], x[1][y], z ? 0x7362 : 0x5140), hi = prmt(x[2][y], x[3][y], z ? 0x7362 : 0x5140);
+          const uint32_t a0 = codes2(lo, 0x4140), a1 = codes2(lo, 0x4342), a2 = codes2(hi, 0x4140), a3 = codes2(hi, 0x4342);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) mma(o[2 * y + z][n], a0, a1, a2, a3, p[u][q][n][0], p[u][q][n][1], M());
+        }
+    }
   }
   // where lane row r stores its D / 8 elements of one query (o[t] holds elements 2 t and 2 t + 1 of a run)
   __device__ __forceinline__ static void store(float* row, int r, const float (&y)[D / 16][2]) {

@@ -509,25 +509,22 @@ __device__ __forceinline__ void join_query(const GatherArgs& a, const Join& x, i
   for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(out + i) = bad ? 0u : pack2<T>(y[i] * inv, y[i + 1] * inv);
 }
 
-// Raises a counter of `n` arrivals; whether this one was the last, which leaves it zero again.
-__device__ __forceinline__ bool last_of(int32_t* cnt, int n, int lane) {
-  __threadfence();
-  __syncwarp();
-  int before = 0;
-  if (lane == 0) before = atomicAdd(cnt, 1);
-  before = __shfl_sync(kAll, before, 0);
+// Raises a counter of `n` arrivals; whether this one was the last, which leaves it zero again.  By one lane, behind a barrier
+// of those whose partials it hands on: one release for all of them.
+__device__ __forceinline__ bool last_of(int32_t* cnt, int n) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(cnt) : "memory");
   if (before != n - 1) return false;
-  __threadfence();
-  if (lane == 0) *cnt = 0;
+  *cnt = 0;
   return true;
 }
 
 // Where there are at least kFlat + 1 pieces, the last to arrive of each group of kGroup workers joins the group's, and the
 // last group the groups.  A group can hold the end of one such (s, h) and the start of another: two counters and
 // two partials a group.
-// A piece of (s, h) that a warp leaves: workers w0 .. w1 hold one each.  state 0: none, 1: counted, 2: counted as the last.
+// A piece of (s, h) that a warp leaves: workers w0 .. w1 hold one each.  s < 0: none.
 struct Left {
-  int s, h, w0, w1, state;
+  int s, h, w0, w1;
 };
 
 // The counter that worker w's piece raises, and to what.
@@ -571,7 +568,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   const uint32_t bars = metas + STAGES * 16;  // [stage][2]: keys, values
   const uint32_t steps = dk::smem_u32(smem) + WARPS * (STAGES * (kStage + 32)) + warp * STAGES * (2 * LOADS * 16);  // [2][stage][part]
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + WARPS * warp_smem<F, NT, STAGES>());
-  if (threadIdx.x == 0) *abort_flag = 0;
+  // bit 2 warp + side of [0]: that piece was the last of its (s, h) or group to arrive; of [1]: its group was the last
+  uint32_t* last = reinterpret_cast<uint32_t*>(smem + WARPS * warp_smem<F, NT, STAGES>() + 4);
+  if (threadIdx.x == 0) *abort_flag = 0, last[0] = last[1] = 0;
+  if (threadIdx.x < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(threadIdx.x ? &maps.v : &maps.k)) : "memory");
   if (lane == 0) {
     for (int i = 0; i < 2 * STAGES; ++i) dk::mbar_init(bars + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -582,9 +582,15 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   // this warp's range [b0, b1) of the batch's tiles
   int total = 0;
   int n = 0;  // tiles of sequence s0 + lane
-  for (int s0 = 0; s0 < a.S; s0 += 32) {
-    n = s0 + lane < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s0 + lane)) : 0;
-    total += __reduce_add_sync(kAll, n);
+  for (int s0 = 0; s0 < a.S; s0 += 4 * 32) {  // (four loads at once)
+    int sum = 0;
+#pragma unroll
+    for (int u = 3; u >= 0; --u) {
+      const int s = s0 + 32 * u + lane;
+      n = s < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s)) : 0;
+      sum += n;
+    }
+    total += __reduce_add_sync(kAll, sum);
   }
   total *= a.H;  // the host has checked that all this stays in int32
   const int all_warps = gridDim.x * WARPS;
@@ -683,7 +689,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   float m[NT][2], l[NT][2], f[NT][2];
   float unit = kLeastStep, per_unit = 1.f / kLeastStep;  // kSteps: values are summed in multiples of `unit`
   Left(*left)[2] = reinterpret_cast<Left(*)[2]>(smem + WARPS * warp_smem<F, NT, STAGES>() + 16);  // side 0: begun before
-  if (lane < 2) left[warp][lane].state = 0;
+  if (lane < 2) left[warp][lane].s = -1;
   __syncwarp();
   bool stuck = false;
   const float rest = PARTS == kTwinColumns ? (c >= 2 ? 1.f : 0.f) : 1.f;
@@ -760,10 +766,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (any & (1 << 16)) poison = true;
       float x[LOADS][NT][4];
       if (any & 0xffff) {
+        if constexpr (F::kSteps) {
+          F::template scores_tile<NT>(kst, r, c, qf, x);
 #pragma unroll
-        for (int u = 0; u < LOADS; ++u) {
-          F::template scores<NT>(kst + u * F::kTile, r, c, qf, x[u]);
-          if constexpr (F::kSteps) {
+          for (int u = 0; u < LOADS; ++u) {
             uint32_t w[2];
             lds(steps + ((phase * STAGES + st) * LOADS + u) * 16, w);
 #pragma unroll
@@ -771,6 +777,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[u][n][j] *= __uint_as_float(w[j >> 1]);
           }
+        } else {
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) F::template scores<NT>(kst + u * F::kTile, r, c, qf, x[u]);
         }
       }
       __syncwarp();
@@ -866,9 +875,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
             step[u][1] *= per_unit;
           }
         }
-#pragma unroll
-        for (int u = 0; u < LOADS; ++u) {
-          uint32_t p[kB][NT][2];
+        // the weights of a part as B operands
+        auto weigh = [&](int u, uint32_t (&p)[kB][NT][2]) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float w[4];
@@ -893,7 +901,19 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
               p[0][n][j] = transpose8(hi);
             }
           }
-          F::template values<NT, kB>(vst + u * F::kTile, r, c, full != 0x0808 ? meta[u] & (KEYS == kWindow ? 0xff0ffff : 0xffff) : 0x0808, p, o);
+        };
+        if constexpr (F::kSteps) {
+          uint32_t p[LOADS][kB][NT][2];
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) weigh(u, p[u]);
+          F::template values_tile<NT, kB>(vst, r, c, p, o);
+        } else {
+#pragma unroll
+          for (int u = 0; u < LOADS; ++u) {
+            uint32_t p[kB][NT][2];
+            weigh(u, p);
+            F::template values<NT, kB>(vst + u * F::kTile, r, c, full != 0x0808 ? meta[u] & (KEYS == kWindow ? 0xff0ffff : 0xffff) : 0x0808, p, o);
+          }
         }
       }
       __syncwarp();
@@ -950,12 +970,19 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         x.h = cur.h;
         x.w0 = cut.owner(p0);
         x.w1 = cut.owner(p0 + cur.tiles - 1);
-        x.state = last_of(arrivals(a, x, id), arrivals_of(x, id), lane) ? 2 : 1;
         if (lane == 0) left[warp][first_t == 0 ? 1 : 0] = x;
       }
     }
     if (i < count) next_head<KEYS, LOADS>(a, cur);
   }
+
+  // Both pieces are counted at the end of the range: one wait for what was stored.
+  __syncwarp();
+  if (!stuck && lane < 2) {
+    const Left x = left[warp][lane];
+    if (x.s >= 0 && last_of(arrivals(a, x, id), arrivals_of(x, id))) atomicOr(&last[0], 1u << (2 * warp + lane));
+  }
+  __syncwarp();
 
   // The joins that fall to this block, a query a warp at a time; then those of groups.
 #pragma unroll 1
@@ -964,9 +991,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     if (*abort_flag) return;
     bool groups = false;
 #pragma unroll 1
-    for (int k = 0; k < 2 * WARPS; ++k) {
+    for (uint32_t todo = last[round]; todo; todo &= todo - 1) {
+      const int k = __ffs(todo) - 1;
       const Left x = left[k >> 1][k & 1];
-      if (x.state != 2) continue;
       const bool many = x.w1 - x.w0 >= kFlat;
       const int of = (k >> 1) * gridDim.x + blockIdx.x;  // the worker whose piece it is
       Join j;
@@ -990,15 +1017,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     }
     if (!groups) return;
     __syncthreads();
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-      const Left x = left[warp][side];
-      if (x.state != 2) continue;
-      bool last = false;
-      if (x.w1 - x.w0 >= kFlat)
-        last = last_of(a.cnt + static_cast<int64_t>(x.s) * a.H + x.h, x.w1 / kGroup - x.w0 / kGroup + 1, lane);
-      __syncwarp();
-      if (lane == 0 && !last) left[warp][side].state = 0;
+    if (lane < 2 && (last[0] >> (2 * warp + lane) & 1u)) {
+      const Left x = left[warp][lane];
+      if (x.w1 - x.w0 >= kFlat && last_of(a.cnt + static_cast<int64_t>(x.s) * a.H + x.h, x.w1 / kGroup - x.w0 / kGroup + 1))
+        atomicOr(&last[1], 1u << (2 * warp + lane));
     }
   }
 }
