@@ -8,13 +8,13 @@ namespace {
 template <typename T, int D>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {
-  using F = gk::RowFormat<T, D>;
+  using F = gk::RowFormat<T, D, 2>;
   typename F::Maps maps;
   maps.k = tk;
   maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, gk::kWindow, 2, 4, 2>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, gk::kWindow, 2, 4, 2>(a, maps, num_sms, stream, workers);
-  return gk::launch<F, 2, gk::kTwoParts, gk::kWindow, 2, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, gk::kWindow, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, gk::kWindow, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  return gk::launch<F, 2, gk::kTwoParts, gk::kWindow, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 
 }  // namespace

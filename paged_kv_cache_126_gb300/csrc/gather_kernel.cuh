@@ -393,6 +393,13 @@ struct Q4Format {
     }
   }
 
+  template <int NT>
+  __device__ __forceinline__ static void scores_tile(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
+                                                     float (&acc)[kLoads][NT][4]) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) scores<NT>(kst + u * kTile, r, c, qf, acc[u]);
+  }
+
   // o[t] += V^T P for the D / 16 groups of 16 elements; p[part][n]: B operands of the weights
   template <int NT, int PARTS>
   __device__ __forceinline__ static void values(uint32_t vst, int r, int c, int meta, const uint32_t (&p)[PARTS][NT][2],
@@ -766,8 +773,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (any & (1 << 16)) poison = true;
       float x[LOADS][NT][4];
       if (any & 0xffff) {
+        F::template scores_tile<NT>(kst, r, c, qf, x);
         if constexpr (F::kSteps) {
-          F::template scores_tile<NT>(kst, r, c, qf, x);
 #pragma unroll
           for (int u = 0; u < LOADS; ++u) {
             uint32_t w[2];
@@ -777,9 +784,6 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[u][n][j] *= __uint_as_float(w[j >> 1]);
           }
-        } else {
-#pragma unroll
-          for (int u = 0; u < LOADS; ++u) F::template scores<NT>(kst + u * F::kTile, r, c, qf, x[u]);
         }
       }
       __syncwarp();

@@ -28,7 +28,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 // 16-bit rows.  A half tile, 8 keys, is one TMA box [D / 64 column groups][8 rows][64 elements] with the
 // 128-byte swizzle: row y of a column group keeps its 16-byte chunk x at x ^ y, so that the eight row
 // addresses of an ldmatrix fall into different banks.
-template <typename T, int D_>
+// L parts a tile.
+template <typename T, int D_, int L = 1>
 struct RowFormat {
   using In = T;
   using M = T;
@@ -42,7 +43,7 @@ struct RowFormat {
   struct Maps {
     CUtensorMap k, v;
   };
-  static constexpr int kLoads = 1;
+  static constexpr int kLoads = L;
   struct Place {
     int slot[2];     // first slot of each half; < 0: nothing to load
   };
@@ -55,8 +56,17 @@ struct RowFormat {
   __device__ __forceinline__ static int issuer(int part) { return part; }
   __device__ __forceinline__ static void load(const GatherArgs&, const CUtensorMap* map, const Place& x, int h, int lane,
                                               int part, uint32_t dst, uint32_t bar, uint32_t more) {
-    if (lane != part) return;
-    dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * kHalfTile + more);
+    if (L == 1) {
+      if (lane != part) return;
+      dk::mbar_arrive_expect_tx(bar, ((x.slot[0] >= 0) + (x.slot[1] >= 0)) * kHalfTile + more);
+    } else {
+      const bool mine = static_cast<unsigned>(lane - part) < L;
+      const unsigned first = __ballot_sync(kAll, mine && x.slot[0] >= 0), second = __ballot_sync(kAll, mine && x.slot[1] >= 0);
+      if (lane == part) dk::mbar_arrive_expect_tx(bar, (__popc(first) + __popc(second)) * kHalfTile + more);
+      __syncwarp();
+      if (!mine) return;
+      dst += (lane - part) * kTile;
+    }
     if (x.slot[0] >= 0) tma_load_4d(dst, map, 0, x.slot[0], 0, h, bar);
     if (x.slot[1] >= 0) tma_load_4d(dst + kHalfTile, map, 0, x.slot[1], 0, h, bar);
   }
@@ -78,19 +88,25 @@ struct RowFormat {
     }
   }
 
+  // A step of all parts, then the next: products that follow one another do not wait for one another's sums.
   template <int NT>
-  __device__ __forceinline__ static void scores(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
-                                                float (&acc)[NT][4]) {
+  __device__ __forceinline__ static void scores_tile(uint32_t kst, int r, int c, const uint32_t (&qf)[NT][D / 16][2],
+                                                     float (&acc)[L][NT][4]) {
     const int lane = 4 * r + c, y = lane & 7, mat = lane >> 3;
     const uint32_t row = kst + (mat & 1) * kHalfTile + y * 128;  // matrices: keys 0..7, 8..15, then the next 8 elements
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    for (int u = 0; u < L; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[u][n][0] = acc[u][n][1] = acc[u][n][2] = acc[u][n][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      uint32_t x[4];
-      ldmatrix4(row + (k >> 2) * 1024 + ((((k & 3) * 2 + (mat >> 1)) ^ y) << 4), x);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma(acc[n], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1], M());
+      for (int u = 0; u < L; ++u) {
+        uint32_t x[4];
+        ldmatrix4(row + u * kTile + (k >> 2) * 1024 + ((((k & 3) * 2 + (mat >> 1)) ^ y) << 4), x);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(acc[u][n], x[0], x[1], x[2], x[3], qf[n][k][0], qf[n][k][1], M());
+      }
     }
   }
 
