@@ -10,6 +10,10 @@
 //
 // A warp takes 16 rows of one frame and head, all in registers: their maximum, then their codes, one pass over the data.
 // Frames of more than 16 tokens are as many warps of one block, which exchange their maxima.
+//
+// 16 chunks of 256 to 512 tokens, 8 heads of 128 in bf16 (50 MB): 8.9 us, 5.6 TB/s, 64 registers (87: 10.2 us); read back (50 MB)
+// 7.5 us, 6.7 TB/s.  A decode step of 64 tokens, 32 heads in fp16: 4.0 us, three loads that wait for one another (lengths, table,
+// step) behind a launch, 4.4 us with a warp a head; read back, up to 16 tokens of each frame (13 MB), 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -112,17 +116,64 @@ __device__ __forceinline__ Unit find_unit(const Append8Args& a, int u, int lane,
   return x;
 }
 
+// How new elements whose largest magnitude has the bits `top` are coded in a frame; `begun`: it holds earlier tokens, with step `was`.
+struct Coding {
+  float r, step;
+  int halvings;
+  bool sound;
+};
+template <typename T>
+__device__ __forceinline__ Coding coding(uint32_t top, bool begun, float was) {
+  Coding x;
+  x.r = 0.f;
+  x.step = __uint_as_float(0x7fffffffu);
+  x.halvings = 0;
+  const float largest = fminf(fmaxf(Bits<T>::value(top), kLeast), kMost);
+  // an earlier step that no append leaves is as good as NaN
+  x.sound = top < Bits<T>::kInf && (!begun || (was >= 0x1p-67f && was <= 0x1p60f));
+  if (!x.sound) return x;
+  if (!begun) {
+    x.r = __uint_as_float(__float_as_uint(__fdiv_rn(127.f, largest)) & 0xffff0000u);
+    x.step = __frcp_rn(x.r);
+    return x;
+  }
+  const uint32_t inv = __float_as_uint(__frcp_rn(was));
+  x.r = __uint_as_float((inv + 0x7fffu + ((inv >> 16) & 1u)) & 0xffff0000u);  // to 8 bits: the r that step is one over
+  const float over = largest * x.r;
+  x.halvings = max(0, static_cast<int>(__float_as_uint(over) >> 23) - 133);  // over / 2^halvings is below 128
+  if (__uint_as_float(__float_as_uint(over) - (static_cast<uint32_t>(x.halvings) << 23)) > 127.f) ++x.halvings;
+  x.r = __uint_as_float(__float_as_uint(x.r) - (static_cast<uint32_t>(x.halvings) << 23));
+  x.step = __uint_as_float(__float_as_uint(was) + (static_cast<uint32_t>(x.halvings) << 23));
+  return x;
+}
+__device__ __forceinline__ float power_of_half(int k) { return __uint_as_float(static_cast<uint32_t>(127 - min(k, 30)) << 23); }
+
+__device__ __forceinline__ uint32_t larger(uint32_t top2, const uint4& w) {  // of magnitudes as bits, two at a time
+  return __vmaxu2(top2, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+}
+template <typename T>
+__device__ __forceinline__ uint2 codes8(uint4 w, const Coding& x, bool past_most) {
+  if (!x.sound) return make_uint2(0x80808080u, 0x80808080u);
+  float2 f[4] = {Bits<T>::unpack(w.x), Bits<T>::unpack(w.y), Bits<T>::unpack(w.z), Bits<T>::unpack(w.w)};
+  if (Bits<T>::kPastMost && past_most) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = make_float2(fminf(fmaxf(f[k].x, -kMost), kMost), fminf(fmaxf(f[k].y, -kMost), kMost));
+  }
+  return make_uint2(codes4(f[0], f[1], x.r), codes4(f[2], f[3], x.r));
+}
+__device__ __forceinline__ void halve8(unsigned char* at, float p) {
+  uint2 y = *reinterpret_cast<const uint2*>(at);
+  y.x = halved4(y.x, p);
+  y.y = halved4(y.y, p);
+  *reinterpret_cast<uint2*>(at) = y;
+}
+
+// Items of one frame (a cache and a head each, keys before values): those of this block's warps where it is the frame's `part`-th.
 template <typename T, int D>
-__global__ void __launch_bounds__(512) append8_kernel(const Append8Args a) {
+__device__ __forceinline__ void append_items(const Append8Args& a, const Unit& x, int part, uint32_t* maxima) {
   constexpr int V = D / 8, kRows = 32 / V, kSteps = 16 / kRows;  // lanes of a row, rows a step, steps of 16 rows
-  __shared__ uint32_t maxima[16];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / V, vec = lane % V;
-  const int u = blockIdx.x / a.blocks_unit, part = blockIdx.x - u * a.blocks_unit;
-  const Unit x = find_unit(a, u, lane, blockIdx.x == 0);
-  if (x.j < 0) return;  // (the whole block)
   const int item = part * (blockDim.x >> (5 + a.log2_slabs)) + (warp >> a.log2_slabs), slab = warp & ((1 << a.log2_slabs) - 1);
   const bool is_v = item >= a.H;
   const int h = is_v ? item - a.H : item;
@@ -152,10 +203,7 @@ __global__ void __launch_bounds__(512) append8_kernel(const Append8Args a) {
   // the largest magnitude, as the bits of T: those of an infinity or more once an element is not finite
   uint32_t top2 = 0;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                   __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
-  }
+  for (int i = 0; i < kSteps; ++i) top2 = larger(top2, w[i]);
   uint32_t top = __reduce_max_sync(kAll, max(top2 & 0xffffu, top2 >> 16));
   if (a.log2_slabs > 0) {
     if (lane == 0) maxima[warp] = top;
@@ -164,59 +212,98 @@ __global__ void __launch_bounds__(512) append8_kernel(const Append8Args a) {
   }
   if (!live) return;
 
-  float r = 0.f, step = __uint_as_float(0x7fffffffu);
-  int halvings = 0;
-  const float largest = fminf(fmaxf(Bits<T>::value(top), kLeast), kMost);
-  // an earlier step that no append leaves is as good as NaN
-  const bool sound = top < Bits<T>::kInf && (from == 0 || (was >= 0x1p-67f && was <= 0x1p60f));
-  if (sound && from == 0) {
-    r = __uint_as_float(__float_as_uint(__fdiv_rn(127.f, largest)) & 0xffff0000u);
-    step = __frcp_rn(r);
-  } else if (sound) {
-    const uint32_t inv = __float_as_uint(__frcp_rn(was));
-    r = __uint_as_float((inv + 0x7fffu + ((inv >> 16) & 1u)) & 0xffff0000u);  // to 8 bits: the r that step is one over
-    const float over = largest * r;
-    halvings = max(0, static_cast<int>(__float_as_uint(over) >> 23) - 133);  // over / 2^halvings is below 128
-    if (__uint_as_float(__float_as_uint(over) - (static_cast<uint32_t>(halvings) << 23)) > 127.f) ++halvings;
-    r = __uint_as_float(__float_as_uint(r) - (static_cast<uint32_t>(halvings) << 23));
-    step = __uint_as_float(__float_as_uint(was) + (static_cast<uint32_t>(halvings) << 23));
-  }
+  const Coding c = coding<T>(top, from > 0, was);
   unsigned char* dst = (is_v ? a.v_cache : a.k_cache) + ((static_cast<int64_t>(frame) * a.H + h) * a.B + at) * D + vec * 8;
-  if (Bits<T>::kPastMost && sound && Bits<T>::value(top) > kMost) {
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(&w[i]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = Bits<T>::unpack(p[k]);
-        p[k] = Bits<T>::pack(fminf(fmaxf(f.x, -kMost), kMost), fminf(fmaxf(f.y, -kMost), kMost));
-      }
-    }
-  }
+  const bool past_most = Bits<T>::value(top) > kMost;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int row = at + i * kRows;
-    if (row >= from && row < past) {
-      uint2 y = make_uint2(0x80808080u, 0x80808080u);
-      if (sound) {
-        y.x = codes4(Bits<T>::unpack(w[i].x), Bits<T>::unpack(w[i].y), r);
-        y.y = codes4(Bits<T>::unpack(w[i].z), Bits<T>::unpack(w[i].w), r);
-      }
-      *reinterpret_cast<uint2*>(dst + i * kRows * D) = y;
-    }
+    if (row >= from && row < past) *reinterpret_cast<uint2*>(dst + i * kRows * D) = codes8<T>(w[i], c, past_most);
   }
-  if (halvings > 0) {
-    const float p = __uint_as_float(static_cast<uint32_t>(127 - min(halvings, 30)) << 23);
+  if (c.halvings > 0) {
+    const float p = power_of_half(c.halvings);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (at + i * kRows >= from) continue;
-      uint2 y = *reinterpret_cast<const uint2*>(dst + i * kRows * D);
-      y.x = halved4(y.x, p);
-      y.y = halved4(y.y, p);
-      *reinterpret_cast<uint2*>(dst + i * kRows * D) = y;
+    for (int i = 0; i < kSteps; ++i)
+      if (at + i * kRows < from) halve8(dst + i * kRows * D, p);
+  }
+  if (slab == 0 && lane == 0 && (from == 0 || c.halvings > 0 || !c.sound)) *step_at = c.step;
+}
+
+// One new token in its frame, as in a decode step: a row of each head is all there is, so a warp takes kStepRows * 32 / V of
+// them (64 tokens of 32 heads: 4.4 us with a warp a head).
+constexpr int kStepRows = 4;
+template <typename T, int D>
+__device__ __forceinline__ void append_token(const Append8Args& a, const Unit& x, int part) {
+  constexpr int V = D / 8, kRows = 32 / V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / V, vec = lane % V;
+  if (warp >= kThreads / 32) return;  // (blocks are larger for frames of more than 64 tokens)
+  const int first = (part * (kThreads / 32) + warp) * kRows * kStepRows + sub;  // this lane's first row, keys' before values'
+  const int begin = x.j << a.log2_B, at = x.first - begin;
+  const int frame = a.block_tables[x.s * a.bt_row + x.j];
+  uint4 w[kStepRows];
+  float was[kStepRows];
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i) {
+    const int row = first + i * kRows;
+    const bool is_v = row >= a.H;
+    const T* src = is_v ? static_cast<const T*>(a.v_new) + x.row0 * a.v_row : static_cast<const T*>(a.k_new) + x.row0 * a.k_row;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (row < 2 * a.H) w[i] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(is_v ? row - a.H : row) * D + vec * 8);
+  }
+  if (frame < 0 || frame >= a.num_blocks) {
+    if (lane == 0) atomicOr(a.status, kDevBadBlock);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i) {
+    const int row = first + i * kRows;
+    was[i] = 0.f;
+    if (at > 0 && row < 2 * a.H) was[i] = row >= a.H ? a.v_scale[frame * a.vs_row + row - a.H] : a.k_scale[frame * a.ks_row + row];
+  }
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i) {
+    const int row = first + i * kRows;
+    uint32_t top = larger(0, w[i]);
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = 1; o < V; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+    if (row >= 2 * a.H) continue;
+    const bool is_v = row >= a.H;
+    const int h = is_v ? row - a.H : row;
+    const Coding c = coding<T>(top, at > 0, was[i]);
+    unsigned char* rows = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(frame) * a.H + h) * a.B * D + vec * 8;
+    *reinterpret_cast<uint2*>(rows + at * D) = codes8<T>(w[i], c, Bits<T>::value(top) > kMost);
+    if (c.halvings > 0) {
+      const float p = power_of_half(c.halvings);
+#pragma unroll 4
+      for (int e = 0; e < at; ++e) halve8(rows + e * D, p);
+    }
+    if (vec == 0 && (at == 0 || c.halvings > 0 || !c.sound))
+      (is_v ? a.v_scale + frame * a.vs_row : a.k_scale + frame * a.ks_row)[h] = c.step;
+  }
+}
+
+// STEP: as many blocks a frame as append_token needs; a frame with more new tokens than one takes its items in turn.
+template <typename T, int D, bool STEP>
+__global__ void __launch_bounds__(512, 2) append8_kernel(const Append8Args a) {
+  __shared__ uint32_t maxima[16];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int u = blockIdx.x / a.blocks_unit, part = blockIdx.x - u * a.blocks_unit;
+  const Unit x = find_unit(a, u, threadIdx.x & 31, blockIdx.x == 0);
+  if (x.j < 0) return;  // (the whole block)
+  if (!STEP) {
+    append_items<T, D>(a, x, part, maxima);
+  } else if (min((x.j + 1) << a.log2_B, x.L) - max(x.j << a.log2_B, x.first) == 1 && x.first >= x.j << a.log2_B) {
+    append_token<T, D>(a, x, part);
+  } else {
+    const int items = blockDim.x >> (5 + a.log2_slabs);
+    for (int i = part; i * items < 2 * a.H; i += a.blocks_unit) {
+      append_items<T, D>(a, x, i, maxima);
+      __syncthreads();  // the maxima are read
     }
   }
-  if (slab == 0 && lane == 0 && (from == 0 || halvings > 0 || !sound)) *step_at = step;
 }
 
 // A warp per token, cache and kSteps * 32 / V heads; a lane reads 8 bytes and writes 16.
@@ -283,12 +370,15 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned threads, void** a
 
 }  // namespace
 
-// Warps of a block; 16 rows each, and a frame's in one block.
+// Threads of a block: 16 rows a warp, and a frame's in one block.
 static int64_t append8_threads(int64_t B) { return B / 16 * 32 > kThreads ? B / 16 * 32 : kThreads; }
 
 bool append8_fits(Append8Args* a) {
   a->log2_slabs = a->B > 16 ? a->log2_B - 4 : 0;
-  const int64_t items = append8_threads(a->B) / 32 >> a->log2_slabs;
+  a->step = a->T <= a->S;
+  const int64_t threads = append8_threads(a->B);
+  const int64_t rows = 32 / (a->D / 8) * kStepRows;  // of a warp of append_token
+  const int64_t items = a->step ? kThreads / 32 * rows : threads / 32 >> a->log2_slabs;
   const int64_t blocks = (2 * static_cast<int64_t>(a->H) + items - 1) / items;
   // frames that hold a new token: every one holds at least one, all but two of a sequence B
   const int64_t units = a->T < a->T / a->B + 2 * static_cast<int64_t>(a->S) ? a->T : a->T / a->B + 2 * static_cast<int64_t>(a->S);
@@ -298,12 +388,16 @@ bool append8_fits(Append8Args* a) {
   return true;
 }
 
+template <typename T>
+static const void* append8_function(const Append8Args& a) {
+  if (a.D == 128)
+    return a.step ? reinterpret_cast<const void*>(&append8_kernel<T, 128, true>) : reinterpret_cast<const void*>(&append8_kernel<T, 128, false>);
+  return a.step ? reinterpret_cast<const void*>(&append8_kernel<T, 64, true>) : reinterpret_cast<const void*>(&append8_kernel<T, 64, false>);
+}
+
 cudaError_t launch_append8(int dtype, const Append8Args& a, cudaStream_t stream) {
   void* args[1] = {const_cast<Append8Args*>(&a)};
-  const void* fn = dtype == PA_F16 ? (a.D == 128 ? reinterpret_cast<const void*>(&append8_kernel<__half, 128>)
-                                                 : reinterpret_cast<const void*>(&append8_kernel<__half, 64>))
-                                   : (a.D == 128 ? reinterpret_cast<const void*>(&append8_kernel<__nv_bfloat16, 128>)
-                                                 : reinterpret_cast<const void*>(&append8_kernel<__nv_bfloat16, 64>));
+  const void* fn = dtype == PA_F16 ? append8_function<__half>(a) : append8_function<__nv_bfloat16>(a);
   return launch_pdl(fn, static_cast<unsigned>(a.units) * a.blocks_unit, static_cast<unsigned>(append8_threads(a.B)), args, stream);
 }
 

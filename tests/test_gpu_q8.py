@@ -70,6 +70,13 @@ def test_bytes_follow_the_definition(pa, dtype, D, H, B):
             assert (o[-1] == 9).all()
 
 
+@pytest.mark.parametrize("dtype,D,H,B", [("f16", 128, 37, 16), ("bf16", 64, 37, 8), ("bf16", 128, 9, 256), ("f16", 64, 70, 128)])
+def test_steps_of_about_one_token(pa, dtype, D, H, B):
+    """No more new tokens than sequences: most of them alone in their frames, some two or three, some over a frame's end, and more heads than a block takes."""
+    chunks = [[1, 1, 1, 1, 1], [0, 2, 0, 1, 2], [0, 3, 1, 0, 1], [B, B, B, B, B], [1, 1, 1, 1, 1], [5, 0, 0, 0, 0], [1, 1, 1, 1, 1], [0, 0, 4, 0, 1]] + [[1, 1, 1, 1, 1]] * 10
+    grow(pa, dtype, D, H, B, chunks, B + H, spread=3.0)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_one_token_at_a_time(pa, dtype):
     """Two frames filled token by token, in the form without query_start; an empty sequence beside them is skipped."""
