@@ -110,7 +110,8 @@ int pa_cache_append(const pa_tensor* k_new, const pa_tensor* v_new,
  * only the one shared frame being written is duplicated.]
  *
  *   k_cache, v_cache  any cache of frames: [num_blocks, B, H, D] as for pa_cache_append,
- *           or the 4-bit rows [num_blocks, H, B, 5 D / 8] of PA_U8 (pa_cache_append_q4).
+ *           the 4-bit rows [num_blocks, H, B, 5 D / 8] of PA_U8 (pa_cache_append_q4), or the
+ *           8-bit rows [num_blocks, H, B, D] (pa_cache_append_q8) and then their steps.
  *   pairs   int32 [n, 2], row = (src frame, dst frame); contiguous.  Both caches
  *           get cache[dst] = cache[src].  Ids outside [0, num_blocks) set
  *           PA_DEV_BAD_COPY and the pair is skipped.  Destinations must be
@@ -478,6 +479,7 @@ int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tens
  *   q, out        [T, Hq, 128] fp16/bf16;  the other arguments, arithmetic, errors and status bits as for
  *                 pa_prefill.  Entries of frames that hold no token attended by a query of the call are not read.
  *   window >= 1, sinks >= 0, scale > 0 and finite, else PA_ERR_INVALID.
+ * Sequences of one call may share frames.  PA_ERR_UNSUPPORTED for T above about a million rows.
  */
 int pa_prefill_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
                       const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* query_start,
@@ -504,8 +506,9 @@ int pa_prefill_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
  *     r /= 2^k, step *= 2^k, and each earlier code n = b - 128 becomes round-half-even(n / 2^k).
  * A NaN or an infinity among the new elements, or a step that no append leaves, makes the step NaN and the new codes 0:
  * the frame's tokens of that head read as NaN until it is begun anew.  Slots behind the last token are left as
- * they were.  A sequence with a bad length or query range sets PA_DEV_BAD_LEN and is skipped (ranges that hold more
- * frames than T rows can: some of them are too), a bad frame id PA_DEV_BAD_BLOCK and the frame is skipped.
+ * they were.  A sequence with a bad length or query range sets PA_DEV_BAD_LEN and is skipped (where query_start
+ * falls from one entry to the next, others may be too), a bad frame id PA_DEV_BAD_BLOCK and the frame is skipped.
+ * PA_ERR_UNSUPPORTED where T / B + 2 S passes 2^25.
  */
 int pa_cache_append_q8(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* block_tables,
                        const pa_tensor* context_lens, const pa_tensor* query_start, const pa_tensor* k_cache,

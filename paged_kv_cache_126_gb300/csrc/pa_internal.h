@@ -262,7 +262,7 @@ struct Append8Args {
   float *k_scale, *v_scale;       // [num_blocks, H], row strides ks_row, vs_row
   int64_t ks_row, vs_row;
   int32_t T, S, H, D, B, log2_B, num_blocks, max_blocks;
-  // set by append8_fits: most frames written to, blocks of each, log2 of a frame's warps, whether there is about one token a sequence
+  // set by append8_fits: units, blocks of each, log2 of a frame's warps, whether there is about one token a sequence
   int32_t units, blocks_unit, log2_slabs, step;
   int32_t* status;
 };

@@ -72,47 +72,63 @@ __device__ __forceinline__ uint32_t halved4(uint32_t w, float p) {
   return codes4(make_float2(f[0], f[1]), make_float2(f[2], f[3]), p);
 }
 
-// The call's frames in order of sequences: which one is the u-th, found by each warp for itself.
+// A frame that holds new tokens, of the call's u-th block: found by each warp for itself.
 struct Unit {
   int s, L, first, row0;  // sequence, its tokens, its first new one and that token's row of k_new
-  int j;                  // position in its table; < 0: there are not so many
+  int j;                  // position in its table; < 0: none
 };
-__device__ __forceinline__ int new_tokens(const Append8Args& a, int s, int* L, int* row0) {
-  *L = a.context_lens[s];
-  *row0 = a.query_start ? a.query_start[s] : s;
-  const int end = a.query_start ? a.query_start[s + 1] : s + min(max(*L, 0), 1);
-  const bool bad = *row0 < 0 || end < *row0 || end > a.T || *L < end - *row0 ||
-                   static_cast<int64_t>(*L) > (static_cast<int64_t>(a.max_blocks) << a.log2_B);
-  return bad ? -1 : end - *row0;
+// New tokens of a sequence that has the rows row0 .. end - 1; -1: a bad length or range.
+__device__ __forceinline__ int new_tokens(const Append8Args& a, int L, int row0, int end) {
+  if (!a.query_start) end = row0 + min(max(L, 0), 1);
+  const bool bad = row0 < 0 || end < row0 || end > a.T || L < end - row0 ||
+                   static_cast<int64_t>(L) > (static_cast<int64_t>(a.max_blocks) << a.log2_B);
+  return bad ? -1 : end - row0;
 }
-__device__ __forceinline__ Unit find_unit(const Append8Args& a, int u, int lane, bool report) {
+// Numbers of units ascend with the sequences.  STEP: a unit is a row, that of a frame's first new token, the others are none.
+// Else sequence s has the units from query_start[s] / B + 2 s on, as many as it can have frames.  The last sequence whose first unit
+// is not behind u is searched 32 at a time, so that a call of many sequences is no slower for it.
+template <bool STEP>
+__device__ __forceinline__ int first_unit_of(const Append8Args& a, int s, int row0) {
+  return STEP ? row0 : (row0 >> a.log2_B) + 2 * s;
+}
+template <bool STEP>
+__device__ __forceinline__ Unit find_unit(const Append8Args& a, int u, int lane) {
   Unit x;
   x.j = -1;
-  int before = 0;
-  for (int s0 = 0; s0 < a.S; s0 += 32) {
-    int L = 0, row0 = 0, n = 0;
-    if (s0 + lane < a.S) n = new_tokens(a, s0 + lane, &L, &row0);
-    if (report && n < 0) atomicOr(a.status, kDevBadLen);
-    const int count = n > 0 ? ((L - 1) >> a.log2_B) - ((L - n) >> a.log2_B) + 1 : 0;
-    int upto = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, upto, o);
-      if (lane >= o) upto += y;
+  int n = 0, end = 0;
+  x.s = u;
+  if (!a.query_start) {
+    x.row0 = u;
+    x.L = a.context_lens[u];
+  } else {
+    int lo = 0, hi = a.S;
+    if (STEP && u < a.S && a.query_start[u] == u && a.query_start[u + 1] == u + 1) lo = u, hi = u + 1;  // a decode step's rows
+    while (hi - lo > 32) {
+      const int step = (hi - lo + 31) >> 5, s = lo + lane * step;
+      const unsigned upto = __ballot_sync(kAll, s < hi && first_unit_of<STEP>(a, s, a.query_start[min(s, a.S)]) <= u);
+      lo += max(0, __popc(upto) - 1) * step;
+      hi = min(hi, lo + step);
     }
-    const unsigned past = __ballot_sync(kAll, before + upto > u);
-    if (past && x.j < 0) {
-      const int f = __ffs(past) - 1;
-      x.s = s0 + f;
-      x.L = __shfl_sync(kAll, L, f);
-      x.first = x.L - __shfl_sync(kAll, n, f);
-      x.row0 = __shfl_sync(kAll, row0, f);
-      x.j = (x.first >> a.log2_B) + u - (before + __shfl_sync(kAll, upto - count, f));
-      if (!report) return x;
-    }
-    before = min(before + __shfl_sync(kAll, upto, 31), 1 << 29);  // (ranges that overlap: no sum passes int32)
+    const int s = min(lo + lane, a.S - 1), row0 = a.query_start[s], L = a.context_lens[s];
+    end = a.query_start[s + 1];
+    const unsigned upto = __ballot_sync(kAll, lo + lane < hi && first_unit_of<STEP>(a, s, row0) <= u);
+    const int f = max(0, __popc(upto) - 1);
+    x.s = min(lo + f, a.S - 1);
+    x.row0 = __shfl_sync(kAll, row0, f);
+    x.L = __shfl_sync(kAll, L, f);
+    end = __shfl_sync(kAll, end, f);
   }
-  if (report && before > a.units && lane == 0) atomicOr(a.status, kDevBadLen);
+  n = new_tokens(a, x.L, x.row0, end);
+  if (n <= 0) return x;
+  x.first = x.L - n;
+  const int i = u - first_unit_of<STEP>(a, x.s, x.row0);
+  if (STEP) {
+    const int token = x.first + i;
+    if (i >= 0 && i < n && (i == 0 || (token & (a.B - 1)) == 0)) x.j = token >> a.log2_B;
+  } else {
+    const int j = (x.first >> a.log2_B) + i;
+    if (i >= 0 && j <= (x.L - 1) >> a.log2_B) x.j = j;
+  }
   return x;
 }
 
@@ -291,7 +307,13 @@ __global__ void __launch_bounds__(512, 2) append8_kernel(const Append8Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int u = blockIdx.x / a.blocks_unit, part = blockIdx.x - u * a.blocks_unit;
-  const Unit x = find_unit(a, u, threadIdx.x & 31, blockIdx.x == 0);
+  if (threadIdx.x < 32) {
+    for (int64_t s = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x; s < a.S; s += static_cast<int64_t>(gridDim.x) * 32) {
+      const int row0 = a.query_start ? a.query_start[s] : static_cast<int>(s);
+      if (new_tokens(a, a.context_lens[s], row0, a.query_start ? a.query_start[s + 1] : 0) < 0) atomicOr(a.status, kDevBadLen);
+    }
+  }
+  const Unit x = find_unit<STEP>(a, u, threadIdx.x & 31);
   if (x.j < 0) return;  // (the whole block)
   if (!STEP) {
     append_items<T, D>(a, x, part, maxima);
@@ -380,8 +402,8 @@ bool append8_fits(Append8Args* a) {
   const int64_t rows = 32 / (a->D / 8) * kStepRows;  // of a warp of append_token
   const int64_t items = a->step ? kThreads / 32 * rows : threads / 32 >> a->log2_slabs;
   const int64_t blocks = (2 * static_cast<int64_t>(a->H) + items - 1) / items;
-  // frames that hold a new token: every one holds at least one, all but two of a sequence B
-  const int64_t units = a->T < a->T / a->B + 2 * static_cast<int64_t>(a->S) ? a->T : a->T / a->B + 2 * static_cast<int64_t>(a->S);
+  // (a sequence's new tokens are in at most a B-th as many frames and two)
+  const int64_t units = a->step ? a->T : a->T / a->B + 2 * static_cast<int64_t>(a->S);
   if (units > 1 << 25 || units * blocks > INT32_MAX) return false;
   a->units = static_cast<int32_t>(units);
   a->blocks_unit = static_cast<int32_t>(blocks);

@@ -101,6 +101,33 @@ def test_one_token_at_a_time(pa, dtype):
         same(g, c)
 
 
+@pytest.mark.parametrize("kind", ["steps", "some", "chunks", "null"])
+def test_thousands_of_sequences(pa, kind):
+    """Sequences are found by a search: of single tokens, of none or a few, of chunks over several frames."""
+    S, H, D, B = 3333, 1, 64, 8
+    gen = torch.Generator().manual_seed(12)
+    fresh = {"steps": torch.ones(S), "some": torch.randint(0, 3, (S,), generator=gen) * (torch.rand(S, generator=gen) < 0.5),
+             "chunks": torch.randint(0, 20, (S,), generator=gen), "null": torch.ones(S)}[kind].int().tolist()
+    lens = [int(n) + c for n, c in zip(torch.randint(0, 30, (S,), generator=gen), fresh)]
+    if kind == "null":
+        lens = [0 if s % 7 == 3 else n for s, n in enumerate(lens)]
+        fresh = [min(n, 1) for n in lens]
+    tables, nb = paged(gen, lens, B)
+    c = [cache8(gen, tables, [n - f for n, f in zip(lens, fresh)], nb, H, B, D, "f16") for _ in range(2)]
+    gpu = [on_gpu(x) for x in c]
+    start = np.arange(S + 1) if kind == "null" else np.cumsum([0] + fresh)
+    rows = [(4 * torch.randn(int(start[-1]), H, D, generator=gen)).half() for _ in range(2)]
+    qs = None if kind == "null" else torch.tensor(start, dtype=torch.int32).cuda()
+    pa.pa_cache_append_q8(rows[0].cuda(), rows[1].cuda(), tables.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), gpu[0][0], gpu[1][0],
+                          gpu[0][1], gpu[1][1], query_start=qs)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_status() == 0
+    for x, r, g in zip(c, rows, gpu):
+        for s, n in enumerate(lens):
+            x.append(tables[s].numpy(), n, r[start[s]:start[s] + fresh[s]].float().numpy())
+        same(g, x)
+
+
 def test_corner_frames(pa):
     """Zeros, one value, the range's ends, NaN, infinities, frames that were NaN, codes next to a border."""
     D, B, H = 64, 8, 1
