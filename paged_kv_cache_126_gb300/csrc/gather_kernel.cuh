@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       const int nf = __shfl_sync(kAll, n, f), uf = __shfl_sync(kAll, upto, f);
       const int rest = b0 - before - (uf - nf) * a.H;
       cur.s = s0 + f;
-      cur.h = rest / nf;
+      cur.h = quotient(rest, nf);
       cur.t = rest - cur.h * nf;
       break;
     }

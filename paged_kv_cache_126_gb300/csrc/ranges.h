@@ -10,6 +10,23 @@
 
 namespace pa {
 
+// a / b for 0 <= a, 0 < b.  On the device from a product with 1 / b in fp32, which is off by less than a * 2^-21 / b + 1: a second product of what is
+// left over is off by at most one.  Half as long as the compiler's division, of which a warp has ten behind one another before
+// its first load.
+PA_RANGES int quotient(int a, int b) {
+#ifdef __CUDA_ARCH__
+  const float inv = __fdividef(1.f, static_cast<float>(b));
+  int q = static_cast<int>(static_cast<float>(a) * inv);
+  int rest = a - q * b;
+  const int more = static_cast<int>(static_cast<float>(rest) * inv);
+  q += more;
+  rest -= more * b;
+  return q + (rest >= b) - (rest < 0);
+#else
+  return a / b;
+#endif
+}
+
 // Parts of 16 keys of L >= 0 tokens; at least one.
 PA_RANGES int parts16(int L) { return ((L > 1 ? L - 1 : 0) >> 4) + 1; }
 
@@ -45,7 +62,7 @@ constexpr int kFlat = 24;      // up to this many pieces are joined at once
 // How a decode's tiles are cut: worker w has the tiles start(w) .. start(w + 1) - 1.
 struct Cut {
   int total, workers, per, rest;  // total = per * workers + rest; workers^2 < 2^31
-  PA_RANGES int start(int w) const { return w * per + static_cast<int>(static_cast<unsigned>(w * rest) / workers); }
+  PA_RANGES int start(int w) const { return w * per + quotient(w * rest, workers); }
   // the worker of tile x: a division in fp32 is off by at most one
   PA_RANGES int owner(int x) const {
     int w = static_cast<int>((x + 0.5f) * (static_cast<float>(workers) / total));
@@ -61,21 +78,23 @@ PA_RANGES Cut cut_tiles(int total, int pairs, int all_warps, int keys) {
   // A join costs as much as about 128 keys: shorter (s, h) are left whole (64 keys of 8 heads: 7.6 us, cut in two
   // 8.8).  Fewer keys a worker where the pieces can still be joined at once (512 keys of 8 heads in pieces of 32 keys
   // 9.1 us, of 64 10.7; 4096 keys 17.3 and 15.8).
-  const int mean = total / pairs;
+  const int mean = quotient(total, pairs);
   const int tiles = mean < 1 << 20 ? mean : 1 << 20;  // of a (s, h), on average
   const int min_keys = tiles * keys <= 2 * kMinKeys ? 2 * kMinKeys : tiles * keys <= kFlat * (kMinKeys / 2) ? kMinKeys / 2 : kMinKeys;
-  const int piece = min_keys > keys ? min_keys / keys : 1;
+  const int piece = min_keys > keys ? min_keys / keys : 1;  // (both powers of two)
+  const int most = piece == 1 ? total : piece == 2 ? total >> 1 : piece == 4 ? total >> 2 : total / piece;
   Cut cut;
-  cut.workers = total / piece > pairs ? total / piece : pairs;
+  cut.workers = most > pairs ? most : pairs;
   if (cut.workers > all_warps) cut.workers = all_warps;
   // no more workers than the longest range needs: fewer pieces in the same time (1 x 16000 tokens: 24 -> 18 us)
-  const int longest = (total - 1) / cut.workers + 1;
-  cut.workers = (total - 1) / longest + 1;
+  const int longest = quotient(total - 1, cut.workers) + 1;
+  cut.workers = quotient(total - 1, longest) + 1;
   // A multiple of the (s, h) where that leaves few warps idle: sequences of one length are then cut at their ends
   // (64 listed frames for 4 x 32 heads: 22.7 -> 19.8 us).
-  if (cut.workers / pairs * pairs * 10 >= cut.workers * 9) cut.workers = cut.workers / pairs * pairs;
+  const int whole = quotient(cut.workers, pairs) * pairs;
+  if (whole * 10 >= cut.workers * 9) cut.workers = whole;
   cut.total = total;
-  cut.per = total / cut.workers;
+  cut.per = quotient(total, cut.workers);
   cut.rest = total - cut.per * cut.workers;
   return cut;
 }
