@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int B = a.B;
   const int fpt = kBN / B;  // frames per key tile
 
+  if (WINDOW) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < NBARS; ++i) {
       uint32_t cnt = 1;
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < 64) hist[tid] = 0;
   if (tid == 0) offu[0] = 0;
   __syncthreads();
+  if (WINDOW) asm volatile("griddepcontrol.wait;" ::: "memory");  // behind all that reads no input
   for (int s = tid; s < a.S; s += blockDim.x) {
     const int qs = a.query_start[s], qe = a.query_start[s + 1];
     const int L = a.context_lens[s];
@@ -482,8 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int n_units = offu[a.S];
+  const int per_unit = SLOTS == kHeads ? a.H >> 1 : a.H;
   if (n_units > a.unit_cap) {  // query ranges overlap beyond the rows given: no work
     if (tid == 0 && blockIdx.x == 0) atomicOr(a.status, kDevBadLen);
+  } else if (WINDOW && static_cast<long long>(n_units) * per_unit <= gridDim.x) {  // an item a block at most, in any order
+    for (int u = tid; u < n_units; u += blockDim.x) order[u] = u;
   } else if (warp == 1) {
     const int mx = *max_nkv;
     auto bucket_of = [&](int u) {
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const int total = n_units > a.unit_cap ? 0 : n_units * (SLOTS == kHeads ? a.H >> 1 : a.H);
+  const int total = n_units > a.unit_cap ? 0 : n_units * per_unit;
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
@@ -535,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ni = 0, kt = 0, qi = 0;
     while (true) {
       int item = 0;
-      if (lane == 0) item = *abort_flag ? total : atomicAdd(a.sched, 1);
+      // (WINDOW: a block's first item is its number)
+      if (lane == 0) item = *abort_flag ? total : !WINDOW ? atomicAdd(a.sched, 1) : ni == 0 ? static_cast<int>(blockIdx.x) : gridDim.x + atomicAdd(a.sched, 1);
       item = __shfl_sync(kFull, item, 0);
       const bool done = item >= total;
       const int sl = ni & 1;
@@ -1064,8 +1070,21 @@ cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMa
   auto kern = prefill_kernel<T, SLOTS>;
   cudaError_t e = kernel_prep(reinterpret_cast<const void*>(kern), kThreads, smem, nullptr);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, a);
-  return cudaGetLastError();
+  if (SLOTS == kCausal) {
+    kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a);
 }
 
 }  // namespace pk
