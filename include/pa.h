@@ -465,8 +465,8 @@ int pa_decode_selected(const pa_tensor* q, const pa_tensor* k_cache, const pa_te
  *                 given up (any value).
  *   window >= 1 (a window of at least L_s is every token), sinks >= 0, else PA_ERR_INVALID.
  * Slots that hold no attended token may hold any bits.  Arithmetic as for pa_decode_selected.
- * PA_ERR_UNSUPPORTED where S * H times a sequence's parts of 16 attended tokens (ceil(window / 16) + ceil(sinks / 16) + 1,
- * or one more than max_blocks * B / 16) passes int32.
+ * PA_ERR_UNSUPPORTED where S * H times a sequence's parts of 16 attended tokens (ceil(window / 16) + ceil(sinks / 16) + 2,
+ * or two more than max_blocks * B / 16) passes int32.
  */
 int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
                      const pa_tensor* block_tables, const pa_tensor* context_lens, int32_t window, int32_t sinks,

@@ -1724,7 +1724,7 @@ int window_args(int32_t window, int32_t sinks, int32_t least, int64_t keys, pa::
   int64_t parts = (static_cast<int64_t>(a->max_blocks) * a->B + 15) / 16;
   // sinks and a window each begin and end inside a part
   if (window > 0) parts = std::min(parts + 1, (static_cast<int64_t>(window) + 15) / 16 + (static_cast<int64_t>(sinks) + 15) / 16 + 1);
-  return tiles_fit(*a, (16 * parts + keys - 1) / keys) ? PA_OK : PA_ERR_UNSUPPORTED;
+  return tiles_fit(*a, (16 * parts + keys - 1) / keys + 1) ? PA_OK : PA_ERR_UNSUPPORTED;  // (an end counts as a tile)
 }
 
 // Workspace of a gathered decode on `workers` warps: an arrival counter per (sequence, head) and two per group

@@ -146,6 +146,10 @@ __device__ __forceinline__ int parts_of(const GatherArgs& a, int L) {
   const int n = min(a.K, (max(L, 0) + a.B - 1) >> a.log2_B);
   return max(1, a.B >= 16 ? n << (a.log2_B - 4) : (n + 1) >> 1);
 }
+// Units that the end of a (s, h) counts as, besides its tiles: a partial, an arrival and the next (s, h)'s plan take a warp about as
+// long as a tile (1.2 us; ranges of equal tiles ended after 25 us with one end in them, after 30 with four).
+template <class F, int KEYS>
+constexpr int kEnd = F::kSteps || KEYS == kWindow ? 1 : 0;
 template <int KEYS, int LOADS>
 __device__ __forceinline__ int tiles_of(const GatherArgs& a, int L) {
   return (parts_of<KEYS>(a, L) + LOADS - 1) / LOADS;
@@ -586,15 +590,16 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // this warp's range [b0, b1) of the batch's tiles
+  // this warp's range [b0, b1) of the batch's units
+  constexpr int END = kEnd<F, KEYS>;
   int total = 0;
-  int n = 0;  // tiles of sequence s0 + lane
+  int n = 0;  // units of a (s, h) of sequence s0 + lane
   for (int s0 = 0; s0 < a.S; s0 += 4 * 32) {  // (four loads at once)
     int sum = 0;
 #pragma unroll
     for (int u = 3; u >= 0; --u) {
       const int s = s0 + 32 * u + lane;
-      n = s < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s)) : 0;
+      n = s < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s)) + END : 0;
       sum += n;
     }
     total += __reduce_add_sync(kAll, sum);
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   cur.s = cur.h = cur.t = 0;
   int before = 0;
   for (int s0 = 0; s0 < a.S && count > 0; s0 += 32) {
-    if (a.S > 32) n = s0 + lane < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s0 + lane)) : 0;
+    if (a.S > 32) n = s0 + lane < a.S ? tiles_of<KEYS, LOADS>(a, checked_len(a, s0 + lane)) + END : 0;
     int upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -631,6 +636,11 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     before += __shfl_sync(kAll, upto, 31) * a.H;
   }
   enter_seq<KEYS, LOADS>(a, cur);
+  int i = 0;  // units done
+  if (END > 0 && cur.t == cur.tiles) {  // (the range begins with the end of a (s, h), which another warp's has the tiles of)
+    i = END;
+    if (i < count) next_head<KEYS, LOADS>(a, cur);
+  }
 
   // The producer's place.  Lane i plans the parts i, i + 32, ... of a (s, h) and issues their copies itself.
   Cursor ahead = cur;
@@ -639,7 +649,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   typename F::Place place;
   int plan_meta = 0;
   float4 plan_steps = make_float4(0.f, 0.f, 0.f, 0.f);  // of the halves' keys, of their values
-  int issued = 0, issue_st = 0, issue_phase = 0;
+  const int begun = i;
+  int issued = i, sent = 0, issue_st = 0, issue_phase = 0;  // units, tiles
   auto note = [&](int part) {  // what the consumer needs to know of a tile
     const int sub = lane - part;
     if (static_cast<unsigned>(sub) >= LOADS) return;
@@ -667,7 +678,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     if constexpr (!F::kSteps) note(part & 31);  // (steps may still be on their way: noted behind both copies)
     // the first tile of a (s, h), or of this warp's part of it, brings the queries along
     const uint32_t dst = stages + issue_st * kStage, bar = bars + 16 * issue_st;
-    const bool first = ahead.t == 0 || issued == 0;
+    const bool first = ahead.t == 0 || issued == begun;
     const uint32_t q_bytes = a.g * D * sizeof(T);
     F::load(a, &maps.k, place, ahead.h, lane, part & 31, dst, bar, first ? q_bytes : 0);
     if (first && lane == F::issuer(part & 31))
@@ -678,14 +689,18 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     if constexpr (F::kSteps) note((ahead.t * LOADS) & 31);
     if (++issue_st == STAGES) issue_st = 0, issue_phase ^= 1;
     ++issued;
-    if (++ahead.t == ahead.tiles && issued < count) {
-      next_head<KEYS, LOADS>(a, ahead);
-      planned = -1;
-      list.seen = 0;
-      list.ended = false;
+    ++sent;
+    if (++ahead.t == ahead.tiles) {
+      issued += END;
+      if (issued < count) {
+        next_head<KEYS, LOADS>(a, ahead);
+        planned = -1;
+        list.seen = 0;
+        list.ended = false;
+      }
     }
   };
-  for (int i = 0; i < STAGES && i < count; ++i) {
+  for (int k = 0; k < STAGES && issued < count; ++k) {
     issue_keys();
     issue_values();
   }
@@ -702,24 +717,25 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   const float rest = PARTS == kTwinColumns ? (c >= 2 ? 1.f : 0.f) : 1.f;
   int st = 0, phase = 0;
 
-  // A copy is stuck: let those in flight land (bounded) before the block retires.  Tile i's keys were waited
-  // for last, or its values (then the keys of tile i + STAGES may be in flight too).
-  auto drain = [&](int i, bool at_values) {
+  // A copy is stuck: let those in flight land (bounded) before the block retires.  The keys of the `got`-th tile were waited
+  // for last, or its values (then the keys of tile got + STAGES may be in flight too).
+  int got = 0;
+  auto drain = [&](bool at_values) {
     const long long t0 = clock64();
-    for (int j = i; j < issued + (at_values && issued < count ? 1 : 0); ++j) {
+    for (int j = got; j < sent + (at_values && issued < count ? 1 : 0); ++j) {
       const uint32_t bar = bars + 16 * (j % STAGES), ph = (j / STAGES) & 1;
-      for (int b = j == i && at_values ? 1 : 0; b < (j < issued ? 2 : 1); ++b)
+      for (int b = j == got && at_values ? 1 : 0; b < (j < sent ? 2 : 1); ++b)
         while (!dk::mbar_try_wait(bar + 8 * b, ph) && clock64() - t0 < dk::kDrainCycles) {
         }
     }
   };
 
-  for (int i = 0; i < count && !stuck;) {
+  while (i < count && !stuck) {
     // a new (s, h): its queries, as columns r (and r - 4 with twin columns)
     const int first_t = cur.t;
     bool poison = false;
     if (!__all_sync(kAll, dk::mbar_wait(bars + 16 * st, phase, abort_flag, a.status))) {
-      drain(i, false);
+      drain(false);
       stuck = true;
       break;
     }
@@ -756,10 +772,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     }
     const int stop = min(count, i + cur.tiles - cur.t);
     cur.t += stop - i;
-    for (; i < stop; ++i) {
+    for (; i < stop; ++i, ++got) {
       const uint32_t kst = stages + st * kStage, vst = kst + kKeys, bar = bars + 16 * st;
       if (!__all_sync(kAll, dk::mbar_wait(bar, phase, abort_flag, a.status))) {
-        drain(i, false);
+        drain(false);
         stuck = true;
         break;
       }
@@ -845,7 +861,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         }
       }
       if (!__all_sync(kAll, dk::mbar_wait(bar + 8, phase, abort_flag, a.status))) {
-        drain(i, true);
+        drain(true);
         stuck = true;
         break;
       }
@@ -968,7 +984,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         }
       if (!whole) {
         // pieces are the workers w0 .. w1: the first's second partial, the others' first
-        const int p0 = b0 + i - cur.t;  // the first tile of (s, h)
+        const int p0 = b0 + i - cur.t;  // the first unit of (s, h)
         Left x;
         x.s = cur.s;
         x.h = cur.h;
@@ -977,6 +993,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         if (lane == 0) left[warp][first_t == 0 ? 1 : 0] = x;
       }
     }
+    if (cur.t == cur.tiles) i += END;
     if (i < count) next_head<KEYS, LOADS>(a, cur);
   }
 
