@@ -174,18 +174,18 @@ struct Q8Format {
 namespace {
 
 // Bound by memory while it streams.  8 warps an SM, two on each scheduler, one stage of 64 keys (206 registers at D = 128): 64 sequences of
-// 512 to 2048 tokens, 32 heads of 128 in fp16 (674 MB) take 111.4 us, 6.05 TB/s; 4 x 16384 in bf16 (538 MB) 85.8 us, 6.27 TB/s, of which
+// 512 to 2048 tokens, 32 heads of 128 in fp16 (674 MB) take 110 us, 6.1 TB/s; 4 x 16384 in bf16 (538 MB) 85 to 87 us, 6.25 TB/s, of which
 // about 4 us pass before the first keys are there and 5 behind the last.  12 warps 118.8 and 94.0 us, 10 warps 114.7 and 90.7 us, 6
-// warps with two stages 132 and 100 us; tiles of 32 keys with 12 warps and two stages 134.6 and 104 us.
+// warps with two stages 132 and 100 us; tiles of 32 keys with 12 warps and two stages 134.6 and 104 us, of 128 keys with 6 warps 132
+// and 93 us.  A tile's parts in a loop instead of unrolled 119 and 94 us; copies issued by one lane instead of four 114.5 and 87.4 us.
 template <typename T, int D, int KEYS>
 cudaError_t by_group(const GatherArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t stream,
                      int* workers) {
   using F = gk::Q8Format<T, D>;
-  typename F::Maps maps;
-  maps.k = tk;
-  maps.v = tv;
-  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, KEYS, 1, 4, 2>(a, maps, num_sms, stream, workers);
-  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, KEYS, 1, 4, 2>(a, maps, num_sms, stream, workers);
+  const typename F::Maps maps = {tk, tv};
+  constexpr int kBlocks = D == 64 ? 3 : 2;  // (of half as many bytes)
+  if (a.g <= 4) return gk::launch<F, 1, gk::kTwinColumns, KEYS, 1, 4, kBlocks>(a, maps, num_sms, stream, workers);
+  if (a.g <= 8) return gk::launch<F, 1, gk::kTwoParts, KEYS, 1, 4, kBlocks>(a, maps, num_sms, stream, workers);
   return gk::launch<F, 2, gk::kTwoParts, KEYS, 1, 4, 2>(a, maps, num_sms, stream, workers);
 }
 

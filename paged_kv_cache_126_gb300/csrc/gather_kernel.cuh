@@ -646,6 +646,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   Cursor ahead = cur;
   List list = {0, false};
   int planned = -1;  // first part of the window of 32 that the lanes have planned; -1: none
+  TilePlan plan;       // it, which the next head of the sequence has too
+  int plan_s = -1, plan_at = -1;
   typename F::Place place;
   int plan_meta = 0;
   float4 plan_steps = make_float4(0.f, 0.f, 0.f, 0.f);  // of the halves' keys, of their values
@@ -664,11 +666,14 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     const int part = ahead.t * LOADS;
     if ((part & ~31) != planned) {
       planned = part & ~31;
-      const TilePlan p = plan_tiles<KEYS>(a, ahead, planned, lane, list);
-      place = F::place(a, p, ahead.h);
-      plan_meta = p.meta;
+      if (END == 0 || ahead.s != plan_s || planned != plan_at) {
+        plan = plan_tiles<KEYS>(a, ahead, planned, lane, list);
+        if (END > 0) plan_s = ahead.s, plan_at = planned;
+      }
+      place = F::place(a, plan, ahead.h);
+      plan_meta = plan.meta;
       if constexpr (F::kSteps) {
-        const int64_t f0 = p.frame[0], f1 = p.frame[1];
+        const int64_t f0 = plan.frame[0], f1 = plan.frame[1];
         plan_steps.x = f0 >= 0 ? a.k_step[f0 * a.ks_row + ahead.h] : 0.f;
         plan_steps.y = f1 >= 0 ? a.k_step[f1 * a.ks_row + ahead.h] : 0.f;
         plan_steps.z = f0 >= 0 ? a.v_step[f0 * a.vs_row + ahead.h] : 0.f;
