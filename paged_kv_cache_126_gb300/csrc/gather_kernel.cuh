@@ -1,5 +1,6 @@
-// Single-query attention over gathered keys: every token of a sequence held in the 4-bit
-// cache, or the tokens of listed frames of a 16-bit cache.
+// Single-query attention over gathered keys: every token of a sequence held in the 4-bit or
+// 8-bit cache, the tokens of listed frames of a 16-bit cache, or a sequence's last tokens and
+// its first few (a window and its sinks) in the 8-bit or a 16-bit cache.
 //
 // For each sequence s and key head h, with the g query heads that share it:
 //     out = sum_j w_j v_j / sum_j w_j,   w_j = exp2(q . k_j * scale * log2(e) - m),

@@ -392,6 +392,33 @@ def test_decode_bad_indexes(pa):
     check_decode(pa, (q, kc, vc, tables, lens), 0.125, "f16")
 
 
+def test_decode_and_read_strided_rows_steps_and_tables(pa):
+    case = decode_case([100, 50, 40], 3, 2, 64, 16, "f16", 16)
+    ref = check_decode(pa, case, 0.1, "f16")
+    q, kc, vc, tables, lens = case
+    (k, ks), (v, vs) = on_gpu(kc), on_gpu(vc)
+    nb = k.shape[0]
+    steps = torch.full((2, nb, 9), float("nan"), device="cuda")
+    steps[0, :, 1:4], steps[1, :, 1:4] = ks, vs
+    wide_q = torch.full((3, 6 * 64 + 8), float("nan"), dtype=torch.float16, device="cuda")
+    wide_q[:, : 6 * 64] = q.flatten(1).cuda()
+    wide_o = torch.full((3, 6 * 64 + 16), 9.0, dtype=torch.float16, device="cuda")
+    wide_t = torch.full((3, 40), -7, dtype=torch.int32, device="cuda")
+    wide_t[:, : tables.shape[1]] = tables.cuda()
+    pa.pa_decode_q8(wide_q[:, : 6 * 64].unflatten(1, (6, 64)), k, v, steps[0, :, 1:4], steps[1, :, 1:4], wide_t[:, : tables.shape[1]], lens.cuda(), 0.1,
+                    wide_o[:, : 6 * 64].unflatten(1, (6, 64)))
+    assert torch.equal(wide_o[:, : 6 * 64].unflatten(1, (6, 64)), ref)
+    assert (wide_o[:, 6 * 64:] == 9).all()
+    slots = torch.arange(nb * 16, dtype=torch.int32).cuda()
+    a, b = (torch.full((2, nb * 16, 3, 64), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wide = torch.full((2, nb * 16, 3 * 64 + 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    pa.pa_cache_read_q8(k, v, ks, vs, slots, a[0], a[1])
+    out = wide[:, :, : 3 * 64].unflatten(2, (3, 64))
+    pa.pa_cache_read_q8(k, v, steps[0, :, 1:4], steps[1, :, 1:4], slots, out[0], out[1])
+    assert torch.equal(out.nan_to_num(5), a.nan_to_num(5)) and (wide[:, :, 3 * 64:] == 9).all()
+    assert pa.pa_get_device_status() == 0
+
+
 def test_decode_same_bits_every_time(pa):
     q, kc, vc, tables, lens = decode_case([9000, 40, 777, 2048], 2, 4, 128, 32, "bf16", 15)
     (k, ks), (v, vs) = on_gpu(kc), on_gpu(vc)
