@@ -215,6 +215,7 @@ __device__ __forceinline__ void append_items(const Append8Args& a, const Unit& x
   }
   float* step_at = (is_v ? a.v_scale : a.k_scale) + (live ? frame * (is_v ? a.vs_row : a.ks_row) + h : 0);
   const float was = live && from > 0 ? *step_at : 0.f;
+  __syncwarp();  // each lane has the old step before one writes the new
 
   // the largest magnitude, as the bits of T: those of an infinity or more once an element is not finite
   uint32_t top2 = 0;
@@ -277,6 +278,7 @@ __device__ __forceinline__ void append_token(const Append8Args& a, const Unit& x
     was[i] = 0.f;
     if (at > 0 && row < 2 * a.H) was[i] = row >= a.H ? a.v_scale[frame * a.vs_row + row - a.H] : a.k_scale[frame * a.ks_row + row];
   }
+  __syncwarp();  // each lane has the old steps before one writes the new
 #pragma unroll
   for (int i = 0; i < kStepRows; ++i) {
     const int row = first + i * kRows;
@@ -404,7 +406,7 @@ bool append8_fits(Append8Args* a) {
   const int64_t blocks = (2 * static_cast<int64_t>(a->H) + items - 1) / items;
   // (a sequence's new tokens are in at most a B-th as many frames and two)
   const int64_t units = a->step ? a->T : a->T / a->B + 2 * static_cast<int64_t>(a->S);
-  if (units > 1 << 25 || units * blocks > INT32_MAX) return false;
+  if (a->T / a->B + 2 * static_cast<int64_t>(a->S) > 1 << 25 || units > 1 << 25 || units * blocks > INT32_MAX) return false;
   a->units = static_cast<int32_t>(units);
   a->blocks_unit = static_cast<int32_t>(blocks);
   return true;

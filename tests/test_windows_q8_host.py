@@ -214,3 +214,10 @@ def test_copy_blocks_takes_8_bit_frames_and_their_steps(pa, no_gpu):
     f = Call(pa, "pa_copy_blocks", kc=D(U8, 4, 2, 16, 64), vc=D(U8, 4, 2, 16, 64), pairs=D(I32, 1, 2), stream=None)
     assert f() == CUDA
     assert f(kc=D(F32, 4, 1, 1, 8), vc=D(F32, 4, 1, 1, 8)) == CUDA
+
+
+def test_append_q8_refuses_what_a_launch_does_not_number(pa, no_gpu):
+    D = lambda *a, **k: desc(pa, *a, **k)
+    f = Call(pa, "pa_cache_append_q8", k=D(F16, 64, 2, 64), v=D(F16, 64, 2, 64), bt=D(I32, 2, 3), cl=D(I32, 2), qs=D(I32, 3), **q8(pa), stream=None)
+    for seqs, code in ((2 ** 24 - 2, CUDA), (2 ** 24 - 1, UNSUPPORTED), (2 ** 31 - 2, UNSUPPORTED)):   # 64 / 16 + 2 S against 2^25
+        assert f(bt=D(I32, seqs, 3), cl=D(I32, seqs), qs=D(I32, seqs + 1)) == code, seqs
