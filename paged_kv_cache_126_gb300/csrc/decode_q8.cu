@@ -123,24 +123,25 @@ struct Q8Format {
   }
 
   // Slots that hold no key hold some whole number, which the weight 0 takes out.  A part's codes are read while the part before
-  // is multiplied.
+  // is multiplied; with more than 8 queries there are no registers for that (69.6 us, read ahead 70.6).
   template <int NT, int PARTS>
   __device__ __forceinline__ static void values_tile(uint32_t vst, int r, int c, const uint32_t (&p)[kLoads][PARTS][NT][2],
                                                      float (&o)[D / 16][NT][4]) {
     constexpr int W = D / 32;  // words of codes a lane reads of a key
-    uint32_t w[2][4][W];
+    constexpr int kAhead = NT == 1;
+    uint32_t w[1 + kAhead][4][W];
     auto read = [&](int u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = 2 * c + (i & 1) + (i >> 1) * 8;
-        lds(vst + u * kTile + (D == 128 ? chunk(key, r) : chunk(key, r >> 1) + (r & 1) * 8), w[u & 1][i]);
+        lds(vst + u * kTile + (D == 128 ? chunk(key, r) : chunk(key, r >> 1) + (r & 1) * 8), w[u & kAhead][i]);
       }
     };
-    read(0);
+    if (kAhead) read(0);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      if (u + 1 < kLoads) read(u + 1);
-      const uint32_t(&x)[4][W] = w[u & 1];
+      if (u + kAhead < kLoads) read(u + kAhead);
+      const uint32_t(&x)[4][W] = w[u & kAhead];
 #pragma unroll
       for (int y = 0; y < W; ++y)
 #pragma unroll

@@ -458,67 +458,98 @@ struct Q4Format {
 };
 
 // ---- the kernel -------------------------------------------------------------------------------------
-// One query's sum of n partials, in order: partial k is slot first + 2 k, and first + e for k = 0.  Into the output
-// row, or into slot `into` (>= 0).
+// The sums of n partials, in order, of C queries from `col` on (those below g): partial k is slot first + 2 k, and first + e for k = 0.
+// Into the output rows, or into slot `into` (>= 0).
 struct Join {
-  int64_t first, into;
-  int e, n, s, h;
+  int first, into, e, n, s, h;
 };
-template <typename T, int D>
-__device__ __forceinline__ void join_query(const GatherArgs& a, const Join& x, int col, int lane) {
-  constexpr int E = D / 32, kDeep = 16;
+template <typename T, int D, int C>
+__device__ __forceinline__ void join_queries(const GatherArgs& a, const Join& x, int col, int lane) {
+  constexpr int E = D / 32, kDeep = 16, kLoad = kDeep / C;
   using V = typename std::conditional<E == 4, float4, float2>::type;
-  float top = -INFINITY, sum = 0.f, y[E] = {};
-  bool bad = false;
-  const int64_t row = 2 * static_cast<int64_t>(a.g);  // rows of [g] between one piece and the next
-  const int64_t at0 = x.first * a.g + col;
+  float top[C], sum[C], y[C][E];
+  bool bad[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    top[i] = -INFINITY;
+    sum[i] = 0.f;
+    bad[i] = false;
+#pragma unroll
+    for (int z = 0; z < E; ++z) y[i][z] = 0.f;
+  }
+  const int row = 2 * a.g;  // rows of [g] between one piece and the next
+  const int at0 = x.first * a.g + col;  // (partials are two a worker and two a group: their elements are few enough for 32 bits)
 #pragma unroll 1
   for (int k0 = 0; k0 < x.n; k0 += kDeep) {
     const int m = min(kDeep, x.n - k0);
-    float2 p = make_float2(-INFINITY, 0.f);
-    if (lane < m) p = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at0 + (k0 + lane) * row + (k0 + lane == 0 ? x.e * a.g : 0));
-    V v[kDeep];
-    int64_t at = at0 + k0 * row + (k0 == 0 ? x.e * a.g : 0);
+    float2 p[C];
 #pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      if (u < m) v[u] = __ldcg(reinterpret_cast<const V*>(a.ws_o + at * D) + lane);
-      if (u == 0) at = at0 + k0 * row;
-      at += row;
+    for (int i = 0; i < C; ++i) {
+      p[i] = make_float2(-INFINITY, 0.f);
+      if (lane < m && col + i < a.g) p[i] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at0 + (k0 + lane) * row + (k0 + lane == 0 ? x.e * a.g : 0) + i);
     }
-    bad = bad || __any_sync(kAll, p.y < 0.f);
-    float t = p.y != 0.f ? p.x : -INFINITY;  // an empty piece has no maximum
+    V v[kLoad][C];
+    int at = at0 + k0 * row + (k0 == 0 ? x.e * a.g : 0);
+    auto load = [&](int u0) {
 #pragma unroll
-    for (int o = 1; o < kDeep; o <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
-    t = fmaxf(__shfl_sync(kAll, t, 0), top);
-    const float less = top == t ? 1.f : dk::ex2(top - t);
-    top = t;
-    const float mine = p.y != 0.f ? dk::ex2(p.x - top) : 0.f;
-    sum = sum * less + mine * p.y;
+      for (int u = 0; u < kLoad; ++u) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) y[i] *= less;
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      const float w = __shfl_sync(kAll, mine, u);
-      if (w != 0.f) {
-        const float* z = reinterpret_cast<const float*>(&v[u]);
-#pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = fmaf(w, z[i], y[i]);
+        for (int i = 0; i < C; ++i)
+          if (u0 + u < m && col + i < a.g) v[u][i] = __ldcg(reinterpret_cast<const V*>(a.ws_o + (at + i) * D) + lane);
+        if (u == 0 && u0 == 0) at = at0 + k0 * row;
+        at += row;
       }
+    };
+    load(0);
+    float mine[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      bad[i] = bad[i] || __any_sync(kAll, p[i].y < 0.f);
+      float t = p[i].y != 0.f ? p[i].x : -INFINITY;  // an empty piece has no maximum
+#pragma unroll
+      for (int o = 1; o < kDeep; o <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, o));
+      t = fmaxf(__shfl_sync(kAll, t, 0), top[i]);
+      const float less = top[i] == t ? 1.f : dk::ex2(top[i] - t);
+      top[i] = t;
+      mine[i] = p[i].y != 0.f ? dk::ex2(p[i].x - t) : 0.f;
+      sum[i] = sum[i] * less + mine[i] * p[i].y;
+#pragma unroll
+      for (int z = 0; z < E; ++z) y[i][z] *= less;
+    }
+#pragma unroll 1
+    for (int u0 = 0; u0 < (C == 1 ? 1 : m); u0 += kLoad) {
+      if (u0 > 0) load(u0);
+#pragma unroll
+      for (int u = 0; u < kLoad; ++u)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const float w = __shfl_sync(kAll, mine[i], u0 + u);
+          if (w != 0.f) {
+            const float* f = reinterpret_cast<const float*>(&v[u][i]);
+#pragma unroll
+            for (int z = 0; z < E; ++z) y[i][z] = fmaf(w, f[z], y[i][z]);
+          }
+        }
     }
   }
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  if (x.into >= 0) {
-    float* p = a.ws_o + (x.into * a.g + col) * D + lane * E;
+  for (int i = 0; i < C; ++i) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = y[i];
-    if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + (x.into * a.g + col) * 2) = make_float2(top, bad ? -1.f : sum);
-    return;
+    for (int o = 1; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(kAll, sum[i], o);
+    if (col + i >= a.g) continue;
+    if (x.into >= 0) {
+      const int to = x.into * a.g + col + i;
+      float* p = a.ws_o + to * D + lane * E;
+#pragma unroll
+      for (int z = 0; z < E; ++z) p[z] = y[i][z];
+      if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + to * 2) = make_float2(top[i], bad[i] ? -1.f : sum[i]);
+      continue;
+    }
+    const float inv = bad[i] || !(sum[i] != 0.f) ? 0.f : 1.f / sum[i];
+    T* out = static_cast<T*>(a.out) + x.s * a.out_row + (static_cast<int64_t>(x.h) * a.g + col + i) * D + lane * E;
+#pragma unroll
+    for (int z = 0; z < E; z += 2) *reinterpret_cast<uint32_t*>(out + z) = bad[i] ? 0u : pack2<T>(y[i][z] * inv, y[i][z + 1] * inv);
   }
-  const float inv = bad || !(sum != 0.f) ? 0.f : 1.f / sum;
-  T* out = static_cast<T*>(a.out) + x.s * a.out_row + (static_cast<int64_t>(x.h) * a.g + col) * D + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(out + i) = bad ? 0u : pack2<T>(y[i] * inv, y[i + 1] * inv);
 }
 
 // Raises a counter of `n` arrivals; whether this one was the last, which leaves it zero again.  By one lane, behind a barrier
@@ -568,6 +599,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   using M = typename F::M;
   constexpr int D = F::D;
   constexpr int kB = PARTS == kTwoParts ? 2 : 1;  // B operands of the weights
+  // Queries of a join that a warp takes at once: four warps have those of a (s, h) on their way together.  (One at a time, 64 sequences of
+  // 512 .. 2048 tokens, 8 heads: windows with 8 and 16 queries a head 67.5 and 79.5 us for 64.9 and 72.1.)
+  constexpr int kJoin = PARTS == kTwinColumns ? 1 : 2 * NT;
+  static_assert((WARPS & (WARPS - 1)) == 0, "chunks of joins go round the warps");
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
@@ -1011,17 +1046,25 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   }
   __syncwarp();
 
-  // The joins that fall to this block, a query a warp at a time; then those of groups.
+  // The joins that fall to this block, kJoin queries a warp at a time; then those of groups.
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
     __syncthreads();
     if (*abort_flag) return;
+    const uint32_t todo = last[round];
     bool groups = false;
+    const int of_chunks = (a.g + kJoin - 1) / kJoin;
+    int q = 0;
 #pragma unroll 1
-    for (uint32_t todo = last[round]; todo; todo &= todo - 1) {
-      const int k = __ffs(todo) - 1;
+    for (uint32_t t = todo; t; t &= t - 1) {
+      const int k = __ffs(t) - 1;
       const Left x = left[k >> 1][k & 1];
       const bool many = x.w1 - x.w0 >= kFlat;
+      groups = groups || (round == 0 && many);
+      // this warp's first chunk of it: chunks of all joins go round the warps (4 x 16384 tokens of 32 heads in 8 bits 85.75 -> 85.2 us)
+      const int at = (warp - q) & (WARPS - 1);
+      q += of_chunks;
+      if (at >= of_chunks) continue;
       const int of = (k >> 1) * gridDim.x + blockIdx.x;  // the worker whose piece it is
       Join j;
       j.s = x.s;
@@ -1029,18 +1072,17 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       j.into = -1;
       if (round == 0 && many) {
         const int g = of / kGroup, lo = max(x.w0, g * kGroup);
-        j.first = 2 * static_cast<int64_t>(lo);
+        j.first = 2 * lo;
         j.e = lo == x.w0 ? 1 : 0;
         j.n = arrivals_of(x, of);
         j.into = 2 * all_warps + 2 * g + j.e;  // partials of groups follow those of workers
-        groups = true;
       } else {
-        j.first = round == 0 ? 2 * static_cast<int64_t>(x.w0) : 2 * static_cast<int64_t>(all_warps) + 2 * (x.w0 / kGroup);
+        j.first = 2 * (round == 0 ? x.w0 : all_warps + x.w0 / kGroup);
         j.e = 1;
         j.n = round == 0 ? x.w1 - x.w0 + 1 : x.w1 / kGroup - x.w0 / kGroup + 1;
       }
 #pragma unroll 1
-      for (int col = (warp + k) % WARPS; col < a.g; col += WARPS) join_query<T, D>(a, j, col, lane);
+      for (int col = at * kJoin; col < a.g; col += WARPS * kJoin) join_queries<T, D, kJoin>(a, j, col, lane);
     }
     if (!groups) return;
     __syncthreads();
