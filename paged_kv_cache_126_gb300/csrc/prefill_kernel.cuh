@@ -798,6 +798,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       theirs = xb[(half ^ 1) * 128 + row];
       return w;
     };
+    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };  // the bits 0 .. n - 1
+    auto swap2 = [](auto (&x)[2]) {
+      const auto y = x[0];
+      x[0] = x[1];
+      x[1] = y;
+    };
+    // Where a tile's code is long (weights in two parts, masks of windows) both slots run the same copy of it, the state of the one at hand
+    // in [0]: instructions that the caches do not hold cost more than moves do.  A window of 4096 over 16384 tokens, 32/8 heads, bf16: 1273 us
+    // with a copy a slot, 1104 so; pa_prefill of 1 x 4000 in bf16 172 and 168, in fp16 128 and
+    // 136 (16 x 512: 238 and 240), which therefore keeps a copy a slot.
+    constexpr bool kRolled = SLOTS != kCausal || kSplitP;
     auto row_sum = [](const uint64_t (&v)[2]) {
       float a0, a1, b0, b1;
       unf2(v[0], a0, a1);
@@ -825,18 +836,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       // per tile of slot q (slot 0 tile j, then slot 1 tile j): scores of this half's 64
       // keys -> weights, O rescaled if the reference moved
+#pragma unroll 1
       for (int j = 0; j < (SLOTS == kSplit ? n0 : n1) && ok; ++j) {
-#pragma unroll
+#pragma unroll kRolled ? 1 : 2
       for (int q = 0; q < 2; ++q) {
-        if ((q == 0 && j >= n0) || (SLOTS == kSplit && q == 1 && j >= n1) || !ok) continue;
-        if (!wait_all(BAR(BS_FULL + q), sc[q] & 1u)) { ok = false; continue; }
-        ++sc[q];
+        const int c = kRolled ? 0 : q;
+        if (j < (q == 0 ? n0 : n1)) {  // (slot 0 may have fewer)
+        if (!wait_all(BAR(BS_FULL + q), sc[c] & 1u)) { ok = false; break; }
+        ++sc[c];
         const uint32_t s_tmem = tmem + lane_base + kTmemS + q * 128;
         // keys of this half a row may see: 64 half + (0 .. nv-1).  Rows of a warp are
         // consecutive positions, so a 32-key chunk is (warp-uniformly) fully visible,
         // fully masked (weight 0, not loaded) or split by the diagonal.
         const int tile = SLOTS == kSplit ? 2 * j + q : j;
-        const int last = WINDOW ? pos[q] - it.shift : pos[q];  // the last key a row sees, in the list
+        const int last = WINDOW ? pos[c] - it.shift : pos[c];  // the last key a row sees, in the list
         const int nvalid = max(0, min(kBN, last - tile * kBN + 1));
         int nv = max(0, min(64, nvalid - 64 * half));
         int from = 0, sinks = 0;  // WINDOW: of those, sinks .. from - 1 are hidden
@@ -860,15 +873,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int cc = 0; cc < 2; ++cc) {
             if (wmax <= cc * 32) break;
             uint32_t(&cur)[32] = sr[cc];
-            if (wmin < (cc + 1) * 32) {
+            if constexpr (WINDOW) {
+              const uint32_t hidden = ~below(nv - cc * 32) | (below(from - cc * 32) & ~below(sinks - cc * 32));
+              if (__any_sync(kFull, hidden != 0u)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (hidden >> i & 1u) cur[i] = __float_as_uint(-INFINITY);
+              }
+            } else if (wmin < (cc + 1) * 32) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (cc * 32 + i >= nv) cur[i] = __float_as_uint(-INFINITY);
-            }
-            if (WINDOW && __any_sync(kFull, from > cc * 32)) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (cc * 32 + i >= sinks && cc * 32 + i < from) cur[i] = __float_as_uint(-INFINITY);
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
@@ -888,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         xb[half * 128 + row] = mine;
         __syncwarp();
         if (lane == 0) mbar_arrive(xbar);
-        const bool spec = kSplitP && __all_sync(kFull, m_ref[q] > -INFINITY && mine * sl2 <= m_ref[q] + 8.f);
+        const bool spec = kSplitP && __all_sync(kFull, m_ref[c] > -INFINITY && mine * sl2 <= m_ref[c] + 8.f);
         uint64_t sum2[2];  // packed fp32 pairs of partial row sums
         auto weights = [&](float mref) {
           if (WINDOW && mref == -INFINITY) mref = 0.f;  // nothing seen yet: every score is -inf
@@ -930,41 +945,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kSplitP) tmem_st16(pcol + 32, wl);
           }
         };
-        if (spec) weights(m_ref[q]);
-        if (!wait_all(xbar, xk & 1u)) { ok = false; continue; }
-        ++xk;
-        const float other = xb[(half ^ 1) * 128 + row];
-        const float m_t = fmaxf(mine, other) * sl2;
-        // one decision per tile, the same in both halves (always on a row's first tile)
+        // (one copy of the weights' code, which is most of the loop's)
         float alpha = 1.f;
-        if (m_t > m_ref[q] + 8.f) {
-          alpha = ex2(m_ref[q] - m_t);
-          m_ref[q] = m_t;
+#pragma unroll 1
+        for (int pass = kSplitP ? 0 : 1; pass < 2; ++pass) {
+          bool now = spec;
+          if (pass == 1) {
+            if (!wait_all(xbar, xk & 1u)) { ok = false; break; }
+            ++xk;
+            const float other = xb[(half ^ 1) * 128 + row];
+            const float m_t = fmaxf(mine, other) * sl2;
+            // one decision per tile, the same in both halves (always on a row's first tile)
+            if (m_t > m_ref[c] + 8.f) {
+              alpha = ex2(m_ref[c] - m_t);
+              m_ref[c] = m_t;
+            }
+            now = !spec || __any_sync(kFull, alpha != 1.f);
+            if (spec && now) tmem_wait_st();  // the stores above land before these
+          }
+          if (now) weights(m_ref[c]);
         }
-        if (!spec || __any_sync(kFull, alpha != 1.f)) {
-          if (spec) tmem_wait_st();  // the stores above land before these
-          weights(m_ref[q]);
-        }
+        if (!ok) break;
         if (j > 0 && __any_sync(kFull, alpha != 1.f)) {
           // O_q holds the previous tiles (the S commit covered their P V); this half's
           // dimensions, rows whose reference did not move scale by 1
           const uint32_t o_tmem = tmem + lane_base + kTmemO + q * 128 + 64 * half;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int d = 0; d < 2; ++d) {
             uint32_t r[32];
-            tmem_ld32_async(o_tmem + c * 32, r);
+            tmem_ld32_async(o_tmem + d * 32, r);
             tmem_wait_ld();
             tie32(r);
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-            tmem_st32(o_tmem + c * 32, r);
+            tmem_st32(o_tmem + d * 32, r);
           }
         }
-        l[q] = l[q] * alpha + row_sum(sum2);
+        l[c] = l[c] * alpha + row_sum(sum2);
         tmem_wait_st();
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(BP_FULL + q));
+        }
+        if constexpr (kRolled) {
+          swap2(pos);
+          swap2(m_ref);
+          swap2(l);
+          swap2(sc);
+        }
       }
       }
       // epilogues, slot 0 then slot 1: wait for the slot's last P V, add the halves'
