@@ -764,10 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // halves exchange it through shared memory (one mbarrier per quadrant, bounded
     // wait), and both take the same decision: the reference max m_ref the weights are
     // taken against moves only when the tile's row max passed it by more than 8 (log2
-    // units), so weights stay <= 2^8 and O is rescaled rarely.  For bf16 a half posts its
-    // max, computes and stores its weights against the current m_ref, and only then reads
-    // the partner's max; when m_ref moves (every row's first tile, rarely afterwards) the
-    // weights are computed again.  Each half keeps a partial row sum; the halves add
+    // units), so weights stay <= 2^8 and O is rescaled rarely.  Each half keeps a partial row sum; the halves add
     // them at the epilogue.  P goes back to TMEM over the half's own 64 score columns
     // (keys 64h + 2k, 64h + 2k + 1 in column 64h + k; bf16 remainders 32 columns on).
     const int half = (warp - kSmxWarp0) >> 2;
@@ -890,20 +887,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx4[(i >> 1) & 3] = fmax3(mx4[(i >> 1) & 3], __uint_as_float(cur[i]), __uint_as_float(cur[i + 1]));
           }
         }
-        // Give the partner half this row's max now.  bf16 (two 16-bit parts per weight):
-        // read the partner's max only after the weights, computed against the current
-        // reference; they are final unless the tile's max passes it by more than 8, which
-        // after a row's first tile is rare, and then computed again from the scores, still
-        // in registers (fp16, with half the weight work, measured faster without this:
-        // 991 against 939 TF/s; bf16 755 against 735).  Each half writes its weights over
-        // its own score columns only, so it may store them before the partner has read
-        // its scores.
+        // Give the partner half this row's max.  Each half writes its weights over its own score columns only.  (bf16 weights computed
+        // before the partner's max is read, and again where it moves the reference: 63.3 us for 59.6, 8 chunks of 256 tokens over 1000 .. 3000,
+        // 32/4 heads, windows of 1000; whole prompts the same.)
         const float mine = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float* xb = xbuf + (xk & 1u) * 256;
         xb[half * 128 + row] = mine;
         __syncwarp();
         if (lane == 0) mbar_arrive(xbar);
-        const bool spec = kSplitP && __all_sync(kFull, m_ref[c] > -INFINITY && mine * sl2 <= m_ref[c] + 8.f);
         uint64_t sum2[2];  // packed fp32 pairs of partial row sums
         auto weights = [&](float mref) {
           if (WINDOW && mref == -INFINITY) mref = 0.f;  // nothing seen yet: every score is -inf
@@ -945,27 +936,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kSplitP) tmem_st16(pcol + 32, wl);
           }
         };
-        // (one copy of the weights' code, which is most of the loop's)
+        if (!wait_all(xbar, xk & 1u)) { ok = false; break; }
+        ++xk;
+        const float other = xb[(half ^ 1) * 128 + row];
+        const float m_t = fmaxf(mine, other) * sl2;
+        // one decision per tile, the same in both halves (always on a row's first tile)
         float alpha = 1.f;
-#pragma unroll 1
-        for (int pass = kSplitP ? 0 : 1; pass < 2; ++pass) {
-          bool now = spec;
-          if (pass == 1) {
-            if (!wait_all(xbar, xk & 1u)) { ok = false; break; }
-            ++xk;
-            const float other = xb[(half ^ 1) * 128 + row];
-            const float m_t = fmaxf(mine, other) * sl2;
-            // one decision per tile, the same in both halves (always on a row's first tile)
-            if (m_t > m_ref[c] + 8.f) {
-              alpha = ex2(m_ref[c] - m_t);
-              m_ref[c] = m_t;
-            }
-            now = !spec || __any_sync(kFull, alpha != 1.f);
-            if (spec && now) tmem_wait_st();  // the stores above land before these
-          }
-          if (now) weights(m_ref[c]);
+        if (m_t > m_ref[c] + 8.f) {
+          alpha = ex2(m_ref[c] - m_t);
+          m_ref[c] = m_t;
         }
-        if (!ok) break;
+        weights(m_ref[c]);
         if (j > 0 && __any_sync(kFull, alpha != 1.f)) {
           // O_q holds the previous tiles (the S commit covered their P V); this half's
           // dimensions, rows whose reference did not move scale by 1
