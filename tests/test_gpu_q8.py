@@ -429,3 +429,11 @@ def test_decode_same_bits_every_time(pa):
         again = torch.empty_like(q)
         pa.pa_decode_q8(q, k, v, ks, vs, tables, lens, 0.1, again)
         assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [3, 5, 8, 12, 16])
+def test_decode_joins_of_many_queries(pa, g, D):
+    """A head of 20000 tokens is joined in groups; of 400 heads of 300 tokens most are in pieces, and a block joins several."""
+    check_decode(pa, decode_case([20000, 3, 0, 5000, 1], 1, g, D, 16, "f16", 30 + g), D ** -0.5, "f16")
+    check_decode(pa, decode_case([300 - i % 7 for i in range(200)], 2, g, D, 16, "bf16", 31 + g), D ** -0.5, "bf16", seqs=range(0, 200, 3))

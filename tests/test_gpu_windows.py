@@ -327,3 +327,19 @@ def test_chunk_more_sequences_than_a_launch_holds(pa):
     lens = [1 + i % 40 for i in range(S)]
     case = chunk_case(lens, [1] * S, 1, 1, 8, "f16", 10, 2, 8)
     check_chunk(pa, case, 10, 2, 0.1, "f16", range(0, S, 401))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [3, 5, 8, 12, 16])
+def test_decode_joins_of_many_queries(pa, g, D):
+    """A window of 12345 tokens is joined in groups; of 400 windows of 260 tokens most are in pieces, and a block joins several."""
+    check_decode(pa, decode_case([40000, 3, 0, 5000, 1], 1, g, D, 16, "f16", 12345, 70, 30 + g), 12345, 70, D ** -0.5, "f16")
+    check_decode(pa, decode_case([300 - i % 7 for i in range(200)], 2, g, D, 16, "bf16", 256, 4, 31 + g), 256, 4, D ** -0.5, "bf16", seqs=range(0, 200, 3))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H,g", [(40, 1), (20, 3), (20, 2), (5, 16)])
+def test_chunk_tiles_of_many_heads_with_windows_and_sinks_inside(pa, dtype, H, g):
+    """Items of both slots, one after another in a block, whose windows begin and sinks end inside a tile."""
+    case = chunk_case([900, 301, 5], [390, 131, 5], H, g, 16, dtype, 333, 21, 7)
+    check_chunk(pa, case, 333, 21, 128 ** -0.5, dtype, list(range(0, 390, 41)) + list(range(391, 526, 17)))
