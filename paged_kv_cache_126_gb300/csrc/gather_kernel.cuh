@@ -727,7 +727,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   };
   auto issue_values = [&]() {  // of the same tile, and on to the next
     F::load(a, &maps.v, place, ahead.h, lane, (ahead.t * LOADS) & 31, stages + issue_st * kStage + kKeys, bars + 16 * issue_st + 8, 0);
-    if constexpr (F::kSteps) note((ahead.t * LOADS) & 31);
+    if constexpr (F::kSteps) {
+      note((ahead.t * LOADS) & 31);
+      __syncwarp();  // no copy's barrier orders these stores: its arrival came before them
+    }
     if (++issue_st == STAGES) issue_st = 0, issue_phase ^= 1;
     ++issued;
     ++sent;
