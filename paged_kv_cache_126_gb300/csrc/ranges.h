@@ -10,20 +10,24 @@
 
 namespace pa {
 
-// a / b for 0 <= a, 0 < b.  On the device from a product with 1 / b in fp32, which is off by less than a * 2^-21 / b + 1: a second product of what is
-// left over is off by at most one.  Half as long as the compiler's division, of which a warp has ten behind one another before
-// its first load.
+// a / b for 0 <= a, 0 < b, given inv = 1 / b to within two steps of fp32.  With the roundings of b, a and the product, a * inv is off by
+// less than 2^-21 of a / b: the first quotient leaves -2^10 < rest < b + 2^10, and rest <= a; the second, of the rest, is off by at most
+// one.  The first may pass int32 (a = 2^31 - 1, b = 1), and so may its product with b: both are unsigned, and the rest is their difference
+// modulo 2^32.
+PA_RANGES int quotient_by(int a, int b, float inv) {
+  const unsigned q = static_cast<unsigned>(static_cast<float>(a) * inv);
+  int rest = static_cast<int>(static_cast<unsigned>(a) - q * static_cast<unsigned>(b));
+  const int more = static_cast<int>(static_cast<float>(rest) * inv);
+  rest -= more * b;
+  return static_cast<int>(q + static_cast<unsigned>(more + (rest >= b) - (rest < 0)));
+}
+// Half as long as the compiler's division, of which a warp has ten behind one another before its first load.  The host, for
+// the tests, goes the same way.
 PA_RANGES int quotient(int a, int b) {
 #ifdef __CUDA_ARCH__
-  const float inv = __fdividef(1.f, static_cast<float>(b));
-  int q = static_cast<int>(static_cast<float>(a) * inv);
-  int rest = a - q * b;
-  const int more = static_cast<int>(static_cast<float>(rest) * inv);
-  q += more;
-  rest -= more * b;
-  return q + (rest >= b) - (rest < 0);
+  return quotient_by(a, b, __fdividef(1.f, static_cast<float>(b)));
 #else
-  return a / b;
+  return quotient_by(a, b, 1.f / static_cast<float>(b));
 #endif
 }
 
