@@ -479,6 +479,8 @@ int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tens
  *   q, out        [T, Hq, 128] fp16/bf16;  the other arguments, arithmetic, errors and status bits as for
  *                 pa_prefill.  Entries of frames that hold no token attended by a query of the call are not read.
  *   window >= 1, sinks >= 0, scale > 0 and finite, else PA_ERR_INVALID.
+ * A query that is not finite, or attends a key that is NaN, has a row of NaN as in pa_decode_window (pa_prefill leaves
+ * zeros there), one whose scores are all -inf zeros.
  * Sequences of one call may share frames.  PA_ERR_UNSUPPORTED for T above about a million rows.
  */
 int pa_prefill_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,

@@ -986,7 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float other = 0.f;
         if (ok && !exchange(l[q], other)) ok = false;
         const float lt = l[q] + other;
-        const bool zero = !ok || !(lt > 0.f);
+        // WINDOW: a sum that is NaN shows, as in the decodes; pa_prefill writes zeros there, as it always has
+        const bool zero = !ok || !(WINDOW ? lt != 0.f : lt > 0.f);
         const float inv = zero ? 0.f : 1.f / lt;
         const bool valid = row < it.nrows[q];
         const uint32_t o_tmem = tmem + lane_base + kTmemO + q * 128 + 64 * half;
@@ -1029,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 2; ++q) f[q] = m_ref[q] == -INFINITY ? 0.f : ex2(m_ref[q] - m);
         const float lt = sum[0] * f[0] + sum[1] * f[1];
-        const bool zero = !ok || !(lt > 0.f);
+        const bool zero = !ok || !(lt != 0.f);
         const float inv = zero ? 0.f : 1.f / lt;
         f[0] *= inv;
         f[1] *= inv;
