@@ -518,7 +518,8 @@ int pa_cache_append_q8(const pa_tensor* k_new, const pa_tensor* v_new, const pa_
 
 /*
  * pa_cache_read_q8 -- rows of the 8-bit cache as 16-bit rows (for pa_prefill over a cached prefix, inspection):
- * k_out, v_out [T, H, D] = (b - 128) * step in fp32, rounded to their type, of the rows at slot_mapping [T].
+ * k_out, v_out [T, H, D] = (b - 128) * step in fp32, rounded to their type, of the rows at slot_mapping [T].  A code may stand
+ * for up to half a step more than its element did (65536 for 65504, say): what is beyond +-65504 is +-65504 in fp16.
  * slot < 0: that output row is left as it was; slot >= num_blocks * B: PA_DEV_BAD_SLOT and the row is left as
  * it was.  The same slot may be read often.
  */
@@ -531,7 +532,8 @@ int pa_cache_read_q8(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
  * (window >= 1, sinks >= 0; else PA_ERR_INVALID).  q, out [S, Hq, D] fp16/bf16; the rest as for pa_decode_window.
  * Codes are exact in the tensor cores' fp16; steps multiply scores and weights in fp32.  A weight times its step is carried as
  * two fp16 parts: to 2^-22 of itself, or where that is more to 2^-32 of the largest weight times the largest step of the
- * sequence's head.  bf16 queries as for pa_decode_q4.  PA_ERR_UNSUPPORTED as for pa_decode_window, in tiles of 64 tokens.
+ * sequence's head.  bf16 queries as for pa_decode_q4, fp16
+ * outputs within +-65504 as for pa_cache_read_q8.  PA_ERR_UNSUPPORTED as for pa_decode_window, in tiles of 64 tokens.
  */
 int pa_decode_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
                  const pa_tensor* v_scale, const pa_tensor* block_tables, const pa_tensor* context_lens,

@@ -33,6 +33,12 @@ def _top_bits(x: np.float32, nearest: bool) -> np.float32:
     return np.uint32(b & 0xFFFF0000).view(np.float32)
 
 
+def largest_kept(x: np.ndarray, dtype: str) -> np.ndarray:
+    """Outputs over the 8-bit cache before they are rounded to `dtype`: codes may stand for up to half a step more than the element they
+    came from, so in fp16 a number beyond its largest is that one.  NaN stays."""
+    return np.clip(x, -65504.0, 65504.0) if dtype == "f16" else x
+
+
 class Cache8:
     """An 8-bit cache: codes uint8 [num_blocks, H, B, D], steps float32 [num_blocks, H]."""
 

@@ -165,8 +165,8 @@ struct Q8Format {
 #pragma unroll
     for (int t = 0; t < D / 16; t += 4)
       *reinterpret_cast<uint4*>(row + r * (D / 8) + 2 * t) =
-          make_uint4(pack2<T>(y[t][0], y[t][1]), pack2<T>(y[t + 1][0], y[t + 1][1]), pack2<T>(y[t + 2][0], y[t + 2][1]),
-                     pack2<T>(y[t + 3][0], y[t + 3][1]));
+          make_uint4(pack_out<T, true>(y[t][0], y[t][1]), pack_out<T, true>(y[t + 1][0], y[t + 1][1]),
+                     pack_out<T, true>(y[t + 2][0], y[t + 2][1]), pack_out<T, true>(y[t + 3][0], y[t + 3][1]));
   }
 };
 

@@ -91,6 +91,15 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) { return as_u32(__floats2half2_rn(x, y)); }
 template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) { return as_u32(__floats2bfloat162_rn(x, y)); }
+// Two numbers of an output.  CAP, over the 8-bit cache, whose codes may stand for half a step more than the element they came from: in
+// fp16 a number beyond the largest is that one.  NaN stays.
+template <typename T, bool CAP>
+__device__ __forceinline__ uint32_t pack_out(float x, float y) {
+  const uint32_t w = pack2<T>(x, y);
+  if (!CAP || !std::is_same<T, __half>::value) return w;
+  const __half2 most = __half2half2(__ushort_as_half(0x7bff));
+  return as_u32(__hmax2_nan(__hmin2_nan(*reinterpret_cast<const __half2*>(&w), most), __hneg2(most)));
+}
 template <typename M>
 __device__ __forceinline__ float2 unpack2(uint32_t x);
 template <>
@@ -463,7 +472,7 @@ struct Q4Format {
 struct Join {
   int first, into, e, n, s, h;
 };
-template <typename T, int D, int C>
+template <typename T, int D, int C, bool CAP>
 __device__ __forceinline__ void join_queries(const GatherArgs& a, const Join& x, int col, int lane) {
   constexpr int E = D / 32, kDeep = 16, kLoad = kDeep / C;
   using V = typename std::conditional<E == 4, float4, float2>::type;
@@ -548,7 +557,7 @@ __device__ __forceinline__ void join_queries(const GatherArgs& a, const Join& x,
     const float inv = bad[i] || !(sum[i] != 0.f) ? 0.f : 1.f / sum[i];
     T* out = static_cast<T*>(a.out) + x.s * a.out_row + (static_cast<int64_t>(x.h) * a.g + col + i) * D + lane * E;
 #pragma unroll
-    for (int z = 0; z < E; z += 2) *reinterpret_cast<uint32_t*>(out + z) = bad[i] ? 0u : pack2<T>(y[i][z] * inv, y[i][z + 1] * inv);
+    for (int z = 0; z < E; z += 2) *reinterpret_cast<uint32_t*>(out + z) = bad[i] ? 0u : pack_out<T, CAP>(y[i][z] * inv, y[i][z + 1] * inv);
   }
 }
 
@@ -1085,7 +1094,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
         j.n = round == 0 ? x.w1 - x.w0 + 1 : x.w1 / kGroup - x.w0 / kGroup + 1;
       }
 #pragma unroll 1
-      for (int col = at * kJoin; col < a.g; col += WARPS * kJoin) join_queries<T, D, kJoin>(a, j, col, lane);
+      for (int col = at * kJoin; col < a.g; col += WARPS * kJoin) join_queries<T, D, kJoin, F::kSteps>(a, j, col, lane);
     }
     if (!groups) return;
     __syncthreads();

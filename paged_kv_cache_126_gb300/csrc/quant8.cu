@@ -38,8 +38,10 @@ struct Bits<__half> {
   static constexpr bool kPastMost = false;  // whether an element may be above kMost
   __device__ __forceinline__ static float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
   __device__ __forceinline__ static float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
+  // what is beyond fp16's largest number is that one (a code may stand for half a step more than its element); NaN stays
   __device__ __forceinline__ static uint32_t pack(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
+    const __half2 most = __half2half2(__ushort_as_half(0x7bff));
+    const __half2 h = __hmax2_nan(__hmin2_nan(__floats2half2_rn(a, b), most), __hneg2(most));
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 };
