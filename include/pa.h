@@ -531,9 +531,9 @@ int pa_cache_read_q8(const pa_tensor* k_cache, const pa_tensor* v_cache, const p
  * pa_decode_q8 -- pa_decode over the 8-bit cache, all tokens (window = 0, sinks = 0) or those of pa_decode_window
  * (window >= 1, sinks >= 0; else PA_ERR_INVALID).  q, out [S, Hq, D] fp16/bf16; the rest as for pa_decode_window.
  * Codes are exact in the tensor cores' fp16; steps multiply scores and weights in fp32.  A weight times its step is carried as
- * two fp16 parts: to 2^-22 of itself, or where that is more to 2^-32 of the largest weight times the largest step of the
- * sequence's head.  bf16 queries as for pa_decode_q4, fp16
- * outputs within +-65504 as for pa_cache_read_q8.  PA_ERR_UNSUPPORTED as for pa_decode_window, in tiles of 64 tokens.
+ * two fp16 parts: to 2^-22 of itself, or where that is more to 2^-31 of the largest weight times the largest step of the
+ * sequence's head.  bf16 queries as for pa_decode_q4, fp16 outputs within +-65504 as for pa_cache_read_q8.
+ * PA_ERR_UNSUPPORTED as for pa_decode_window, in tiles of 64 tokens.
  */
 int pa_decode_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
                  const pa_tensor* v_scale, const pa_tensor* block_tables, const pa_tensor* context_lens,
