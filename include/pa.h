@@ -479,6 +479,12 @@ int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tens
  *   q, out        [T, Hq, 128] fp16/bf16;  the other arguments, arithmetic, errors and status bits as for
  *                 pa_prefill.  Entries of frames that hold no token attended by a query of the call are not read.
  *   window >= 1, sinks >= 0, scale > 0 and finite, else PA_ERR_INVALID.
+ * A weight goes into the value product as one number in fp16, to 2^-11 of itself (pa_decode_window: 2^-22) or, where that is
+ * more, to 2^-25 of the row's largest, and as two in bf16, to 2^-16 of itself.
+ * Every slot of a frame that the call reads must hold finite values, those of tokens that no query or not every query
+ * attends and those beyond L_s among them: their weight is 0, but they are multiplied, so that a value that is not finite
+ * can make NaN of that element of any row of its sequence and head.  (pa_decode_window leaves such slots out.)  Keys
+ * there may hold any bits.
  * A query that is not finite, or attends a key that is NaN, has a row of NaN as in pa_decode_window (pa_prefill leaves
  * zeros there), one whose scores are all -inf zeros.
  * Sequences of one call may share frames.  PA_ERR_UNSUPPORTED for T above about a million rows.

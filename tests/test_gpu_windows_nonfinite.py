@@ -87,3 +87,21 @@ def test_rows_whose_scores_are_all_minus_infinity(pa, dtype, H, g):
     case[1][..., 0] = float("-inf")
     out = run(pa, case, window, sinks)
     assert not out.any() and not single(pa, case, window, sinks, 200).any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H,g", KINDS)
+def test_values(pa, dtype, H, g):
+    """A value that is not finite reaches that element of the rows that attend it, perhaps of others of its sequence and head, and
+    nothing else."""
+    window, sinks, n, c, at = 150, 5, 700, 300, 512
+    case = chunk_case([n, 90], [c, 60], H, g, 16, dtype, window, sinks, 5)
+    clean = run(pa, case, window, sinks)
+    case[2][int(case[3][0, at // 16]), at % 16, 0, 9] = float("inf")
+    out = run(pa, case, window, sinks)
+    p = torch.arange(n - c, n)
+    seen = (at <= p) & (at > p - window)
+    assert not torch.isfinite(out[: c, : g, 9][seen.cuda()]).any()
+    keep = torch.ones(out.shape, dtype=torch.bool, device="cuda")
+    keep[: c, : g, 9] = False
+    assert torch.equal(out[keep], clean[keep])
