@@ -95,10 +95,10 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) { ret
 // fp16 a number beyond the largest is that one.  NaN stays.
 template <typename T, bool CAP>
 __device__ __forceinline__ uint32_t pack_out(float x, float y) {
-  const uint32_t w = pack2<T>(x, y);
-  if (!CAP || !std::is_same<T, __half>::value) return w;
-  const __half2 most = __half2half2(__ushort_as_half(0x7bff));
-  return as_u32(__hmax2_nan(__hmin2_nan(*reinterpret_cast<const __half2*>(&w), most), __hneg2(most)));
+  if (!CAP || !std::is_same<T, __half>::value) return pack2<T>(x, y);
+  uint32_t w;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+  return w;
 }
 template <typename M>
 __device__ __forceinline__ float2 unpack2(uint32_t x);

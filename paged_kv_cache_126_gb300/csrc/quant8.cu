@@ -40,9 +40,9 @@ struct Bits<__half> {
   __device__ __forceinline__ static float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
   // what is beyond fp16's largest number is that one (a code may stand for half a step more than its element); NaN stays
   __device__ __forceinline__ static uint32_t pack(float a, float b) {
-    const __half2 most = __half2half2(__ushort_as_half(0x7bff));
-    const __half2 h = __hmax2_nan(__hmin2_nan(__floats2half2_rn(a, b), most), __hneg2(most));
-    return *reinterpret_cast<const uint32_t*>(&h);
+    uint32_t h;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+    return h;
   }
 };
 template <>
