@@ -174,7 +174,8 @@ struct Q8Format {
 
 namespace {
 
-// Bound by memory while it streams.  8 warps an SM, two on each scheduler, one stage of 64 keys (206 registers at D = 128): 64 sequences of
+// Bound by memory while it streams.  8 warps an SM, two on each scheduler, one stage of 64 keys (heads of 128: 216 registers with up to 4
+// queries a key head, 218 with up to 8, 255 and 20 to 40 bytes of spill stores with more): 64 sequences of
 // 512 to 2048 tokens, 32 heads of 128 in fp16 (674 MB) take 110 us, 6.1 TB/s; 4 x 16384 in bf16 (538 MB) 85 to 87 us, 6.25 TB/s, of which
 // about 4 us pass before the first keys are there and 5 behind the last.  12 warps 118.8 and 94.0 us, 10 warps 114.7 and 90.7 us, 6
 // warps with two stages 132 and 100 us; tiles of 32 keys with 12 warps and two stages 134.6 and 104 us, of 128 keys with 6 warps 132

@@ -11,7 +11,7 @@
 // A warp takes 16 rows of one frame and head, all in registers: their maximum, then their codes, one pass over the data.
 // Frames of more than 16 tokens are as many warps of one block, which exchange their maxima.
 //
-// 16 chunks of 256 to 512 tokens, 8 heads of 128 in bf16 (50 MB): 8.9 us, 5.6 TB/s, 64 registers (87: 10.2 us); read back (50 MB)
+// 16 chunks of 256 to 512 tokens, 8 heads of 128 in bf16 (50 MB): 8.9 us, 5.6 TB/s, 64 registers, of which D = 128 spills 4 to 16 bytes (87, none: 10.2 us); read back (50 MB)
 // 7.5 us, 6.7 TB/s.  A decode step of 64 tokens, 32 heads in fp16: 4.0 us, three loads that wait for one another (lengths, table,
 // step) behind a launch, 4.4 us with a warp a head; read back, up to 16 tokens of each frame (13 MB), 3.5 us.
 #include <cuda_bf16.h>
