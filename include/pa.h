@@ -485,8 +485,8 @@ int pa_decode_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tens
  * attends and those beyond L_s among them: their weight is 0, but they are multiplied, so that a value that is not finite
  * can make NaN of that element of any row of its sequence and head.  (pa_decode_window leaves such slots out.)  Keys
  * there may hold any bits.
- * A query that is not finite, or attends a key that is NaN, has a row of NaN as in pa_decode_window (pa_prefill leaves
- * zeros there), one whose scores are all -inf zeros.
+ * A row among whose scores is a NaN or +inf is NaN, as in pa_decode_window (pa_prefill leaves zeros there); one whose
+ * scores are all -inf is zero.
  * Sequences of one call may share frames.  PA_ERR_UNSUPPORTED for T above about a million rows.
  */
 int pa_prefill_window(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
